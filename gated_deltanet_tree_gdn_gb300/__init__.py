@@ -10,6 +10,13 @@ Python face of libgdntree (C ABI in include/gdn_tree.h):
                                     # commit_verify_packed)
     parent, j, score, n = build_topw(cand_logp, w, max_depth)   # the draft tree
 
+Serving a hybrid model around it (ragged batches, states in a pool, a paged cache):
+
+    o, pool = prefill(...)          # the gated delta rule over whole prompts
+    o, pool = decode_step(...)      # ... and for one token a sequence
+    o, lse = attend(...)            # trees or tokens over a paged cache with a shared prefix
+    new_len = cache_append(...)     # accepted rows (or a prompt's) join the cache
+
 Build the library first with ``python -m gated_deltanet_tree_gdn_gb300.build``.
 """
 
@@ -17,7 +24,8 @@ from ._binding import (  # noqa: F401
     BF16, F32, OK, EINVAL, EUNSUPPORTED, ECUDA, STATUS_OK, STATUS_BAD_TREE,
     STATUS_BAD_PATH, STATUS_TIMEOUT, SYMBOLS, Dims, GdnTreeError, commit, commit_verify,
     library_path, load, strerror, verify, verify_recurrent, verify_packed, commit_packed,
-    commit_verify_packed, STATUS_BAD_LAYOUT, build_topw,
+    commit_verify_packed, STATUS_BAD_LAYOUT, build_topw, AttendDims, prefill, decode_step,
+    attend, attend_workspace, cache_append,
 )
 from .build import build_library  # noqa: F401
 

@@ -21,12 +21,19 @@ STATUS_OK, STATUS_BAD_TREE, STATUS_BAD_PATH, STATUS_TIMEOUT, STATUS_BAD_LAYOUT =
 
 SYMBOLS = ("gdn_tree_verify", "gdn_tree_commit", "gdn_tree_commit_verify",
            "gdn_tree_verify_recurrent", "gdn_tree_verify_packed", "gdn_tree_commit_packed",
-           "gdn_tree_commit_verify_packed", "gdn_tree_build_topw", "gdn_tree_strerror",
-           "gdn_tree_version")
+           "gdn_tree_commit_verify_packed", "gdn_tree_build_topw", "gdn_tree_prefill",
+           "gdn_tree_decode_step", "gdn_tree_attend", "gdn_tree_attend_workspace",
+           "gdn_tree_cache_append", "gdn_tree_strerror", "gdn_tree_version")
 
 
 class Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "Hqk", "Hv", "dk", "dv", "dtype")]
+
+
+class AttendDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "N", "Hq", "Hkv", "D", "dtype",
+                                              "page_size", "n_pages", "table_width",
+                                              "prefix_len")]
 
 
 class GdnTreeError(RuntimeError):
@@ -77,6 +84,19 @@ def load(path: str | None = None):
     lib.gdn_tree_commit_verify_packed.restype = ctypes.c_int
     lib.gdn_tree_build_topw.argtypes = [fp, i32, i32, i32, i32, i32, ip, ip, fp, ip, vp]
     lib.gdn_tree_build_topw.restype = ctypes.c_int
+    lib.gdn_tree_prefill.argtypes = [vp, vp, vp, fp, fp, ip, i32, fp, fp, ip, i32, vp, Dims, ip,
+                                     vp]
+    lib.gdn_tree_prefill.restype = ctypes.c_int
+    lib.gdn_tree_decode_step.argtypes = [vp, vp, vp, fp, fp, fp, fp, ip, i32, vp, Dims, ip, vp]
+    lib.gdn_tree_decode_step.restype = ctypes.c_int
+    lib.gdn_tree_attend.argtypes = [vp, vp, vp, ip, ip, vp, vp, ip, ip, ip, ctypes.c_float, vp,
+                                    fp, AttendDims, ip, vp, ctypes.c_size_t, vp]
+    lib.gdn_tree_attend.restype = ctypes.c_int
+    lib.gdn_tree_attend_workspace.argtypes = [AttendDims]
+    lib.gdn_tree_attend_workspace.restype = ctypes.c_size_t
+    lib.gdn_tree_cache_append.argtypes = [vp, vp, ip, ip, i32, ip, vp, vp, ip, ip, ip, AttendDims,
+                                          ip, vp]
+    lib.gdn_tree_cache_append.restype = ctypes.c_int
     lib.gdn_tree_strerror.argtypes = [ctypes.c_int]
     lib.gdn_tree_strerror.restype = ctypes.c_char_p
     lib.gdn_tree_version.argtypes = []
@@ -464,3 +484,216 @@ def build_topw(cand_logp, w: int, max_depth: int, *, parent=None, cand_index=Non
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_build_topw")
     return parent, cand_index, score, n_built
+
+
+# ---------------------------------------------------------------------------
+# serving a hybrid model: prefill, decoding step, attention, cache
+# ---------------------------------------------------------------------------
+
+def _most_rows(cu) -> int:
+    return int((cu[1:] - cu[:-1]).max().item()) if cu.shape[0] > 1 else 0
+
+
+def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None, N_max=None,
+            pool_out=None, o=None, dev_status=None, stream=None):
+    """The gated delta rule over whole sequences (C ABI gdn_tree_prefill).
+    Returns (o, pool_out).
+
+    q, k [T,Hqk,dk], v [T,Hv,dv] (bf16 or fp32); log_alpha, beta [T,Hv]; cu_tokens [B+1]
+    int32 row offsets; state_pool [n_slots,Hv,dk,dv] fp32 with state_slot [B] (None: slot
+    b) holds the state each sequence starts from.  o [T,Hv,dv] is allocated when not given;
+    pool_out=state_pool updates in place, a new pool starts as a copy of state_pool.
+    N_max is the longest sequence (computed from cu_tokens on the host if None)."""
+    T, Hqk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    B = cu_tokens.shape[0] - 1
+    dt = q.dtype
+    code = _dtype_code(q)
+    _check(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+    _check(q, "q", dt)
+    _check(k, "k", dt, (T, Hqk, dk))
+    _check(v, "v", dt, (T, Hv, dv))
+    _check(log_alpha, "log_alpha", torch.float32, (T, Hv))
+    _check(beta, "beta", torch.float32, (T, Hv))
+    _check(state_pool, "state_pool", torch.float32, (state_pool.shape[0], Hv, dk, dv))
+    n_slots = _slots(state_slot, B, state_pool)
+    if N_max is None:
+        N_max = _most_rows(cu_tokens)
+    if pool_out is None:
+        pool_out = state_pool.clone()
+    if o is None:
+        o = torch.empty((T, Hv, dv), dtype=dt, device=q.device)
+    _check(pool_out, "pool_out", torch.float32, state_pool.shape)
+    _check(o, "o", dt, (T, Hv, dv))
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+    rc = load().gdn_tree_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
+                                 _ptr(cu_tokens), T, _ptr(state_pool), _ptr(pool_out),
+                                 _ptr(state_slot), n_slots, _ptr(o),
+                                 Dims(B, N_max, Hqk, Hv, dk, dv, code), _ptr(dev_status),
+                                 _stream(stream))
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_prefill")
+    return o, pool_out
+
+
+def decode_step(q, k, v, log_alpha, beta, state_pool, *, state_slot=None, pool_out=None, o=None,
+                dev_status=None, stream=None):
+    """The gated delta rule for one token of each sequence (C ABI gdn_tree_decode_step).
+    Returns (o, pool_out).
+
+    q, k [B,Hqk,dk], v [B,Hv,dv] (bf16 or fp32); log_alpha, beta [B,Hv] fp32; state_pool
+    [n_slots,Hv,dk,dv] fp32 with state_slot [B] (None: slot b).  pool_out=state_pool steps
+    in place; a new pool starts as a copy of state_pool."""
+    B, Hqk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    dt = q.dtype
+    code = _dtype_code(q)
+    _check(q, "q", dt)
+    _check(k, "k", dt, (B, Hqk, dk))
+    _check(v, "v", dt, (B, Hv, dv))
+    _check(log_alpha, "log_alpha", torch.float32, (B, Hv))
+    _check(beta, "beta", torch.float32, (B, Hv))
+    _check(state_pool, "state_pool", torch.float32, (state_pool.shape[0], Hv, dk, dv))
+    n_slots = _slots(state_slot, B, state_pool)
+    if pool_out is None:
+        pool_out = state_pool.clone()
+    if o is None:
+        o = torch.empty((B, Hv, dv), dtype=dt, device=q.device)
+    _check(pool_out, "pool_out", torch.float32, state_pool.shape)
+    _check(o, "o", dt, (B, Hv, dv))
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+    rc = load().gdn_tree_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
+                                     _ptr(state_pool), _ptr(pool_out), _ptr(state_slot), n_slots,
+                                     _ptr(o), Dims(B, 1, Hqk, Hv, dk, dv, code),
+                                     _ptr(dev_status), _stream(stream))
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_decode_step")
+    return o, pool_out
+
+
+def _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt):
+    n_pages, page = k_cache.shape[0], k_cache.shape[1]
+    _check(k_cache, "k_cache", dt, (n_pages, page, Hkv, D))
+    _check(v_cache, "v_cache", dt, (n_pages, page, Hkv, D))
+    _check(page_table, "page_table", torch.int32, (B, page_table.shape[1]))
+    _check(context_len, "context_len", torch.int32, (B,))
+    return n_pages, page, page_table.shape[1]
+
+
+def attend_workspace(dims: AttendDims) -> int:
+    """Bytes of device memory that ``attend`` needs for these dims."""
+    return load().gdn_tree_attend_workspace(dims)
+
+
+_attend_cache: dict = {}
+
+
+def attend(q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len, *,
+           prefix_pages=None, prefix_len=0, scale=None, N_max=None, o=None, lse=None,
+           workspace=None, dev_status=None, stream=None):
+    """Attention of draft trees over a paged cache with a shared prefix (C ABI
+    gdn_tree_attend).  Returns (o, lse).
+
+    q [T,Hq,D] and the rows' own k, v [T,Hkv,D] (both None: the rows see the cache alone);
+    parent [T] int32 (None: every sequence's rows are a chain, causal attention); cu_nodes
+    [B+1]; k_cache, v_cache [n_pages,page_size,Hkv,D]; page_table [B,width] int32 and
+    context_len [B] int32: each sequence's own context; prefix_pages [ceil(prefix_len /
+    page_size)] int32: the rows that every sequence sees before its own.  scale defaults to
+    1/sqrt(D).  o [T,Hq,D], lse [T,Hq] fp32 and workspace (``attend_workspace`` bytes, uint8)
+    are allocated when not given.  N_max is the most rows of one sequence (computed from
+    cu_nodes on the host if None)."""
+    T, Hq, D = q.shape
+    B = cu_nodes.shape[0] - 1
+    Hkv = k_cache.shape[2]
+    dt = q.dtype
+    code = _dtype_code(q)
+    _check(q, "q", dt)
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together or not at all")
+    if k is not None:
+        _check(k, "k", dt, (T, Hkv, D))
+        _check(v, "v", dt, (T, Hkv, D))
+    if parent is not None:
+        _check(parent, "parent", torch.int32, (T,))
+    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+    n_pages, page, width = _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt)
+    if prefix_len:
+        _check(prefix_pages, "prefix_pages", torch.int32, (-(-prefix_len // page),))
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
+    if o is None:
+        o = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _check(o, "o", dt, (T, Hq, D))
+    _check(lse, "lse", torch.float32, (T, Hq))
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+    lib = load()
+    key = (B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len)
+    known = _attend_cache.get(key)
+    if known is None:
+        d = AttendDims(*key)
+        known = d, lib.gdn_tree_attend_workspace(d)
+        if len(_attend_cache) < 256:
+            _attend_cache[key] = known
+    d, need = known
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, {need} are needed")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    rc = lib.gdn_tree_attend(_ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(cu_nodes),
+                             _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(context_len),
+                             _ptr(prefix_pages) if prefix_len else None,
+                             D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), d,
+                             _ptr(dev_status), _ptr(workspace) if need else None, need,
+                             _stream(stream))
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_attend")
+    return o, lse
+
+
+def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, path=None,
+                 path_len=None, N_max=None, new_len=None, dev_status=None, stream=None):
+    """Rows join the paged cache of their sequences (C ABI gdn_tree_cache_append): the
+    attention's counterpart of ``commit``.  Returns new_len [B] int32, the context lengths
+    after the call.
+
+    k, v [T,Hkv,D]; with path [B,Lmax] and path_len [B] int32 the accepted nodes of each
+    tree, else all rows of each sequence.  k_cache, v_cache [n_pages,page_size,Hkv,D] are
+    written in place at rows context_len[b] .. of the pages that page_table [B,width]
+    already holds.  context_len itself is not changed."""
+    T, Hkv, D = k.shape
+    B = cu_nodes.shape[0] - 1
+    dt = k.dtype
+    code = _dtype_code(k)
+    _check(k, "k", dt)
+    _check(v, "v", dt, (T, Hkv, D))
+    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+    n_pages, page, width = _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt)
+    Lmax = 0
+    if (path is None) != (path_len is None):
+        raise ValueError("path and path_len are given together or not at all")
+    if path is not None:
+        Lmax = path.shape[1]
+        _check(path, "path", torch.int32, (B, Lmax))
+        _check(path_len, "path_len", torch.int32, (B,))
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
+    if new_len is None:
+        new_len = torch.empty((B,), dtype=torch.int32, device=k.device)
+    _check(new_len, "new_len", torch.int32, (B,))
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+    d = AttendDims(B, T, N_max, Hkv, Hkv, D, code, page, n_pages, width, 0)
+    rc = load().gdn_tree_cache_append(_ptr(k), _ptr(v), _ptr(path), _ptr(path_len), Lmax,
+                                      _ptr(cu_nodes), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(page_table), _ptr(context_len), _ptr(new_len), d,
+                                      _ptr(dev_status), _stream(stream))
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_cache_append")
+    return new_len

@@ -62,6 +62,28 @@ int check_dims(const gdn_tree_dims& d) {
   return GDN_TREE_OK;
 }
 
+// the dims of a rule over sequences of any length (prefill, decoding step)
+int check_rule_dims(gdn_tree_dims d) {
+  if (d.N < 0) return GDN_TREE_EINVAL;
+  d.N = 1;  // the tree calls' limit on N does not apply
+  return check_dims(d);
+}
+
+int check_attend_dims(const gdn_tree_attend_dims& d) {
+  if (d.B < 0 || d.T < 0 || d.N < 0 || d.Hq <= 0 || d.Hkv <= 0 || d.D <= 0 || d.page_size < 1 ||
+      d.n_pages < 0 || d.table_width < 0 || d.prefix_len < 0)
+    return GDN_TREE_EINVAL;
+  if (d.Hq % d.Hkv != 0) return GDN_TREE_EINVAL;
+  if (d.dtype != GDN_TREE_BF16 && d.dtype != GDN_TREE_F32) return GDN_TREE_EUNSUPPORTED;
+  if (!supported_head_dim(d.D) || d.B > 65535) return GDN_TREE_EUNSUPPORTED;
+  // positions within a sequence and rows of a key head's query block are 32-bit numbers
+  if ((long long)d.table_width * d.page_size > 0x7fffffffll - 4096 ||
+      d.prefix_len > 0x7fffffff - 4096 || (long long)d.T * d.Hq > 0x7fffffffll - 4096 ||
+      (long long)d.Hkv * d.D > 0x7fffffffll / 8)
+    return GDN_TREE_EUNSUPPORTED;
+  return GDN_TREE_OK;
+}
+
 // Per-sequence status words start at GDN_TREE_STATUS_OK; the kernels raise
 // them with atomicMax, so that no unit's report can be lost to another's.
 cudaError_t clear_status(int32_t* st, int B, cudaStream_t stream) {
@@ -401,6 +423,139 @@ int gdn_tree_build_topw(const float* cand_logp, int32_t B, int32_t N, int32_t c,
   const cudaError_t err = gdn::launch_tree_topw(cand_logp, B, N, c, w, max_depth, parent,
                                                 cand_index, score, n_built,
                                                 static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+static int rule_call(const void* q, const void* k, const void* v, const float* log_alpha,
+                     const float* beta, const float* pool_in, float* pool_out, void* o,
+                     const gdn_tree_dims& dims, const gdn::SeqLayout& lay, int32_t T,
+                     int32_t* dev_status, bool step, void* stream) {
+  const void* ptrs[] = {pool_in, pool_out};
+  for (const void* p : ptrs)
+    if (p == nullptr || !aligned16(p)) return GDN_TREE_EINVAL;
+  const void* rows[] = {q, k, v, log_alpha, beta, o};
+  for (const void* p : rows)
+    if ((p == nullptr && T > 0) || !aligned16(p)) return GDN_TREE_EINVAL;
+  if (dev_status && !aligned4(dev_status)) return GDN_TREE_EINVAL;
+  const int slots = lay.slot ? lay.n_slots : dims.B;
+  if (partial_overlap(pool_in, pool_out, (size_t)slots * dims.Hv * dims.dk * dims.dv * 4))
+    return GDN_TREE_EINVAL;
+  const gdn::RuleArgs a{q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, dev_status, lay};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
+  const cudaError_t err = step ? gdn::launch_decode_step(a, st) : gdn::launch_prefill(a, st);
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_prefill(const void* q, const void* k, const void* v, const float* log_alpha,
+                     const float* beta, const int32_t* cu_tokens, int32_t T,
+                     const float* pool_in, float* pool_out, const int32_t* state_slot,
+                     int32_t n_slots, void* o, gdn_tree_dims dims, int32_t* dev_status,
+                     void* stream) {
+  int rc = check_rule_dims(dims);
+  if (rc != GDN_TREE_OK) return rc;
+  gdn::SeqLayout lay;
+  rc = check_packed(cu_tokens, T, state_slot, n_slots, dims.B, &lay);
+  if (rc != GDN_TREE_OK) return rc;
+  if (dims.B == 0) return GDN_TREE_OK;  // nothing to do
+  return rule_call(q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, lay, T, dev_status,
+                   false, stream);
+}
+
+int gdn_tree_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,
+                         const float* beta, const float* pool_in, float* pool_out,
+                         const int32_t* state_slot, int32_t n_slots, void* o,
+                         gdn_tree_dims dims, int32_t* dev_status, void* stream) {
+  dims.N = 1;
+  const int rc = check_rule_dims(dims);
+  if (rc != GDN_TREE_OK) return rc;
+  if (n_slots < 0 || (state_slot == nullptr && n_slots < dims.B)) return GDN_TREE_EINVAL;
+  if (state_slot != nullptr && !aligned4(state_slot)) return GDN_TREE_EINVAL;
+  if (dims.B == 0) return GDN_TREE_OK;  // nothing to do
+  gdn::SeqLayout lay;
+  lay.slot = state_slot;
+  lay.n_slots = n_slots;
+  return rule_call(q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, lay, dims.B, dev_status,
+                   true, stream);
+}
+
+size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims) {
+  if (check_attend_dims(dims) != GDN_TREE_OK || dims.B == 0 || dims.T == 0 || dims.N == 0)
+    return 0;
+  return gdn::attend_workspace_bytes(dims);
+}
+
+int gdn_tree_attend(const void* q, const void* k, const void* v, const int32_t* parent,
+                    const int32_t* cu_nodes, const void* k_cache, const void* v_cache,
+                    const int32_t* page_table, const int32_t* context_len,
+                    const int32_t* prefix_pages, float scale, void* o, float* lse,
+                    gdn_tree_attend_dims dims, int32_t* dev_status, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const int rc = check_attend_dims(dims);
+  if (rc != GDN_TREE_OK) return rc;
+  if (dims.N > gdn::kMaxNLongHost) return GDN_TREE_EUNSUPPORTED;
+  if (dims.B == 0 || dims.T == 0 || dims.N == 0) return GDN_TREE_OK;  // nothing to do
+  if ((k == nullptr) != (v == nullptr)) return GDN_TREE_EINVAL;
+  const void* need[] = {q, o};
+  for (const void* p : need)
+    if (p == nullptr || !aligned16(p)) return GDN_TREE_EINVAL;
+  // the cache may be absent where no row of it can be seen
+  const bool cached = dims.n_pages > 0 && (dims.prefix_len > 0 || dims.table_width > 0);
+  const void* cache[] = {k_cache, v_cache};
+  for (const void* p : cache)
+    if ((cached && p == nullptr) || !aligned16(p)) return GDN_TREE_EINVAL;
+  if (!aligned16(k) || !aligned16(v)) return GDN_TREE_EINVAL;
+  const void* ints[] = {cu_nodes, context_len};
+  for (const void* p : ints)
+    if (p == nullptr || !aligned4(p)) return GDN_TREE_EINVAL;
+  const void* opt[] = {parent, page_table, prefix_pages, lse, dev_status};
+  for (const void* p : opt)
+    if (!aligned4(p)) return GDN_TREE_EINVAL;
+  if ((dims.table_width > 0 && page_table == nullptr) ||
+      (dims.prefix_len > 0 && prefix_pages == nullptr))
+    return GDN_TREE_EINVAL;
+  const size_t want = gdn::attend_workspace_bytes(dims);
+  if (want > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < want))
+    return GDN_TREE_EINVAL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
+  const gdn::AttendArgs a{q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len,
+                          prefix_pages, scale, o, lse, dims, dev_status, workspace};
+  const cudaError_t err = gdn::launch_attend(a, st);
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_cache_append(const void* k, const void* v, const int32_t* path,
+                          const int32_t* path_len, int32_t Lmax, const int32_t* cu_nodes,
+                          void* k_cache, void* v_cache, const int32_t* page_table,
+                          const int32_t* context_len, int32_t* new_len,
+                          gdn_tree_attend_dims dims, int32_t* dev_status, void* stream) {
+  dims.Hq = dims.Hkv;
+  dims.prefix_len = 0;
+  const int rc = check_attend_dims(dims);
+  if (rc != GDN_TREE_OK) return rc;
+  if ((path_len == nullptr) != (path == nullptr) && !(path_len != nullptr && Lmax == 0))
+    return GDN_TREE_EINVAL;
+  if (path_len != nullptr && Lmax < 0) return GDN_TREE_EINVAL;
+  if (dims.B == 0) return GDN_TREE_OK;
+  const bool rows = dims.T > 0 && dims.table_width > 0 && dims.n_pages > 0;
+  const void* data[] = {k, v, k_cache, v_cache};
+  for (const void* p : data)
+    if ((rows && p == nullptr) || !aligned16(p)) return GDN_TREE_EINVAL;
+  const void* ints[] = {cu_nodes, context_len};
+  for (const void* p : ints)
+    if (p == nullptr || !aligned4(p)) return GDN_TREE_EINVAL;
+  const void* opt[] = {path, path_len, page_table, new_len, dev_status};
+  for (const void* p : opt)
+    if (!aligned4(p)) return GDN_TREE_EINVAL;
+  if (dims.table_width > 0 && page_table == nullptr) return GDN_TREE_EINVAL;
+  if (new_len && any_overlap(new_len, (size_t)dims.B * 4, context_len, (size_t)dims.B * 4))
+    return GDN_TREE_EINVAL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
+  const gdn::AppendArgs a{k, v, path, path_len, Lmax, cu_nodes, k_cache, v_cache, page_table,
+                          context_len, new_len, dims, dev_status};
+  const cudaError_t err = gdn::launch_cache_append(a, st);
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
 }
 

@@ -159,6 +159,52 @@ cudaError_t launch_tree_topw(const float* cand_logp, int B, int N, int c, int w,
 // single-branch recurrent verification (the measurement baseline)
 cudaError_t launch_verify_recurrent(const VerifyArgs& a, cudaStream_t stream);
 
+// the gated delta rule over whole sequences (lay.cu set) or one token of each (lay.cu
+// null): rows q .. o as in the packed layout, states pool_in -> pool_out
+struct RuleArgs {
+  const void *q, *k, *v;
+  const float *log_alpha, *beta;
+  const float* pool_in;
+  float* pool_out;
+  void* o;
+  gdn_tree_dims d;
+  int32_t* dev_status;
+  SeqLayout lay = {};
+};
+cudaError_t launch_prefill(const RuleArgs& a, cudaStream_t stream);
+cudaError_t launch_decode_step(const RuleArgs& a, cudaStream_t stream);
+
+// attention over a paged cache with a shared prefix
+struct AttendArgs {
+  const void *q, *k, *v;
+  const int32_t *parent, *cu;
+  const void *k_cache, *v_cache;
+  const int32_t *page_table, *context_len, *prefix_pages;
+  float scale;
+  void* o;
+  float* lse;
+  gdn_tree_attend_dims d;
+  int32_t* dev_status;
+  void* workspace;
+};
+size_t attend_workspace_bytes(const gdn_tree_attend_dims& d);
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream);
+cudaError_t launch_attend_generic(const AttendArgs& a, cudaStream_t stream);
+
+// rows of accepted paths (or all rows) into the pages of a cache
+struct AppendArgs {
+  const void *k, *v;
+  const int32_t *path, *path_len;
+  int32_t Lmax;
+  const int32_t* cu;
+  void *k_cache, *v_cache;
+  const int32_t *page_table, *context_len;
+  int32_t* new_len;
+  gdn_tree_attend_dims d;
+  int32_t* dev_status;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
+
 bool commit_verify_tc_supported(const gdn_tree_dims& d, int prev_N, int Lmax);
 cudaError_t launch_commit_verify_tc(const CommitVerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_commit_verify(const CommitVerifyArgs& a, cudaStream_t stream);

@@ -69,6 +69,7 @@
 #ifndef GDN_TREE_H
 #define GDN_TREE_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -287,6 +288,132 @@ int gdn_tree_commit_verify_packed(const int32_t *prev_path, const int32_t *prev_
 int gdn_tree_build_topw(const float *cand_logp, int32_t B, int32_t N, int32_t c, int32_t w,
                         int32_t max_depth, int32_t *parent, int32_t *cand_index, float *score,
                         int32_t *n_built, void *stream);
+
+/*
+ * Serving a hybrid model around the tree verification
+ * ---------------------------------------------------
+ * The four calls below are what a server of Gated DeltaNet layers (and of the
+ * attention layers between them) needs next to verify and commit: the state of a
+ * prompt, a step without a draft, the attention of a draft tree over a paged
+ * cache, and the rows that join that cache.  They use the packed layout above:
+ * sequence b owns rows cu[b] .. cu[b+1]-1 of the packed arrays, its state is
+ * pool[state_slot[b]].  Ownership, alignment, asynchrony and dev_status are as for
+ * the other calls; dims.N is the most rows of one sequence.
+ */
+
+/*
+ * gdn_tree_prefill -- the gated delta rule over whole sequences (prompts).
+ *
+ * For every sequence b and v-head h, from S = pool_in[state_slot[b]][h], for each
+ * of its tokens t in order:
+ *     S <- alpha_t (I - beta_t k_t k_t^T) S + beta_t k_t v_t^T,   o_t = S^T q_t,
+ * and pool_out[state_slot[b]][h] = S at the end (a sequence of no tokens keeps its
+ * state: it is copied).  State slots that no sequence names are left as they are.
+ *
+ *   cu_tokens   [B + 1] int32: 0 <= cu_tokens[b] <= cu_tokens[b+1] <= T and
+ *               cu_tokens[b+1] - cu_tokens[b] <= dims.N
+ *   q, k        [T, Hqk, dk];  v, o [T, Hv, dv];  log_alpha, beta [T, Hv]
+ *   pool_in, pool_out  [n_slots, Hv, dk, dv] fp32; pool_out may be pool_in
+ *               (in place), any other overlap is refused.  Slots must be distinct.
+ *   log_alpha   any value <= 0, -inf (alpha = 0, the state is forgotten) included
+ * A sequence whose rows or slot are out of range gets GDN_TREE_STATUS_BAD_LAYOUT
+ * and its outputs are left unwritten.  dims.N has no upper limit here.
+ */
+int gdn_tree_prefill(const void *q, const void *k, const void *v, const float *log_alpha,
+                     const float *beta, const int32_t *cu_tokens, int32_t T,
+                     const float *pool_in, float *pool_out, const int32_t *state_slot,
+                     int32_t n_slots, void *o, gdn_tree_dims dims, int32_t *dev_status,
+                     void *stream);
+
+/*
+ * gdn_tree_decode_step -- the same rule for one token of each of B sequences:
+ * q, k [B, Hqk, dk], v, o [B, Hv, dv], log_alpha, beta [B, Hv]; dims.N is ignored.
+ */
+int gdn_tree_decode_step(const void *q, const void *k, const void *v, const float *log_alpha,
+                         const float *beta, const float *pool_in, float *pool_out,
+                         const int32_t *state_slot, int32_t n_slots, void *o,
+                         gdn_tree_dims dims, int32_t *dev_status, void *stream);
+
+/* Shapes of the attention calls.  G = Hq / Hkv query heads share a key head. */
+typedef struct {
+  int32_t B;         /* sequences                                               */
+  int32_t T;         /* rows (nodes, tokens) of the packed arrays               */
+  int32_t N;         /* the most rows of one sequence                           */
+  int32_t Hq, Hkv;   /* query heads, key/value heads (Hq a multiple of Hkv)     */
+  int32_t D;         /* head size: 16, 32, 48, ..., 128                         */
+  int32_t dtype;     /* GDN_TREE_BF16 or GDN_TREE_F32: q, k, v, o and the cache */
+  int32_t page_size; /* rows of a cache page (>= 1, any number)                 */
+  int32_t n_pages;   /* pages of the cache                                      */
+  int32_t table_width; /* entries of a row of page_table                        */
+  int32_t prefix_len;  /* rows of the shared prefix (0: none)                   */
+} gdn_tree_attend_dims;
+
+/*
+ * gdn_tree_attend -- attention of draft trees over a paged cache, the prefix that
+ * all sequences share computed once for all of them.
+ *
+ * Row i of sequence b sees, in this order, the prefix_len shared rows, the
+ * context_len[b] rows of its own context, and the rows of its own tree on the
+ * root-to-i path (i included).  For each query head h, with the key head h / G:
+ *     o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i),
+ *     lse_i = log sum_j exp(scale q_i.k_j).
+ * A tree of one node is the decoding of a single token; a chain (parent NULL) is
+ * the causal attention of a chunk of a prompt.
+ *
+ *   q, o         [T, Hq, D];  k, v [T, Hkv, D]: the rows' own keys and values, not
+ *                yet in the cache.  k and v may both be NULL: the rows then see the
+ *                cache alone.
+ *   parent       [T] int32, -1 <= parent < i within the sequence, or NULL: a chain
+ *   cu_nodes     [B + 1] int32, as above; a sequence has at most dims.N rows
+ *   k_cache, v_cache  [n_pages, page_size, Hkv, D]
+ *   page_table   [B, table_width] int32: row p of sequence b's context is row
+ *                p % page_size of page page_table[b][p / page_size]; entries past
+ *                its context are not read
+ *   context_len  [B] int32, 0 <= context_len[b] <= table_width * page_size
+ *   prefix_pages [ceil(prefix_len / page_size)] int32: the shared prefix's pages
+ *                (NULL when prefix_len is 0)
+ *   lse          [T, Hq] fp32 or NULL
+ *   workspace    gdn_tree_attend_workspace(dims) bytes of device memory, 16-byte
+ *                aligned (NULL when that is 0); its contents are not kept
+ * A row that sees nothing (no context, k and v NULL) gives o = 0, lse = -inf.
+ * Cache rows past a length are not used, whatever they hold.
+ * Limits: 1 <= N <= 1024; D in {16, 32, ..., 128}; B <= 65535.
+ * dev_status[b]: GDN_TREE_STATUS_BAD_TREE (a parent out of range) or
+ * GDN_TREE_STATUS_BAD_LAYOUT (rows, length or page out of range: nothing outside the
+ * arrays is read) or GDN_TREE_STATUS_TIMEOUT; that sequence's o and lse are then
+ * unspecified.  A bad page of the shared prefix is every sequence's error.
+ */
+int gdn_tree_attend(const void *q, const void *k, const void *v, const int32_t *parent,
+                    const int32_t *cu_nodes, const void *k_cache, const void *v_cache,
+                    const int32_t *page_table, const int32_t *context_len,
+                    const int32_t *prefix_pages, float scale, void *o, float *lse,
+                    gdn_tree_attend_dims dims, int32_t *dev_status, void *workspace,
+                    size_t workspace_bytes, void *stream);
+size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims);
+
+/*
+ * gdn_tree_cache_append -- rows join the cache of their sequences: the attention's
+ * counterpart of the state commitment.  For each sequence b and j < n_b,
+ *     cache row context_len[b] + j of sequence b  <-  row cu_nodes[b] + path[b][j]
+ * of k and v, and new_len[b] = context_len[b] + n_b, where n_b = path_len[b] (an
+ * accepted root-to-node path of a draft tree).  With path and path_len NULL all rows
+ * of the sequence are appended in order (a prompt), and Lmax is ignored.
+ *
+ *   path         [B, Lmax] int32, entries 0 <= path < rows of the sequence
+ *   path_len     [B] int32, 0 <= path_len[b] <= Lmax
+ *   new_len      [B] int32 or NULL; must not overlap context_len
+ * page_table must already hold the pages that the new rows fall into.  Other shapes
+ * as for gdn_tree_attend (dims.Hq and prefix_len are ignored; N has no upper limit).
+ * The pages written must belong to one sequence each.
+ * dev_status[b]: GDN_TREE_STATUS_BAD_PATH or GDN_TREE_STATUS_BAD_LAYOUT; the rows at
+ * fault are not written, and with an invalid cu_nodes, path_len or context_len none
+ * are and new_len[b] = context_len[b].
+ */
+int gdn_tree_cache_append(const void *k, const void *v, const int32_t *path,
+                          const int32_t *path_len, int32_t Lmax, const int32_t *cu_nodes,
+                          void *k_cache, void *v_cache, const int32_t *page_table,
+                          const int32_t *context_len, int32_t *new_len,
+                          gdn_tree_attend_dims dims, int32_t *dev_status, void *stream);
 
 /* Human-readable text for a return code or a device status code. */
 const char *gdn_tree_strerror(int code);
