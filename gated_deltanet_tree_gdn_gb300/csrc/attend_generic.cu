@@ -115,6 +115,7 @@ attend_generic_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
       }
       __syncthreads();
       float s[kKeys], top = m;
+      bool seen[kKeys];
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) {
         const int j = ln + kLanes * i;
@@ -132,6 +133,7 @@ attend_generic_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
           if (!tree) sees = sees && jj <= node;
           else sees = sees && ((sAnc[r * (kMaxNLong / 32) + (jj >> 5 & (kMaxNLong / 32 - 1))] >> (jj & 31)) & 1u);
         }
+        seen[i] = sees;
         s[i] = sees ? acc : -INFINITY;
         top = fmaxf(top, s[i]);
       }
@@ -145,7 +147,7 @@ attend_generic_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
       for (int i = 0; i < kKeys; ++i) {
         const float p = expf(s[i] - base);  // (-inf: 0)
         sum += p;
-        sP[r * (kN + 1) + ln + kLanes * i] = p;
+        sP[r * (kN + 1) + ln + kLanes * i] = seen[i] ? p : -1.f;
       }
 #pragma unroll
       for (int off = 1; off < kLanes; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -156,6 +158,7 @@ attend_generic_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
       for (int i = 0; i < kCols; ++i) O[i] *= keep;
       for (int j = 0; j < kN; ++j) {
         const float p = sP[r * (kN + 1) + j];
+        if (p < 0.f) continue;  // not seen, whatever v holds
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
           const int c = ln + kLanes * i;
@@ -199,12 +202,6 @@ cudaError_t launch_typed(const AttendArgs& a, cudaStream_t stream) {
 cudaError_t launch_attend_generic(const AttendArgs& a, cudaStream_t stream) {
   return a.d.dtype == GDN_TREE_BF16 ? launch_typed<__nv_bfloat16>(a, stream)
                                     : launch_typed<float>(a, stream);
-}
-
-size_t attend_workspace_bytes(const gdn_tree_attend_dims&) { return 0; }
-
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
-  return launch_attend_generic(a, stream);
 }
 
 }  // namespace gdn

@@ -1,0 +1,734 @@
+// attend_tc.cu -- attention over a paged cache on the tensor cores (bf16, D <= 128):
+// blocks of 256 query rows against 128 keys at a time, and the joining of parts.
+//
+// A unit is one key head, up to 256 query rows (two tiles of 128: row = node * G + g) and
+// a range of key tiles; it computes, with the running maximum and sum of a softmax,
+//     S = Q K^T,  P = exp2(c S - m),  l += sum P,  O += P V        (c = scale log2 e)
+// and writes O / l, or, where the keys of the rows are cut into parts, the part's O / l
+// and lse, which attend_join_kernel adds up:
+//     lse = log sum_s e^{lse_s},   o = sum_s e^{lse_s - lse} o_s.
+// Two kinds of units:
+//   - a sequence's: the rows of one sequence against its own context and tree (and, where
+//     a sequence has rows enough to fill the tiles, the shared prefix);
+//   - the prefix's: 256 rows of the whole batch, whatever sequence they are of, against
+//     the shared prefix, which is then read once for every 256 rows of the batch and not
+//     once for every sequence.
+//
+// Roles (11 warps, so that a thread may hold 168 registers): warps 0-3 and 4-7 the softmax
+// of row tile 0 and 1, a thread a row; warp 8 brings K tiles, warp 9 V tiles (16-byte
+// cp.async, so that any page size and any page order works and rows past a length are
+// filled with zeros, whatever they hold); one thread of warp 10 issues the MMAs.  S and O are fp32 in TMEM; P goes back to TMEM as
+// bf16 over the S it came from and is the A operand of P V.  Issue order P0 V, S0', P1 V,
+// S1': one tile's MMAs run while the other's softmax does.
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the one its
+// sums use (exact either way: P and l stay far below the overflow of their types).
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTile = 128;               // rows of a tile, keys of a tile
+constexpr int kThreads = 11 * 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
+
+struct TcArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  const int32_t *parent, *cu;
+  const __nv_bfloat16 *k_cache, *v_cache;
+  const int32_t *table, *ctx, *prefix_pages;
+  float scale;
+  __nv_bfloat16* o;
+  float* lse;
+  gdn_tree_attend_dims d;
+  int32_t* dev_status;
+  float* part_o;    // [slots][T * Hq][D] or null
+  float* part_lse;  // [slots][T * Hq]
+  int slot0;        // first slot of this launch's parts
+  int splits;       // parts of a row's keys in this launch
+  int tiles;        // 256-row blocks a sequence (a batch, for prefix units)
+  int min_rows;     // sequences of fewer rows are not this kernel's
+  bool prefix_units;   // units of the shared prefix over the whole batch
+  bool with_prefix;    // a sequence's units include the prefix
+};
+
+template <int DP>
+struct Smem {
+  static constexpr uint32_t kQ = kTile * DP * 2;   // one row tile
+  static constexpr uint32_t kKV = kTile * DP * 2;  // one K or V tile
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + 2 * kQ;
+  static constexpr uint32_t OFF_V = OFF_K + 2 * kKV;
+  static constexpr uint32_t OFF_PARENT = OFF_V + 2 * kKV;
+  static constexpr uint32_t OFF_BAR = OFF_PARENT + kMaxNLong * 4;
+  static constexpr uint32_t kBytes = OFF_BAR + 256 + 1024;  // + alignment slack
+};
+
+struct Bars {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], drain;
+  uint32_t tmem;
+  int abort;
+  uint32_t badv[2][4];  // own rows of a V tile that hold infinities or NaN (by stage)
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Bars* s,
+                                         uint64_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (ld_acquire_shared(&s->abort)) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      st_release_shared(&s->abort, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+// the same for a whole warp: every lane gets the same answer
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* s,
+                                          uint64_t limit) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, s, limit));
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16u : 0u)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 16-byte chunk n8 of V row `key`, the operand [keys x DP] with DP contiguous
+template <int DP>
+__device__ __forceinline__ uint32_t v_chunk(int key, int n8) {
+  const int r = key & 7;
+  return (uint32_t)((key >> 3) * (DP / 64 * 1024) + (n8 >> 3) * 1024 + r * 128 +
+                    (((n8 & 7) ^ r) << 4));
+}
+
+// bits of a packed pair of bf16 that are infinities or NaN
+__device__ __forceinline__ bool nonfinite2(uint32_t x) {
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+  if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+  if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+  return x;
+}
+
+enum Segment { kPrefix = 0, kContext = 1, kOwn = 2 };
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64_t limit_ns) {
+  using L = Smem<DP>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  Bars* S = reinterpret_cast<Bars*>(smem + L::OFF_BAR);
+  int32_t* sParent = reinterpret_cast<int32_t*>(smem + L::OFF_PARENT);
+  const gdn_tree_attend_dims& d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = d.Hq / d.Hkv;
+
+  // ---- the unit: rows [r0, r1) of key head hk, key tiles [i0, i1) -------------------
+  const int split = blockIdx.x % a.splits;
+  int u = blockIdx.x / a.splits;
+  const int t = u % a.tiles;
+  u /= a.tiles;
+  const int hk = u % d.Hkv, b = u / d.Hkv;  // (prefix units: b = 0)
+  int first = 0, n = 0, ctx = 0;
+  if (!a.prefix_units) {
+    const int stop = a.cu[b + 1];
+    first = a.cu[b];
+    n = stop - first;
+    ctx = a.ctx[b];
+    const long long cap = (long long)d.table_width * d.page_size;
+    if (first < 0 || n < 0 || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
+      if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+      return;
+    }
+    if (n * G < a.min_rows) return;
+  }
+  const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
+  const int r0 = first * G + t * 2 * kTile;
+  if (r0 >= rows_end) return;
+  const int rows = min(2 * kTile, rows_end - r0);
+  const bool two = rows > kTile;
+  const bool own = a.k != nullptr && !a.prefix_units;
+  const bool tree = own && a.parent != nullptr;
+  const int plen = a.prefix_units || a.with_prefix ? d.prefix_len : 0;
+  const int nP = (plen + kTile - 1) / kTile, nC = (ctx + kTile - 1) / kTile;
+  // own keys past the last row's node are seen by none of these rows
+  const int seen = own ? (r0 + rows - 1) / G - first + 1 : 0;
+  const int nO = (seen + kTile - 1) / kTile;
+  const int all = nP + nC + nO;
+  const int i0 = (int)((long long)all * split / a.splits);
+  const int i1 = (int)((long long)all * (split + 1) / a.splits);
+  const int ntiles = i1 - i0;
+  // key tile i: its segment, first key and keys (own tiles from the last to the first, so
+  // that a row follows its path upwards once)
+  auto tile_of = [&](int i, int& seg, int& j0, int& len) {
+    if (i < nP) { seg = kPrefix; j0 = i * kTile; len = plen; }
+    else if (i < nP + nC) { seg = kContext; j0 = (i - nP) * kTile; len = ctx; }
+    else { seg = kOwn; j0 = (all - 1 - i) * kTile; len = seen; }
+  };
+
+  // ---- set up ------------------------------------------------------------------------
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&S->kfull[s], 32);
+      mbar_init(&S->kempty[s], 1);
+      mbar_init(&S->vfull[s], 32);
+      mbar_init(&S->vempty[s], 1);
+      mbar_init(&S->sfull[s], 1);
+      mbar_init(&S->pready[s], kTile);
+      mbar_init(&S->pvdone[s], 1);
+    }
+    mbar_init(&S->drain, 1);
+    S->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 10) tmem_alloc(&S->tmem, 512);
+  // Q, negated where the scale is negative (the maximum is then taken with c >= 0)
+  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+  for (int e = tid; e < 2 * kTile * (DP / 8); e += kThreads) {
+    const int r = e / (DP / 8), c8 = e % (DP / 8);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < rows && 8 * c8 < d.D) {
+      const int rho = r0 + r, tok = rho / G, g = rho - tok * G;
+      x = *reinterpret_cast<const uint4*>(a.q + ((size_t)tok * d.Hq + hk * G + g) * d.D + 8 * c8);
+      x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+    }
+    *reinterpret_cast<uint4*>(smem + L::OFF_Q + (r / kTile) * L::kQ + sw128_chunk(r % kTile, c8)) = x;
+  }
+  bool bad = false;
+  if (tree)
+    for (int i = tid; i < n; i += kThreads) {
+      const int p = a.parent[first + i];
+      bad |= p < -1 || p >= i;
+      sParent[i] = p;
+    }
+  fence_proxy_async_smem();
+  tc_fence_before_sync();
+  bad = __syncthreads_or(bad);
+  tc_fence_after_sync();
+  const uint32_t tmem = S->tmem;
+  constexpr uint32_t kStage = L::kKV;
+
+  if (bad) {
+    if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_TREE);
+  } else if (warp == 8 || warp == 9) {
+    // ---- producers: K (warp 8) or V (warp 9) --------------------------------------------
+    const bool isV = warp == 9;
+    uint64_t* full = isV ? S->vfull : S->kfull;
+    uint64_t* empty = isV ? S->vempty : S->kempty;
+    const __nv_bfloat16* cache = isV ? a.v_cache : a.k_cache;
+    const __nv_bfloat16* mine = isV ? a.v : a.k;
+    const uint32_t base = smem_addr(smem + (isV ? L::OFF_V : L::OFF_K));
+    constexpr int kChunks = DP / 8;             // 16-byte chunks a row
+    constexpr int kRowsAtOnce = 32 / kChunks;   // rows a warp instruction covers
+    const int c8 = lane % kChunks;
+    const bool in_row = 8 * c8 < d.D;
+    for (int i = i0; i < i1; ++i) {
+      const int at = i - i0, st = at & 1;
+      int seg, j0, len;
+      tile_of(i, seg, j0, len);
+      // lane l looks up rows l, 32 + l, 64 + l, 96 + l of the tile
+      int row[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + 32 * e + lane;
+        row[e] = -1;
+        if (j < len) {
+          if (seg == kOwn) {
+            row[e] = first + j;
+          } else {
+            const int pi = j / d.page_size;
+            const int pg = seg == kPrefix ? a.prefix_pages[pi]
+                                          : a.table[(size_t)b * d.table_width + pi];
+            if (pg >= 0 && pg < d.n_pages)
+              row[e] = pg * d.page_size + (j - pi * d.page_size);
+            else if (a.dev_status) {  // a bad page of the prefix is every sequence's error
+              if (seg == kPrefix)
+                for (int bb = 0; bb < d.B; ++bb)
+                  atomicMax(a.dev_status + bb, GDN_TREE_STATUS_BAD_LAYOUT);
+              else
+                atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+            }
+          }
+        }
+      }
+      if (at >= 2 && !wait_warp(&empty[st], ((at >> 1) & 1) ^ 1, S, limit_ns)) break;
+      const __nv_bfloat16* src = (seg == kOwn ? mine : cache) + (size_t)hk * d.D + 8 * c8;
+      const size_t stride = (size_t)d.Hkv * d.D;
+      const uint32_t dst = base + st * kStage;
+      if (isV && seg == kOwn) {
+        // own rows are masked for some of the query rows only: what is not finite is kept
+        // out of the product (0 * inf) and added to the rows that see it at the end
+        if (lane < 4) S->badv[st][lane] = 0u;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
+            const int r = rr + lane / kChunks, key = 32 * e + r;
+            const int x = __shfl_sync(0xffffffffu, row[e], r);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (x >= 0 && in_row) w = *reinterpret_cast<const uint4*>(src + x * stride);
+            if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
+              atomicOr(&S->badv[st][key >> 5], 1u << (key & 31));
+              w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+            }
+            *reinterpret_cast<uint4*>(smem + L::OFF_V + st * kStage + v_chunk<DP>(key, c8)) = w;
+          }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
+            const int r = rr + lane / kChunks, key = 32 * e + r;
+            const int x = __shfl_sync(0xffffffffu, row[e], r);
+            const bool take = x >= 0 && in_row;
+            cp_async16_zfill(dst + (isV ? v_chunk<DP>(key, c8) : sw128_chunk(key, c8)),
+                             take ? src + x * stride : src, take);
+          }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(&full[st]);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 10) {
+    // ---- MMAs --------------------------------------------------------------------------
+    if (lane == 0 && ntiles > 0) {
+      const uint32_t aQ = smem_addr(smem + L::OFF_Q), aK = smem_addr(smem + L::OFF_K),
+                     aV = smem_addr(smem + L::OFF_V);
+      constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t idO = idesc_bf16_f32_bmn(kTile, DP);
+      auto issue_s = [&](int tile, int st) {
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+          const uint32_t off = (uint32_t)((s >> 2) * kSw128TileBytes + (s & 3) * 32);
+          umma_bf16(tmem + tile * kTile, desc_sw128_kmajor(aQ + tile * L::kQ + off),
+                    desc_sw128_kmajor(aK + st * kStage + off), idS, s > 0);
+        }
+        umma_commit(&S->sfull[tile]);
+      };
+      auto issue_pv = [&](int tile, int st, bool acc) {
+        constexpr uint32_t sbo = DP / 64 * 1024;
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          umma_ts(tmem + 2 * kTile + tile * kTile, tmem + tile * kTile + 8 * s,
+                  desc_sw128_mnmajor(aV + st * kStage + (uint32_t)s * 2 * sbo, 1024, sbo), idO,
+                  acc || s > 0);
+        umma_commit(&S->pvdone[tile]);
+      };
+      bool ok = wait_bar(&S->kfull[0], 0, S, limit_ns);
+      if (ok) {
+        issue_s(0, 0);
+        if (two) issue_s(1, 0);
+        umma_commit(&S->kempty[0]);
+      }
+      for (int at = 0; ok && at < ntiles; ++at) {
+        const int st = at & 1, nx = (at + 1) & 1;
+        const uint32_t ph = (at >> 1) & 1;
+        const bool more = at + 1 < ntiles;
+        ok = wait_bar(&S->vfull[st], ph, S, limit_ns) &&
+             wait_bar(&S->pready[0], at & 1, S, limit_ns);
+        if (!ok) break;
+        tc_fence_after_sync();
+        issue_pv(0, st, at > 0);
+        if (!two) umma_commit(&S->vempty[st]);
+        if (more) {
+          ok = wait_bar(&S->kfull[nx], ((at + 1) >> 1) & 1, S, limit_ns);
+          if (!ok) break;
+          issue_s(0, nx);
+          if (!two) umma_commit(&S->kempty[nx]);
+        }
+        if (two) {
+          ok = wait_bar(&S->pready[1], at & 1, S, limit_ns);
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue_pv(1, st, at > 0);
+          umma_commit(&S->vempty[st]);
+          if (more) {
+            issue_s(1, nx);
+            umma_commit(&S->kempty[nx]);
+          }
+        }
+      }
+      // whatever was issued is done before TMEM and the operands go
+      umma_commit(&S->drain);
+      mbar_wait(&S->drain, 0, limit_ns);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- softmax: a thread a row ---------------------------------------------------------
+    const int tile = warp >> 2, r = tile * kTile + (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = tl + tile * kTile, tO = tl + 2 * kTile + tile * kTile;
+    const float c = fabsf(a.scale) * kLog2e;
+    const int rho = min(r0 + r, rows_end - 1), tok = rho / G, node = tok - first;
+    const bool live = r < rows;
+    int walk = node;                   // the next node of the path that is not yet masked
+    float mref = -INFINITY, l = 0.f;   // of c s
+    bool ok = true, poison = false;
+    if (tile == 0 || two) {
+      for (int i = i0; i < i1; ++i) {
+        const int at = i - i0;
+        int seg, j0, len;
+        tile_of(i, seg, j0, len);
+        ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns);
+        if (!ok) break;
+        tc_fence_after_sync();
+        // the keys of this tile that the row sees, a bit a key
+        uint32_t w[4];
+        const int valid = len - j0;
+        const bool masked = seg == kOwn || valid < kTile;
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int left = (seg == kOwn && !tree ? min(valid, node - j0 + 1) : valid) - 32 * e;
+            w[e] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+          }
+          if (seg == kOwn && tree) {
+            uint64_t lo = 0, hi = 0;
+            // a split that holds an upper part of the path's tiles only skips the others
+            while (walk >= j0 + kTile) walk = sParent[walk];
+            while (walk >= j0) {
+              const int off = walk - j0;
+              if (off < 64) lo |= 1ull << off;
+              else hi |= 1ull << (off - 64);
+              walk = sParent[walk];
+            }
+            w[0] &= (uint32_t)lo; w[1] &= (uint32_t)(lo >> 32);
+            w[2] &= (uint32_t)hi; w[3] &= (uint32_t)(hi >> 32);
+          }
+        }
+        float top = -INFINITY;
+        if (!masked) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x[32];
+            tmem_ld_32cols(tS + 32 * e, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, x[j]);
+          }
+          top = c * mx;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x[32];
+            tmem_ld_32cols(tS + 32 * e, x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              top = fmaxf(top, (w[e] >> j) & 1u ? c * x[j] : -INFINITY);
+          }
+        }
+        // (NaN scores: fmaxf drops them here, and they come back as NaN weights)
+        const bool grow = top > mref + kGrow;  // (mref = -inf: any finite top)
+        if (__any_sync(0xffffffffu, grow)) {
+          const float to = grow ? top : mref;
+          const float keep = grow ? (mref == -INFINITY ? 0.f : ex2(mref - to)) : 1.f;
+          if (at > 0) {
+            // O of the tiles before is complete once their last product is
+            ok = wait_warp(&S->pvdone[tile], (at - 1) & 1, S, limit_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e) {
+              float x[32];
+              tmem_ld_32cols(tO + 32 * e, x);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] *= keep;
+              tmem_st_32cols(tO + 32 * e, x);
+            }
+          }
+          l *= keep;
+          mref = to;
+        }
+        const float base = mref == -INFINITY ? 0.f : mref;
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[32];
+          tmem_ld_32cols(tS + 32 * e, x);
+          uint32_t pk[16];
+          if (!masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = ex2(fmaf(c, x[j], -base));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              x[j] = (w[e] >> j) & 1u ? ex2(fmaf(c, x[j], -base)) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            sum += x[2 * j] + x[2 * j + 1];
+            pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+          }
+          tmem_st_16(tS + 16 * e, pk);
+        }
+        l += sum;
+        if (seg == kOwn) {
+          // (the V tile is read behind its barrier: its bits are written by then)
+          ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns);
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) poison |= (w[e] & S->badv[at & 1][e]) != 0u;
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before_sync();
+        mbar_arrive(&S->pready[tile]);
+      }
+      if (ok && ntiles > 0) {
+        ok = wait_warp(&S->pvdone[tile], (ntiles - 1) & 1, S, limit_ns);
+        tc_fence_after_sync();
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (l NaN: kept)
+      const size_t out = (size_t)tok * d.Hq + hk * G + (rho - tok * G);
+      const size_t slot = (size_t)(a.slot0 + split) * d.T * d.Hq + out;
+      if (ok) {
+#pragma unroll 1
+        for (int e = 0; e < DP / 32; ++e) {
+          float x[32];
+          if (ntiles > 0) {
+            tmem_ld_32cols(tO + 32 * e, x);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = l == 0.f ? 0.f : x[j] * inv;
+          if (poison && live) {  // rare: the seen rows' infinities and NaN
+            for (int nd = node; nd >= 0; nd = tree ? sParent[nd] : nd - 1)
+              for (int j = 0; j < 32 && 32 * e + j < d.D; ++j) {
+                const float vv = __bfloat162float(
+                    a.v[((size_t)(first + nd) * d.Hkv + hk) * d.D + 32 * e + j]);
+                if (!isfinite(vv)) x[j] += vv;
+              }
+          }
+          if (live && a.part_o) {
+            float* po = a.part_o + slot * d.D + 32 * e;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              if (32 * e + j < d.D)
+                *reinterpret_cast<float4*>(po + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          } else if (live) {
+            __nv_bfloat16* oo = a.o + out * d.D + 32 * e;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              if (32 * e + j < d.D)
+                *reinterpret_cast<uint4*>(oo + j) =
+                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
+                               pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+          }
+          __syncwarp();
+        }
+        if (live) {
+          const float z = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
+          if (a.part_o) a.part_lse[slot] = z;
+          else if (a.lse) a.lse[out] = z;
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 10) tmem_dealloc(tmem, 512);
+  if (tid == 0 && S->abort && a.dev_status) {
+    if (a.prefix_units)
+      for (int bb = 0; bb < d.B; ++bb) atomicMax(a.dev_status + bb, GDN_TREE_STATUS_TIMEOUT);
+    else
+      atomicMax(a.dev_status + b, GDN_TREE_STATUS_TIMEOUT);
+  }
+}
+
+// ---- joining the parts: a warp a row (node * Hq + h of sequence b) -----------------------
+__global__ void __launch_bounds__(256)
+attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse, int slots,
+                   const int32_t* __restrict__ cu, gdn_tree_attend_dims d, int groups,
+                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
+  const int b = blockIdx.x / groups, lane = threadIdx.x & 31, D = d.D;
+  const int first = cu[b], stop = cu[b + 1];
+  const long long at = (long long)(blockIdx.x % groups) * 8 + (threadIdx.x >> 5);
+  // (a sequence whose rows are out of range was reported, and has no parts)
+  if (first < 0 || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq) return;
+  const size_t rows = (size_t)d.T * d.Hq, row = (size_t)first * d.Hq + at;
+  float top = -INFINITY;
+  for (int s = lane; s < slots; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  float sum = 0.f;
+  if (top > -INFINITY)
+    for (int s = lane; s < slots; s += 32) sum += expf(part_lse[s * rows + row] - top);
+  sum = warp_sum(sum);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  if (4 * lane < D)
+    for (int s = 0; s < slots; ++s) {
+      const float z = part_lse[s * rows + row];
+      if (z == -INFINITY) continue;  // a part that saw nothing
+      const float w = expf(z - top) * inv;
+      const float4 y = *reinterpret_cast<const float4*>(part_o + ((size_t)s * rows + row) * D + 4 * lane);
+      x[0] = fmaf(w, y.x, x[0]);
+      x[1] = fmaf(w, y.y, x[1]);
+      x[2] = fmaf(w, y.z, x[2]);
+      x[3] = fmaf(w, y.w, x[3]);
+    }
+  if (4 * lane < D)
+    *reinterpret_cast<uint2*>(o + row * D + 4 * lane) =
+        make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  if (lse && lane == 0) lse[row] = sum > 0.f ? top + logf(sum) : (top == -INFINITY ? -INFINITY : sum);
+}
+
+// ---- the plan: what runs for these dims --------------------------------------------------
+struct Plan {
+  bool tc = false;
+  bool shared = false;     // the prefix as units of its own
+  int prefix_splits = 0, prefix_tiles = 0;
+  int seq_splits = 1, seq_tiles = 0;
+  int slots = 0;           // parts of a row (0: the kernel writes o itself)
+};
+
+Plan plan_of(const gdn_tree_attend_dims& d) {
+  Plan p;
+  p.tc = d.dtype == GDN_TREE_BF16;
+  if (!p.tc) return p;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  const int G = d.Hq / d.Hkv;
+  const long long rows = (long long)d.T * G;  // of a key head
+  auto tiles = [](long long r) { return (int)((r + 2 * kTile - 1) / (2 * kTile)); };
+  // the prefix gets units of its own where the sequences' rows leave its tiles half empty
+  p.shared = d.prefix_len > 0 && d.B > 1 && rows < (long long)d.B * kTile;
+  p.seq_tiles = tiles((long long)d.N * G);
+  const long long units = (long long)d.B * d.Hkv * p.seq_tiles;
+  const long long keys = (long long)d.table_width * d.page_size + d.N + (p.shared ? 0 : d.prefix_len);
+  // parts of at least 4 key tiles, until every SM has a unit
+  auto splits = [&](long long n, long long k) {
+    const long long most = (k + 4 * kTile - 1) / (4 * kTile);
+    const long long want = n >= sms ? 1 : sms / n;
+    return (int)(want < most ? want : most < 1 ? 1 : most);
+  };
+  p.seq_splits = splits(units, keys);
+  if (p.shared) {
+    p.prefix_tiles = tiles(rows);
+    p.prefix_splits = splits((long long)d.Hkv * p.prefix_tiles, d.prefix_len);
+  }
+  p.slots = p.prefix_splits + p.seq_splits;
+  if (p.slots == 1) p.slots = 0;
+  return p;
+}
+
+size_t part_floats(const gdn_tree_attend_dims& d, const Plan& p) {
+  return (size_t)p.slots * d.T * d.Hq * d.D;
+}
+
+template <int DP>
+cudaError_t launch_units(const TcArgs& t, long long blocks, cudaStream_t stream) {
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Smem<DP>::kBytes);
+  if (err != cudaSuccess) return err;
+  attend_tc_kernel<DP><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
+      t, wait_hooks().limit_ns);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(const gdn_tree_attend_dims& d) {
+  const Plan p = plan_of(d);
+  if (!p.slots) return 0;
+  return (part_floats(d, p) + (size_t)p.slots * d.T * d.Hq) * sizeof(float);
+}
+
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
+  const gdn_tree_attend_dims& d = a.d;
+  const Plan p = plan_of(d);
+  if (!p.tc) return launch_attend_generic(a, stream);
+  typedef const __nv_bfloat16* bf;
+  TcArgs t{};
+  t.q = static_cast<bf>(a.q);
+  t.k = static_cast<bf>(a.k);
+  t.v = static_cast<bf>(a.v);
+  t.parent = a.parent;
+  t.cu = a.cu;
+  t.k_cache = static_cast<bf>(a.k_cache);
+  t.v_cache = static_cast<bf>(a.v_cache);
+  t.table = a.page_table;
+  t.ctx = a.context_len;
+  t.prefix_pages = a.prefix_pages;
+  t.scale = a.scale;
+  t.o = static_cast<__nv_bfloat16*>(a.o);
+  t.lse = a.lse;
+  t.d = d;
+  t.dev_status = a.dev_status;
+  if (p.slots) {
+    t.part_o = static_cast<float*>(a.workspace);
+    t.part_lse = t.part_o + part_floats(d, p);
+  }
+  auto units = [&](const TcArgs& x, long long blocks) {
+    return d.D <= 64 ? launch_units<64>(x, blocks, stream) : launch_units<128>(x, blocks, stream);
+  };
+  cudaError_t err = cudaSuccess;
+  if (p.shared) {
+    t.prefix_units = true;
+    t.splits = p.prefix_splits;
+    t.tiles = p.prefix_tiles;
+    err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits);
+    if (err != cudaSuccess) return err;
+  }
+  t.prefix_units = false;
+  t.with_prefix = !p.shared;
+  t.slot0 = p.prefix_splits;
+  t.splits = p.seq_splits;
+  t.tiles = p.seq_tiles;
+  err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits);
+  if (err != cudaSuccess || !p.slots) return err;
+  const int groups = (int)(((long long)d.N * d.Hq + 7) / 8);
+  if ((long long)d.B * groups > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  attend_join_kernel<<<(unsigned)(d.B * groups), 256, 0, stream>>>(
+      t.part_o, t.part_lse, p.slots, t.cu, d, groups, t.o, t.lse);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

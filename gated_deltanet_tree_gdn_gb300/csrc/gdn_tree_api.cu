@@ -76,8 +76,10 @@ int check_attend_dims(const gdn_tree_attend_dims& d) {
   if (d.Hq % d.Hkv != 0) return GDN_TREE_EINVAL;
   if (d.dtype != GDN_TREE_BF16 && d.dtype != GDN_TREE_F32) return GDN_TREE_EUNSUPPORTED;
   if (!supported_head_dim(d.D) || d.B > 65535) return GDN_TREE_EUNSUPPORTED;
-  // positions within a sequence and rows of a key head's query block are 32-bit numbers
-  if ((long long)d.table_width * d.page_size > 0x7fffffffll - 4096 ||
+  // positions within a sequence, rows of the cache and of a key head's query block are
+  // 32-bit numbers (element offsets are not)
+  if ((long long)d.n_pages * d.page_size > 0x7fffffffll ||
+      (long long)d.table_width * d.page_size > 0x7fffffffll - 4096 ||
       d.prefix_len > 0x7fffffff - 4096 || (long long)d.T * d.Hq > 0x7fffffffll - 4096 ||
       (long long)d.Hkv * d.D > 0x7fffffffll / 8)
     return GDN_TREE_EUNSUPPORTED;

@@ -350,6 +350,31 @@ def test_attend_scales_and_sharp_rows(size, scale):
     check_attend(o, lse, x, scale=scale)
 
 
+@pytest.mark.parametrize("dtype,D,nodes", [("bf16", 128, [60, 150]), ("bf16", 64, [1, 40]),
+                                           ("f32", 64, [30, 40])])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_attend_unseen_nodes_may_hold_anything(dtype, D, nodes, what):
+    """Infinities and NaN in the keys and values of nodes that a row does not see leave the
+    row alone; the rows that see them get them."""
+    x = attend_inputs(nodes, [70, 0], 40, 8, 2, D, 32, dtype, seed=11)
+    good = run_attend(x)
+    bad = [int(x["cu"][b] + n - 1) for b, n in enumerate(nodes)]  # the last node is a leaf
+    x["k"][bad], x["v"][bad] = what, what
+    x["v"][bad, :, 1::2] = 1.0  # beside finite values
+    o, lse = run_attend(x)
+    rest = np.setdiff1d(np.arange(sum(nodes)), bad)
+    assert torch.equal(o[rest], good[0][rest]) and torch.equal(lse[rest], good[1][rest])
+    assert not np.isfinite(host(o[bad])[:, :, ::2]).any()
+    # a value alone that is not finite: the columns that it sits in, no others
+    x = attend_inputs(nodes, [70, 0], 40, 8, 2, D, 32, dtype, seed=11)
+    x["v"][bad, :, 3] = what
+    o, lse = run_attend(x)
+    assert torch.equal(o[rest], good[0][rest]) and torch.equal(lse, good[1])
+    keep = np.setdiff1d(np.arange(D), [3])
+    assert torch.equal(o[:, :, keep], good[0][:, :, keep])
+    assert not np.isfinite(host(o[bad])[:, :, 3]).any()
+
+
 def test_attend_is_deterministic():
     x = attend_inputs([1] * 20, [50 * i for i in range(20)], 2000, 8, 2, 128, 64, "bf16", seed=5)
     first = run_attend(x)
