@@ -14,15 +14,23 @@
 //     the shared prefix, which is then read once for every 256 rows of the batch and not
 //     once for every sequence.
 //
-// Roles (11 warps, so that a thread may hold 168 registers): warps 0-3 and 4-7 the softmax
-// of row tile 0 and 1, a thread a row; warp 8 brings K tiles, warp 9 V tiles (16-byte
-// cp.async, so that any page size and any page order works and rows past a length are
-// filled with zeros, whatever they hold); one thread of warp 10 issues the MMAs.  S and O are fp32 in TMEM; P goes back to TMEM as
-// bf16 over the S it came from and is the A operand of P V.  Issue order P0 V, S0', P1 V,
-// S1': one tile's MMAs run while the other's softmax does.
+// Roles (19 warps): warps 0-7 and 8-15 the softmax of row tile 0 and 1, two threads a row
+// (one for keys 0-63 of a tile, one for 64-127); warp 16 brings K tiles, warp 17 V tiles;
+// one thread of warp 18 issues the MMAs.  A whole tile of cache rows comes by TMA, a box a
+// page (a box a tile where pages are larger); the last tile of a length, the tree's own
+// rows and pages that do not fit the tiles come by 16-byte cp.async row by row, which
+// fills rows past a length with zeros, whatever the page holds there (0 * NaN is NaN).
+// S and O are fp32 in TMEM; P goes back to TMEM as bf16 over the S it came from and is the
+// A operand of P V.  Issue order P0 V, S0', P1 V, S1': one tile's MMAs (1024 cycles for
+// D = 128) run while the other's softmax does, which has to take no longer; with one
+// thread a row it took 2150 cycles, and a tile of keys 4100.  The two threads of a row
+// (of warps w and w + 4) exchange their maxima; each adds up its own half, and keeps its
+// half of P in the columns of S that only it reads.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one its
 // sums use (exact either way: P and l stay far below the overflow of their types).
+#include <string.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100.cuh"
@@ -33,7 +41,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kTile = 128;               // rows of a tile, keys of a tile
-constexpr int kThreads = 11 * 32;
+constexpr int kSoftmax = 512;             // softmax threads: two a row
+constexpr int kThreads = kSoftmax + 3 * 32;
+constexpr int kWarpK = kSoftmax / 32, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
+constexpr int kHalf = kTile / 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
@@ -56,6 +67,7 @@ struct TcArgs {
   int min_rows;     // sequences of fewer rows are not this kernel's
   bool prefix_units;   // units of the shared prefix over the whole batch
   bool with_prefix;    // a sequence's units include the prefix
+  int box_rows;        // rows of a TMA box (0: no tile of the cache comes by TMA)
 };
 
 template <int DP>
@@ -67,23 +79,27 @@ struct Smem {
   static constexpr uint32_t OFF_V = OFF_K + 2 * kKV;
   static constexpr uint32_t OFF_PARENT = OFF_V + 2 * kKV;
   static constexpr uint32_t OFF_BAR = OFF_PARENT + kMaxNLong * 4;
-  static constexpr uint32_t kBytes = OFF_BAR + 256 + 1024;  // + alignment slack
+  static constexpr uint32_t kBytes = OFF_BAR + 4096 + 1024;  // + alignment slack
 };
 
 struct Bars {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], drain;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2], drain;
   uint32_t tmem;
   int abort;
+  float top[2][2][kTile];  // a row's maximum over each half of a tile
   uint32_t badv[2][4];  // own rows of a V tile that hold infinities or NaN (by stage)
 };
 
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Bars* s,
                                          uint64_t limit) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  // (the clock is read once in a while: reading it takes longer than most of these waits)
+  uint64_t t0 = 0;
+  for (uint32_t tries = 0; !mbar_try_wait(bar, parity); ++tries) {
+    if ((tries & 63u) != 63u) continue;
     if (ld_acquire_shared(&s->abort)) return false;
-    if (globaltimer_ns() - t0 > limit) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit) {
       st_release_shared(&s->abort, 1);
       return false;
     }
@@ -129,17 +145,25 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (x, y) <- c (x, y) + b, and (s, t) += (x, y): two fp32 lanes an instruction
+__device__ __forceinline__ void fma2(float& x, float& y, float c, float b) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(c), "f"(b));
+}
+__device__ __forceinline__ void add2(float& s, float& t, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(s), "+f"(t)
+      : "f"(x), "f"(y));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 16-byte chunk n8 of V row `key`, the operand [keys x DP] with DP contiguous
-template <int DP>
-__device__ __forceinline__ uint32_t v_chunk(int key, int n8) {
-  const int r = key & 7;
-  return (uint32_t)((key >> 3) * (DP / 64 * 1024) + (n8 >> 3) * 1024 + r * 128 +
-                    (((n8 & 7) ^ r) << 4));
 }
 
 // bits of a packed pair of bf16 that are infinities or NaN
@@ -152,10 +176,38 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
+static_assert(sizeof(Bars) <= 4096, "the barriers fit their place");
+
 enum Segment { kPrefix = 0, kContext = 1, kOwn = 2 };
 
+// a page number out of range: the sequence's error, every sequence's for the prefix
+__device__ __noinline__ void report_page(const TcArgs& a, bool prefix, int b) {
+  if (!a.dev_status) return;
+  if (!prefix) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+  else
+    for (int i = 0; i < a.d.B; ++i) atomicMax(a.dev_status + i, GDN_TREE_STATUS_BAD_LAYOUT);
+}
+
+// adds the infinities and NaN of the values on a row's path to columns [c0, c1) of its
+// result (they were kept out of the product, which masks by zero weights)
+__device__ __noinline__ void add_nonfinite(const TcArgs& a, size_t out, size_t slot, int first,
+                                           int node, int hk, int c0, int c1) {
+  for (int col = c0; col < min(c1, a.d.D); ++col) {
+    float x = 0.f;
+    for (int nd = node; nd >= 0; nd = a.parent ? a.parent[first + nd] : nd - 1) {
+      const float v = __bfloat162float(a.v[((size_t)(first + nd) * a.d.Hkv + hk) * a.d.D + col]);
+      if (!isfinite(v)) x += v;
+    }
+    if (isfinite(x)) continue;
+    if (a.part_o) a.part_o[slot * a.d.D + col] += x;
+    else a.o[out * a.d.D + col] = __float2bfloat16_rn(__bfloat162float(a.o[out * a.d.D + col]) + x);
+  }
+}
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64_t limit_ns) {
+__global__ void __launch_bounds__(kThreads, 1)
+attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
+                 const __grid_constant__ CUtensorMap mapV, uint64_t limit_ns) {
   using L = Smem<DP>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -212,19 +264,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
   // ---- set up ------------------------------------------------------------------------
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&S->kfull[s], 32);
+      mbar_init(&S->kfull[s], 1);
       mbar_init(&S->kempty[s], 1);
-      mbar_init(&S->vfull[s], 32);
+      mbar_init(&S->vfull[s], 1);
       mbar_init(&S->vempty[s], 1);
       mbar_init(&S->sfull[s], 1);
-      mbar_init(&S->pready[s], kTile);
+      mbar_init(&S->pready[s], kSoftmax / 2);
       mbar_init(&S->pvdone[s], 1);
+      mbar_init(&S->lsum[s], kSoftmax / 2);
     }
     mbar_init(&S->drain, 1);
     S->abort = 0;
     mbar_fence_init();
   }
-  if (warp == 10) tmem_alloc(&S->tmem, 512);
+  if (warp == kWarpMma) tmem_alloc(&S->tmem, 512);
   // Q, negated where the scale is negative (the maximum is then taken with c >= 0)
   const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
   for (int e = tid; e < 2 * kTile * (DP / 8); e += kThreads) {
@@ -253,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
 
   if (bad) {
     if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_TREE);
-  } else if (warp == 8 || warp == 9) {
-    // ---- producers: K (warp 8) or V (warp 9) --------------------------------------------
-    const bool isV = warp == 9;
+  } else if (warp == kWarpK || warp == kWarpV) {
+    // ---- producers: K or V --------------------------------------------
+    const bool isV = warp == kWarpV;
     uint64_t* full = isV ? S->vfull : S->kfull;
     uint64_t* empty = isV ? S->vempty : S->kempty;
     const __nv_bfloat16* cache = isV ? a.v_cache : a.k_cache;
@@ -269,6 +322,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
       const int at = i - i0, st = at & 1;
       int seg, j0, len;
       tile_of(i, seg, j0, len);
+      if (a.box_rows && seg != kOwn && len - j0 >= kTile) {
+        // a whole tile: lane l brings box l
+        const int boxes = kTile / a.box_rows;
+        int crow = 0;
+        if (lane < boxes) {
+          const int j = j0 + lane * a.box_rows, pi = j / d.page_size;
+          const int pg = seg == kPrefix ? a.prefix_pages[pi]
+                                        : a.table[(size_t)b * d.table_width + pi];
+          // (a row past the last one reads zeros)
+          crow = pg >= 0 && pg < d.n_pages ? pg * d.page_size + (j - pi * d.page_size)
+                                           : d.n_pages * d.page_size;
+          if (pg < 0 || pg >= d.n_pages) report_page(a, seg == kPrefix, b);
+        }
+        if (at >= 2 && !wait_warp(&empty[st], ((at >> 1) & 1) ^ 1, S, limit_ns)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStage);
+        __syncwarp();
+        if (lane < boxes) {
+          unsigned char* to = smem + (isV ? L::OFF_V : L::OFF_K) + st * kStage + lane * a.box_rows * 128;
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            tma_load_3d(to + c * kSw128TileBytes, isV ? &mapV : &mapK, &full[st], 64 * c, hk, crow);
+        }
+        continue;
+      }
       // lane l looks up rows l, 32 + l, 64 + l, 96 + l of the tile
       int row[4];
 #pragma unroll
@@ -284,13 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
                                           : a.table[(size_t)b * d.table_width + pi];
             if (pg >= 0 && pg < d.n_pages)
               row[e] = pg * d.page_size + (j - pi * d.page_size);
-            else if (a.dev_status) {  // a bad page of the prefix is every sequence's error
-              if (seg == kPrefix)
-                for (int bb = 0; bb < d.B; ++bb)
-                  atomicMax(a.dev_status + bb, GDN_TREE_STATUS_BAD_LAYOUT);
-              else
-                atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
-            }
+            else
+              report_page(a, seg == kPrefix, b);
           }
         }
       }
@@ -298,42 +370,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
       const __nv_bfloat16* src = (seg == kOwn ? mine : cache) + (size_t)hk * d.D + 8 * c8;
       const size_t stride = (size_t)d.Hkv * d.D;
       const uint32_t dst = base + st * kStage;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
+          const int r = rr + lane / kChunks, key = 32 * e + r;
+          const int x = __shfl_sync(0xffffffffu, row[e], r);
+          const bool take = x >= 0 && in_row;
+          cp_async16_zfill(dst + sw128_chunk(key, c8), take ? src + x * stride : src, take);
+        }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (isV && seg == kOwn) {
         // own rows are masked for some of the query rows only: what is not finite is kept
         // out of the product (0 * inf) and added to the rows that see it at the end
         if (lane < 4) S->badv[st][lane] = 0u;
         __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
-            const int r = rr + lane / kChunks, key = 32 * e + r;
-            const int x = __shfl_sync(0xffffffffu, row[e], r);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (x >= 0 && in_row) w = *reinterpret_cast<const uint4*>(src + x * stride);
-            if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
-              atomicOr(&S->badv[st][key >> 5], 1u << (key & 31));
-              w = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
-            }
-            *reinterpret_cast<uint4*>(smem + L::OFF_V + st * kStage + v_chunk<DP>(key, c8)) = w;
+#pragma unroll 8
+        for (int key = lane / kChunks; key < kTile; key += kRowsAtOnce) {
+          uint4* at16 = reinterpret_cast<uint4*>(smem + L::OFF_V + st * kStage + sw128_chunk(key, c8));
+          uint4 w = *at16;
+          if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
+            atomicOr(&S->badv[st][key >> 5], 1u << (key & 31));
+            *at16 = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
           }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
-            const int r = rr + lane / kChunks, key = 32 * e + r;
-            const int x = __shfl_sync(0xffffffffu, row[e], r);
-            const bool take = x >= 0 && in_row;
-            cp_async16_zfill(dst + (isV ? v_chunk<DP>(key, c8) : sw128_chunk(key, c8)),
-                             take ? src + x * stride : src, take);
-          }
+        }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
-      mbar_arrive(&full[st]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 10) {
+  } else if (warp == kWarpMma) {
     // ---- MMAs --------------------------------------------------------------------------
     if (lane == 0 && ntiles > 0) {
       const uint32_t aQ = smem_addr(smem + L::OFF_Q), aK = smem_addr(smem + L::OFF_K),
@@ -350,11 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
         umma_commit(&S->sfull[tile]);
       };
       auto issue_pv = [&](int tile, int st, bool acc) {
-        constexpr uint32_t sbo = DP / 64 * 1024;
+        // (V: keys are K rows, D contiguous; 8-key groups 1 KB apart, 64-column blocks 16 KB)
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          umma_ts(tmem + 2 * kTile + tile * kTile, tmem + tile * kTile + 8 * s,
-                  desc_sw128_mnmajor(aV + st * kStage + (uint32_t)s * 2 * sbo, 1024, sbo), idO,
+          umma_ts(tmem + 2 * kTile + tile * kTile,
+                  tmem + tile * kTile + (s >> 2) * kHalf + 8 * (s & 3),
+                  desc_sw128_mnmajor(aV + st * kStage + (uint32_t)s * 2048, kSw128TileBytes, 1024), idO,
                   acc || s > 0);
         umma_commit(&S->pvdone[tile]);
       };
@@ -397,16 +465,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
       mbar_wait(&S->drain, 0, limit_ns);
     }
     __syncwarp();
-  } else if (warp < 8) {
-    // ---- softmax: a thread a row ---------------------------------------------------------
-    const int tile = warp >> 2, r = tile * kTile + (warp & 3) * 32 + lane;
+  } else {
+    // ---- softmax: two threads a row --------------------------------------------------------
+    const int tile = warp >> 3, half = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
+    const int r = tile * kTile + lr;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tS = tl + tile * kTile, tO = tl + 2 * kTile + tile * kTile;
+    const uint32_t tS = tl + tile * kTile + kHalf * half, tO = tl + 2 * kTile + tile * kTile;
+    const int pair = 1 + tile * 4 + (warp & 3);  // named barrier of warps w and w + 4
     const float c = fabsf(a.scale) * kLog2e;
     const int rho = min(r0 + r, rows_end - 1), tok = rho / G, node = tok - first;
     const bool live = r < rows;
     int walk = node;                   // the next node of the path that is not yet masked
-    float mref = -INFINITY, l = 0.f;   // of c s
+    float mref = -INFINITY, l = 0.f;   // of c s; l: this half's
     bool ok = true, poison = false;
     if (tile == 0 || two) {
       for (int i = i0; i < i1; ++i) {
@@ -414,46 +484,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
         int seg, j0, len;
         tile_of(i, seg, j0, len);
         ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns);
-        if (!ok) break;
+        if (!ok) {  // (the other warp may be at the exchange already: it is not left there)
+          asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
+          break;
+        }
         tc_fence_after_sync();
-        // the keys of this tile that the row sees, a bit a key
-        uint32_t w[4];
         const int valid = len - j0;
         const bool masked = seg == kOwn || valid < kTile;
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int left = (seg == kOwn && !tree ? min(valid, node - j0 + 1) : valid) - 32 * e;
-            w[e] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-          }
-          if (seg == kOwn && tree) {
-            uint64_t lo = 0, hi = 0;
-            // a split that holds an upper part of the path's tiles only skips the others
-            while (walk >= j0 + kTile) walk = sParent[walk];
-            while (walk >= j0) {
-              const int off = walk - j0;
-              if (off < 64) lo |= 1ull << off;
-              else hi |= 1ull << (off - 64);
-              walk = sParent[walk];
-            }
-            w[0] &= (uint32_t)lo; w[1] &= (uint32_t)(lo >> 32);
-            w[2] &= (uint32_t)hi; w[3] &= (uint32_t)(hi >> 32);
-          }
-        }
+        uint32_t w[2];  // the keys of this half of the tile that the row sees, a bit a key
         float top = -INFINITY;
         if (!masked) {
-          float mx = -INFINITY;
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 2; ++e) {
             float x[32];
             tmem_ld_32cols(tS + 32 * e, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, x[j]);
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
           }
-          top = c * mx;
+          top = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 2; ++e) {
+            const int left = (seg == kOwn && !tree ? min(valid, node - j0 + 1) : valid) -
+                             kHalf * half - 32 * e;
+            w[e] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+          }
+          if (seg == kOwn && tree) {
+            uint64_t on = 0;
+            // (a part that begins below the row's node first walks up to its own tiles)
+            while (walk >= j0 + kTile) walk = sParent[walk];
+            for (; walk >= j0; walk = sParent[walk]) {
+              const int off = walk - j0 - kHalf * half;
+              if (off >= 0 && off < kHalf) on |= 1ull << off;
+            }
+            w[0] &= (uint32_t)on;
+            w[1] &= (uint32_t)(on >> 32);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             float x[32];
             tmem_ld_32cols(tS + 32 * e, x);
 #pragma unroll
@@ -461,6 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
               top = fmaxf(top, (w[e] >> j) & 1u ? c * x[j] : -INFINITY);
           }
         }
+        // the row's maximum: the other half's beside this one's
+        S->top[tile][half][lr] = top;
+        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+        top = fmaxf(top, S->top[tile][half ^ 1][lr]);
         // (NaN scores: fmaxf drops them here, and they come back as NaN weights)
         const bool grow = top > mref + kGrow;  // (mref = -inf: any finite top)
         if (__any_sync(0xffffffffu, grow)) {
@@ -472,46 +546,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll
-            for (int e = 0; e < DP / 32; ++e) {
-              float x[32];
-              tmem_ld_32cols(tO + 32 * e, x);
+            for (int e = 0; e < DP / 64; ++e) {  // this half's columns of O
+              float y[32];
+              const uint32_t to32 = tO + DP / 2 * half + 32 * e;
+              tmem_ld_32cols(to32, y);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] *= keep;
-              tmem_st_32cols(tO + 32 * e, x);
+              for (int j = 0; j < 32; ++j) y[j] *= keep;
+              tmem_st_32cols(to32, y);
             }
           }
           l *= keep;
           mref = to;
         }
         const float base = mref == -INFINITY ? 0.f : mref;
-        float sum = 0.f;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           float x[32];
-          tmem_ld_32cols(tS + 32 * e, x);
           uint32_t pk[16];
-          if (!masked) {
+          tmem_ld_32cols(tS + 32 * e, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = ex2(fmaf(c, x[j], -base));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              x[j] = (w[e] >> j) & 1u ? ex2(fmaf(c, x[j], -base)) : 0.f;
+          for (int j = 0; j < 32; j += 2) {
+            fma2(x[j], x[j + 1], c, -base);
+            x[j] = ex2(x[j]);
+            x[j + 1] = ex2(x[j + 1]);
+          }
+          if (masked) {
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = (w[e] >> j) & 1u ? x[j] : 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            sum += x[2 * j] + x[2 * j + 1];
-            pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+          for (int j = 0; j < 32; j += 2) {
+            add2(sum[0], sum[1], x[j], x[j + 1]);
+            pk[j / 2] = pack_bf16(x[j], x[j + 1]);
           }
           tmem_st_16(tS + 16 * e, pk);
         }
-        l += sum;
+        l += sum[0] + sum[1];
         if (seg == kOwn) {
           // (the V tile is read behind its barrier: its bits are written by then)
           ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns);
           if (!ok) break;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) poison |= (w[e] & S->badv[at & 1][e]) != 0u;
+          for (int e = 0; e < 2; ++e) poison |= (w[e] & S->badv[at & 1][2 * half + e]) != 0u;
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
@@ -521,47 +598,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
         ok = wait_warp(&S->pvdone[tile], (ntiles - 1) & 1, S, limit_ns);
         tc_fence_after_sync();
       }
+      // the row's sum: both halves' (the exchange goes through the Q tiles, read by now)
+      float* sL = reinterpret_cast<float*>(smem + L::OFF_Q) + tile * 4 * kTile;
+      int* sPoison = reinterpret_cast<int*>(sL + 2 * kTile);
+      sL[half * kTile + lr] = l;
+      sPoison[half * kTile + lr] = poison;
+      mbar_arrive(&S->lsum[tile]);
+      ok = wait_warp(&S->lsum[tile], 0, S, limit_ns) && ok;
+      l = sL[lr] + sL[kTile + lr];
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (l NaN: kept)
       const size_t out = (size_t)tok * d.Hq + hk * G + (rho - tok * G);
       const size_t slot = (size_t)(a.slot0 + split) * d.T * d.Hq + out;
       if (ok) {
 #pragma unroll 1
-        for (int e = 0; e < DP / 32; ++e) {
-          float x[32];
+        for (int e = 0; e < DP / 64; ++e) {
+          const int col = DP / 2 * half + 32 * e;
+          float y[32];
           if (ntiles > 0) {
-            tmem_ld_32cols(tO + 32 * e, x);
+            tmem_ld_32cols(tO + col, y);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0.f;
+            for (int j = 0; j < 32; ++j) y[j] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = l == 0.f ? 0.f : x[j] * inv;
-          if (poison && live) {  // rare: the seen rows' infinities and NaN
-            for (int nd = node; nd >= 0; nd = tree ? sParent[nd] : nd - 1)
-              for (int j = 0; j < 32 && 32 * e + j < d.D; ++j) {
-                const float vv = __bfloat162float(
-                    a.v[((size_t)(first + nd) * d.Hkv + hk) * d.D + 32 * e + j]);
-                if (!isfinite(vv)) x[j] += vv;
-              }
-          }
+          for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
           if (live && a.part_o) {
-            float* po = a.part_o + slot * d.D + 32 * e;
+            float* po = a.part_o + slot * d.D + col;
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              if (32 * e + j < d.D)
-                *reinterpret_cast<float4*>(po + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+              if (col + j < d.D)
+                *reinterpret_cast<float4*>(po + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
           } else if (live) {
-            __nv_bfloat16* oo = a.o + out * d.D + 32 * e;
+            __nv_bfloat16* oo = a.o + out * d.D + col;
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-              if (32 * e + j < d.D)
+              if (col + j < d.D)
                 *reinterpret_cast<uint4*>(oo + j) =
-                    make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
-                               pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                    make_uint4(pack_bf16(y[j], y[j + 1]), pack_bf16(y[j + 2], y[j + 3]),
+                               pack_bf16(y[j + 4], y[j + 5]), pack_bf16(y[j + 6], y[j + 7]));
           }
           __syncwarp();
         }
-        if (live) {
+        // (either half may have seen them)
+        if (sPoison[lr] + sPoison[kTile + lr] != 0 && live)
+          add_nonfinite(a, out, slot, first, node, hk, DP / 2 * half, DP / 2 * (half + 1));
+        if (live && half == 0) {
           const float z = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
           if (a.part_o) a.part_lse[slot] = z;
           else if (a.lse) a.lse[out] = z;
@@ -572,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(TcArgs a, uint64
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 10) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
   if (tid == 0 && S->abort && a.dev_status) {
     if (a.prefix_units)
       for (int bb = 0; bb < d.B; ++bb) atomicMax(a.dev_status + bb, GDN_TREE_STATUS_TIMEOUT);
@@ -662,14 +743,15 @@ size_t part_floats(const gdn_tree_attend_dims& d, const Plan& p) {
 }
 
 template <int DP>
-cudaError_t launch_units(const TcArgs& t, long long blocks, cudaStream_t stream) {
+cudaError_t launch_units(const TcArgs& t, const CUtensorMap& mapK, const CUtensorMap& mapV,
+                         long long blocks, cudaStream_t stream) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<DP>::kBytes);
   if (err != cudaSuccess) return err;
   attend_tc_kernel<DP><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
-      t, wait_hooks().limit_ns);
+      t, mapK, mapV, wait_hooks().limit_ns);
   return cudaGetLastError();
 }
 
@@ -706,8 +788,20 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     t.part_o = static_cast<float*>(a.workspace);
     t.part_lse = t.part_o + part_floats(d, p);
   }
+  // whole tiles by TMA where pages and tiles divide one another
+  CUtensorMap mapK, mapV;
+  memset(&mapK, 0, sizeof mapK);
+  memset(&mapV, 0, sizeof mapV);
+  const int box = d.page_size < kTile ? d.page_size : kTile;
+  const long long cache_rows = (long long)d.n_pages * d.page_size;
+  if (d.D % 64 == 0 && box % 8 == 0 && kTile % box == 0 && d.page_size % box == 0 &&
+      cache_rows > 0 && cache_rows < 0x7fffffffll && a.k_cache &&
+      encode_head_rows_map(&mapK, a.k_cache, cache_rows, d.Hkv, d.D, box) &&
+      encode_head_rows_map(&mapV, a.v_cache, cache_rows, d.Hkv, d.D, box))
+    t.box_rows = box;
   auto units = [&](const TcArgs& x, long long blocks) {
-    return d.D <= 64 ? launch_units<64>(x, blocks, stream) : launch_units<128>(x, blocks, stream);
+    return d.D <= 64 ? launch_units<64>(x, mapK, mapV, blocks, stream)
+                     : launch_units<128>(x, mapK, mapV, blocks, stream);
   };
   cudaError_t err = cudaSuccess;
   if (p.shared) {

@@ -137,6 +137,11 @@ cudaError_t launch_verify_mid(const VerifyArgs& a, cudaStream_t stream);
 // 32 columns x 128 rows each (false when the driver's encoder is unavailable)
 bool encode_state_map(CUtensorMap* map, const float* base, long long n_states);
 
+// 128-byte-swizzled TMA map of bf16 rows [rows, heads, width] (width a multiple of 64):
+// boxes of 64 columns x one head x box_rows rows
+bool encode_head_rows_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
+                          int box_rows);
+
 bool verify_tc_supported(const gdn_tree_dims& d);
 cudaError_t launch_verify_tc(const VerifyArgs& a, cudaStream_t stream);
 
