@@ -16,10 +16,9 @@
 //
 // Roles (19 warps): warps 0-7 and 8-15 the softmax of row tile 0 and 1, two threads a row
 // (one for keys 0-63 of a tile, one for 64-127); warp 16 brings K tiles, warp 17 V tiles;
-// one thread of warp 18 issues the MMAs.  A whole tile of cache rows comes by TMA, a box a
-// page (a box a tile where pages are larger); the last tile of a length, the tree's own
-// rows and pages that do not fit the tiles come by 16-byte cp.async row by row, which
-// fills rows past a length with zeros, whatever the page holds there (0 * NaN is NaN).
+// warp 18 issues the MMAs.  Tiles come by TMA, a box a page (a box a tile where pages are
+// larger, and for the tree's own rows); pages that do not fit the tiles, and head sizes
+// other than 64 and 128, come by 16-byte cp.async row by row.
 // S and O are fp32 in TMEM; P goes back to TMEM as bf16 over the S it came from and is the
 // A operand of P V.  Issue order P0 V, S0', P1 V, S1': one tile's MMAs (1024 cycles for
 // D = 128) run while the other's softmax does, which has to take no longer; with one
@@ -67,7 +66,8 @@ struct TcArgs {
   int min_rows;     // sequences of fewer rows are not this kernel's
   bool prefix_units;   // units of the shared prefix over the whole batch
   bool with_prefix;    // a sequence's units include the prefix
-  int box_rows;        // rows of a TMA box (0: no tile of the cache comes by TMA)
+  int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
+  bool own_box;        // the tree's own rows come by TMA
 };
 
 template <int DP>
@@ -83,7 +83,7 @@ struct Smem {
 };
 
 struct Bars {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2], drain;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2], vraw, ready, drain;
   uint32_t tmem;
   int abort;
   float top[2][2][kTile];  // a row's maximum over each half of a tile
@@ -113,16 +113,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Bars* 
   return __all_sync(0xffffffffu, wait_bar(bar, parity, s, limit));
 }
 
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -131,6 +121,36 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[1
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+
+// 64 consecutive fp32 columns of this warp's 32 lanes, in two loads and one wait
+__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[2][32]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[e][0]), "=f"(v[e][1]), "=f"(v[e][2]), "=f"(v[e][3]), "=f"(v[e][4]),
+          "=f"(v[e][5]), "=f"(v[e][6]), "=f"(v[e][7]), "=f"(v[e][8]), "=f"(v[e][9]),
+          "=f"(v[e][10]), "=f"(v[e][11]), "=f"(v[e][12]), "=f"(v[e][13]), "=f"(v[e][14]),
+          "=f"(v[e][15]), "=f"(v[e][16]), "=f"(v[e][17]), "=f"(v[e][18]), "=f"(v[e][19]),
+          "=f"(v[e][20]), "=f"(v[e][21]), "=f"(v[e][22]), "=f"(v[e][23]), "=f"(v[e][24]),
+          "=f"(v[e][25]), "=f"(v[e][26]), "=f"(v[e][27]), "=f"(v[e][28]), "=f"(v[e][29]),
+          "=f"(v[e][30]), "=f"(v[e][31])
+        : "r"(taddr + 32 * e));
+  // (the values pass through the wait, so that nothing uses them before it)
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[e][0]), "+f"(v[e][1]), "+f"(v[e][2]), "+f"(v[e][3]), "+f"(v[e][4]),
+                   "+f"(v[e][5]), "+f"(v[e][6]), "+f"(v[e][7]), "+f"(v[e][8]), "+f"(v[e][9]),
+                   "+f"(v[e][10]), "+f"(v[e][11]), "+f"(v[e][12]), "+f"(v[e][13]),
+                   "+f"(v[e][14]), "+f"(v[e][15]), "+f"(v[e][16]), "+f"(v[e][17]),
+                   "+f"(v[e][18]), "+f"(v[e][19]), "+f"(v[e][20]), "+f"(v[e][21]),
+                   "+f"(v[e][22]), "+f"(v[e][23]), "+f"(v[e][24]), "+f"(v[e][25]),
+                   "+f"(v[e][26]), "+f"(v[e][27]), "+f"(v[e][28])
+                 :: "memory");
 }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
@@ -166,6 +186,55 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// One thread's 64 weights of a tile: exp2(c s - base) of 64 TMEM columns as bf16 pairs in
+// pk, their fp32 sum, and the largest c s - base.  192 instructions where nothing is
+// masked (the masked form, 64 selections more, is a branch of its own: folded into one by
+// the compiler the selections would run for every tile).
+template <bool kMasked>
+__device__ __forceinline__ void weights(uint32_t tS, float c, float base, const uint32_t (&w)[2],
+                                        float& top, float& total, uint32_t (&pk)[2][16]) {
+  float x[2][32], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  tmem_ld_64(tS, x);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) fma2(x[e][j], x[e][j + 1], c, -base);
+    if (kMasked) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[e][j] = (w[e] >> j) & 1u ? x[e][j] : -INFINITY;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      mx[0] = fmaxf(mx[0], fmaxf(x[e][j], x[e][j + 1]));
+      mx[1] = fmaxf(mx[1], fmaxf(x[e][j + 2], x[e][j + 3]));
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      x[e][j] = ex2(x[e][j]);
+      x[e][j + 1] = ex2(x[e][j + 1]);
+      add2(sum[0], sum[1], x[e][j], x[e][j + 1]);
+      pk[e][j / 2] = pack_bf16(x[e][j], x[e][j + 1]);
+    }
+  }
+  top = fmaxf(mx[0], mx[1]);
+  total = sum[0] + sum[1];
+}
+
+// the largest c s of 64 TMEM columns
+template <bool kMasked>
+__device__ __forceinline__ float largest(uint32_t tS, float c, const uint32_t (&w)[2]) {
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float x[32];
+    tmem_ld_32cols(tS + 32 * e, x);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (!kMasked || ((w[e] >> j) & 1u)) mx[j & 1] = fmaxf(mx[j & 1], c * x[j]);
+  }
+  return fmaxf(mx[0], mx[1]);
+}
+
 // bits of a packed pair of bf16 that are infinities or NaN
 __device__ __forceinline__ bool nonfinite2(uint32_t x) {
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
@@ -194,7 +263,9 @@ __device__ __noinline__ void add_nonfinite(const TcArgs& a, size_t out, size_t s
                                            int node, int hk, int c0, int c1) {
   for (int col = c0; col < min(c1, a.d.D); ++col) {
     float x = 0.f;
-    for (int nd = node; nd >= 0; nd = a.parent ? a.parent[first + nd] : nd - 1) {
+    for (int nd = node, up; nd >= 0; nd = up) {
+      up = a.parent ? a.parent[first + nd] : nd - 1;
+      if (up >= nd) up = -1;  // (a bad tree, reported)
       const float v = __bfloat162float(a.v[((size_t)(first + nd) * a.d.Hkv + hk) * a.d.D + col]);
       if (!isfinite(v)) x += v;
     }
@@ -207,7 +278,9 @@ __device__ __noinline__ void add_nonfinite(const TcArgs& a, size_t out, size_t s
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
-                 const __grid_constant__ CUtensorMap mapV, uint64_t limit_ns) {
+                 const __grid_constant__ CUtensorMap mapV,
+                 const __grid_constant__ CUtensorMap mapKo,
+                 const __grid_constant__ CUtensorMap mapVo, uint64_t limit_ns) {
   using L = Smem<DP>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -273,125 +346,120 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       mbar_init(&S->pvdone[s], 1);
       mbar_init(&S->lsum[s], kSoftmax / 2);
     }
+    mbar_init(&S->vraw, 1);
+    mbar_init(&S->ready, kSoftmax);  // Q and the tree are in shared memory
     mbar_init(&S->drain, 1);
     S->abort = 0;
     mbar_fence_init();
   }
   if (warp == kWarpMma) tmem_alloc(&S->tmem, 512);
-  // Q, negated where the scale is negative (the maximum is then taken with c >= 0)
-  const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-  for (int e = tid; e < 2 * kTile * (DP / 8); e += kThreads) {
-    const int r = e / (DP / 8), c8 = e % (DP / 8);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < rows && 8 * c8 < d.D) {
-      const int rho = r0 + r, tok = rho / G, g = rho - tok * G;
-      x = *reinterpret_cast<const uint4*>(a.q + ((size_t)tok * d.Hq + hk * G + g) * d.D + 8 * c8);
-      x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-    }
-    *reinterpret_cast<uint4*>(smem + L::OFF_Q + (r / kTile) * L::kQ + sw128_chunk(r % kTile, c8)) = x;
-  }
-  bool bad = false;
-  if (tree)
-    for (int i = tid; i < n; i += kThreads) {
-      const int p = a.parent[first + i];
-      bad |= p < -1 || p >= i;
-      sParent[i] = p;
-    }
-  fence_proxy_async_smem();
   tc_fence_before_sync();
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = S->tmem;
   constexpr uint32_t kStage = L::kKV;
 
-  if (bad) {
-    if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_TREE);
-  } else if (warp == kWarpK || warp == kWarpV) {
-    // ---- producers: K or V --------------------------------------------
+  if (warp == kWarpK || warp == kWarpV) {
+    // ---- producers: K or V --------------------------------------------------------------
     const bool isV = warp == kWarpV;
     uint64_t* full = isV ? S->vfull : S->kfull;
     uint64_t* empty = isV ? S->vempty : S->kempty;
-    const __nv_bfloat16* cache = isV ? a.v_cache : a.k_cache;
-    const __nv_bfloat16* mine = isV ? a.v : a.k;
-    const uint32_t base = smem_addr(smem + (isV ? L::OFF_V : L::OFF_K));
+    unsigned char* stage0 = smem + (isV ? L::OFF_V : L::OFF_K);
     constexpr int kChunks = DP / 8;             // 16-byte chunks a row
     constexpr int kRowsAtOnce = 32 / kChunks;   // rows a warp instruction covers
     const int c8 = lane % kChunks;
     const bool in_row = 8 * c8 < d.D;
+    uint32_t raw_phase = 0;
+    auto row_of = [&](int seg, int j) -> int {  // key j's row in the cache, -1: a bad page
+      const int pi = j / d.page_size;
+      const int pg = seg == kPrefix ? a.prefix_pages[pi] : a.table[(size_t)b * d.table_width + pi];
+      if (pg >= 0 && pg < d.n_pages) return pg * d.page_size + (j - pi * d.page_size);
+      report_page(a, seg == kPrefix, b);
+      return -1;
+    };
     for (int i = i0; i < i1; ++i) {
       const int at = i - i0, st = at & 1;
       int seg, j0, len;
       tile_of(i, seg, j0, len);
-      if (a.box_rows && seg != kOwn && len - j0 >= kTile) {
-        // a whole tile: lane l brings box l
-        const int boxes = kTile / a.box_rows;
+      const int valid = min(len - j0, kTile);
+      unsigned char* stage = stage0 + st * kStage;
+      // V rows that are masked for every row (past a length) or for some (the tree's) must
+      // not meet a zero weight with an infinity or a NaN: they pass through this warp
+      const bool fix = isV && (seg == kOwn || valid < kTile);
+      if (seg == kOwn ? a.own_box : a.box_rows != 0) {
+        const int box = seg == kOwn ? kTile : a.box_rows;
+        const int boxes = (valid + box - 1) / box;
         int crow = 0;
         if (lane < boxes) {
-          const int j = j0 + lane * a.box_rows, pi = j / d.page_size;
-          const int pg = seg == kPrefix ? a.prefix_pages[pi]
-                                        : a.table[(size_t)b * d.table_width + pi];
-          // (a row past the last one reads zeros)
-          crow = pg >= 0 && pg < d.n_pages ? pg * d.page_size + (j - pi * d.page_size)
-                                           : d.n_pages * d.page_size;
-          if (pg < 0 || pg >= d.n_pages) report_page(a, seg == kPrefix, b);
+          crow = seg == kOwn ? first + j0 : row_of(seg, j0 + lane * box);
+          if (crow < 0) crow = d.n_pages * d.page_size;  // (past the last row: reads zeros)
         }
         if (at >= 2 && !wait_warp(&empty[st], ((at >> 1) & 1) ^ 1, S, limit_ns)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStage);
+        uint64_t* bar = fix ? &S->vraw : &full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * DP * 2));
         __syncwarp();
         if (lane < boxes) {
-          unsigned char* to = smem + (isV ? L::OFF_V : L::OFF_K) + st * kStage + lane * a.box_rows * 128;
+          const CUtensorMap* map = seg == kOwn ? (isV ? &mapVo : &mapKo) : (isV ? &mapV : &mapK);
 #pragma unroll
           for (int c = 0; c < DP / 64; ++c)
-            tma_load_3d(to + c * kSw128TileBytes, isV ? &mapV : &mapK, &full[st], 64 * c, hk, crow);
+            tma_load_3d(stage + c * kSw128TileBytes + lane * box * 128, map, bar, 64 * c, hk, crow);
         }
-        continue;
-      }
-      // lane l looks up rows l, 32 + l, 64 + l, 96 + l of the tile
-      int row[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + 32 * e + lane;
-        row[e] = -1;
-        if (j < len) {
-          if (seg == kOwn) {
-            row[e] = first + j;
-          } else {
-            const int pi = j / d.page_size;
-            const int pg = seg == kPrefix ? a.prefix_pages[pi]
-                                          : a.table[(size_t)b * d.table_width + pi];
-            if (pg >= 0 && pg < d.n_pages)
-              row[e] = pg * d.page_size + (j - pi * d.page_size);
-            else
-              report_page(a, seg == kPrefix, b);
-          }
-        }
-      }
-      if (at >= 2 && !wait_warp(&empty[st], ((at >> 1) & 1) ^ 1, S, limit_ns)) break;
-      const __nv_bfloat16* src = (seg == kOwn ? mine : cache) + (size_t)hk * d.D + 8 * c8;
-      const size_t stride = (size_t)d.Hkv * d.D;
-      const uint32_t dst = base + st * kStage;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
-          const int r = rr + lane / kChunks, key = 32 * e + r;
-          const int x = __shfl_sync(0xffffffffu, row[e], r);
-          const bool take = x >= 0 && in_row;
-          cp_async16_zfill(dst + sw128_chunk(key, c8), take ? src + x * stride : src, take);
-        }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (isV && seg == kOwn) {
-        // own rows are masked for some of the query rows only: what is not finite is kept
-        // out of the product (0 * inf) and added to the rows that see it at the end
-        if (lane < 4) S->badv[st][lane] = 0u;
         __syncwarp();
+        if (!fix) continue;
+        if (!wait_warp(&S->vraw, raw_phase, S, limit_ns)) break;
+        raw_phase ^= 1u;
+      } else {
+        // lane l looks up rows l, 32 + l, 64 + l, 96 + l of the tile
+        int row[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 32 * e + lane;
+          row[e] = j >= valid ? -1 : seg == kOwn ? first + j0 + j : row_of(seg, j0 + j);
+        }
+        if (at >= 2 && !wait_warp(&empty[st], ((at >> 1) & 1) ^ 1, S, limit_ns)) break;
+        const __nv_bfloat16* src = (seg == kOwn ? (isV ? a.v : a.k) : (isV ? a.v_cache : a.k_cache)) +
+                                   (size_t)hk * d.D + 8 * c8;
+        const size_t stride = (size_t)d.Hkv * d.D;
+        const uint32_t dst = smem_addr(stage);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
 #pragma unroll 8
-        for (int key = lane / kChunks; key < kTile; key += kRowsAtOnce) {
-          uint4* at16 = reinterpret_cast<uint4*>(smem + L::OFF_V + st * kStage + sw128_chunk(key, c8));
-          uint4 w = *at16;
-          if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
-            atomicOr(&S->badv[st][key >> 5], 1u << (key & 31));
-            *at16 = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+          for (int rr = 0; rr < 32; rr += kRowsAtOnce) {
+            const int r = rr + lane / kChunks;
+            const int x = __shfl_sync(0xffffffffu, row[e], r);
+            const bool take = x >= 0 && in_row;
+            cp_async16_zfill(dst + sw128_chunk(32 * e + r, c8), take ? src + x * stride : src, take);
+          }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      if (fix) {
+        for (int key = valid + lane / kChunks; key < kTile; key += kRowsAtOnce)
+          *reinterpret_cast<uint4*>(stage + sw128_chunk(key, c8)) = make_uint4(0, 0, 0, 0);
+        if (seg == kOwn) {
+          // what is not finite is kept out of the product and added to the rows that see
+          // it at the end; a multiple of zero tells whether there is any
+          if (lane < 4) S->badv[st][lane] = 0u;
+          __syncwarp();
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 8
+          for (int key = lane / kChunks; key < valid; key += kRowsAtOnce) {
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + sw128_chunk(key, c8));
+            acc[0] = __hfma2(reinterpret_cast<const __nv_bfloat162&>(w.x), zero, acc[0]);
+            acc[1] = __hfma2(reinterpret_cast<const __nv_bfloat162&>(w.y), zero, acc[1]);
+            acc[2] = __hfma2(reinterpret_cast<const __nv_bfloat162&>(w.z), zero, acc[2]);
+            acc[3] = __hfma2(reinterpret_cast<const __nv_bfloat162&>(w.w), zero, acc[3]);
+          }
+          const float2 t0 = __bfloat1622float2(__hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3])));
+          if (__any_sync(0xffffffffu, isnan(t0.x + t0.y))) {
+            for (int key = lane / kChunks; key < valid; key += kRowsAtOnce) {
+              uint4* at16 = reinterpret_cast<uint4*>(stage + sw128_chunk(key, c8));
+              const uint4 w = *at16;
+              if (nonfinite2(w.x) || nonfinite2(w.y) || nonfinite2(w.z) || nonfinite2(w.w)) {
+                atomicOr(&S->badv[st][key >> 5], 1u << (key & 31));
+                *at16 = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+              }
+            }
           }
         }
       }
@@ -401,71 +469,101 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kWarpMma) {
-    // ---- MMAs --------------------------------------------------------------------------
-    if (lane == 0 && ntiles > 0) {
-      const uint32_t aQ = smem_addr(smem + L::OFF_Q), aK = smem_addr(smem + L::OFF_K),
-                     aV = smem_addr(smem + L::OFF_V);
+    // ---- MMAs: the warp waits together, one lane issues ---------------------------------
+    if (ntiles > 0) {
       constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t idO = idesc_bf16_f32_bmn(kTile, DP);
-      auto issue_s = [&](int tile, int st) {
+      const uint64_t dQ = desc_sw128_kmajor(smem_addr(smem + L::OFF_Q));
+      const uint64_t dK = desc_sw128_kmajor(smem_addr(smem + L::OFF_K));
+      // (V: keys are K rows, D contiguous; 8-key groups 1 KB apart, 64-column blocks 16 KB)
+      const uint64_t dV = desc_sw128_mnmajor(smem_addr(smem + L::OFF_V), kSw128TileBytes, 1024);
+      auto issue_s = [&](int tile, int st, bool last_of_k) {
+        if (elect_one()) {
+          const uint32_t to = tmem + tile * kTile;
+          const uint64_t q = dQ + tile * (L::kQ >> 4), k = dK + st * (kStage >> 4);
 #pragma unroll
-        for (int s = 0; s < DP / 16; ++s) {
-          const uint32_t off = (uint32_t)((s >> 2) * kSw128TileBytes + (s & 3) * 32);
-          umma_bf16(tmem + tile * kTile, desc_sw128_kmajor(aQ + tile * L::kQ + off),
-                    desc_sw128_kmajor(aK + st * kStage + off), idS, s > 0);
+          for (int s = 0; s < DP / 16; ++s) {
+            const uint32_t off = ((s >> 2) * kSw128TileBytes + (s & 3) * 32) >> 4;
+            if (s == 0) umma_ss<false>(to, q + off, k + off, idS);
+            else umma_ss<true>(to, q + off, k + off, idS);
+          }
+          umma_commit(&S->sfull[tile]);
+          if (last_of_k) umma_commit(&S->kempty[st]);
         }
-        umma_commit(&S->sfull[tile]);
+        __syncwarp();
       };
-      auto issue_pv = [&](int tile, int st, bool acc) {
-        // (V: keys are K rows, D contiguous; 8-key groups 1 KB apart, 64-column blocks 16 KB)
+      auto issue_pv = [&](int tile, int st, bool first_tile, bool last_of_v) {
+        if (elect_one()) {
+          const uint32_t to = tmem + 2 * kTile + tile * kTile, p = tmem + tile * kTile;
+          const uint64_t v = dV + st * (kStage >> 4);
+          if (first_tile) umma_ts<false>(to, p, v, idO);
+          else umma_ts<true>(to, p, v, idO);
 #pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          umma_ts(tmem + 2 * kTile + tile * kTile,
-                  tmem + tile * kTile + (s >> 2) * kHalf + 8 * (s & 3),
-                  desc_sw128_mnmajor(aV + st * kStage + (uint32_t)s * 2048, kSw128TileBytes, 1024), idO,
-                  acc || s > 0);
-        umma_commit(&S->pvdone[tile]);
+          for (int s = 1; s < kTile / 16; ++s)
+            umma_ts<true>(to, p + (s >> 2) * kHalf + 8 * (s & 3), v + ((s * 2048) >> 4), idO);
+          umma_commit(&S->pvdone[tile]);
+          if (last_of_v) umma_commit(&S->vempty[st]);
+        }
+        __syncwarp();
       };
-      bool ok = wait_bar(&S->kfull[0], 0, S, limit_ns);
+      bool ok = wait_warp(&S->ready, 0, S, limit_ns) && wait_warp(&S->kfull[0], 0, S, limit_ns);
       if (ok) {
-        issue_s(0, 0);
-        if (two) issue_s(1, 0);
-        umma_commit(&S->kempty[0]);
+        issue_s(0, 0, !two);
+        if (two) issue_s(1, 0, true);
       }
       for (int at = 0; ok && at < ntiles; ++at) {
         const int st = at & 1, nx = (at + 1) & 1;
-        const uint32_t ph = (at >> 1) & 1;
         const bool more = at + 1 < ntiles;
-        ok = wait_bar(&S->vfull[st], ph, S, limit_ns) &&
-             wait_bar(&S->pready[0], at & 1, S, limit_ns);
+        ok = wait_warp(&S->vfull[st], (at >> 1) & 1, S, limit_ns) &&
+             wait_warp(&S->pready[0], at & 1, S, limit_ns);
         if (!ok) break;
         tc_fence_after_sync();
-        issue_pv(0, st, at > 0);
-        if (!two) umma_commit(&S->vempty[st]);
+        issue_pv(0, st, at == 0, !two);
         if (more) {
-          ok = wait_bar(&S->kfull[nx], ((at + 1) >> 1) & 1, S, limit_ns);
+          ok = wait_warp(&S->kfull[nx], ((at + 1) >> 1) & 1, S, limit_ns);
           if (!ok) break;
-          issue_s(0, nx);
-          if (!two) umma_commit(&S->kempty[nx]);
+          issue_s(0, nx, !two);
         }
         if (two) {
-          ok = wait_bar(&S->pready[1], at & 1, S, limit_ns);
+          ok = wait_warp(&S->pready[1], at & 1, S, limit_ns);
           if (!ok) break;
           tc_fence_after_sync();
-          issue_pv(1, st, at > 0);
-          umma_commit(&S->vempty[st]);
-          if (more) {
-            issue_s(1, nx);
-            umma_commit(&S->kempty[nx]);
-          }
+          issue_pv(1, st, at == 0, true);
+          if (more) issue_s(1, nx, true);
         }
       }
       // whatever was issued is done before TMEM and the operands go
-      umma_commit(&S->drain);
+      if (elect_one()) umma_commit(&S->drain);
+      __syncwarp();
       mbar_wait(&S->drain, 0, limit_ns);
     }
     __syncwarp();
   } else {
+    // Q, negated where the scale is negative (the maximum is then taken with c >= 0), and
+    // the tree (a parent that is not earlier is an error; taken as a root meanwhile)
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
+    for (int e = tid; e < 2 * kTile * (DP / 8); e += kSoftmax) {
+      const int r = e / (DP / 8), c8 = e % (DP / 8);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < rows && 8 * c8 < d.D) {
+        const int rho = r0 + r, tok = rho / G, g = rho - tok * G;
+        x = *reinterpret_cast<const uint4*>(a.q + ((size_t)tok * d.Hq + hk * G + g) * d.D + 8 * c8);
+        x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+      }
+      *reinterpret_cast<uint4*>(smem + L::OFF_Q + (r / kTile) * L::kQ + sw128_chunk(r % kTile, c8)) = x;
+    }
+    if (tree)
+      for (int i = tid; i < n; i += kSoftmax) {
+        const int p = a.parent[first + i];
+        const bool bad = p < -1 || p >= i;
+        sParent[i] = bad ? -1 : p;
+        if (bad && a.dev_status) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_TREE);
+      }
+    fence_proxy_async_smem();
+    __syncwarp();
+    mbar_arrive(&S->ready);
+    bool ok = wait_warp(&S->ready, 0, S, limit_ns);
     // ---- softmax: two threads a row --------------------------------------------------------
     const int tile = warp >> 3, half = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
     const int r = tile * kTile + lr;
@@ -477,33 +575,23 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     const bool live = r < rows;
     int walk = node;                   // the next node of the path that is not yet masked
     float mref = -INFINITY, l = 0.f;   // of c s; l: this half's
-    bool ok = true, poison = false;
+    bool poison = false;
     if (tile == 0 || two) {
-      for (int i = i0; i < i1; ++i) {
+      for (int i = i0; ok && i < i1; ++i) {
         const int at = i - i0;
         int seg, j0, len;
         tile_of(i, seg, j0, len);
         ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns);
-        if (!ok) {  // (the other warp may be at the exchange already: it is not left there)
-          asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
+        if (!ok) {  // (the other warp may be at its exchanges already: it is not left there)
+          for (int e = at == 0 ? 3 : 1; e > 0; --e)
+            asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
           break;
         }
         tc_fence_after_sync();
         const int valid = len - j0;
         const bool masked = seg == kOwn || valid < kTile;
         uint32_t w[2];  // the keys of this half of the tile that the row sees, a bit a key
-        float top = -INFINITY;
-        if (!masked) {
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x[32];
-            tmem_ld_32cols(tS + 32 * e, x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-          }
-          top = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        } else {
+        if (masked) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int left = (seg == kOwn && !tree ? min(valid, node - j0 + 1) : valid) -
@@ -522,67 +610,57 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
             w[1] &= (uint32_t)(on >> 32);
           }
           __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x[32];
-            tmem_ld_32cols(tS + 32 * e, x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              top = fmaxf(top, (w[e] >> j) & 1u ? c * x[j] : -INFINITY);
-          }
         }
-        // the row's maximum: the other half's beside this one's
-        S->top[tile][half][lr] = top;
-        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-        top = fmaxf(top, S->top[tile][half ^ 1][lr]);
-        // (NaN scores: fmaxf drops them here, and they come back as NaN weights)
-        const bool grow = top > mref + kGrow;  // (mref = -inf: any finite top)
-        if (__any_sync(0xffffffffu, grow)) {
-          const float to = grow ? top : mref;
-          const float keep = grow ? (mref == -INFINITY ? 0.f : ex2(mref - to)) : 1.f;
+        if (at == 0) {  // the first tile's own maximum, so that its weights are made once
+          const float mine = masked ? largest<true>(tS, c, w) : largest<false>(tS, c, w);
+          S->top[tile][half][lr] = mine;
+          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+          mref = fmaxf(mine, S->top[tile][half ^ 1][lr]);
+          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+        }
+        uint32_t pk[2][16];
+        float sum;
+        // the weights for the maximum that the sums use; where the row's own maximum turns
+        // out to have grown by too much, O and l are rescaled and the weights made again
+        for (bool again = false;; again = true) {
+          const float base = mref == -INFINITY ? 0.f : mref;
+          float mine;
+          if (masked) weights<true>(tS, c, base, w, mine, sum, pk);
+          else weights<false>(tS, c, base, w, mine, sum, pk);
+          if (again) break;
+          // the row's maximum, over base: the other half's beside this one's
+          // (NaN scores: fmaxf drops them here; their weights and sums are NaN)
+          S->top[tile][half][lr] = mine;
+          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+          const float top = fmaxf(mine, S->top[tile][half ^ 1][lr]);
+          const bool grow = top > (mref == -INFINITY ? -INFINITY : kGrow);
+          if (!__any_sync(0xffffffffu, grow)) break;
+          const float to = grow ? base + top : mref;
+          const float keep = grow ? (mref == -INFINITY ? 0.f : ex2(-top)) : 1.f;
           if (at > 0) {
             // O of the tiles before is complete once their last product is
             ok = wait_warp(&S->pvdone[tile], (at - 1) & 1, S, limit_ns);
             if (!ok) break;
             tc_fence_after_sync();
+#pragma unroll 1
+            for (int e = 0; e < DP / 32; ++e) {  // this half's columns of O, 16 at a time
+              float y[16];
+              uint32_t z[16];
+              const uint32_t at16 = tO + DP / 2 * half + 16 * e;
+              tmem_ld_16cols(at16, y);
 #pragma unroll
-            for (int e = 0; e < DP / 64; ++e) {  // this half's columns of O
-              float y[32];
-              const uint32_t to32 = tO + DP / 2 * half + 32 * e;
-              tmem_ld_32cols(to32, y);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) y[j] *= keep;
-              tmem_st_32cols(to32, y);
+              for (int j = 0; j < 16; ++j) z[j] = __float_as_uint(y[j] * keep);
+              tmem_st_16(at16, z);
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           }
           l *= keep;
           mref = to;
         }
-        const float base = mref == -INFINITY ? 0.f : mref;
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x[32];
-          uint32_t pk[16];
-          tmem_ld_32cols(tS + 32 * e, x);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            fma2(x[j], x[j + 1], c, -base);
-            x[j] = ex2(x[j]);
-            x[j + 1] = ex2(x[j + 1]);
-          }
-          if (masked) {
-            #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = (w[e] >> j) & 1u ? x[j] : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            add2(sum[0], sum[1], x[j], x[j + 1]);
-            pk[j / 2] = pack_bf16(x[j], x[j + 1]);
-          }
-          tmem_st_16(tS + 16 * e, pk);
-        }
-        l += sum[0] + sum[1];
+        if (!ok) break;
+        tmem_st_16(tS, pk[0]);
+        tmem_st_16(tS + 16, pk[1]);
+        l += sum;
         if (seg == kOwn) {
           // (the V tile is read behind its barrier: its bits are written by then)
           ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns);
@@ -743,15 +821,15 @@ size_t part_floats(const gdn_tree_attend_dims& d, const Plan& p) {
 }
 
 template <int DP>
-cudaError_t launch_units(const TcArgs& t, const CUtensorMap& mapK, const CUtensorMap& mapV,
-                         long long blocks, cudaStream_t stream) {
+cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[4], long long blocks,
+                         cudaStream_t stream) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<DP>::kBytes);
   if (err != cudaSuccess) return err;
   attend_tc_kernel<DP><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
-      t, mapK, mapV, wait_hooks().limit_ns);
+      t, map[0], map[1], map[2], map[3], wait_hooks().limit_ns);
   return cudaGetLastError();
 }
 
@@ -788,20 +866,22 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     t.part_o = static_cast<float*>(a.workspace);
     t.part_lse = t.part_o + part_floats(d, p);
   }
-  // whole tiles by TMA where pages and tiles divide one another
-  CUtensorMap mapK, mapV;
-  memset(&mapK, 0, sizeof mapK);
-  memset(&mapV, 0, sizeof mapV);
+  // cache tiles by TMA where pages and tiles divide one another
+  CUtensorMap map[4];
+  memset(map, 0, sizeof map);
   const int box = d.page_size < kTile ? d.page_size : kTile;
   const long long cache_rows = (long long)d.n_pages * d.page_size;
   if (d.D % 64 == 0 && box % 8 == 0 && kTile % box == 0 && d.page_size % box == 0 &&
       cache_rows > 0 && cache_rows < 0x7fffffffll && a.k_cache &&
-      encode_head_rows_map(&mapK, a.k_cache, cache_rows, d.Hkv, d.D, box) &&
-      encode_head_rows_map(&mapV, a.v_cache, cache_rows, d.Hkv, d.D, box))
+      encode_head_rows_map(&map[0], a.k_cache, cache_rows, d.Hkv, d.D, box) &&
+      encode_head_rows_map(&map[1], a.v_cache, cache_rows, d.Hkv, d.D, box))
     t.box_rows = box;
+  t.own_box = d.D % 64 == 0 && a.k &&
+              encode_head_rows_map(&map[2], a.k, d.T, d.Hkv, d.D, kTile) &&
+              encode_head_rows_map(&map[3], a.v, d.T, d.Hkv, d.D, kTile);
   auto units = [&](const TcArgs& x, long long blocks) {
-    return d.D <= 64 ? launch_units<64>(x, mapK, mapV, blocks, stream)
-                     : launch_units<128>(x, mapK, mapV, blocks, stream);
+    return d.D <= 64 ? launch_units<64>(x, map, blocks, stream)
+                     : launch_units<128>(x, map, blocks, stream);
   };
   cudaError_t err = cudaSuccess;
   if (p.shared) {

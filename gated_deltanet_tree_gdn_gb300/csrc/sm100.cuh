@@ -370,6 +370,40 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// One lane of a converged warp, the same one every time.  Code behind it is known to be a
+// single thread's, which lets an MMA's descriptors stay in uniform registers: an MMA of
+// M = 128, N = 32 .. 128 then issues in the 16 .. 64 cycles it takes; behind `lane == 0`
+// it takes at least 46 cycles to issue, and 87 to 168 with a predicate and descriptors
+// worked out for each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// MMAs whose accumulation is known when the code is compiled: D[tmem] (+)= A B, A in
+// shared memory (_ss) or bf16 pairs in TMEM columns (_ts)
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
 // ---- operand layouts and MMA sequences shared by the tensor-core kernels -------
 
 // one 64-wide K block of a 128-row K-major bf16 tile: 128 rows x 128 bytes
