@@ -308,7 +308,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
       return;
     }
-    if (n * G < a.min_rows) return;
+    if (n * G <= kAttendFewRows) return;  // (attend_few.cu's)
   }
   const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
   const int r0 = first * G + t * 2 * kTile;
@@ -749,7 +749,9 @@ attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
   const int first = cu[b], stop = cu[b + 1];
   const long long at = (long long)(blockIdx.x % groups) * 8 + (threadIdx.x >> 5);
   // (a sequence whose rows are out of range was reported, and has no parts)
-  if (first < 0 || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq) return;
+  if (first < 0 || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq ||
+      (stop - first) * (d.Hq / d.Hkv) <= kAttendFewRows)  // (attend_few.cu adds those up itself)
+    return;
   const size_t rows = (size_t)d.T * d.Hq, row = (size_t)first * d.Hq + at;
   float top = -INFINITY;
   for (int s = lane; s < slots; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
@@ -783,7 +785,8 @@ struct Plan {
   bool tc = false;
   bool shared = false;     // the prefix as units of its own
   int prefix_splits = 0, prefix_tiles = 0;
-  int seq_splits = 1, seq_tiles = 0;
+  bool many = false;       // some sequence may have more rows than attend_few.cu takes
+  int seq_splits = 0, seq_tiles = 0;
   int slots = 0;           // parts of a row (0: the kernel writes o itself)
 };
 
@@ -803,16 +806,17 @@ Plan plan_of(const gdn_tree_attend_dims& d) {
   // parts of at least 4 key tiles, until every SM has a unit
   auto splits = [&](long long n, long long k) {
     const long long most = (k + 4 * kTile - 1) / (4 * kTile);
-    const long long want = n >= sms ? 1 : sms / n;
+    const long long want = n >= sms ? 1 : sms / n < kAttendMaxParts ? sms / n : kAttendMaxParts;
     return (int)(want < most ? want : most < 1 ? 1 : most);
   };
-  p.seq_splits = splits(units, keys);
+  p.many = (long long)d.N * G > kAttendFewRows;
+  if (p.many) p.seq_splits = splits(units, keys);
   if (p.shared) {
     p.prefix_tiles = tiles(rows);
     p.prefix_splits = splits((long long)d.Hkv * p.prefix_tiles, d.prefix_len);
   }
   p.slots = p.prefix_splits + p.seq_splits;
-  if (p.slots == 1) p.slots = 0;
+  if (!p.shared && p.seq_splits <= 1) p.slots = 0;
   return p;
 }
 
@@ -891,6 +895,10 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits);
     if (err != cudaSuccess) return err;
   }
+  // sequences of few rows, with the prefix's parts added up on the spot
+  err = launch_attend_few(a, p.shared ? 0 : d.prefix_len, t.part_o, t.part_lse, p.prefix_splits,
+                          stream);
+  if (err != cudaSuccess || !p.many) return err;
   t.prefix_units = false;
   t.with_prefix = !p.shared;
   t.slot0 = p.prefix_splits;

@@ -194,6 +194,12 @@ struct AttendArgs {
 };
 size_t attend_workspace_bytes(const gdn_tree_attend_dims& d);
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream);
+// sequences of at most kAttendFewRows query rows a key head (others are left alone); parts
+// of the rows' keys that other units took ([parts][T * Hq][D], [parts][T * Hq]) are added
+constexpr int kAttendFewRows = 16;
+constexpr int kAttendMaxParts = 64;  // of the shared prefix
+cudaError_t launch_attend_few(const AttendArgs& a, int prefix_len, const float* part_o,
+                              const float* part_lse, int parts, cudaStream_t stream);
 cudaError_t launch_attend_generic(const AttendArgs& a, cudaStream_t stream);
 
 // rows of accepted paths (or all rows) into the pages of a cache
