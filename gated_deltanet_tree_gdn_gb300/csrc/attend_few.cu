@@ -362,7 +362,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
       S.cl[r] = L;
     }
   }
-  cluster.sync();
+  if (C > 1) cluster.sync();
+  else __syncthreads();
 
   // ---- the rows' weights: the cluster's CTAs and the prefix's parts -----------------------
   const size_t T = (size_t)d.T * d.Hq;
@@ -444,7 +445,7 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
     }
     *reinterpret_cast<uint2*>(o + at * d.D + x) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
 template <int DP>
@@ -482,13 +483,13 @@ cudaError_t launch_dp(const AttendArgs& a, int plen, const float* part_o, const 
 cudaError_t launch_attend_few(const AttendArgs& a, int prefix_len, const float* part_o,
                               const float* part_lse, int parts, cudaStream_t stream) {
   const gdn_tree_attend_dims& d = a.d;
-  // CTAs a sequence and key head: until the SMs are filled twice over (two CTAs each), as
-  // long as a warp has 16 keys to take
+  // CTAs a sequence and key head: as many as run at once (two an SM; half as many again
+  // are let through), as long as a warp has 16 keys to take
   const int sms = sm_count() > 0 ? sm_count() : 152;
   const long long units = (long long)d.B * d.Hkv;
   const long long keys = (long long)d.table_width * d.page_size + d.N + prefix_len;
   int cluster = 1;
-  while (cluster < kMaxCluster && units * cluster < 4 * sms && keys > 16 * kWarps * cluster)
+  while (cluster < kMaxCluster && units * cluster * 2 <= 3 * sms && keys > 16 * kWarps * cluster)
     cluster *= 2;
   return d.D <= 64 ? launch_dp<64>(a, prefix_len, part_o, part_lse, parts, cluster, stream)
                    : launch_dp<128>(a, prefix_len, part_o, part_lse, parts, cluster, stream);
