@@ -24,8 +24,8 @@ from ._binding import (  # noqa: F401
     BF16, F32, OK, EINVAL, EUNSUPPORTED, ECUDA, STATUS_OK, STATUS_BAD_TREE,
     STATUS_BAD_PATH, STATUS_TIMEOUT, SYMBOLS, Dims, GdnTreeError, commit, commit_verify,
     library_path, load, strerror, verify, verify_recurrent, verify_packed, commit_packed,
-    commit_verify_packed, STATUS_BAD_LAYOUT, build_topw, AttendDims, prefill, decode_step,
-    attend, attend_workspace, cache_append,
+    commit_verify_packed, STATUS_BAD_LAYOUT, build_topw, AttendDims, prefill,
+    prefill_workspace, decode_step, attend, attend_workspace, cache_append,
 )
 from .build import build_library  # noqa: F401
 

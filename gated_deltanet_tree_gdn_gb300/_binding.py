@@ -21,7 +21,7 @@ STATUS_OK, STATUS_BAD_TREE, STATUS_BAD_PATH, STATUS_TIMEOUT, STATUS_BAD_LAYOUT =
 
 SYMBOLS = ("gdn_tree_verify", "gdn_tree_commit", "gdn_tree_commit_verify",
            "gdn_tree_verify_recurrent", "gdn_tree_verify_packed", "gdn_tree_commit_packed",
-           "gdn_tree_commit_verify_packed", "gdn_tree_build_topw", "gdn_tree_prefill",
+           "gdn_tree_commit_verify_packed", "gdn_tree_build_topw", "gdn_tree_prefill", "gdn_tree_prefill_workspace",
            "gdn_tree_decode_step", "gdn_tree_attend", "gdn_tree_attend_workspace",
            "gdn_tree_cache_append", "gdn_tree_strerror", "gdn_tree_version")
 
@@ -85,7 +85,9 @@ def load(path: str | None = None):
     lib.gdn_tree_build_topw.argtypes = [fp, i32, i32, i32, i32, i32, ip, ip, fp, ip, vp]
     lib.gdn_tree_build_topw.restype = ctypes.c_int
     lib.gdn_tree_prefill.argtypes = [vp, vp, vp, fp, fp, ip, i32, fp, fp, ip, i32, vp, Dims, ip,
-                                     vp]
+                                     vp, ctypes.c_size_t, vp]
+    lib.gdn_tree_prefill_workspace.argtypes = [Dims, i32]
+    lib.gdn_tree_prefill_workspace.restype = ctypes.c_size_t
     lib.gdn_tree_prefill.restype = ctypes.c_int
     lib.gdn_tree_decode_step.argtypes = [vp, vp, vp, fp, fp, fp, fp, ip, i32, vp, Dims, ip, vp]
     lib.gdn_tree_decode_step.restype = ctypes.c_int
@@ -494,8 +496,26 @@ def _most_rows(cu) -> int:
     return int((cu[1:] - cu[:-1]).max().item()) if cu.shape[0] > 1 else 0
 
 
+def _workspace(given, need, device):
+    """The workspace to pass: the caller's, one of our own, or none where none is needed."""
+    if given is not None:
+        _check(given, "workspace", torch.uint8)
+        if given.numel() < need:
+            raise ValueError(f"workspace has {given.numel()} bytes, {need} are needed")
+    return None if not need else given if given is not None else torch.empty(
+        need, dtype=torch.uint8, device=device)
+
+
+_prefill_cache: dict = {}
+
+
+def prefill_workspace(dims: Dims, T: int) -> int:
+    """Bytes of device memory that ``prefill`` needs for these dims and T rows."""
+    return load().gdn_tree_prefill_workspace(dims, T)
+
+
 def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None, N_max=None,
-            pool_out=None, o=None, dev_status=None, stream=None):
+            pool_out=None, o=None, workspace=None, dev_status=None, stream=None):
     """The gated delta rule over whole sequences (C ABI gdn_tree_prefill).
     Returns (o, pool_out).
 
@@ -503,7 +523,7 @@ def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None,
     int32 row offsets; state_pool [n_slots,Hv,dk,dv] fp32 with state_slot [B] (None: slot
     b) holds the state each sequence starts from.  o [T,Hv,dv] is allocated when not given;
     pool_out=state_pool updates in place, a new pool starts as a copy of state_pool.
-    N_max is the longest sequence (computed from cu_tokens on the host if None)."""
+    workspace (``prefill_workspace`` bytes, uint8) is allocated when not given.  N_max is the longest sequence (computed from cu_tokens on the host if None)."""
     T, Hqk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = cu_tokens.shape[0] - 1
@@ -527,11 +547,19 @@ def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None,
     _check(o, "o", dt, (T, Hv, dv))
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (B,))
+    key = (B, N_max, Hqk, Hv, dk, dv, code, T)
+    known = _prefill_cache.get(key)
+    if known is None:
+        d = Dims(*key[:7])
+        known = d, prefill_workspace(d, T)
+        if len(_prefill_cache) < 256:
+            _prefill_cache[key] = known
+    d, need = known
+    workspace = _workspace(workspace, need, q.device)
     rc = load().gdn_tree_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                  _ptr(cu_tokens), T, _ptr(state_pool), _ptr(pool_out),
-                                 _ptr(state_slot), n_slots, _ptr(o),
-                                 Dims(B, N_max, Hqk, Hv, dk, dv, code), _ptr(dev_status),
-                                 _stream(stream))
+                                 _ptr(state_slot), n_slots, _ptr(o), d, _ptr(dev_status),
+                                 _ptr(workspace), need, _stream(stream))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_prefill")
     return o, pool_out
@@ -640,17 +668,12 @@ def attend(q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len,
         if len(_attend_cache) < 256:
             _attend_cache[key] = known
     d, need = known
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-        if workspace.numel() < need:
-            raise ValueError(f"workspace has {workspace.numel()} bytes, {need} are needed")
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _workspace(workspace, need, q.device)
     rc = lib.gdn_tree_attend(_ptr(q), _ptr(k), _ptr(v), _ptr(parent), _ptr(cu_nodes),
                              _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(context_len),
                              _ptr(prefix_pages) if prefix_len else None,
                              D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), d,
-                             _ptr(dev_status), _ptr(workspace) if need else None, need,
+                             _ptr(dev_status), _ptr(workspace), need,
                              _stream(stream))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_attend")

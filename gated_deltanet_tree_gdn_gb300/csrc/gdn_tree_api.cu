@@ -431,7 +431,8 @@ int gdn_tree_build_topw(const float* cand_logp, int32_t B, int32_t N, int32_t c,
 static int rule_call(const void* q, const void* k, const void* v, const float* log_alpha,
                      const float* beta, const float* pool_in, float* pool_out, void* o,
                      const gdn_tree_dims& dims, const gdn::SeqLayout& lay, int32_t T,
-                     int32_t* dev_status, bool step, void* stream) {
+                     int32_t* dev_status, bool step, void* workspace, size_t workspace_bytes,
+                     void* stream) {
   const void* ptrs[] = {pool_in, pool_out};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return GDN_TREE_EINVAL;
@@ -442,10 +443,13 @@ static int rule_call(const void* q, const void* k, const void* v, const float* l
   const int slots = lay.slot ? lay.n_slots : dims.B;
   if (partial_overlap(pool_in, pool_out, (size_t)slots * dims.Hv * dims.dk * dims.dv * 4))
     return GDN_TREE_EINVAL;
+  const size_t want = step ? 0 : gdn::prefill_workspace_bytes(dims, T);
+  if (want > 0 && (workspace == nullptr || !aligned16(workspace) || workspace_bytes < want))
+    return GDN_TREE_EINVAL;
   const gdn::RuleArgs a{q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, dev_status, lay};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
-  const cudaError_t err = step ? gdn::launch_decode_step(a, st) : gdn::launch_prefill(a, st);
+  const cudaError_t err = step ? gdn::launch_decode_step(a, st) : gdn::launch_prefill(a, workspace, st);
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
 }
 
@@ -453,7 +457,7 @@ int gdn_tree_prefill(const void* q, const void* k, const void* v, const float* l
                      const float* beta, const int32_t* cu_tokens, int32_t T,
                      const float* pool_in, float* pool_out, const int32_t* state_slot,
                      int32_t n_slots, void* o, gdn_tree_dims dims, int32_t* dev_status,
-                     void* stream) {
+                     void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_rule_dims(dims);
   if (rc != GDN_TREE_OK) return rc;
   gdn::SeqLayout lay;
@@ -461,7 +465,12 @@ int gdn_tree_prefill(const void* q, const void* k, const void* v, const float* l
   if (rc != GDN_TREE_OK) return rc;
   if (dims.B == 0) return GDN_TREE_OK;  // nothing to do
   return rule_call(q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, lay, T, dev_status,
-                   false, stream);
+                   false, workspace, workspace_bytes, stream);
+}
+
+size_t gdn_tree_prefill_workspace(gdn_tree_dims dims, int32_t T) {
+  if (check_rule_dims(dims) != GDN_TREE_OK || dims.B == 0 || T <= 0) return 0;
+  return gdn::prefill_workspace_bytes(dims, T);
 }
 
 int gdn_tree_decode_step(const void* q, const void* k, const void* v, const float* log_alpha,
@@ -478,7 +487,7 @@ int gdn_tree_decode_step(const void* q, const void* k, const void* v, const floa
   lay.slot = state_slot;
   lay.n_slots = n_slots;
   return rule_call(q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, lay, dims.B, dev_status,
-                   true, stream);
+                   true, nullptr, 0, stream);
 }
 
 size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims) {

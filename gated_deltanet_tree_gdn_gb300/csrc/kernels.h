@@ -176,7 +176,12 @@ struct RuleArgs {
   int32_t* dev_status;
   SeqLayout lay = {};
 };
-cudaError_t launch_prefill(const RuleArgs& a, cudaStream_t stream);
+size_t prefill_workspace_bytes(const gdn_tree_dims& d, int32_t T);
+cudaError_t launch_prefill(const RuleArgs& a, void* workspace, cudaStream_t stream);
+// the chunked form on the tensor cores (bf16, dk = dv = 128)
+bool prefill_tc_supported(const gdn_tree_dims& d);
+size_t prefill_tc_workspace_bytes(const gdn_tree_dims& d, int32_t T);
+cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t stream);
 cudaError_t launch_decode_step(const RuleArgs& a, cudaStream_t stream);
 
 // attention over a paged cache with a shared prefix

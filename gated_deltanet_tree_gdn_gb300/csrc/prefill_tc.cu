@@ -1,0 +1,759 @@
+// prefill_tc.cu -- the gated delta rule over whole sequences in chunks of 64 tokens, on the
+// tensor cores (bf16, dk = dv = 128).
+//
+// With g_t the sum of log alpha over the chunk up to token t, S the state before the chunk,
+// K, Q, V the chunk's rows (Yang et al., "Gated Delta Networks", the chunkwise form):
+//     X[t,s] = beta_t e^{g_t - g_s} k_t.k_s  (s < t),     T = (I + X)^-1,
+//     Y[t,s] =        e^{g_t - g_s} q_t.k_s  (s <= t),    Z = Y T,
+//     R = diag(beta) (V - diag(e^g) K S),                 U = T R,
+//     O = diag(e^g) Q S + Z R,
+//     S <- e^{g_C} S + K^T diag(e^{g_C - g}) U.
+// T and Z do not depend on the state, so a first kernel computes them for every chunk and
+// head at once; a second one runs over each sequence's chunks.  Z (instead of Y U) gives
+// U and O from one product, [T; Z] R, as [K; Q] S gives the two products with the state.
+//
+// The columns of S, V, R, U and O do not mix: the second kernel's CTA takes 32 of the 128
+// value columns of one sequence and head (four times the CTAs of a head each, and a quarter
+// of the work between two dependent products).  A chunk is three dependent steps,
+//     D1 = [K; Q] S,   D2 = [T; Z] R,   D3 = K^T (w U),
+// each an MMA of M = 128 and N = 3 x 32: the right-hand operand is an fp32 matrix as three
+// bf16 parts side by side, x = hi + mid + lo exactly (8 bits each, by truncation), and the
+// three results are added in fp32.  K and Q are exact in bf16; T and Z, computed in fp32,
+// are three bf16 parts too; S itself lives in fp32 registers.  The state is within 1e-6 of
+// the exact rule on ordinary inputs (two parts a matrix would give 3e-6, and 1e-5 of the
+// largest entry where all keys are the same).
+//
+// What bounds it: the chain of dependent steps (MMA, TMEM to registers, split, shared
+// memory, MMA), not bytes or tensor rate, unless there are sequences and heads enough to
+// fill the SMs.
+#include <string.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kC = 64;        // tokens of a chunk
+constexpr int kD = 128;       // dk = dv
+constexpr int kW = 32;        // value columns of a CTA
+constexpr int kSlices = kD / kW;
+constexpr uint32_t kTileTZ = 128 * 128;            // [T; Z], one part: 128 rows x 64, 128-byte rows
+constexpr uint32_t kTZBytes = 3 * kTileTZ;
+constexpr uint32_t kAuxBytes = 1024;               // e^g, beta, e^{gC - g} [64] each, e^gC
+constexpr uint32_t kSlotBytes = kTZBytes + kAuxBytes;
+constexpr uint32_t kTileKQ = 2 * 128 * 128;        // [K; Q]: 128 rows x 128, two 64-column blocks
+constexpr size_t kWorkspaceTarget = (size_t)256 << 20;
+constexpr int kMinSegment = 8;                     // chunks a launch pair, at least
+
+// Chunks [c0, c0 + span) of every sequence are one segment; where all chunks fit the
+// workspace there is one, with slots packed by row position (dense = true), else
+// slot = b * span + c - c0.
+struct Segment {
+  int c0, span;
+  bool dense;
+};
+
+__host__ __device__ inline long long dense_slots(long long T, long long B) { return T / kC + B + 1; }
+
+// slot of sequence b's chunk c: cu / 64 + b is past the last slot of sequence b - 1
+__device__ __forceinline__ size_t slot_of(const Segment& s, const int32_t* cu, int b, int c) {
+  return s.dense ? (size_t)(cu[b] / kC + b + c) : (size_t)b * s.span + (c - s.c0);
+}
+
+// ---- waits -----------------------------------------------------------------------------
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* abort,
+                                         uint64_t limit) {
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (uint32_t tries = 0; !mbar_try_wait(bar, parity); ++tries) {
+    if ((tries & 63u) != 63u) continue;
+    if (ld_acquire_shared(abort)) { ok = false; break; }
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > limit) {
+      st_release_shared(abort, 1);
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);  // (a whole warp waits together)
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// e^{a - b} for log-decay sums
+__device__ __forceinline__ float decay(df a, df b) { return ex2(kLog2e * df_diff(a, b)); }
+
+// bits 16 .. 31 of a and b as one word (a below)
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, 0x7632);
+}
+// a pair as three bf16 pairs, exactly: truncated to 8 bits three times
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  hi = high_halves(ua, ub);
+  const float ra = a - __uint_as_float(ua & 0xffff0000u), rb = b - __uint_as_float(ub & 0xffff0000u);
+  const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
+  mid = high_halves(va, vb);
+  lo = high_halves(__float_as_uint(ra - __uint_as_float(va & 0xffff0000u)),
+                   __float_as_uint(rb - __uint_as_float(vb & 0xffff0000u)));
+}
+
+// 8 consecutive values of row r of [T; Z] as three parts
+__device__ __forceinline__ void store_tz(unsigned char* base, int r, int c8, const float (&x)[8]) {
+  uint4 hi, mid, lo;
+  split3(x[0], x[1], hi.x, mid.x, lo.x);
+  split3(x[2], x[3], hi.y, mid.y, lo.y);
+  split3(x[4], x[5], hi.z, mid.z, lo.z);
+  split3(x[6], x[7], hi.w, mid.w, lo.w);
+  const uint32_t off = sw128_chunk(r, c8);
+  *reinterpret_cast<uint4*>(base + off) = hi;
+  *reinterpret_cast<uint4*>(base + kTileTZ + off) = mid;
+  *reinterpret_cast<uint4*>(base + 2 * kTileTZ + off) = lo;
+}
+
+// zero rows [from, 64) of the K half of a [K; Q] tile (whole warp)
+__device__ __forceinline__ void zero_k_rows(unsigned char* tile, int from, int lane) {
+  for (int e = from * 16 + lane; e < kC * 16; e += 32) {
+    const int r = e >> 4, c = e & 15;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * kSw128TileBytes + r * 128 + ((c & 7) << 4)) =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+
+// the [K; Q] tile of a chunk: rows 0-63 K, 64-127 Q, by TMA (one thread)
+__device__ __forceinline__ void load_kq(unsigned char* tile, const CUtensorMap* mapK,
+                                        const CUtensorMap* mapQ, uint64_t* bar, int hq, int row) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    tma_load_3d(tile + c * kSw128TileBytes, mapK, bar, 64 * c, hq, row);
+    tma_load_3d(tile + c * kSw128TileBytes + kC * 128, mapQ, bar, 64 * c, hq, row);
+  }
+}
+
+// ---- first kernel: T and Z of every chunk and head --------------------------------------
+constexpr int kPrepThreads = 256;
+constexpr int kXld = 68;  // floats a row of X^T (16-byte rows)
+
+struct PrepShared {
+  float XT[kC][kXld];     // X^T: [s][t]
+  float T[kC][kXld];      // T: [s][j]
+  df g[kC];
+  float beta[kC];
+  uint64_t bar, mma;
+  uint32_t tmem;
+  int abort;
+};
+constexpr uint32_t kPrepBytes = kTileKQ + kTZBytes + sizeof(PrepShared) + 1024;
+
+__global__ void __launch_bounds__(kPrepThreads, 2)
+prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
+                    const __grid_constant__ CUtensorMap mapQ, const float* __restrict__ log_alpha,
+                    const float* __restrict__ beta, gdn_tree_dims d, SeqLayout lay, Segment seg,
+                    unsigned char* ws, int32_t* dev_status, uint64_t limit_ns) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* sKQ = smem;
+  unsigned char* sTZ = smem + kTileKQ;
+  PrepShared& P = *reinterpret_cast<PrepShared*>(smem + kTileKQ + kTZBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hq = blockIdx.x % d.Hqk, slot = blockIdx.x / d.Hqk;
+  int b, c;
+  if (seg.dense) {  // the last sequence whose first slot is not past this one
+    int lo = 0, hi = d.B - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (lay.cu[m] / kC + m <= slot) lo = m;
+      else hi = m - 1;
+    }
+    b = lo;
+    c = slot - (lay.cu[b] / kC + b);
+  } else {
+    b = slot / seg.span;
+    c = seg.c0 + slot % seg.span;
+  }
+  const int n = lay.count(b, d.N);
+  if (c < 0 || n <= c * kC) return;  // (an invalid sequence is reported by the second kernel)
+  const int nc = min(kC, n - c * kC);
+  const size_t row = (size_t)lay.cu[b] + (size_t)c * kC;
+
+  if (tid == 0) {
+    mbar_init(&P.bar, 1);
+    mbar_init(&P.mma, 1);
+    P.abort = 0;
+    mbar_fence_init();
+    mbar_arrive_expect_tx(&P.bar, kTileKQ);
+    load_kq(sKQ, &mapK, &mapQ, &P.bar, hq, (int)row);
+  }
+  if (warp == 0) tmem_alloc(&P.tmem, 128);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = P.tmem;
+  // [K; Q] K^T: lanes 0-63 the rows k_t.k_s, lanes 64-127 q_t.k_s
+  if (warp == 0) {
+    if (wait_bar(&P.bar, 0, &P.abort, limit_ns) && elect_one()) {
+      constexpr uint32_t id = idesc_bf16_f32(128, kC);
+      const uint64_t a = desc_sw128_kmajor(smem_addr(sKQ));
+#pragma unroll
+      for (int s = 0; s < kD / 16; ++s) {
+        const uint32_t off = ((s >> 2) * kSw128TileBytes + (s & 3) * 32) >> 4;
+        if (s == 0) umma_ss<false>(tmem, a + off, a + off, id);
+        else umma_ss<true>(tmem, a + off, a + off, id);
+      }
+      umma_commit(&P.mma);
+    }
+    __syncwarp();
+  }
+  // thread: TMEM lane 32 (warp & 3) + lane, columns 32 half ..
+  const int half = warp >> 2, ln = 32 * (warp & 3) + lane, t = ln & (kC - 1);
+  const bool isq = ln >= kC;
+  const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  bool ok = wait_bar(&P.mma, 0, &P.abort, limit_ns);
+  tc_fence_after_sync();
+  ok = __syncthreads_and(ok);  // (every warp goes on, or none)
+  float gram[32];
+  if (ok) tmem_ld_32cols(tl + 32 * half, gram);
+  uint32_t phase = 1;
+
+  for (int h = hq * (d.Hv / d.Hqk); ok && h < (hq + 1) * (d.Hv / d.Hqk); ++h) {
+    __syncthreads();  // the last head's arrays and tiles have been read
+    if (tid < 32) {
+      // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
+      // differences of sums stay defined
+      df x[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 2 * lane + e;
+        float la = i < nc ? log_alpha[(row + i) * d.Hv + h] : 0.f;
+        if (la < -1e4f) la = -1e4f;
+        x[e] = df{la, 0.f};
+        P.beta[i] = i < nc ? beta[(row + i) * d.Hv + h] : 0.f;
+      }
+      x[1] = df_add(x[0], x[1]);
+      df run = x[1];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const df y = {__shfl_up_sync(0xffffffffu, run.hi, off), __shfl_up_sync(0xffffffffu, run.lo, off)};
+        if (lane >= off) run = df_add(y, run);
+      }
+      const df before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+      P.g[2 * lane] = lane > 0 ? df_add(before, x[0]) : x[0];
+      P.g[2 * lane + 1] = run;
+    }
+    __syncthreads();
+    unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
+    if (tid < kC) {
+      float* aux = reinterpret_cast<float*>(out + kTZBytes);
+      const df last = P.g[kC - 1];  // (rows past the sequence add nothing to g)
+      aux[tid] = ex2(kLog2e * df_value(P.g[tid]));
+      aux[kC + tid] = P.beta[tid];
+      aux[2 * kC + tid] = tid < nc ? decay(last, P.g[tid]) : 0.f;
+      if (tid == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
+    }
+    {  // X (transposed) in fp32; Y in rows 64-127 of the [T; Z] tiles
+      const df gt = P.g[t];
+      const float bt = P.beta[t];
+      const bool live = t < nc;
+#pragma unroll
+      for (int c8 = 0; c8 < 4; ++c8) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int s = 32 * half + 8 * c8 + e;
+          const bool on = live && (isq ? s <= t : s < t);
+          y[e] = on ? decay(gt, P.g[s]) * gram[8 * c8 + e] : 0.f;
+          if (!isq) P.XT[s][t] = bt * y[e];
+        }
+        if (isq) {
+          store_tz(sTZ, ln, 4 * half + c8, y);
+        }
+      }
+    }
+    __syncthreads();
+    // T column by column, 16 rows at a time: the rows above as products (thread: column j,
+    // 4 rows), then the 16 among themselves (a thread a column)
+    {
+      const int j = tid & (kC - 1), rq = tid >> 6;
+#pragma unroll 1
+      for (int r0 = 0; r0 < kC; r0 += 16) {
+        const int i0 = r0 + 4 * rq;
+        float acc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = i0 + e == j ? 1.f : 0.f;
+#pragma unroll 4
+        for (int s = 0; s < r0; ++s) {
+          const float ts = P.T[s][j];
+          const float4 x = *reinterpret_cast<const float4*>(&P.XT[s][i0]);
+          acc[0] = fmaf(-x.x, ts, acc[0]);
+          acc[1] = fmaf(-x.y, ts, acc[1]);
+          acc[2] = fmaf(-x.z, ts, acc[2]);
+          acc[3] = fmaf(-x.w, ts, acc[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) P.T[i0 + e][j] = acc[e];
+        __syncthreads();
+        if (tid < kC) {
+          float u[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) u[i] = P.T[r0 + i][j];
+#pragma unroll
+          for (int s = 0; s < 15; ++s)
+#pragma unroll
+            for (int i = s + 1; i < 16; ++i) u[i] = fmaf(-P.XT[r0 + s][r0 + i], u[s], u[i]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) P.T[r0 + i][j] = u[i];
+        }
+        __syncthreads();
+      }
+    }
+    // T in rows 0-63 of the tiles
+    for (int e = tid; e < kC * 8; e += kPrepThreads) {
+      const int r = e >> 3, c8 = e & 7;
+      float x[8];
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&P.T[r][8 * c8]);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&P.T[r][8 * c8 + 4]);
+      store_tz(sTZ, r, c8, x);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before_sync();
+    __syncthreads();
+    // Z = Y T: lanes 64-127 of [T; Y] T (T as an operand whose rows are the inner index)
+    if (warp == 0) {
+      tc_fence_after_sync();
+      if (elect_one()) {
+        constexpr uint32_t id = idesc_bf16_f32_bmn(128, kC);
+        const uint64_t a = desc_sw128_kmajor(smem_addr(sTZ));
+        const uint64_t bt = desc_sw128_mnmajor(smem_addr(sTZ), kSw128TileBytes, 1024);
+#pragma unroll
+        for (int p = 0; p < 6; ++p) {  // the products of parts above 2^-24
+          constexpr int kA[6] = {0, 0, 1, 1, 0, 2}, kB[6] = {0, 1, 0, 1, 2, 0};
+          const uint64_t ap = a + kA[p] * (kTileTZ >> 4), bp = bt + kB[p] * (kTileTZ >> 4);
+#pragma unroll
+          for (int s = 0; s < kC / 16; ++s) {
+            if (p == 0 && s == 0) umma_ss<false>(tmem + 64, ap + ((s * 32) >> 4), bp + ((s * 2048) >> 4), id);
+            else umma_ss<true>(tmem + 64, ap + ((s * 32) >> 4), bp + ((s * 2048) >> 4), id);
+          }
+        }
+        umma_commit(&P.mma);
+      }
+      __syncwarp();
+    }
+    ok = wait_bar(&P.mma, phase, &P.abort, limit_ns);
+    phase ^= 1u;
+    tc_fence_after_sync();
+    if (ok && isq) {
+      float z[32];
+      tmem_ld_32cols(tl + 64 + 32 * half, z);
+#pragma unroll
+      for (int c8 = 0; c8 < 4; ++c8) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = z[8 * c8 + e];
+        store_tz(sTZ, ln, 4 * half + c8, y);
+      }
+    }
+    tc_fence_before_sync();
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    for (int e = tid; e < (int)(kTZBytes / 16); e += kPrepThreads)
+      reinterpret_cast<uint4*>(out)[e] = reinterpret_cast<const uint4*>(sTZ)[e];
+  }
+  // (after a timeout: the copies and MMAs in flight end, or their bounded waits do)
+  if (P.abort && warp == 0) {
+    mbar_wait(&P.bar, 0, limit_ns);
+    mbar_wait(&P.mma, phase ^ 1u, limit_ns);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (tid == 0 && P.abort && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
+  if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
+// ---- second kernel: the chunks of a sequence, 32 value columns a CTA ----------------------
+constexpr int kScanCompute = 256;                       // two threads a TMEM lane
+constexpr int kScanThreads = kScanCompute + 64;         // + a loading and an issuing warp
+constexpr int kWarpLoad = kScanCompute / 32, kWarpMma = kWarpLoad + 1;
+constexpr int kStages = 2;
+// right-hand operands: rows of 3 x 32 bf16 (hi, mid | lo, unused) in two 64-column atoms
+constexpr uint32_t kOperandS = 128 * 256, kOperandR = kC * 256;
+
+struct ScanBars {
+  uint64_t raw, full[kStages], empty[kStages], d1, d2, d3, r_ready, u_ready, s_ready, drain;
+  uint32_t tmem;
+  int abort;
+};
+struct ScanSmem {
+  static constexpr uint32_t OFF_KQ = 0;
+  static constexpr uint32_t OFF_TZ = OFF_KQ + kStages * kTileKQ;
+  static constexpr uint32_t OFF_S = OFF_TZ + kStages * kTZBytes;
+  static constexpr uint32_t OFF_R = OFF_S + kOperandS;
+  static constexpr uint32_t OFF_BAR = OFF_R + kOperandR;
+  static constexpr uint32_t kBytes = OFF_BAR + 256 + 1024;
+};
+
+// 16 consecutive values (columns 16 ch ..) of row r as three parts
+__device__ __forceinline__ void store_parts(unsigned char* base, int r, int ch,
+                                            const float (&x)[16]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint4 hi, mid, lo;
+    split3(x[8 * e + 0], x[8 * e + 1], hi.x, mid.x, lo.x);
+    split3(x[8 * e + 2], x[8 * e + 3], hi.y, mid.y, lo.y);
+    split3(x[8 * e + 4], x[8 * e + 5], hi.z, mid.z, lo.z);
+    split3(x[8 * e + 6], x[8 * e + 7], hi.w, mid.w, lo.w);
+    *reinterpret_cast<uint4*>(base + mn_chunk(r, 2 * ch + e)) = hi;
+    *reinterpret_cast<uint4*>(base + mn_chunk(r, 4 + 2 * ch + e)) = mid;
+    *reinterpret_cast<uint4*>(base + mn_chunk(r, 8 + 2 * ch + e)) = lo;
+  }
+}
+
+// the sum of the three results of 16 columns of a row
+__device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[16]) {
+  float y[16], z[16];
+  tmem_ld_16cols(taddr, x);
+  tmem_ld_16cols(taddr + 32, y);
+  tmem_ld_16cols(taddr + 64, z);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] += y[i] + z[i];
+}
+
+__global__ void __launch_bounds__(kScanThreads, 1)
+prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
+                    const __grid_constant__ CUtensorMap mapQ, const __nv_bfloat16* __restrict__ v,
+                    const float* pool_in, float* pool_out, __nv_bfloat16* __restrict__ o,
+                    gdn_tree_dims d, SeqLayout lay, Segment seg, const unsigned char* ws,
+                    int32_t* dev_status, uint64_t limit_ns) {
+  using L = ScanSmem;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int slice = blockIdx.x % kSlices;
+  const int h = (blockIdx.x / kSlices) % d.Hv, b = blockIdx.x / kSlices / d.Hv;
+  const int hq = h / (d.Hv / d.Hqk);
+  const int n = lay.count(b, d.N), st = lay.state(b);
+  if (n < 0 || st < 0) {
+    if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    return;
+  }
+  const int chunks = (n + kC - 1) / kC;
+  const int c_end = min(chunks, seg.c0 + seg.span);
+  if (seg.c0 > 0 && c_end <= seg.c0) return;  // this sequence ended in an earlier segment
+  const size_t row0 = (size_t)lay.cu[b];
+  const size_t soff = ((size_t)st * d.Hv + h) * kD * kD + (size_t)slice * kW;
+
+  if (tid == 0) {
+    mbar_init(&B->raw, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&B->full[s], 1);
+      mbar_init(&B->empty[s], 1);
+    }
+    mbar_init(&B->d1, 1);
+    mbar_init(&B->d2, 1);
+    mbar_init(&B->d3, 1);
+    mbar_init(&B->drain, 1);
+    mbar_init(&B->r_ready, kScanCompute);
+    mbar_init(&B->u_ready, kScanCompute / 2);
+    mbar_init(&B->s_ready, kScanCompute);
+    B->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&B->tmem, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = B->tmem;
+  constexpr uint32_t kD1 = 0, kD2 = 96, kD3 = 192;  // TMEM columns
+
+  if (warp == kWarpLoad) {
+    uint32_t raw_phase = 0;
+    for (int c = seg.c0; c < c_end; ++c) {
+      const int i = c - seg.c0, s = i % kStages;
+      if (i >= kStages && !wait_bar(&B->empty[s], ((i / kStages) & 1) ^ 1, &B->abort, limit_ns)) break;
+      const int nc = min(kC, n - c * kC);
+      unsigned char* kq = smem + L::OFF_KQ + s * kTileKQ;
+      // (the last chunk's tile passes through this warp: rows past the sequence are not
+      // its own, and a zero weight must not meet what they hold)
+      uint64_t* bar = nc < kC ? &B->raw : &B->full[s];
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, kTileKQ + kTZBytes);
+        load_kq(kq, &mapK, &mapQ, bar, hq, (int)(row0 + (size_t)c * kC));
+        const unsigned char* from = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
+        bulk_load(smem + L::OFF_TZ + s * kTZBytes, from, kTZBytes, bar);
+      }
+      __syncwarp();
+      if (nc < kC) {
+        if (!wait_bar(&B->raw, raw_phase, &B->abort, limit_ns)) break;
+        raw_phase ^= 1u;
+        zero_k_rows(kq, nc, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B->full[s]);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    constexpr uint32_t id1 = idesc_bf16_f32_bmn(128, 3 * kW), id2 = idesc_bf16_f32_bmn(128, 2 * kW),
+                       id4 = idesc_bf16_f32_bmn(128, kW);
+    constexpr uint32_t id3 = idesc_bf16_f32_amn_bmn(128, 3 * kW);
+    const uint64_t dKQ = desc_sw128_kmajor(smem_addr(smem + L::OFF_KQ));
+    const uint64_t dKt = desc_sw128_mnmajor(smem_addr(smem + L::OFF_KQ), kSw128TileBytes, 1024);
+    const uint64_t dTZ = desc_sw128_kmajor(smem_addr(smem + L::OFF_TZ));
+    const uint64_t dS = desc_sw128_mnmajor(smem_addr(smem + L::OFF_S), kMnLbo, kMnSbo);
+    const uint64_t dR = desc_sw128_mnmajor(smem_addr(smem + L::OFF_R), kMnLbo, kMnSbo);
+    bool ok = true;
+    for (int c = seg.c0; ok && c < c_end; ++c) {
+      const int i = c - seg.c0, s = i % kStages;
+      ok = wait_bar(&B->full[s], (i / kStages) & 1, &B->abort, limit_ns) &&
+           wait_bar(&B->s_ready, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = dKQ + s * (kTileKQ >> 4);
+#pragma unroll
+        for (int e = 0; e < kD / 16; ++e) {
+          const uint32_t off = ((e >> 2) * kSw128TileBytes + (e & 3) * 32) >> 4;
+          if (e == 0) umma_ss<false>(tmem + kD1, a + off, dS + ((e * 2 * kMnSbo) >> 4), id1);
+          else umma_ss<true>(tmem + kD1, a + off, dS + ((e * 2 * kMnSbo) >> 4), id1);
+        }
+        umma_commit(&B->d1);
+      }
+      __syncwarp();
+      ok = wait_bar(&B->r_ready, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = dTZ + s * (kTZBytes >> 4);
+#pragma unroll
+        for (int e = 0; e < kC / 16; ++e) {  // hi (hi, mid, lo)
+          if (e == 0) umma_ss<false>(tmem + kD2, a + ((e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id1);
+          else umma_ss<true>(tmem + kD2, a + ((e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id1);
+        }
+#pragma unroll
+        for (int e = 0; e < kC / 16; ++e)    // mid (hi, mid)
+          umma_ss<true>(tmem + kD2, a + ((kTileTZ + e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id2);
+#pragma unroll
+        for (int e = 0; e < kC / 16; ++e)    // lo (hi)
+          umma_ss<true>(tmem + kD2, a + ((2 * kTileTZ + e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id4);
+        umma_commit(&B->d2);
+      }
+      __syncwarp();
+      ok = wait_bar(&B->u_ready, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (elect_one()) {
+        const uint64_t a = dKt + s * (kTileKQ >> 4);
+#pragma unroll
+        for (int e = 0; e < kC / 16; ++e) {
+          if (e == 0) umma_ss<false>(tmem + kD3, a + ((e * 2048) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id3);
+          else umma_ss<true>(tmem + kD3, a + ((e * 2048) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id3);
+        }
+        umma_commit(&B->d3);
+        umma_commit(&B->empty[s]);
+      }
+      __syncwarp();
+    }
+    // whatever was issued is done before TMEM and the operands go
+    if (elect_one()) umma_commit(&B->drain);
+    __syncwarp();
+    mbar_wait(&B->drain, 0, limit_ns);
+  } else {
+    // ---- compute: thread (TMEM lane ln, column half ch) -------------------------------------
+    const int ch = warp >> 2, ln = 32 * (warp & 3) + lane;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * ch;
+    const bool isq = ln >= kC;
+    const int t = ln & (kC - 1);
+    unsigned char* sS = smem + L::OFF_S;
+    unsigned char* sR = smem + L::OFF_R;
+    // row ln of the state, 16 columns
+    float S[16];
+    const float* src = (seg.c0 == 0 ? pool_in : pool_out) + soff + (size_t)ln * kD + 16 * ch;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(S + 4 * e) = *reinterpret_cast<const float4*>(src + 4 * e);
+    bool ok = true;
+    if (seg.c0 < c_end) {
+      store_parts(sS, ln, ch, S);
+      fence_proxy_async_smem();
+      mbar_arrive(&B->s_ready);
+    }
+    // this token's v (16 columns) and weights, a chunk ahead
+    uint4 vn[2];
+    float gam_n, beta_n, w_n, gC_n;
+    auto fetch = [&](int c) {
+      const bool live = c * kC + t < n;
+      const float* aux = reinterpret_cast<const float*>(
+          ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes + kTZBytes);
+      gam_n = aux[t];
+      beta_n = aux[kC + t];
+      w_n = aux[2 * kC + t];
+      gC_n = aux[3 * kC];
+      vn[0] = vn[1] = make_uint4(0, 0, 0, 0);
+      if (!isq && live) {
+        const uint4* p = reinterpret_cast<const uint4*>(
+            v + ((row0 + (size_t)c * kC + t) * d.Hv + h) * kD + slice * kW + 16 * ch);
+        vn[0] = __ldg(p);
+        vn[1] = __ldg(p + 1);
+      }
+    };
+    if (seg.c0 < c_end) fetch(seg.c0);
+    for (int c = seg.c0; c < c_end; ++c) {
+      const int i = c - seg.c0;
+      const bool live = c * kC + t < n;
+      const uint4 vv[2] = {vn[0], vn[1]};
+      const float gam = gam_n, bt = beta_n, w = w_n, gC = gC_n;
+      if (c + 1 < c_end) fetch(c + 1);
+      ok = wait_bar(&B->d1, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      float x[16];
+      load_sum(tl + kD1, x);
+      if (!isq) {
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vv);
+        float r[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float ve = __uint_as_float((e & 1) ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16);
+          r[e] = live ? bt * fmaf(-gam, x[e], ve) : 0.f;
+        }
+        store_parts(sR, t, ch, r);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&B->r_ready);
+      ok = wait_bar(&B->d2, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      float y[16];
+      load_sum(tl + kD2, y);
+      if (!isq) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = live ? w * y[e] : 0.f;
+        store_parts(sR, t, ch, y);
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        mbar_arrive(&B->u_ready);
+      } else if (live) {
+        uint32_t p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 q2 = __floats2bfloat162_rn(fmaf(gam, x[2 * e], y[2 * e]),
+                                                          fmaf(gam, x[2 * e + 1], y[2 * e + 1]));
+          p[e] = *reinterpret_cast<const uint32_t*>(&q2);
+        }
+        uint4* to = reinterpret_cast<uint4*>(
+            o + ((row0 + (size_t)c * kC + t) * d.Hv + h) * kD + slice * kW + 16 * ch);
+        to[0] = make_uint4(p[0], p[1], p[2], p[3]);
+        to[1] = make_uint4(p[4], p[5], p[6], p[7]);
+      }
+      __syncwarp();
+      ok = wait_bar(&B->d3, i & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      tc_fence_after_sync();
+      load_sum(tl + kD3, x);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) S[e] = fmaf(gC, S[e], x[e]);
+      if (c + 1 < c_end) {
+        store_parts(sS, ln, ch, S);
+        fence_proxy_async_smem();
+        tc_fence_before_sync();
+        mbar_arrive(&B->s_ready);
+      }
+    }
+    if (ok) {
+      float* to = pool_out + soff + (size_t)ln * kD + 16 * ch;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4*>(to + 4 * e) = *reinterpret_cast<const float4*>(S + 4 * e);
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (B->abort) {
+    // the copies in flight end (or their bounded waits do) before this CTA does
+    if (warp == kWarpLoad)
+      for (int s = 0; s < kStages; ++s)
+        for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->full[s], ph, 1000000);
+    __syncthreads();
+    if (tid == 0 && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
+  }
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+// the segments for these dims: chunks a launch pair, and whether one pair does for all
+Segment plan(const gdn_tree_dims& d, long long T) {
+  const size_t head = (size_t)d.Hv * kSlotBytes;
+  const long long longest = ((long long)d.N + kC - 1) / kC;
+  if (dense_slots(T, d.B) * head <= kWorkspaceTarget) return Segment{0, (int)longest, true};
+  long long span = (long long)(kWorkspaceTarget / head) / d.B;
+  if (span < kMinSegment) span = kMinSegment;
+  if (span > longest) span = longest;
+  if (span > 0) {  // (segments of equal length)
+    const long long count = (longest + span - 1) / span;
+    span = (longest + count - 1) / count;
+  }
+  // (long batches of short sequences: packing may still be the smaller)
+  if (dense_slots(T, d.B) <= span * d.B) return Segment{0, (int)longest, true};
+  return Segment{0, (int)span, false};
+}
+
+}  // namespace
+
+bool prefill_tc_supported(const gdn_tree_dims& d) {
+  return d.dtype == GDN_TREE_BF16 && d.dk == kD && d.dv == kD && verify_tc_supported(
+             gdn_tree_dims{1, 1, d.Hqk, d.Hv, kD, kD, GDN_TREE_BF16});
+}
+
+size_t prefill_tc_workspace_bytes(const gdn_tree_dims& d, int32_t T) {
+  const Segment s = plan(d, T);
+  return (size_t)(s.dense ? dense_slots(T, d.B) : (long long)s.span * d.B) * d.Hv * kSlotBytes;
+}
+
+cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t stream) {
+  const gdn_tree_dims& d = a.d;
+  CUtensorMap mapK, mapQ;
+  if (!encode_head_rows_map(&mapK, a.k, a.lay.T, d.Hqk, kD, kC) ||
+      !encode_head_rows_map(&mapQ, a.q, a.lay.T, d.Hqk, kD, kC))
+    return cudaErrorInvalidValue;
+  cudaError_t err = cudaFuncSetAttribute(prefill_prep_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepBytes);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(prefill_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               ScanSmem::kBytes);
+  if (err != cudaSuccess) return err;
+  Segment s = plan(d, a.lay.T);
+  const long long slots = s.dense ? dense_slots(a.lay.T, d.B) : (long long)s.span * d.B;
+  const long long scan = (long long)d.B * d.Hv * kSlices;
+  if (slots * d.Hqk > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const uint64_t limit = wait_hooks().limit_ns;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const int longest = (d.N + kC - 1) / kC;
+  for (s.c0 = 0; s.c0 == 0 || s.c0 < longest; s.c0 += s.span) {
+    if (longest > 0) {
+      prefill_prep_kernel<<<(unsigned)(slots * d.Hqk), kPrepThreads, kPrepBytes, stream>>>(
+          mapK, mapQ, a.log_alpha, a.beta, d, a.lay, s, ws, a.dev_status, limit);
+      if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    prefill_scan_kernel<<<(unsigned)scan, kScanThreads, ScanSmem::kBytes, stream>>>(
+        mapK, mapQ, static_cast<const __nv_bfloat16*>(a.v), a.pool_in, a.pool_out,
+        static_cast<__nv_bfloat16*>(a.o), d, a.lay, s, ws, a.dev_status, limit);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    if (s.span == 0) break;  // (no tokens at all: the states are copied)
+  }
+  return cudaSuccess;
+}
+
+}  // namespace gdn

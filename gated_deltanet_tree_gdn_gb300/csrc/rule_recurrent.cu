@@ -184,8 +184,20 @@ cudaError_t launch_recurrent(const RuleArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_prefill(const RuleArgs& a, cudaStream_t stream) {
-  return launch_recurrent(a, stream);
+// The chunked kernels from kChunkedFrom tokens of the longest sequence on.  Below it their
+// two launches and the first chunk's chain cost more than the tokens one by one.
+constexpr int kChunkedFrom = 17;
+static bool chunked(const gdn_tree_dims& d, int32_t T) {
+  return d.N >= kChunkedFrom && T > 0 && prefill_tc_supported(d);
+}
+
+size_t prefill_workspace_bytes(const gdn_tree_dims& d, int32_t T) {
+  return chunked(d, T) ? prefill_tc_workspace_bytes(d, T) : 0;
+}
+
+cudaError_t launch_prefill(const RuleArgs& a, void* workspace, cudaStream_t stream) {
+  return chunked(a.d, a.lay.T) ? launch_prefill_tc(a, workspace, stream)
+                               : launch_recurrent(a, stream);
 }
 
 cudaError_t launch_decode_step(const RuleArgs& a, cudaStream_t stream) {

@@ -316,14 +316,20 @@ int gdn_tree_build_topw(const float *cand_logp, int32_t B, int32_t N, int32_t c,
  *   pool_in, pool_out  [n_slots, Hv, dk, dv] fp32; pool_out may be pool_in
  *               (in place), any other overlap is refused.  Slots must be distinct.
  *   log_alpha   any value <= 0, -inf (alpha = 0, the state is forgotten) included
+ *   workspace   gdn_tree_prefill_workspace(dims, T) bytes of device memory, 16-byte
+ *               aligned (NULL when that is 0); its contents are not kept
  * A sequence whose rows or slot are out of range gets GDN_TREE_STATUS_BAD_LAYOUT
- * and its outputs are left unwritten.  dims.N has no upper limit here.
+ * and its outputs are left unwritten (where cu_tokens decreases, the sequences after
+ * are unspecified too).  dims.N has no upper limit here.  bf16 with dk = dv = 128 is
+ * computed in chunks of 64 tokens: an infinity or NaN in a token's inputs may reach the
+ * outputs of the tokens before it in its chunk, not only those after it.
  */
 int gdn_tree_prefill(const void *q, const void *k, const void *v, const float *log_alpha,
                      const float *beta, const int32_t *cu_tokens, int32_t T,
                      const float *pool_in, float *pool_out, const int32_t *state_slot,
                      int32_t n_slots, void *o, gdn_tree_dims dims, int32_t *dev_status,
-                     void *stream);
+                     void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_tree_prefill_workspace(gdn_tree_dims dims, int32_t T);
 
 /*
  * gdn_tree_decode_step -- the same rule for one token of each of B sequences:

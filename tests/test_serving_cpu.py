@@ -29,10 +29,11 @@ def rule_dims(**kw):
     return gt.Dims(**d)
 
 
-def prefill(lib, dims=None, T=32, n_slots=4, pool_out=None, q=P(0), cu=P(6), slot=P(9)):
+def prefill(lib, dims=None, T=32, n_slots=4, pool_out=None, q=P(0), cu=P(6), slot=P(9), ws=P(12),
+            ws_bytes=1 << 60):
     return lib.gdn_tree_prefill(q, P(1), P(2), P(3), P(4), cu, T, P(7),
                                 P(8) if pool_out is None else pool_out, slot, n_slots, P(10),
-                                dims or rule_dims(), None, None)
+                                dims or rule_dims(), None, ws, ws_bytes, None)
 
 
 def step(lib, dims=None, n_slots=4, pool_out=None, q=P(0), slot=P(9)):
@@ -61,6 +62,20 @@ def test_rule_arguments(lib):
     assert prefill(lib, cu=None) == gt.EINVAL
     assert prefill(lib, T=-1) == gt.EINVAL
     assert prefill(lib, rule_dims(N=-1)) == gt.EINVAL
+
+
+def test_prefill_workspace(lib):
+    """The workspace grows with the rows up to a bound, and one that is too small is refused.
+    (Without a GPU no tensor map can be made: the chunked kernels are then not chosen.)"""
+    d = rule_dims(N=5000, dk=128, dv=128)
+    need = lib.gdn_tree_prefill_workspace(d, 10000)
+    if need:
+        assert prefill(lib, d, T=10000, ws_bytes=need - 1) == gt.EINVAL
+        assert prefill(lib, d, T=10000, ws=None) == gt.EINVAL
+        assert need <= lib.gdn_tree_prefill_workspace(d, 20000)
+    assert lib.gdn_tree_prefill_workspace(rule_dims(N=5000, dk=64), 10000) == 0
+    assert lib.gdn_tree_prefill_workspace(rule_dims(Hv=3), 10000) == 0
+    assert lib.gdn_tree_prefill_workspace(d, 0) == 0
 
 
 def attend_dims(**kw):
