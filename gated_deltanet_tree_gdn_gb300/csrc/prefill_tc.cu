@@ -46,7 +46,7 @@ constexpr uint32_t kTZBytes = 3 * kTileTZ;
 constexpr uint32_t kAuxBytes = 1024;               // e^g, beta, e^{gC - g} [64] each, e^gC
 constexpr uint32_t kSlotBytes = kTZBytes + kAuxBytes;
 constexpr uint32_t kTileKQ = 2 * 128 * 128;        // [K; Q]: 128 rows x 128, two 64-column blocks
-constexpr size_t kWorkspaceTarget = (size_t)256 << 20;
+constexpr size_t kWorkspaceTarget = (size_t)512 << 20;
 constexpr int kMinSegment = 8;                     // chunks a launch pair, at least
 
 // Chunks [c0, c0 + span) of every sequence are one segment; where all chunks fit the
@@ -96,16 +96,24 @@ __device__ __forceinline__ float decay(df a, df b) { return ex2(kLog2e * df_diff
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) {
   return __byte_perm(a, b, 0x7632);
 }
+// (x, y) - (a, b), two fp32 lanes an instruction
+__device__ __forceinline__ void sub2(float& x, float& y, uint32_t a, uint32_t b) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "sub.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(a), "r"(b));
+}
 // a pair as three bf16 pairs, exactly: truncated to 8 bits three times
 __device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid,
                                        uint32_t& lo) {
-  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
   hi = high_halves(ua, ub);
-  const float ra = a - __uint_as_float(ua & 0xffff0000u), rb = b - __uint_as_float(ub & 0xffff0000u);
-  const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
-  mid = high_halves(va, vb);
-  lo = high_halves(__float_as_uint(ra - __uint_as_float(va & 0xffff0000u)),
-                   __float_as_uint(rb - __uint_as_float(vb & 0xffff0000u)));
+  sub2(a, b, ua & 0xffff0000u, ub & 0xffff0000u);
+  ua = __float_as_uint(a), ub = __float_as_uint(b);
+  mid = high_halves(ua, ub);
+  sub2(a, b, ua & 0xffff0000u, ub & 0xffff0000u);
+  lo = high_halves(__float_as_uint(a), __float_as_uint(b));
 }
 
 // 8 consecutive values of row r of [T; Z] as three parts
@@ -141,21 +149,53 @@ __device__ __forceinline__ void load_kq(unsigned char* tile, const CUtensorMap* 
 }
 
 // ---- first kernel: T and Z of every chunk and head --------------------------------------
+// T = (I + X)^-1 by blocks: the four 16 x 16 blocks of the diagonal column by column, then
+// twice the block below the diagonal of a pair, T21 = -T22 X21 T11 (16, then 32 rows).
+// Z = Y T on the tensor cores.  Bound by the latency of these short steps: three CTAs an SM
+// hide it in one another (one array for X and T, and T over K and Q, make them fit).
 constexpr int kPrepThreads = 256;
-constexpr int kXld = 68;  // floats a row of X^T (16-byte rows)
+constexpr int kAld = 68;  // floats a row (16-byte rows)
 
 struct PrepShared {
-  float XT[kC][kXld];     // X^T: [s][t]
-  float T[kC][kXld];      // T: [s][j]
+  // below and on the diagonal T, above it X^T (X[t][s] at [s][t]); a diagonal block that is
+  // done holds T^T above its diagonal
+  float A[kC][kAld];
+  float P[kC / 2][kC / 2 + 4];  // a product of blocks on its way
   df g[kC];
-  float beta[kC];
+  float beta[kC], up[kC], down[kC];  // e^{g - g_mid}, e^{g_mid - g}
   uint64_t bar, mma;
   uint32_t tmem;
-  int abort;
+  int abort, mild;
 };
-constexpr uint32_t kPrepBytes = kTileKQ + kTZBytes + sizeof(PrepShared) + 1024;
+constexpr uint32_t kPrepTiles = kTZBytes > kTileKQ ? kTZBytes : kTileKQ;  // [K; Q], then [T; Z]
+constexpr uint32_t kPrepBytes = kPrepTiles + sizeof(PrepShared) + 1024;
 
-__global__ void __launch_bounds__(kPrepThreads, 2)
+// Block product of T's recursion for the pair of n x n blocks at `o` (n = 16 or 32), by
+// threads (row i, columns kCols jq ..): first P = X21 T11, then T21 = -T22 P, into P.
+template <int n, int kCols, bool kSecond>
+__device__ __forceinline__ void block_product(PrepShared& S, int o, int po, int i, int jq,
+                                              float (&acc)[kCols]) {
+  const int j = kCols * jq;
+#pragma unroll
+  for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    float x, y[kCols];
+    if (!kSecond) {  // X21[i][k] T11[k][j ..], T11 lower triangular
+      x = S.A[o + k][o + n + i];
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) y[e] = j + e <= k ? S.A[o + k][o + j + e] : 0.f;
+    } else {         // T22[i][k] P[k][j ..], T22 lower triangular (its transpose is above)
+      x = k <= i ? -S.A[o + n + k][o + n + i] : 0.f;
+#pragma unroll
+      for (int e = 0; e < kCols; ++e) y[e] = S.P[po + k][j + e];
+    }
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc[e] = fmaf(x, y[e], acc[e]);
+  }
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 3)
 prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapQ, const float* __restrict__ log_alpha,
                     const float* __restrict__ beta, gdn_tree_dims d, SeqLayout lay, Segment seg,
@@ -164,8 +204,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* sKQ = smem;
-  unsigned char* sTZ = smem + kTileKQ;
-  PrepShared& P = *reinterpret_cast<PrepShared*>(smem + kTileKQ + kTZBytes);
+  unsigned char* sTZ = smem;
+  PrepShared& P = *reinterpret_cast<PrepShared*>(smem + kPrepTiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hq = blockIdx.x % d.Hqk, slot = blockIdx.x / d.Hqk;
   int b, c;
@@ -222,13 +262,11 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   bool ok = wait_bar(&P.mma, 0, &P.abort, limit_ns);
   tc_fence_after_sync();
   ok = __syncthreads_and(ok);  // (every warp goes on, or none)
-  float gram[32];
-  if (ok) tmem_ld_32cols(tl + 32 * half, gram);
   uint32_t phase = 1;
 
   for (int h = hq * (d.Hv / d.Hqk); ok && h < (hq + 1) * (d.Hv / d.Hqk); ++h) {
-    __syncthreads();  // the last head's arrays and tiles have been read
-    if (tid < 32) {
+    unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
+    if (warp == 0) {
       // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
       // differences of sums stay defined
       df x[2];
@@ -248,82 +286,125 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
         if (lane >= off) run = df_add(y, run);
       }
       const df before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
-      P.g[2 * lane] = lane > 0 ? df_add(before, x[0]) : x[0];
+      const df g0 = lane > 0 ? df_add(before, x[0]) : x[0];
+      P.g[2 * lane] = g0;
       P.g[2 * lane + 1] = run;
-    }
-    __syncthreads();
-    unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
-    if (tid < kC) {
+      // within e^+-40 of the middle every weight is a product of two factors
+      const df mid = {__shfl_sync(0xffffffffu, run.hi, 15), __shfl_sync(0xffffffffu, run.lo, 15)};
+      const float d0 = df_diff(g0, mid), d1 = df_diff(run, mid);
+      P.up[2 * lane] = ex2(kLog2e * d0);
+      P.up[2 * lane + 1] = ex2(kLog2e * d1);
+      P.down[2 * lane] = ex2(-kLog2e * d0);
+      P.down[2 * lane + 1] = ex2(-kLog2e * d1);
+      const bool mild = fabsf(d0) <= 40.f && fabsf(d1) <= 40.f;
+      const bool all = __all_sync(0xffffffffu, mild);
+      if (lane == 0) P.mild = all;
+      const df last = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
       float* aux = reinterpret_cast<float*>(out + kTZBytes);
-      const df last = P.g[kC - 1];  // (rows past the sequence add nothing to g)
-      aux[tid] = ex2(kLog2e * df_value(P.g[tid]));
-      aux[kC + tid] = P.beta[tid];
-      aux[2 * kC + tid] = tid < nc ? decay(last, P.g[tid]) : 0.f;
-      if (tid == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // (rows past the sequence add nothing to g)
+        const int i = 2 * lane + e;
+        const df gi = e ? run : g0;
+        aux[i] = ex2(kLog2e * df_value(gi));
+        aux[kC + i] = P.beta[i];
+        aux[2 * kC + i] = i < nc ? decay(last, gi) : 0.f;
+      }
+      if (lane == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
     }
-    {  // X (transposed) in fp32; Y in rows 64-127 of the [T; Z] tiles
-      const df gt = P.g[t];
-      const float bt = P.beta[t];
+    float gram[32];
+    tmem_ld_32cols(tl + 32 * half, gram);
+    __syncthreads();
+    {  // X^T in fp32 above the diagonal; Y in rows 64-127 of the [T; Z] tiles
       const bool live = t < nc;
+      if (P.mild) {
+        const float f = (isq ? 1.f : P.beta[t]) * P.up[t];
 #pragma unroll
-      for (int c8 = 0; c8 < 4; ++c8) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int s = 32 * half + 8 * c8 + e;
-          const bool on = live && (isq ? s <= t : s < t);
-          y[e] = on ? decay(gt, P.g[s]) * gram[8 * c8 + e] : 0.f;
-          if (!isq) P.XT[s][t] = bt * y[e];
+        for (int e = 0; e < 32; e += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&P.down[32 * half + e]);
+          gram[e] *= f * w.x;
+          gram[e + 1] *= f * w.y;
+          gram[e + 2] *= f * w.z;
+          gram[e + 3] *= f * w.w;
         }
-        if (isq) {
+      } else {
+        const df gt = P.g[t];
+        const float f = isq ? 1.f : P.beta[t];
+#pragma unroll 4
+        for (int e = 0; e < 32; ++e) {
+          const int s = 32 * half + e;
+          const float w = s <= t ? f * decay(gt, P.g[s]) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i == e) gram[i] *= w;
+        }
+      }
+      if (!isq) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int s = 32 * half + e;
+          if (s < t) P.A[s][t] = live ? gram[e] : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = live && 32 * half + 8 * c8 + e <= t ? gram[8 * c8 + e] : 0.f;
           store_tz(sTZ, ln, 4 * half + c8, y);
         }
       }
     }
     __syncthreads();
-    // T column by column, 16 rows at a time: the rows above as products (thread: column j,
-    // 4 rows), then the 16 among themselves (a thread a column)
-    {
-      const int j = tid & (kC - 1), rq = tid >> 6;
-#pragma unroll 1
-      for (int r0 = 0; r0 < kC; r0 += 16) {
-        const int i0 = r0 + 4 * rq;
-        float acc[4];
+    if (tid < kC) {  // the diagonal blocks: a thread a column
+      const int o = tid & ~15, j = tid & 15;
+      float u[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = i0 + e == j ? 1.f : 0.f;
-#pragma unroll 4
-        for (int s = 0; s < r0; ++s) {
-          const float ts = P.T[s][j];
-          const float4 x = *reinterpret_cast<const float4*>(&P.XT[s][i0]);
-          acc[0] = fmaf(-x.x, ts, acc[0]);
-          acc[1] = fmaf(-x.y, ts, acc[1]);
-          acc[2] = fmaf(-x.z, ts, acc[2]);
-          acc[3] = fmaf(-x.w, ts, acc[3]);
-        }
+      for (int i = 0; i < 16; ++i) u[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) P.T[i0 + e][j] = acc[e];
-        __syncthreads();
-        if (tid < kC) {
-          float u[16];
+      for (int s = 0; s < 15; ++s)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = P.T[r0 + i][j];
+        for (int i = s + 1; i < 16; ++i) u[i] = fmaf(-P.A[o + s][o + i], u[s], u[i]);
+      __syncwarp();
 #pragma unroll
-          for (int s = 0; s < 15; ++s)
+      for (int i = 0; i < 16; ++i)
+        if (i >= j) P.A[o + i][o + j] = P.A[o + j][o + i] = u[i];
+    }
+    __syncthreads();
+    {  // pairs of 16-row blocks: threads (pair, row i, 2 columns)
+      const int pr = tid >> 7, i = tid & 15, jq = (tid >> 4) & 7, o = 32 * pr;
+      float acc[2];
+      block_product<16, 2, false>(P, o, 16 * pr, i, jq, acc);
+      P.P[16 * pr + i][2 * jq] = acc[0];
+      P.P[16 * pr + i][2 * jq + 1] = acc[1];
+      __syncthreads();
+      block_product<16, 2, true>(P, o, 16 * pr, i, jq, acc);
 #pragma unroll
-            for (int i = s + 1; i < 16; ++i) u[i] = fmaf(-P.XT[r0 + s][r0 + i], u[s], u[i]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) P.T[r0 + i][j] = u[i];
-        }
-        __syncthreads();
+      for (int e = 0; e < 2; ++e) {
+        P.A[o + 16 + i][o + 2 * jq + e] = acc[e];
+        if (pr == 1) P.A[o + 2 * jq + e][o + 16 + i] = acc[e];
       }
     }
-    // T in rows 0-63 of the tiles
+    __syncthreads();
+    {  // the pair of 32-row blocks: threads (row i, 4 columns)
+      const int i = tid & 31, jq = tid >> 5;
+      float acc[4];
+      block_product<32, 4, false>(P, 0, 0, i, jq, acc);
+      *reinterpret_cast<float4*>(&P.P[i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      __syncthreads();
+      block_product<32, 4, true>(P, 0, 0, i, jq, acc);
+      *reinterpret_cast<float4*>(&P.A[32 + i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    }
+    __syncthreads();
+    // T in rows 0-63 of the tiles, here and in the workspace
+#pragma unroll
     for (int e = tid; e < kC * 8; e += kPrepThreads) {
       const int r = e >> 3, c8 = e & 7;
       float x[8];
-      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&P.T[r][8 * c8]);
-      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&P.T[r][8 * c8 + 4]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 8 * c8 + i <= r ? P.A[r][8 * c8 + i] : 0.f;
       store_tz(sTZ, r, c8, x);
+      store_tz(out, r, c8, x);
     }
     fence_proxy_async_smem();
     tc_fence_before_sync();
@@ -353,21 +434,18 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     phase ^= 1u;
     tc_fence_after_sync();
     if (ok && isq) {
-      float z[32];
-      tmem_ld_32cols(tl + 64 + 32 * half, z);
+      tmem_ld_32cols(tl + 64 + 32 * half, gram);
 #pragma unroll
       for (int c8 = 0; c8 < 4; ++c8) {
         float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = z[8 * c8 + e];
-        store_tz(sTZ, ln, 4 * half + c8, y);
+        for (int e = 0; e < 8; ++e) y[e] = gram[8 * c8 + e];
+        store_tz(out, ln, 4 * half + c8, y);
       }
     }
     tc_fence_before_sync();
     ok = __syncthreads_and(ok);
-    if (!ok) break;
-    for (int e = tid; e < (int)(kTZBytes / 16); e += kPrepThreads)
-      reinterpret_cast<uint4*>(out)[e] = reinterpret_cast<const uint4*>(sTZ)[e];
+    tc_fence_after_sync();
   }
   // (after a timeout: the copies and MMAs in flight end, or their bounded waits do)
   if (P.abort && warp == 0) {
@@ -626,7 +704,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float ve = __uint_as_float((e & 1) ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16);
-          r[e] = live ? bt * fmaf(-gam, x[e], ve) : 0.f;
+          r[e] = bt * fmaf(-gam, x[e], ve);  // (rows past the sequence: k = v = beta = 0)
         }
         store_parts(sR, t, ch, r);
         fence_proxy_async_smem();
@@ -640,7 +718,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       load_sum(tl + kD2, y);
       if (!isq) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = live ? w * y[e] : 0.f;
+        for (int e = 0; e < 16; ++e) y[e] *= w;
         store_parts(sR, t, ch, y);
         fence_proxy_async_smem();
         tc_fence_before_sync();
