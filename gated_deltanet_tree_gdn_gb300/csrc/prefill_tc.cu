@@ -170,28 +170,58 @@ struct PrepShared {
 constexpr uint32_t kPrepTiles = kTZBytes > kTileKQ ? kTZBytes : kTileKQ;  // [K; Q], then [T; Z]
 constexpr uint32_t kPrepBytes = kPrepTiles + sizeof(PrepShared) + 1024;
 
-// Block product of T's recursion for the pair of n x n blocks at `o` (n = 16 or 32), by
-// threads (row i, columns kCols jq ..): first P = X21 T11, then T21 = -T22 P, into P.
+// (a, b) += x (c, d), two fp32 lanes an instruction
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float c, float d) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(c), "f"(d));
+}
+
+// T21 = -T22 X21 T11 for the pair of n x n blocks at `o`: a thread takes row i and columns
+// j .. j + kCols of P = X21 T11, then (kSecond) of -T22 P.  T11 and T22 are triangular: k
+// runs from j in the first product, to i in the second.
 template <int n, int kCols, bool kSecond>
-__device__ __forceinline__ void block_product(PrepShared& S, int o, int po, int i, int jq,
+__device__ __forceinline__ void block_product(PrepShared& S, int o, int po, int i, int j,
                                               float (&acc)[kCols]) {
-  const int j = kCols * jq;
 #pragma unroll
   for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    float x, y[kCols];
-    if (!kSecond) {  // X21[i][k] T11[k][j ..], T11 lower triangular
-      x = S.A[o + k][o + n + i];
+  if (!kSecond) {
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) y[e] = j + e <= k ? S.A[o + k][o + j + e] : 0.f;
-    } else {         // T22[i][k] P[k][j ..], T22 lower triangular (its transpose is above)
-      x = k <= i ? -S.A[o + n + k][o + n + i] : 0.f;
+    for (int k = j; k < j + kCols; ++k) {
+      const float x = S.A[o + k][o + n + i];
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) y[e] = S.P[po + k][j + e];
+      for (int e = 0; e < kCols; ++e)
+        if (j + e <= k) acc[e] = fmaf(x, S.A[o + k][o + j + e], acc[e]);
     }
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) acc[e] = fmaf(x, y[e], acc[e]);
+#pragma unroll 4
+    for (int k = j + kCols; k < n; ++k) {
+      const float x = S.A[o + k][o + n + i];
+      const float* y = &S.A[o + k][o + j];
+      if (kCols == 4) {
+        const float4 z = *reinterpret_cast<const float4*>(y);
+        fma2(acc[0], acc[1], x, z.x, z.y);
+        fma2(acc[kCols - 2], acc[kCols - 1], x, z.z, z.w);
+      } else {
+        const float2 z = *reinterpret_cast<const float2*>(y);
+        fma2(acc[0], acc[1], x, z.x, z.y);
+      }
+    }
+  } else {
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float x = k <= i ? -S.A[o + n + k][o + n + i] : 0.f;
+      const float* y = &S.P[po + k][j];
+      if (kCols == 4) {
+        const float4 z = *reinterpret_cast<const float4*>(y);
+        fma2(acc[0], acc[1], x, z.x, z.y);
+        fma2(acc[kCols - 2], acc[kCols - 1], x, z.z, z.w);
+      } else {
+        const float2 z = *reinterpret_cast<const float2*>(y);
+        fma2(acc[0], acc[1], x, z.x, z.y);
+      }
+    }
   }
 }
 
@@ -207,7 +237,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   unsigned char* sTZ = smem;
   PrepShared& P = *reinterpret_cast<PrepShared*>(smem + kPrepTiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hq = blockIdx.x % d.Hqk, slot = blockIdx.x / d.Hqk;
+  const int h = blockIdx.x % d.Hv, slot = blockIdx.x / d.Hv;
+  const int hq = h / (d.Hv / d.Hqk);
   int b, c;
   if (seg.dense) {  // the last sequence whose first slot is not past this one
     int lo = 0, hi = d.B - 1;
@@ -262,9 +293,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   bool ok = wait_bar(&P.mma, 0, &P.abort, limit_ns);
   tc_fence_after_sync();
   ok = __syncthreads_and(ok);  // (every warp goes on, or none)
-  uint32_t phase = 1;
-
-  for (int h = hq * (d.Hv / d.Hqk); ok && h < (hq + 1) * (d.Hv / d.Hqk); ++h) {
+  if (ok) {
     unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
     if (warp == 0) {
       // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
@@ -329,13 +358,10 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
       } else {
         const df gt = P.g[t];
         const float f = isq ? 1.f : P.beta[t];
-#pragma unroll 4
+#pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int s = 32 * half + e;
-          const float w = s <= t ? f * decay(gt, P.g[s]) : 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i == e) gram[i] *= w;
+          gram[e] *= s <= t ? f * decay(gt, P.g[s]) : 0.f;
         }
       }
       if (!isq) {
@@ -374,11 +400,11 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     {  // pairs of 16-row blocks: threads (pair, row i, 2 columns)
       const int pr = tid >> 7, i = tid & 15, jq = (tid >> 4) & 7, o = 32 * pr;
       float acc[2];
-      block_product<16, 2, false>(P, o, 16 * pr, i, jq, acc);
+      block_product<16, 2, false>(P, o, 16 * pr, i, 2 * jq, acc);
       P.P[16 * pr + i][2 * jq] = acc[0];
       P.P[16 * pr + i][2 * jq + 1] = acc[1];
       __syncthreads();
-      block_product<16, 2, true>(P, o, 16 * pr, i, jq, acc);
+      block_product<16, 2, true>(P, o, 16 * pr, i, 2 * jq, acc);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         P.A[o + 16 + i][o + 2 * jq + e] = acc[e];
@@ -389,10 +415,10 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     {  // the pair of 32-row blocks: threads (row i, 4 columns)
       const int i = tid & 31, jq = tid >> 5;
       float acc[4];
-      block_product<32, 4, false>(P, 0, 0, i, jq, acc);
+      block_product<32, 4, false>(P, 0, 0, i, 4 * jq, acc);
       *reinterpret_cast<float4*>(&P.P[i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
       __syncthreads();
-      block_product<32, 4, true>(P, 0, 0, i, jq, acc);
+      block_product<32, 4, true>(P, 0, 0, i, 4 * jq, acc);
       *reinterpret_cast<float4*>(&P.A[32 + i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
     __syncthreads();
@@ -430,8 +456,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
       }
       __syncwarp();
     }
-    ok = wait_bar(&P.mma, phase, &P.abort, limit_ns);
-    phase ^= 1u;
+    ok = wait_bar(&P.mma, 1, &P.abort, limit_ns);
     tc_fence_after_sync();
     if (ok && isq) {
       tmem_ld_32cols(tl + 64 + 32 * half, gram);
@@ -443,14 +468,12 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
         store_tz(out, ln, 4 * half + c8, y);
       }
     }
-    tc_fence_before_sync();
-    ok = __syncthreads_and(ok);
-    tc_fence_after_sync();
   }
   // (after a timeout: the copies and MMAs in flight end, or their bounded waits do)
   if (P.abort && warp == 0) {
     mbar_wait(&P.bar, 0, limit_ns);
-    mbar_wait(&P.mma, phase ^ 1u, limit_ns);
+    mbar_wait(&P.mma, 0, limit_ns);
+    mbar_wait(&P.mma, 1, limit_ns);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -815,13 +838,13 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   Segment s = plan(d, a.lay.T);
   const long long slots = s.dense ? dense_slots(a.lay.T, d.B) : (long long)s.span * d.B;
   const long long scan = (long long)d.B * d.Hv * kSlices;
-  if (slots * d.Hqk > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (slots * d.Hv > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   const uint64_t limit = wait_hooks().limit_ns;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const int longest = (d.N + kC - 1) / kC;
   for (s.c0 = 0; s.c0 == 0 || s.c0 < longest; s.c0 += s.span) {
     if (longest > 0) {
-      prefill_prep_kernel<<<(unsigned)(slots * d.Hqk), kPrepThreads, kPrepBytes, stream>>>(
+      prefill_prep_kernel<<<(unsigned)(slots * d.Hv), kPrepThreads, kPrepBytes, stream>>>(
           mapK, mapQ, a.log_alpha, a.beta, d, a.lay, s, ws, a.dev_status, limit);
       if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
