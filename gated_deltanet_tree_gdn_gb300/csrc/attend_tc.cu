@@ -342,12 +342,12 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       mbar_init(&S->vfull[s], 1);
       mbar_init(&S->vempty[s], 1);
       mbar_init(&S->sfull[s], 1);
-      mbar_init(&S->pready[s], kSoftmax / 2);
+      mbar_init(&S->pready[s], kSoftmax / 64);  // (warps)
       mbar_init(&S->pvdone[s], 1);
-      mbar_init(&S->lsum[s], kSoftmax / 2);
+      mbar_init(&S->lsum[s], kSoftmax / 64);
     }
     mbar_init(&S->vraw, 1);
-    mbar_init(&S->ready, kSoftmax);  // Q and the tree are in shared memory
+    mbar_init(&S->ready, kSoftmax / 32);  // Q and the tree are in shared memory
     mbar_init(&S->drain, 1);
     S->abort = 0;
     mbar_fence_init();
@@ -562,7 +562,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       }
     fence_proxy_async_smem();
     __syncwarp();
-    mbar_arrive(&S->ready);
+    mbar_arrive_warp(&S->ready);
     bool ok = wait_warp(&S->ready, 0, S, limit_ns);
     // ---- softmax: two threads a row --------------------------------------------------------
     const int tile = warp >> 3, half = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
@@ -670,7 +670,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
-        mbar_arrive(&S->pready[tile]);
+        mbar_arrive_warp(&S->pready[tile]);
       }
       if (ok && ntiles > 0) {
         ok = wait_warp(&S->pvdone[tile], (ntiles - 1) & 1, S, limit_ns);
@@ -681,7 +681,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       int* sPoison = reinterpret_cast<int*>(sL + 2 * kTile);
       sL[half * kTile + lr] = l;
       sPoison[half * kTile + lr] = poison;
-      mbar_arrive(&S->lsum[tile]);
+      mbar_arrive_warp(&S->lsum[tile]);
       ok = wait_warp(&S->lsum[tile], 0, S, limit_ns) && ok;
       l = sL[lr] + sL[kTile + lr];
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (l NaN: kept)

@@ -39,8 +39,7 @@ using namespace sm100;
 
 constexpr int kC = 64;        // tokens of a chunk
 constexpr int kD = 128;       // dk = dv
-constexpr int kW = 32;        // value columns of a CTA
-constexpr int kSlices = kD / kW;
+constexpr int kW = 32;        // value columns of a chain (a CTA runs one or two)
 constexpr uint32_t kTileTZ = 128 * 128;            // [T; Z], one part: 128 rows x 64, 128-byte rows
 constexpr uint32_t kTZBytes = 3 * kTileTZ;
 constexpr uint32_t kAuxBytes = 1024;               // e^g, beta, e^{gC - g} [64] each, e^gC
@@ -271,6 +270,52 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = P.tmem;
+  unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
+  if (warp == 1) {
+    // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
+    // differences of sums stay defined
+    df x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      float la = i < nc ? log_alpha[(row + i) * d.Hv + h] : 0.f;
+      if (la < -1e4f) la = -1e4f;
+      x[e] = df{la, 0.f};
+      P.beta[i] = i < nc ? beta[(row + i) * d.Hv + h] : 0.f;
+    }
+    x[1] = df_add(x[0], x[1]);
+    df run = x[1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const df y = {__shfl_up_sync(0xffffffffu, run.hi, off), __shfl_up_sync(0xffffffffu, run.lo, off)};
+      if (lane >= off) run = df_add(y, run);
+    }
+    const df before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+    const df g0 = lane > 0 ? df_add(before, x[0]) : x[0];
+    P.g[2 * lane] = g0;
+    P.g[2 * lane + 1] = run;
+    // within e^+-40 of the middle every weight is a product of two factors
+    const df mid = {__shfl_sync(0xffffffffu, run.hi, 15), __shfl_sync(0xffffffffu, run.lo, 15)};
+    const float d0 = df_diff(g0, mid), d1 = df_diff(run, mid);
+    P.up[2 * lane] = ex2(kLog2e * d0);
+    P.up[2 * lane + 1] = ex2(kLog2e * d1);
+    P.down[2 * lane] = ex2(-kLog2e * d0);
+    P.down[2 * lane + 1] = ex2(-kLog2e * d1);
+    const bool mild = fabsf(d0) <= 40.f && fabsf(d1) <= 40.f;
+    const bool all = __all_sync(0xffffffffu, mild);
+    if (lane == 0) P.mild = all;
+    const df last = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+    float* aux = reinterpret_cast<float*>(out + kTZBytes);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // (rows past the sequence add nothing to g)
+      const int i = 2 * lane + e;
+      const df gi = e ? run : g0;
+      aux[i] = ex2(kLog2e * df_value(gi));
+      aux[kC + i] = P.beta[i];
+      aux[2 * kC + i] = i < nc ? decay(last, gi) : 0.f;
+    }
+    if (lane == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
+  }
   // [K; Q] K^T: lanes 0-63 the rows k_t.k_s, lanes 64-127 q_t.k_s
   if (warp == 0) {
     if (wait_bar(&P.bar, 0, &P.abort, limit_ns) && elect_one()) {
@@ -294,55 +339,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   tc_fence_after_sync();
   ok = __syncthreads_and(ok);  // (every warp goes on, or none)
   if (ok) {
-    unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
-    if (warp == 0) {
-      // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
-      // differences of sums stay defined
-      df x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        float la = i < nc ? log_alpha[(row + i) * d.Hv + h] : 0.f;
-        if (la < -1e4f) la = -1e4f;
-        x[e] = df{la, 0.f};
-        P.beta[i] = i < nc ? beta[(row + i) * d.Hv + h] : 0.f;
-      }
-      x[1] = df_add(x[0], x[1]);
-      df run = x[1];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const df y = {__shfl_up_sync(0xffffffffu, run.hi, off), __shfl_up_sync(0xffffffffu, run.lo, off)};
-        if (lane >= off) run = df_add(y, run);
-      }
-      const df before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
-      const df g0 = lane > 0 ? df_add(before, x[0]) : x[0];
-      P.g[2 * lane] = g0;
-      P.g[2 * lane + 1] = run;
-      // within e^+-40 of the middle every weight is a product of two factors
-      const df mid = {__shfl_sync(0xffffffffu, run.hi, 15), __shfl_sync(0xffffffffu, run.lo, 15)};
-      const float d0 = df_diff(g0, mid), d1 = df_diff(run, mid);
-      P.up[2 * lane] = ex2(kLog2e * d0);
-      P.up[2 * lane + 1] = ex2(kLog2e * d1);
-      P.down[2 * lane] = ex2(-kLog2e * d0);
-      P.down[2 * lane + 1] = ex2(-kLog2e * d1);
-      const bool mild = fabsf(d0) <= 40.f && fabsf(d1) <= 40.f;
-      const bool all = __all_sync(0xffffffffu, mild);
-      if (lane == 0) P.mild = all;
-      const df last = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
-      float* aux = reinterpret_cast<float*>(out + kTZBytes);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // (rows past the sequence add nothing to g)
-        const int i = 2 * lane + e;
-        const df gi = e ? run : g0;
-        aux[i] = ex2(kLog2e * df_value(gi));
-        aux[kC + i] = P.beta[i];
-        aux[2 * kC + i] = i < nc ? decay(last, gi) : 0.f;
-      }
-      if (lane == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
-    }
     float gram[32];
     tmem_ld_32cols(tl + 32 * half, gram);
-    __syncthreads();
     {  // X^T in fp32 above the diagonal; Y in rows 64-127 of the [T; Z] tiles
       const bool live = t < nc;
       if (P.mild) {
@@ -388,9 +386,14 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
 #pragma unroll
       for (int i = 0; i < 16; ++i) u[i] = i == j ? 1.f : 0.f;
 #pragma unroll
-      for (int s = 0; s < 15; ++s)
+      for (int s = 0; s < 15; ++s) {
+        float x[16];  // column s of X, 16-byte pieces (those that hold rows past s)
 #pragma unroll
-        for (int i = s + 1; i < 16; ++i) u[i] = fmaf(-P.A[o + s][o + i], u[s], u[i]);
+        for (int i = 4 * ((s + 1) / 4); i < 16; i += 4)
+          *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(&P.A[o + s][o + i]);
+#pragma unroll
+        for (int i = s + 1; i < 16; ++i) u[i] = fmaf(-x[i], u[s], u[i]);
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -482,26 +485,40 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
-// ---- second kernel: the chunks of a sequence, 32 value columns a CTA ----------------------
-constexpr int kScanCompute = 256;                       // two threads a TMEM lane
-constexpr int kScanThreads = kScanCompute + 64;         // + a loading and an issuing warp
-constexpr int kWarpLoad = kScanCompute / 32, kWarpMma = kWarpLoad + 1;
+// ---- second kernel: the chunks of a sequence, 32 value columns a chain ---------------------
+// A CTA runs one chain of dependent steps (4300 cycles a chunk, of which its MMAs are 1250),
+// or two, over the same keys, queries and [T; Z], whose steps fill one another's waits: two
+// where there are chains enough for every SM either way.
+constexpr int kChainThreads = 256;   // two threads a TMEM lane, 16 columns each
 constexpr int kStages = 2;
-// right-hand operands: rows of 3 x 32 bf16 (hi, mid | lo, unused) in two 64-column atoms
-constexpr uint32_t kOperandS = 128 * 256, kOperandR = kC * 256;
+// right-hand operands: rows of 3 x 32 bf16 (hi, mid | lo, unused) in two 64-column atoms; S
+// for the first product, then R, then w U (64 rows) in the same place
+constexpr uint32_t kOperand = kD * 256;
 
+struct ChainBars {
+  uint64_t d1, d2, d3, r_ready, u_ready, s_ready, drain;
+};
 struct ScanBars {
-  uint64_t raw, full[kStages], empty[kStages], d1, d2, d3, r_ready, u_ready, s_ready, drain;
+  uint64_t raw, full[kStages], empty[kStages];
+  ChainBars chain[2];
   uint32_t tmem;
   int abort;
 };
-struct ScanSmem {
+static_assert(sizeof(ScanBars) <= 256, "the barriers fit their place");
+
+template <int kChains>
+struct Scan {
+  static constexpr int kSlices = kD / kW / kChains;
+  static constexpr int kCompute = kChains * kChainThreads;
+  // + a loading warp and an issuing one for each chain
+  static constexpr int kThreads = kCompute + 32 + 32 * kChains;
+  static constexpr int kWarpLoad = kCompute / 32, kWarpMma = kWarpLoad + 1;
+  static constexpr uint32_t kTmemColumns = 256 * kChains;
   static constexpr uint32_t OFF_KQ = 0;
   static constexpr uint32_t OFF_TZ = OFF_KQ + kStages * kTileKQ;
-  static constexpr uint32_t OFF_S = OFF_TZ + kStages * kTZBytes;
-  static constexpr uint32_t OFF_R = OFF_S + kOperandS;
-  static constexpr uint32_t OFF_BAR = OFF_R + kOperandR;
-  static constexpr uint32_t kBytes = OFF_BAR + 256 + 1024;
+  static constexpr uint32_t OFF_X = OFF_TZ + kStages * kSlotBytes;  // ([T; Z] and weights)
+  static constexpr uint32_t OFF_BAR = OFF_X + kChains * kOperand;
+  static constexpr uint32_t kBytes = OFF_BAR + 256;
 };
 
 // 16 consecutive values (columns 16 ch ..) of row r as three parts
@@ -520,30 +537,37 @@ __device__ __forceinline__ void store_parts(unsigned char* base, int r, int ch,
   }
 }
 
-// the sum of the three results of 16 columns of a row
+// the sum of the three results of 16 columns of a row (8 columns at a time: 24 registers)
 __device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[16]) {
-  float y[16], z[16];
-  tmem_ld_16cols(taddr, x);
-  tmem_ld_16cols(taddr + 32, y);
-  tmem_ld_16cols(taddr + 64, z);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] += y[i] + z[i];
+  for (int e = 0; e < 2; ++e) {
+    float r[24];
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(r[8 * p]), "=f"(r[8 * p + 1]), "=f"(r[8 * p + 2]), "=f"(r[8 * p + 3]),
+                     "=f"(r[8 * p + 4]), "=f"(r[8 * p + 5]), "=f"(r[8 * p + 6]), "=f"(r[8 * p + 7])
+                   : "r"(taddr + p * kW + 8 * e));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[8 * e + i] = r[i] + (r[8 + i] + r[16 + i]);
+  }
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1)
+template <int kChains>
+__global__ void __launch_bounds__(Scan<kChains>::kThreads, 1)
 prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
-                    const __grid_constant__ CUtensorMap mapQ, const __nv_bfloat16* __restrict__ v,
+                    const __grid_constant__ CUtensorMap mapQ,
+                    const __grid_constant__ CUtensorMap mapV, const __nv_bfloat16* __restrict__ v,
                     const float* pool_in, float* pool_out, __nv_bfloat16* __restrict__ o,
                     gdn_tree_dims d, SeqLayout lay, Segment seg, const unsigned char* ws,
                     int32_t* dev_status, uint64_t limit_ns) {
-  using L = ScanSmem;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  using L = Scan<kChains>;
+  extern __shared__ __align__(1024) unsigned char smem[];
   ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int slice = blockIdx.x % kSlices;
-  const int h = (blockIdx.x / kSlices) % d.Hv, b = blockIdx.x / kSlices / d.Hv;
+  const int slice = blockIdx.x % L::kSlices;
+  const int h = (blockIdx.x / L::kSlices) % d.Hv, b = blockIdx.x / L::kSlices / d.Hv;
   const int hq = h / (d.Hv / d.Hqk);
   const int n = lay.count(b, d.N), st = lay.state(b);
   if (n < 0 || st < 0) {
@@ -554,34 +578,39 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   const int c_end = min(chunks, seg.c0 + seg.span);
   if (seg.c0 > 0 && c_end <= seg.c0) return;  // this sequence ended in an earlier segment
   const size_t row0 = (size_t)lay.cu[b];
-  const size_t soff = ((size_t)st * d.Hv + h) * kD * kD + (size_t)slice * kW;
 
   if (tid == 0) {
     mbar_init(&B->raw, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&B->full[s], 1);
-      mbar_init(&B->empty[s], 1);
+      mbar_init(&B->empty[s], kChains);
     }
-    mbar_init(&B->d1, 1);
-    mbar_init(&B->d2, 1);
-    mbar_init(&B->d3, 1);
-    mbar_init(&B->drain, 1);
-    mbar_init(&B->r_ready, kScanCompute);
-    mbar_init(&B->u_ready, kScanCompute / 2);
-    mbar_init(&B->s_ready, kScanCompute);
-    B->abort = 0;
+    for (int x = 0; x < kChains; ++x) {
+      ChainBars& C = B->chain[x];
+      mbar_init(&C.d1, 1);
+      mbar_init(&C.d2, 1);
+      mbar_init(&C.d3, 1);
+      mbar_init(&C.drain, 1);
+      mbar_init(&C.r_ready, kChainThreads / 32);  // (warps)
+      mbar_init(&C.u_ready, kChainThreads / 64);
+      mbar_init(&C.s_ready, kChainThreads / 32);
+    }
+    // (the swizzled tiles need their 1024-byte boundary)
+    B->abort = (smem_addr(smem) & 1023u) != 0;
     mbar_fence_init();
   }
-  if (warp == kWarpMma) tmem_alloc(&B->tmem, 512);
+  if (warp == L::kWarpMma) tmem_alloc(&B->tmem, L::kTmemColumns);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = B->tmem;
-  constexpr uint32_t kD1 = 0, kD2 = 96, kD3 = 192;  // TMEM columns
+  const uint32_t tmem0 = B->tmem;
+  // TMEM columns of a chain; D3 takes D1's place (all have read D1 before U is there)
+  constexpr uint32_t kD1 = 0, kD2 = 3 * kW, kD3 = 0;
+  const bool run = B->abort == 0;
 
-  if (warp == kWarpLoad) {
-    uint32_t raw_phase = 0;
-    for (int c = seg.c0; c < c_end; ++c) {
+  if (warp == L::kWarpLoad) {
+    const unsigned char* tz = ws + (slot_of(seg, lay.cu, b, seg.c0) * d.Hv + h) * (size_t)kSlotBytes;
+    for (int c = seg.c0; run && c < c_end; ++c) {
       const int i = c - seg.c0, s = i % kStages;
       if (i >= kStages && !wait_bar(&B->empty[s], ((i / kStages) & 1) ^ 1, &B->abort, limit_ns)) break;
       const int nc = min(kC, n - c * kC);
@@ -590,151 +619,157 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       // its own, and a zero weight must not meet what they hold)
       uint64_t* bar = nc < kC ? &B->raw : &B->full[s];
       if (elect_one()) {
-        mbar_arrive_expect_tx(bar, kTileKQ + kTZBytes);
+        mbar_arrive_expect_tx(bar, kTileKQ + kSlotBytes);
         load_kq(kq, &mapK, &mapQ, bar, hq, (int)(row0 + (size_t)c * kC));
-        const unsigned char* from = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
-        bulk_load(smem + L::OFF_TZ + s * kTZBytes, from, kTZBytes, bar);
+        bulk_load(smem + L::OFF_TZ + s * kSlotBytes, tz, kSlotBytes, bar);
+        // (v goes straight to the compute threads' registers, a chunk ahead: from L2)
+        tma_prefetch_l2_3d(&mapV, slice * kChains * kW, h, (int)(row0 + (size_t)(c + 1) * kC));
       }
       __syncwarp();
+      tz += (size_t)d.Hv * kSlotBytes;
       if (nc < kC) {
-        if (!wait_bar(&B->raw, raw_phase, &B->abort, limit_ns)) break;
-        raw_phase ^= 1u;
+        if (!wait_bar(&B->raw, 0, &B->abort, limit_ns)) break;
         zero_k_rows(kq, nc, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B->full[s]);
       }
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp >= L::kWarpMma) {
+    const int x = warp - L::kWarpMma;
+    ChainBars& C = B->chain[x];
+    const uint32_t tmem = tmem0 + 256 * x;
     constexpr uint32_t id1 = idesc_bf16_f32_bmn(128, 3 * kW), id2 = idesc_bf16_f32_bmn(128, 2 * kW),
                        id4 = idesc_bf16_f32_bmn(128, kW);
     constexpr uint32_t id3 = idesc_bf16_f32_amn_bmn(128, 3 * kW);
     const uint64_t dKQ = desc_sw128_kmajor(smem_addr(smem + L::OFF_KQ));
     const uint64_t dKt = desc_sw128_mnmajor(smem_addr(smem + L::OFF_KQ), kSw128TileBytes, 1024);
     const uint64_t dTZ = desc_sw128_kmajor(smem_addr(smem + L::OFF_TZ));
-    const uint64_t dS = desc_sw128_mnmajor(smem_addr(smem + L::OFF_S), kMnLbo, kMnSbo);
-    const uint64_t dR = desc_sw128_mnmajor(smem_addr(smem + L::OFF_R), kMnLbo, kMnSbo);
-    bool ok = true;
+    const uint64_t dX = desc_sw128_mnmajor(smem_addr(smem + L::OFF_X + x * kOperand), kMnLbo, kMnSbo);
+    constexpr uint32_t kStep = (2 * kMnSbo) >> 4;  // 16 rows of the right-hand operand
+    // (the operands that the compute warps wrote reach the tensor cores' proxy by this warp's
+    // fence, one for all of them, behind the barrier: a fence in each of their warps took a
+    // third of their time)
+    bool ok = run;
     for (int c = seg.c0; ok && c < c_end; ++c) {
       const int i = c - seg.c0, s = i % kStages;
+      const uint64_t kq = dKQ + s * (kTileKQ >> 4), kt = dKt + s * (kTileKQ >> 4),
+                     tz = dTZ + s * (kSlotBytes >> 4);
       ok = wait_bar(&B->full[s], (i / kStages) & 1, &B->abort, limit_ns) &&
-           wait_bar(&B->s_ready, i & 1, &B->abort, limit_ns);
+           wait_bar(&C.s_ready, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
+      fence_proxy_async_smem();
       if (elect_one()) {
-        const uint64_t a = dKQ + s * (kTileKQ >> 4);
 #pragma unroll
         for (int e = 0; e < kD / 16; ++e) {
           const uint32_t off = ((e >> 2) * kSw128TileBytes + (e & 3) * 32) >> 4;
-          if (e == 0) umma_ss<false>(tmem + kD1, a + off, dS + ((e * 2 * kMnSbo) >> 4), id1);
-          else umma_ss<true>(tmem + kD1, a + off, dS + ((e * 2 * kMnSbo) >> 4), id1);
+          if (e == 0) umma_ss<false>(tmem + kD1, kq + off, dX + e * kStep, id1);
+          else umma_ss<true>(tmem + kD1, kq + off, dX + e * kStep, id1);
         }
-        umma_commit(&B->d1);
+        umma_commit(&C.d1);
       }
       __syncwarp();
-      ok = wait_bar(&B->r_ready, i & 1, &B->abort, limit_ns);
+      ok = wait_bar(&C.r_ready, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
+      fence_proxy_async_smem();
       if (elect_one()) {
-        const uint64_t a = dTZ + s * (kTZBytes >> 4);
 #pragma unroll
         for (int e = 0; e < kC / 16; ++e) {  // hi (hi, mid, lo)
-          if (e == 0) umma_ss<false>(tmem + kD2, a + ((e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id1);
-          else umma_ss<true>(tmem + kD2, a + ((e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id1);
+          if (e == 0) umma_ss<false>(tmem + kD2, tz + ((e * 32) >> 4), dX + e * kStep, id1);
+          else umma_ss<true>(tmem + kD2, tz + ((e * 32) >> 4), dX + e * kStep, id1);
         }
 #pragma unroll
         for (int e = 0; e < kC / 16; ++e)    // mid (hi, mid)
-          umma_ss<true>(tmem + kD2, a + ((kTileTZ + e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id2);
+          umma_ss<true>(tmem + kD2, tz + ((kTileTZ + e * 32) >> 4), dX + e * kStep, id2);
 #pragma unroll
         for (int e = 0; e < kC / 16; ++e)    // lo (hi)
-          umma_ss<true>(tmem + kD2, a + ((2 * kTileTZ + e * 32) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id4);
-        umma_commit(&B->d2);
+          umma_ss<true>(tmem + kD2, tz + ((2 * kTileTZ + e * 32) >> 4), dX + e * kStep, id4);
+        umma_commit(&C.d2);
       }
       __syncwarp();
-      ok = wait_bar(&B->u_ready, i & 1, &B->abort, limit_ns);
+      ok = wait_bar(&C.u_ready, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
+      fence_proxy_async_smem();
       if (elect_one()) {
-        const uint64_t a = dKt + s * (kTileKQ >> 4);
 #pragma unroll
         for (int e = 0; e < kC / 16; ++e) {
-          if (e == 0) umma_ss<false>(tmem + kD3, a + ((e * 2048) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id3);
-          else umma_ss<true>(tmem + kD3, a + ((e * 2048) >> 4), dR + ((e * 2 * kMnSbo) >> 4), id3);
+          if (e == 0) umma_ss<false>(tmem + kD3, kt + ((e * 2048) >> 4), dX + e * kStep, id3);
+          else umma_ss<true>(tmem + kD3, kt + ((e * 2048) >> 4), dX + e * kStep, id3);
         }
-        umma_commit(&B->d3);
+        umma_commit(&C.d3);
         umma_commit(&B->empty[s]);
       }
       __syncwarp();
     }
     // whatever was issued is done before TMEM and the operands go
-    if (elect_one()) umma_commit(&B->drain);
+    if (elect_one()) umma_commit(&C.drain);
     __syncwarp();
-    mbar_wait(&B->drain, 0, limit_ns);
+    mbar_wait(&C.drain, 0, limit_ns);
   } else {
-    // ---- compute: thread (TMEM lane ln, column half ch) -------------------------------------
-    const int ch = warp >> 2, ln = 32 * (warp & 3) + lane;
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * ch;
+    // ---- compute: thread (chain, TMEM lane ln, column half ch) --------------------------------
+    const int x0 = warp / (kChainThreads / 32), ch = (warp >> 2) & 1, ln = 32 * (warp & 3) + lane;
+    ChainBars& C = B->chain[x0];
+    const uint32_t tl = tmem0 + 256 * x0 + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * ch;
     const bool isq = ln >= kC;
     const int t = ln & (kC - 1);
-    unsigned char* sS = smem + L::OFF_S;
-    unsigned char* sR = smem + L::OFF_R;
+    const int col = (slice * kChains + x0) * kW + 16 * ch;  // first value column
+    const size_t soff = ((size_t)st * d.Hv + h) * kD * kD + (size_t)ln * kD + col;
+    unsigned char* sX = smem + L::OFF_X + x0 * kOperand;
     // row ln of the state, 16 columns
     float S[16];
-    const float* src = (seg.c0 == 0 ? pool_in : pool_out) + soff + (size_t)ln * kD + 16 * ch;
+    const float* src = (seg.c0 == 0 ? pool_in : pool_out) + soff;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<float4*>(S + 4 * e) = *reinterpret_cast<const float4*>(src + 4 * e);
-    bool ok = true;
+    bool ok = run;
     if (seg.c0 < c_end) {
-      store_parts(sS, ln, ch, S);
-      fence_proxy_async_smem();
-      mbar_arrive(&B->s_ready);
+      store_parts(sX, ln, ch, S);
+      mbar_arrive_warp(&C.s_ready);
     }
-    // this token's v (16 columns) and weights, a chunk ahead
+    // this token's v (16 columns) and weights, a chunk ahead (the pointers go along: nothing
+    // is looked up on the way)
     uint4 vn[2];
-    float gam_n, beta_n, w_n, gC_n;
-    auto fetch = [&](int c) {
-      const bool live = c * kC + t < n;
-      const float* aux = reinterpret_cast<const float*>(
-          ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes + kTZBytes);
-      gam_n = aux[t];
-      beta_n = aux[kC + t];
-      w_n = aux[2 * kC + t];
-      gC_n = aux[3 * kC];
+    const size_t v_step = (size_t)kC * d.Hv * kD;
+    const size_t first = ((row0 + (size_t)seg.c0 * kC + t) * d.Hv + h) * kD + col;
+    const __nv_bfloat16* vp = v + first;
+    __nv_bfloat16* op = o + first;
+    int left = n - seg.c0 * kC - t;  // > 0: the token is there
+    auto fetch_v = [&](bool live) {
       vn[0] = vn[1] = make_uint4(0, 0, 0, 0);
       if (!isq && live) {
-        const uint4* p = reinterpret_cast<const uint4*>(
-            v + ((row0 + (size_t)c * kC + t) * d.Hv + h) * kD + slice * kW + 16 * ch);
-        vn[0] = __ldg(p);
-        vn[1] = __ldg(p + 1);
+        vn[0] = __ldg(reinterpret_cast<const uint4*>(vp));
+        vn[1] = __ldg(reinterpret_cast<const uint4*>(vp) + 1);
       }
+      vp += v_step;
     };
-    if (seg.c0 < c_end) fetch(seg.c0);
-    for (int c = seg.c0; c < c_end; ++c) {
-      const int i = c - seg.c0;
-      const bool live = c * kC + t < n;
-      const uint4 vv[2] = {vn[0], vn[1]};
-      const float gam = gam_n, bt = beta_n, w = w_n, gC = gC_n;
-      if (c + 1 < c_end) fetch(c + 1);
-      ok = wait_bar(&B->d1, i & 1, &B->abort, limit_ns);
+    if (seg.c0 < c_end) fetch_v(left > 0);
+    for (int c = seg.c0; ok && c < c_end; ++c) {
+      const int i = c - seg.c0, s = i % kStages;
+      ok = wait_bar(&B->full[s], (i / kStages) & 1, &B->abort, limit_ns);
+      if (!ok) break;
+      const float* aux = reinterpret_cast<const float*>(smem + L::OFF_TZ + s * kSlotBytes + kTZBytes);
+      const float gam = aux[t], bt = aux[kC + t], w = aux[2 * kC + t], gC = aux[3 * kC];
+      ok = wait_bar(&C.d1, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
       float x[16];
       load_sum(tl + kD1, x);
       if (!isq) {
-        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vv);
-        float r[16];
+        const uint32_t* vw = reinterpret_cast<const uint32_t*>(vn);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float ve = __uint_as_float((e & 1) ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16);
-          r[e] = bt * fmaf(-gam, x[e], ve);  // (rows past the sequence: k = v = beta = 0)
+          x[e] = bt * fmaf(-gam, x[e], ve);  // (rows past the sequence: k = v = beta = 0)
         }
-        store_parts(sR, t, ch, r);
-        fence_proxy_async_smem();
+        store_parts(sX, t, ch, x);
       }
       tc_fence_before_sync();
-      mbar_arrive(&B->r_ready);
-      ok = wait_bar(&B->d2, i & 1, &B->abort, limit_ns);
+      mbar_arrive_warp(&C.r_ready);
+      if (c + 1 < c_end) fetch_v(left > kC);  // (the next chunk's, a chunk ahead of its use)
+      ok = wait_bar(&C.d2, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
       float y[16];
@@ -742,11 +777,10 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       if (!isq) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) y[e] *= w;
-        store_parts(sR, t, ch, y);
-        fence_proxy_async_smem();
+        store_parts(sX, t, ch, y);
         tc_fence_before_sync();
-        mbar_arrive(&B->u_ready);
-      } else if (live) {
+        mbar_arrive_warp(&C.u_ready);
+      } else if (left > 0) {
         uint32_t p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -754,27 +788,27 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
                                                           fmaf(gam, x[2 * e + 1], y[2 * e + 1]));
           p[e] = *reinterpret_cast<const uint32_t*>(&q2);
         }
-        uint4* to = reinterpret_cast<uint4*>(
-            o + ((row0 + (size_t)c * kC + t) * d.Hv + h) * kD + slice * kW + 16 * ch);
+        uint4* to = reinterpret_cast<uint4*>(op);
         to[0] = make_uint4(p[0], p[1], p[2], p[3]);
         to[1] = make_uint4(p[4], p[5], p[6], p[7]);
       }
       __syncwarp();
-      ok = wait_bar(&B->d3, i & 1, &B->abort, limit_ns);
+      ok = wait_bar(&C.d3, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
       load_sum(tl + kD3, x);
 #pragma unroll
       for (int e = 0; e < 16; ++e) S[e] = fmaf(gC, S[e], x[e]);
       if (c + 1 < c_end) {
-        store_parts(sS, ln, ch, S);
-        fence_proxy_async_smem();
+        store_parts(sX, ln, ch, S);
         tc_fence_before_sync();
-        mbar_arrive(&B->s_ready);
+        mbar_arrive_warp(&C.s_ready);
       }
+      op += v_step;
+      left -= kC;
     }
     if (ok) {
-      float* to = pool_out + soff + (size_t)ln * kD + 16 * ch;
+      float* to = pool_out + soff;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float4*>(to + 4 * e) = *reinterpret_cast<const float4*>(S + 4 * e);
@@ -785,13 +819,15 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   tc_fence_after_sync();
   if (B->abort) {
     // the copies in flight end (or their bounded waits do) before this CTA does
-    if (warp == kWarpLoad)
-      for (int s = 0; s < kStages; ++s)
-        for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait(&B->full[s], ph, 1000000);
+    if (warp == L::kWarpLoad)
+      for (uint32_t ph = 0; ph < 2; ++ph) {
+        for (int s = 0; s < kStages; ++s) mbar_wait(&B->full[s], ph, 1000000);
+        mbar_wait(&B->raw, ph, 1000000);
+      }
     __syncthreads();
     if (tid == 0 && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
   }
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == L::kWarpMma) tmem_dealloc(tmem0, L::kTmemColumns);
 }
 
 // the segments for these dims: chunks a launch pair, and whether one pair does for all
@@ -825,19 +861,26 @@ size_t prefill_tc_workspace_bytes(const gdn_tree_dims& d, int32_t T) {
 
 cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t stream) {
   const gdn_tree_dims& d = a.d;
-  CUtensorMap mapK, mapQ;
+  CUtensorMap mapK, mapQ, mapV;
   if (!encode_head_rows_map(&mapK, a.k, a.lay.T, d.Hqk, kD, kC) ||
-      !encode_head_rows_map(&mapQ, a.q, a.lay.T, d.Hqk, kD, kC))
+      !encode_head_rows_map(&mapQ, a.q, a.lay.T, d.Hqk, kD, kC) ||
+      !encode_head_rows_map(&mapV, a.v, a.lay.T, d.Hv, kD, kC))
     return cudaErrorInvalidValue;
   cudaError_t err = cudaFuncSetAttribute(prefill_prep_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepBytes);
   if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(prefill_scan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               ScanSmem::kBytes);
+    err = cudaFuncSetAttribute(prefill_scan_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Scan<1>::kBytes);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(prefill_scan_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Scan<2>::kBytes);
   if (err != cudaSuccess) return err;
   Segment s = plan(d, a.lay.T);
   const long long slots = s.dense ? dense_slots(a.lay.T, d.B) : (long long)s.span * d.B;
-  const long long scan = (long long)d.B * d.Hv * kSlices;
+  // one chain a CTA while there is an SM for each
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  const bool two = (long long)d.B * d.Hv * Scan<1>::kSlices > sms;
+  const long long scan = (long long)d.B * d.Hv * (two ? Scan<2>::kSlices : Scan<1>::kSlices);
   if (slots * d.Hv > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   const uint64_t limit = wait_hooks().limit_ns;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -848,9 +891,13 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
           mapK, mapQ, a.log_alpha, a.beta, d, a.lay, s, ws, a.dev_status, limit);
       if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
-    prefill_scan_kernel<<<(unsigned)scan, kScanThreads, ScanSmem::kBytes, stream>>>(
-        mapK, mapQ, static_cast<const __nv_bfloat16*>(a.v), a.pool_in, a.pool_out,
-        static_cast<__nv_bfloat16*>(a.o), d, a.lay, s, ws, a.dev_status, limit);
+    auto run = [&](auto kernel, int threads, uint32_t bytes) {
+      kernel<<<(unsigned)scan, threads, bytes, stream>>>(
+          mapK, mapQ, mapV, static_cast<const __nv_bfloat16*>(a.v), a.pool_in, a.pool_out,
+          static_cast<__nv_bfloat16*>(a.o), d, a.lay, s, ws, a.dev_status, limit);
+    };
+    if (two) run(prefill_scan_kernel<2>, Scan<2>::kThreads, Scan<2>::kBytes);
+    else run(prefill_scan_kernel<1>, Scan<1>::kThreads, Scan<1>::kBytes);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     if (s.span == 0) break;  // (no tokens at all: the states are copied)
   }
