@@ -425,15 +425,16 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
       *reinterpret_cast<float4*>(&P.A[32 + i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
     __syncthreads();
-    // T in rows 0-63 of the tiles, here and in the workspace
+    // T in rows 0-63 of the tiles
 #pragma unroll
     for (int e = tid; e < kC * 8; e += kPrepThreads) {
       const int r = e >> 3, c8 = e & 7;
       float x[8];
+      *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(&P.A[r][8 * c8]);
+      *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(&P.A[r][8 * c8 + 4]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 8 * c8 + i <= r ? P.A[r][8 * c8 + i] : 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = 8 * c8 + i <= r ? x[i] : 0.f;
       store_tz(sTZ, r, c8, x);
-      store_tz(out, r, c8, x);
     }
     fence_proxy_async_smem();
     tc_fence_before_sync();
@@ -468,8 +469,16 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = gram[8 * c8 + e];
-        store_tz(out, ln, 4 * half + c8, y);
+        store_tz(sTZ, ln, 4 * half + c8, y);
       }
+    }
+    // the tiles go to the workspace as they lie
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0 && ok) {
+      bulk_store(out, sTZ, kTZBytes);
+      bulk_commit_group();
+      bulk_wait_all();
     }
   }
   // (after a timeout: the copies and MMAs in flight end, or their bounded waits do)
@@ -521,9 +530,33 @@ struct Scan {
   static constexpr uint32_t kBytes = OFF_BAR + 256;
 };
 
-// 16 consecutive values (columns 16 ch ..) of row r as three parts
-__device__ __forceinline__ void store_parts(unsigned char* base, int r, int ch,
-                                            const float (&x)[16]) {
+// two fp32 lanes an instruction: (a, b) * w; (a, b) * x + (c, d); (a, b) + (c, d)
+__device__ __forceinline__ void mul2(float& a, float& b, float w) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(w));
+}
+__device__ __forceinline__ void mad2(float& a, float& b, float x, float c, float d) {
+  asm("{\n\t.reg .b64 p, q, r;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
+      "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
+  asm("{\n\t.reg .b64 p, q;\n\t"
+      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(c), "f"(d));
+}
+
+// 16 consecutive values of a row as three parts; `at`: the shared address of their first
+// chunk (mn_chunk(row, 2 ch) of an operand; the swizzle makes the next chunk bit 4 of it and
+// the middle part bit 6, the third part lies an atom further)
+__device__ __forceinline__ void store_parts(uint32_t at, const float (&x)[16]) {
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     uint4 hi, mid, lo;
@@ -531,14 +564,42 @@ __device__ __forceinline__ void store_parts(unsigned char* base, int r, int ch,
     split3(x[8 * e + 2], x[8 * e + 3], hi.y, mid.y, lo.y);
     split3(x[8 * e + 4], x[8 * e + 5], hi.z, mid.z, lo.z);
     split3(x[8 * e + 6], x[8 * e + 7], hi.w, mid.w, lo.w);
-    *reinterpret_cast<uint4*>(base + mn_chunk(r, 2 * ch + e)) = hi;
-    *reinterpret_cast<uint4*>(base + mn_chunk(r, 4 + 2 * ch + e)) = mid;
-    *reinterpret_cast<uint4*>(base + mn_chunk(r, 8 + 2 * ch + e)) = lo;
+    const uint32_t to = at ^ (16u * e);
+    auto st = [](uint32_t p, uint4 w) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(w.x), "r"(w.y),
+                   "r"(w.z), "r"(w.w)
+                   : "memory");
+    };
+    st(to, hi);
+    st(to ^ 64u, mid);
+    st(to + kMnLbo, lo);
   }
 }
 
 // the sum of the three results of 16 columns of a row (8 columns at a time: 24 registers)
+template <bool kOnce>
 __device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[16]) {
+  if (kOnce) {  // all at once, where there are registers for it: one wait
+    float y[16], z[16];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      float(&r)[16] = p == 0 ? x : p == 1 ? y : z;
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+          "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+          : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+            "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+            "=f"(r[14]), "=f"(r[15])
+          : "r"(taddr + p * kW));
+    }
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      add2(y[i], y[i + 1], z[i], z[i + 1]);
+      add2(x[i], x[i + 1], y[i], y[i + 1]);
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float r[24];
@@ -550,7 +611,12 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[16]) {
                    : "r"(taddr + p * kW + 8 * e));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[8 * e + i] = r[i] + (r[8 + i] + r[16 + i]);
+    for (int i = 0; i < 8; i += 2) {
+      add2(r[8 + i], r[9 + i], r[16 + i], r[17 + i]);
+      add2(r[i], r[i + 1], r[8 + i], r[9 + i]);
+      x[8 * e + i] = r[i];
+      x[8 * e + i + 1] = r[i + 1];
+    }
   }
 }
 
@@ -717,7 +783,9 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
     const int t = ln & (kC - 1);
     const int col = (slice * kChains + x0) * kW + 16 * ch;  // first value column
     const size_t soff = ((size_t)st * d.Hv + h) * kD * kD + (size_t)ln * kD + col;
-    unsigned char* sX = smem + L::OFF_X + x0 * kOperand;
+    // where this thread's parts go: row ln of S, row t of R and w U
+    const uint32_t sX = smem_addr(smem + L::OFF_X + x0 * kOperand);
+    const uint32_t to_s = sX + mn_chunk(ln, 2 * ch), to_r = sX + mn_chunk(t, 2 * ch);
     // row ln of the state, 16 columns
     float S[16];
     const float* src = (seg.c0 == 0 ? pool_in : pool_out) + soff;
@@ -726,7 +794,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       *reinterpret_cast<float4*>(S + 4 * e) = *reinterpret_cast<const float4*>(src + 4 * e);
     bool ok = run;
     if (seg.c0 < c_end) {
-      store_parts(sX, ln, ch, S);
+      store_parts(to_s, S);
       mbar_arrive_warp(&C.s_ready);
     }
     // this token's v (16 columns) and weights, a chunk ahead (the pointers go along: nothing
@@ -756,15 +824,16 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       if (!ok) break;
       tc_fence_after_sync();
       float x[16];
-      load_sum(tl + kD1, x);
+      load_sum<kChains == 1>(tl + kD1, x);
       if (!isq) {
         const uint32_t* vw = reinterpret_cast<const uint32_t*>(vn);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float ve = __uint_as_float((e & 1) ? vw[e >> 1] & 0xffff0000u : vw[e >> 1] << 16);
-          x[e] = bt * fmaf(-gam, x[e], ve);  // (rows past the sequence: k = v = beta = 0)
+        for (int e = 0; e < 16; e += 2) {  // (rows past the sequence: k = v = beta = 0)
+          const uint32_t v2 = vw[e >> 1];
+          mad2(x[e], x[e + 1], -gam, __uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
+          mul2(x[e], x[e + 1], bt);
         }
-        store_parts(sX, t, ch, x);
+        store_parts(to_r, x);
       }
       tc_fence_before_sync();
       mbar_arrive_warp(&C.r_ready);
@@ -773,11 +842,11 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       if (!ok) break;
       tc_fence_after_sync();
       float y[16];
-      load_sum(tl + kD2, y);
+      load_sum<kChains == 1>(tl + kD2, y);
       if (!isq) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] *= w;
-        store_parts(sX, t, ch, y);
+        for (int e = 0; e < 16; e += 2) mul2(y[e], y[e + 1], w);
+        store_parts(to_r, y);
         tc_fence_before_sync();
         mbar_arrive_warp(&C.u_ready);
       } else if (left > 0) {
@@ -796,11 +865,11 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
       ok = wait_bar(&C.d3, i & 1, &B->abort, limit_ns);
       if (!ok) break;
       tc_fence_after_sync();
-      load_sum(tl + kD3, x);
+      load_sum<kChains == 1>(tl + kD3, x);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[e] = fmaf(gC, S[e], x[e]);
+      for (int e = 0; e < 16; e += 2) mad2(S[e], S[e + 1], gC, x[e], x[e + 1]);
       if (c + 1 < c_end) {
-        store_parts(sX, ln, ch, S);
+        store_parts(to_s, S);
         tc_fence_before_sync();
         mbar_arrive_warp(&C.s_ready);
       }
