@@ -54,9 +54,21 @@ cache_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
     }
     const size_t src = (size_t)(first + node) * vecs;
     const size_t dst = ((size_t)page * d.page_size + (size_t)(at % d.page_size)) * vecs;
-    for (int i = lane; i < vecs; i += 32) {
-      k_cache[dst + i] = k[src + i];
-      v_cache[dst + i] = v[src + i];
+    // eight loads of a lane in flight (a row of 8 heads of 128 bf16, k and v, is one round)
+    for (int i0 = lane; i0 < vecs; i0 += 4 * 32) {
+      uint4 x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + 32 * e < vecs) {
+          x[e] = __ldcs(k + src + i0 + 32 * e);
+          y[e] = __ldcs(v + src + i0 + 32 * e);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + 32 * e < vecs) {
+          k_cache[dst + i0 + 32 * e] = x[e];
+          v_cache[dst + i0 + 32 * e] = y[e];
+        }
     }
   }
 }

@@ -13,6 +13,7 @@
 // A warp's loads of one row cover kCols * 4 contiguous bytes.
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace {
@@ -160,6 +161,135 @@ rule_recurrent_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
   }
 }
 
+// ---- one token of many sequences: a state a CTA, by bulk copies ----------------------------
+// Bound by DRAM: a 64 KB state (dk rows of 128 columns) is read and written whole.  It comes
+// and goes as one contiguous piece each way (cp.async.bulk), three CTAs an SM; four CTAs a
+// state with 16-byte accesses of 128-byte row pieces reached 5.5 TB/s, and 5.0 TB/s with
+// sixteen CTAs an SM.  Thread (rg, cl): rows 16 rg .., columns 4 cl .. + 3.
+constexpr int kBulkThreads = 256;
+constexpr int kBulkRows = kMaxD / (kBulkThreads / 32);  // rows a warp
+
+struct BulkShared {
+  float k[kMaxD], q[kMaxD], qk[kBulkThreads / 32];
+  float4 s[kBulkThreads / 32][32], r[kBulkThreads / 32][32];  // each warp's S^T k and S^T q
+  uint64_t bar;
+};
+constexpr uint32_t kBulkBytes = kMaxD * kMaxD * 4 + sizeof(BulkShared);
+
+template <typename T>
+__global__ void __launch_bounds__(kBulkThreads, 3)
+rule_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                 const float* __restrict__ log_alpha, const float* __restrict__ beta,
+                 const float* pool_in, float* pool_out, T* __restrict__ o, gdn_tree_dims d,
+                 SeqLayout lay, int32_t* dev_status, uint64_t limit_ns) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  float4(*sS)[32] = reinterpret_cast<float4(*)[32]>(smem);  // [dk][128 columns]
+  BulkShared& P = *reinterpret_cast<BulkShared*>(smem + kMaxD * kMaxD * 4);
+  const int h = blockIdx.x % d.Hv, b = blockIdx.x / d.Hv;
+  const int tid = threadIdx.x, rg = tid >> 5, cl = tid & 31;
+  const int hq = h / (d.Hv / d.Hqk);
+  const int st = lay.state(b);
+  if (st < 0) {
+    if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    return;
+  }
+  const size_t soff = ((size_t)st * d.Hv + h) * d.dk * kMaxD;
+  const uint32_t bytes = (uint32_t)d.dk * kMaxD * 4;
+  if (tid == 0) {
+    sm100::mbar_init(&P.bar, 1);
+    sm100::mbar_fence_init();
+    sm100::mbar_arrive_expect_tx(&P.bar, bytes);
+    sm100::bulk_load(smem, pool_in + soff, bytes, &P.bar);
+  }
+  if (tid < d.dk) P.k[tid] = to_f32(k[((size_t)b * d.Hqk + hq) * d.dk + tid]);
+  if (tid >= kMaxD && tid - kMaxD < d.dk)
+    P.q[tid - kMaxD] = to_f32(q[((size_t)b * d.Hqk + hq) * d.dk + tid - kMaxD]);
+  const size_t unit = (size_t)b * d.Hv + h;
+  const float a = expf(log_alpha[unit]), bt = beta[unit];
+  float vv[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[unit * kMaxD + 4 * cl + e]);
+  __syncthreads();
+  const bool ok = sm100::mbar_wait(&P.bar, 0, limit_ns);
+  float4 S[kBulkRows], s = make_float4(0.f, 0.f, 0.f, 0.f), r = s;
+  float qk = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBulkRows; ++i) {
+    const int row = rg * kBulkRows + i;
+    if (row < d.dk) {
+      S[i] = sS[row][cl];
+      const float ki = P.k[row], qi = P.q[row];
+      s.x = fmaf(ki, S[i].x, s.x);
+      s.y = fmaf(ki, S[i].y, s.y);
+      s.z = fmaf(ki, S[i].z, s.z);
+      s.w = fmaf(ki, S[i].w, s.w);
+      r.x = fmaf(qi, S[i].x, r.x);
+      r.y = fmaf(qi, S[i].y, r.y);
+      r.z = fmaf(qi, S[i].z, r.z);
+      r.w = fmaf(qi, S[i].w, r.w);
+      qk = fmaf(qi, ki, qk);
+    }
+  }
+  P.s[rg][cl] = s;
+  P.r[rg][cl] = r;
+  if (cl == 0) P.qk[rg] = qk;
+  // (a timeout leaves the copy in flight: it is waited for once more before the CTA ends)
+  if (__syncthreads_or(!ok)) {
+    sm100::mbar_wait(&P.bar, 0, limit_ns);
+    if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
+    return;
+  }
+  s = P.s[0][cl];
+  r = P.r[0][cl];
+  qk = P.qk[0];
+#pragma unroll
+  for (int w = 1; w < kBulkThreads / 32; ++w) {
+    const float4 x = P.s[w][cl], y = P.r[w][cl];
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
+    qk += P.qk[w];
+  }
+  const float4 u = make_float4(bt * (vv[0] - a * s.x), bt * (vv[1] - a * s.y),
+                               bt * (vv[2] - a * s.z), bt * (vv[3] - a * s.w));
+#pragma unroll
+  for (int i = 0; i < kBulkRows; ++i) {
+    const int row = rg * kBulkRows + i;
+    if (row < d.dk) {
+      const float ki = P.k[row];
+      sS[row][cl] = make_float4(fmaf(ki, u.x, a * S[i].x), fmaf(ki, u.y, a * S[i].y),
+                                fmaf(ki, u.z, a * S[i].z), fmaf(ki, u.w, a * S[i].w));
+    }
+  }
+  sm100::fence_proxy_async_smem();
+  if (rg == 0) {
+    T* ot = o + unit * kMaxD + 4 * cl;
+    ot[0] = from_f32<T>(fmaf(a, r.x, qk * u.x));
+    ot[1] = from_f32<T>(fmaf(a, r.y, qk * u.y));
+    ot[2] = from_f32<T>(fmaf(a, r.z, qk * u.z));
+    ot[3] = from_f32<T>(fmaf(a, r.w, qk * u.w));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    sm100::bulk_store(pool_out + soff, smem, bytes);
+    sm100::bulk_commit_group();
+    sm100::bulk_wait_all();
+  }
+}
+
+template <typename T>
+cudaError_t launch_step_bulk(const RuleArgs& a, cudaStream_t stream) {
+  const gdn_tree_dims& d = a.d;
+  auto kernel = rule_step_kernel<T>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kBulkBytes);
+  if (err != cudaSuccess) return err;
+  kernel<<<(unsigned)(d.B * d.Hv), kBulkThreads, kBulkBytes, stream>>>(
+      static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v),
+      a.log_alpha, a.beta, a.pool_in, a.pool_out, static_cast<T*>(a.o), d, a.lay, a.dev_status,
+      wait_hooks().limit_ns);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_typed(const RuleArgs& a, cudaStream_t stream) {
   const gdn_tree_dims& d = a.d;
@@ -201,6 +331,13 @@ cudaError_t launch_prefill(const RuleArgs& a, void* workspace, cudaStream_t stre
 }
 
 cudaError_t launch_decode_step(const RuleArgs& a, cudaStream_t stream) {
+  // a state a CTA once there are two for every SM; with fewer, four CTAs a state have it
+  // sooner
+  const gdn_tree_dims& d = a.d;
+  const long long units = (long long)d.B * d.Hv;
+  if (d.dv == kMaxD && units >= 2 * (sm_count() > 0 ? sm_count() : 152) && units <= 0x7fffffffll)
+    return d.dtype == GDN_TREE_BF16 ? launch_step_bulk<__nv_bfloat16>(a, stream)
+                                    : launch_step_bulk<float>(a, stream);
   return launch_recurrent(a, stream);
 }
 

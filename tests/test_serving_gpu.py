@@ -193,6 +193,7 @@ def test_prefill_bad_layout_is_reported():
 
 @pytest.mark.parametrize("B,Hqk,Hv,dk,dv,dtype", [
     (1, 16, 32, 128, 128, "bf16"), (5, 2, 4, 128, 128, "bf16"), (33, 1, 2, 128, 128, "bf16"),
+    (40, 4, 8, 128, 128, "bf16"), (160, 1, 2, 96, 128, "f32"), (311, 1, 1, 16, 128, "bf16"),
     (3, 2, 2, 64, 32, "bf16"), (2, 1, 3, 16, 16, "f32"), (4, 2, 4, 128, 128, "f32"),
     (3, 1, 1, 80, 112, "f32")])
 @pytest.mark.parametrize("gates", ["mixed", "strong", "reset"])
