@@ -77,6 +77,11 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
+// The prefix's units run before this kernel, which may start beside their last ones: from
+// here on their parts are there.  (Every CTA comes here, so that this kernel never ends
+// before theirs.)
+__device__ __forceinline__ void prefix_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int DP>
 struct Shared {
   static constexpr int kLd = DP + 8;  // (rows 16 bytes apart in the banks)
@@ -119,10 +124,14 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
   const long long cap = (long long)d.table_width * d.page_size;
   if (first < 0 || n < 0 || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
     if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    prefix_done();
     return;  // (every CTA of the cluster)
   }
   const int rows = n * G;
-  if (rows == 0 || rows > kRows) return;
+  if (rows == 0 || rows > kRows) {
+    prefix_done();
+    return;
+  }
   const bool own = k != nullptr, tree = own && parent != nullptr;
   if (tid < n) {
     const int p = tree ? parent[first + tid] : tid - 1;
@@ -365,6 +374,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
   if (C > 1) cluster.sync();
   else __syncthreads();
 
+  prefix_done();
+
   // ---- the rows' weights: the cluster's CTAs and the prefix's parts -----------------------
   const size_t T = (size_t)d.T * d.Hq;
   auto out_row = [&](int r) {
@@ -463,12 +474,14 @@ cudaError_t launch_dp(const AttendArgs& a, int plen, const float* part_o, const 
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared<DP>);
   cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 0 ? 2 : 1;  // (beside the prefix's units, where there are any)
   typedef const __nv_bfloat16* bf;
   err = cudaLaunchKernelEx(&cfg, kernel, static_cast<bf>(a.q), static_cast<bf>(a.k),
                            static_cast<bf>(a.v), a.parent, a.cu, static_cast<bf>(a.k_cache),

@@ -19,12 +19,12 @@
 // warp 18 issues the MMAs.  Tiles come by TMA, a box a page (a box a tile where pages are
 // larger, and for the tree's own rows); pages that do not fit the tiles, and head sizes
 // other than 64 and 128, come by 16-byte cp.async row by row.
-// S and O are fp32 in TMEM; P goes back to TMEM as bf16 over the S it came from and is the
-// A operand of P V.  Issue order P0 V, S0', P1 V, S1': one tile's MMAs (1024 cycles for
-// D = 128) run while the other's softmax does, which has to take no longer; with one
-// thread a row it took 2150 cycles, and a tile of keys 4100.  The two threads of a row
-// (of warps w and w + 4) exchange their maxima; each adds up its own half, and keeps its
-// half of P in the columns of S that only it reads.
+// S and O are fp32 in TMEM; P goes back to TMEM as bf16 over the S it came from, each thread
+// of a row its half in columns that only it reads, and is the A operand of P V.  Issue order
+// P0 V, S0', P1 V, S1': one tile's MMAs (1030 cycles for D = 128) run while the other's
+// softmax does.  That softmax, 1500 cycles, is what bounds a tile of keys (3000 cycles; one
+// thread a row: 4100).  Making the next S in two halves around P V, so that half of the
+// softmax starts sooner, was slower (4100: products of 64 keys cost more than they free).
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one its
 // sums use (exact either way: P and l stay far below the overflow of their types).
@@ -44,6 +44,7 @@ constexpr int kSoftmax = 512;             // softmax threads: two a row
 constexpr int kThreads = kSoftmax + 3 * 32;
 constexpr int kWarpK = kSoftmax / 32, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 constexpr int kHalf = kTile / 2;
+constexpr int kMaxSorted = 256;          // sequences that every unit may rank by length
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
@@ -68,6 +69,7 @@ struct TcArgs {
   bool with_prefix;    // a sequence's units include the prefix
   int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
   bool own_box;        // the tree's own rows come by TMA
+  bool by_length;      // units of long contexts first (more units than SMs, kMaxSorted sequences at most)
 };
 
 template <int DP>
@@ -86,6 +88,7 @@ struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2], vraw, ready, drain;
   uint32_t tmem;
   int abort;
+  int unit_b;
   float top[2][2][kTile];  // a row's maximum over each half of a tile
   uint32_t badv[2][4];  // own rows of a V tile that hold infinities or NaN (by stage)
 };
@@ -296,7 +299,22 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   int u = blockIdx.x / a.splits;
   const int t = u % a.tiles;
   u /= a.tiles;
-  const int hk = u % d.Hkv, b = u / d.Hkv;  // (prefix units: b = 0)
+  const int hk = u % d.Hkv;
+  int b = u / d.Hkv;  // (prefix units: 0)
+  if (a.by_length) {  // the longest contexts first: the SMs end closer together
+    int* len = sParent;
+    if (tid < d.B) len[tid] = a.ctx[tid];
+    __syncthreads();
+    if (tid < d.B) {
+      const int mine = len[tid];
+      int rank = 0;
+      for (int j = 0; j < d.B; ++j) rank += len[j] > mine || (len[j] == mine && j < tid);
+      if (rank == b) S->unit_b = tid;
+    }
+    __syncthreads();
+    b = S->unit_b;
+    __syncthreads();
+  }
   int first = 0, n = 0, ctx = 0;
   if (!a.prefix_units) {
     const int stop = a.cu[b + 1];
@@ -333,6 +351,9 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     else if (i < nP + nC) { seg = kContext; j0 = (i - nP) * kTile; len = ctx; }
     else { seg = kOwn; j0 = (all - 1 - i) * kTile; len = seen; }
   };
+
+  // (attend_few.cu may start; it waits for this kernel's end before it reads its parts)
+  if (a.prefix_units) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- set up ------------------------------------------------------------------------
   if (tid == 0) {
@@ -511,6 +532,8 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         issue_s(0, 0, !two);
         if (two) issue_s(1, 0, true);
       }
+      // (both tiles written out: a loop over them takes the descriptors out of the uniform
+      // registers, and 8 % longer)
       for (int at = 0; ok && at < ntiles; ++at) {
         const int st = at & 1, nx = (at + 1) & 1;
         const bool more = at + 1 < ntiles;
@@ -569,7 +592,12 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     const int r = tile * kTile + lr;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + tile * kTile + kHalf * half, tO = tl + 2 * kTile + tile * kTile;
-    const int pair = 1 + tile * 4 + (warp & 3);  // named barrier of warps w and w + 4
+    // The two warps of a row, w and w + 4, meet at a named barrier (an mbarrier, with its
+    // limit on waiting, made a tile of keys 13 % longer).  It cannot be left waiting: a warp
+    // whose wait runs out goes on through all tiles, with every wait at once given up, and
+    // writes nothing.
+    const int pair = 1 + tile * 4 + (warp & 3);
+    auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     const float c = fabsf(a.scale) * kLog2e;
     const int rho = min(r0 + r, rows_end - 1), tok = rho / G, node = tok - first;
     const bool live = r < rows;
@@ -577,16 +605,11 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     float mref = -INFINITY, l = 0.f;   // of c s; l: this half's
     bool poison = false;
     if (tile == 0 || two) {
-      for (int i = i0; ok && i < i1; ++i) {
+      for (int i = i0; i < i1; ++i) {
         const int at = i - i0;
         int seg, j0, len;
         tile_of(i, seg, j0, len);
-        ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns);
-        if (!ok) {  // (the other warp may be at its exchanges already: it is not left there)
-          for (int e = at == 0 ? 3 : 1; e > 0; --e)
-            asm volatile("bar.arrive %0, 64;" ::"r"(pair) : "memory");
-          break;
-        }
+        ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns) && ok;
         tc_fence_after_sync();
         const int valid = len - j0;
         const bool masked = seg == kOwn || valid < kTile;
@@ -614,9 +637,9 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         if (at == 0) {  // the first tile's own maximum, so that its weights are made once
           const float mine = masked ? largest<true>(tS, c, w) : largest<false>(tS, c, w);
           S->top[tile][half][lr] = mine;
-          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+          meet();
           mref = fmaxf(mine, S->top[tile][half ^ 1][lr]);
-          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+          meet();
         }
         uint32_t pk[2][16];
         float sum;
@@ -631,7 +654,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
           // the row's maximum, over base: the other half's beside this one's
           // (NaN scores: fmaxf drops them here; their weights and sums are NaN)
           S->top[tile][half][lr] = mine;
-          asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+          meet();
           const float top = fmaxf(mine, S->top[tile][half ^ 1][lr]);
           const bool grow = top > (mref == -INFINITY ? -INFINITY : kGrow);
           if (!__any_sync(0xffffffffu, grow)) break;
@@ -639,8 +662,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
           const float keep = grow ? (mref == -INFINITY ? 0.f : ex2(-top)) : 1.f;
           if (at > 0) {
             // O of the tiles before is complete once their last product is
-            ok = wait_warp(&S->pvdone[tile], (at - 1) & 1, S, limit_ns);
-            if (!ok) break;
+            ok = wait_warp(&S->pvdone[tile], (at - 1) & 1, S, limit_ns) && ok;
             tc_fence_after_sync();
 #pragma unroll 1
             for (int e = 0; e < DP / 32; ++e) {  // this half's columns of O, 16 at a time
@@ -657,14 +679,12 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
           l *= keep;
           mref = to;
         }
-        if (!ok) break;
         tmem_st_16(tS, pk[0]);
         tmem_st_16(tS + 16, pk[1]);
         l += sum;
         if (seg == kOwn) {
           // (the V tile is read behind its barrier: its bits are written by then)
-          ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns);
-          if (!ok) break;
+          ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns) && ok;
 #pragma unroll
           for (int e = 0; e < 2; ++e) poison |= (w[e] & S->badv[at & 1][2 * half + e]) != 0u;
         }
@@ -904,6 +924,8 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   t.slot0 = p.prefix_splits;
   t.splits = p.seq_splits;
   t.tiles = p.seq_tiles;
+  t.by_length = d.B > 1 && d.B <= kMaxSorted && p.seq_splits == 1 &&
+                (long long)d.B * d.Hkv * p.seq_tiles > sm_count();
   err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits);
   if (err != cudaSuccess || !p.slots) return err;
   const int groups = (int)(((long long)d.N * d.Hq + 7) / 8);
