@@ -44,7 +44,7 @@ constexpr int kSoftmax = 512;             // softmax threads: two a row
 constexpr int kThreads = kSoftmax + 3 * 32;
 constexpr int kWarpK = kSoftmax / 32, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 constexpr int kHalf = kTile / 2;
-constexpr int kMaxSorted = 256;          // sequences that every unit may rank by length
+constexpr int kMaxSorted = 64;           // sequences that every warp may rank by length
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
@@ -69,8 +69,11 @@ struct TcArgs {
   bool with_prefix;    // a sequence's units include the prefix
   int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
   bool own_box;        // the tree's own rows come by TMA
+  bool q_box;          // Q too: G divides a tile, and the scale is not negative
   bool by_length;      // units of long contexts first (more units than SMs, kMaxSorted sequences at most)
 };
+
+constexpr uint32_t kBarBytes = 5120;
 
 template <int DP>
 struct Smem {
@@ -81,15 +84,16 @@ struct Smem {
   static constexpr uint32_t OFF_V = OFF_K + 2 * kKV;
   static constexpr uint32_t OFF_PARENT = OFF_V + 2 * kKV;
   static constexpr uint32_t OFF_BAR = OFF_PARENT + kMaxNLong * 4;
-  static constexpr uint32_t kBytes = OFF_BAR + 4096 + 1024;  // + alignment slack
+  static constexpr uint32_t kBytes = OFF_BAR + kBarBytes + 1024;  // + alignment slack
 };
 
 struct Bars {
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2], vraw, ready, drain;
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2];
+  uint64_t vraw, ready, qfull, drain;
   uint32_t tmem;
   int abort;
-  int unit_b;
-  float top[2][2][kTile];  // a row's maximum over each half of a tile
+  float top[2][2][kTile];  // a row's maximum over each half of a tile; at the end its sums
+  int poison[2][2][kTile];  // whether the half saw values that are not finite
   uint32_t badv[2][4];  // own rows of a V tile that hold infinities or NaN (by stage)
 };
 
@@ -248,7 +252,32 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
-static_assert(sizeof(Bars) <= 4096, "the barriers fit their place");
+static_assert(sizeof(Bars) <= kBarBytes, "the barriers fit their place");
+
+// The sequence that comes `want`-th when the longest contexts come first (ties in order): each
+// warp ranks them for itself, two a lane.  Long units first, the SMs end closer together.
+__device__ __forceinline__ int ranked(const int32_t* ctx, int B, int want, int lane) {
+  const int none = -2147483647 - 1;
+  const int x0 = lane < B ? ctx[lane] : none, x1 = lane + 32 < B ? ctx[lane + 32] : none;
+  int r0 = 0, r1 = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const int y = __shfl_sync(0xffffffffu, x0, j);
+    r0 += y > x0 || (y == x0 && j < lane);
+    r1 += y >= x1;
+  }
+  if (B > 32) {
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+      const int y = __shfl_sync(0xffffffffu, x1, j);
+      r0 += y > x0;
+      r1 += y > x1 || (y == x1 && j < lane);
+    }
+  }
+  const uint32_t m0 = __ballot_sync(0xffffffffu, lane < B && r0 == want);
+  const uint32_t m1 = __ballot_sync(0xffffffffu, lane + 32 < B && r1 == want);
+  return m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+}
 
 enum Segment { kPrefix = 0, kContext = 1, kOwn = 2 };
 
@@ -283,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapV,
                  const __grid_constant__ CUtensorMap mapKo,
-                 const __grid_constant__ CUtensorMap mapVo, uint64_t limit_ns) {
+                 const __grid_constant__ CUtensorMap mapVo,
+                 const __grid_constant__ CUtensorMap mapQ, uint64_t limit_ns) {
   using L = Smem<DP>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -301,20 +331,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   u /= a.tiles;
   const int hk = u % d.Hkv;
   int b = u / d.Hkv;  // (prefix units: 0)
-  if (a.by_length) {  // the longest contexts first: the SMs end closer together
-    int* len = sParent;
-    if (tid < d.B) len[tid] = a.ctx[tid];
-    __syncthreads();
-    if (tid < d.B) {
-      const int mine = len[tid];
-      int rank = 0;
-      for (int j = 0; j < d.B; ++j) rank += len[j] > mine || (len[j] == mine && j < tid);
-      if (rank == b) S->unit_b = tid;
-    }
-    __syncthreads();
-    b = S->unit_b;
-    __syncthreads();
-  }
+  if (a.by_length) b = ranked(a.ctx, d.B, b, lane);
   int first = 0, n = 0, ctx = 0;
   if (!a.prefix_units) {
     const int stop = a.cu[b + 1];
@@ -368,6 +385,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       mbar_init(&S->lsum[s], kSoftmax / 64);
     }
     mbar_init(&S->vraw, 1);
+    mbar_init(&S->qfull, 1);
     mbar_init(&S->ready, kSoftmax / 32);  // Q and the tree are in shared memory
     mbar_init(&S->drain, 1);
     S->abort = 0;
@@ -492,6 +510,15 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   } else if (warp == kWarpMma) {
     // ---- MMAs: the warp waits together, one lane issues ---------------------------------
     if (ntiles > 0) {
+      if (a.q_box && elect_one()) {  // (rows past the unit's are somebody's, and not used)
+        mbar_arrive_expect_tx(&S->qfull, (two ? 2 : 1) * L::kQ);
+        for (int x = 0; x < (two ? 2 : 1); ++x)
+#pragma unroll
+          for (int c = 0; c < DP / 64; ++c)
+            tma_load_3d(smem + L::OFF_Q + x * L::kQ + c * kSw128TileBytes, &mapQ, &S->qfull, 64 * c,
+                        hk * G, (r0 + x * kTile) / G);
+      }
+      __syncwarp();
       constexpr uint32_t idS = idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t idO = idesc_bf16_f32_bmn(kTile, DP);
       const uint64_t dQ = desc_sw128_kmajor(smem_addr(smem + L::OFF_Q));
@@ -527,7 +554,8 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         }
         __syncwarp();
       };
-      bool ok = wait_warp(&S->ready, 0, S, limit_ns) && wait_warp(&S->kfull[0], 0, S, limit_ns);
+      bool ok = wait_warp(a.q_box ? &S->qfull : &S->ready, 0, S, limit_ns) &&
+                wait_warp(&S->kfull[0], 0, S, limit_ns);
       if (ok) {
         issue_s(0, 0, !two);
         if (two) issue_s(1, 0, true);
@@ -566,7 +594,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     // the tree (a parent that is not earlier is an error; taken as a root meanwhile)
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll 4
-    for (int e = tid; e < 2 * kTile * (DP / 8); e += kSoftmax) {
+    for (int e = tid; !a.q_box && e < 2 * kTile * (DP / 8); e += kSoftmax) {
       const int r = e / (DP / 8), c8 = e % (DP / 8);
       uint4 x = make_uint4(0, 0, 0, 0);
       if (r < rows && 8 * c8 < d.D) {
@@ -696,18 +724,21 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         ok = wait_warp(&S->pvdone[tile], (ntiles - 1) & 1, S, limit_ns);
         tc_fence_after_sync();
       }
-      // the row's sum: both halves' (the exchange goes through the Q tiles, read by now)
-      float* sL = reinterpret_cast<float*>(smem + L::OFF_Q) + tile * 4 * kTile;
-      int* sPoison = reinterpret_cast<int*>(sL + 2 * kTile);
-      sL[half * kTile + lr] = l;
-      sPoison[half * kTile + lr] = poison;
+      // the row's sum: both halves'
+      S->top[tile][half][lr] = l;
+      S->poison[tile][half][lr] = poison;
       mbar_arrive_warp(&S->lsum[tile]);
       ok = wait_warp(&S->lsum[tile], 0, S, limit_ns) && ok;
-      l = sL[lr] + sL[kTile + lr];
+      l = S->top[tile][0][lr] + S->top[tile][1][lr];
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (l NaN: kept)
-      const size_t out = (size_t)tok * d.Hq + hk * G + (rho - tok * G);
-      const size_t slot = (size_t)(a.slot0 + split) * d.T * d.Hq + out;
+      const int out = tok * d.Hq + hk * G + (rho - tok * G);
+      const size_t slot0 = (size_t)(a.slot0 + split) * d.T * d.Hq, slot = slot0 + out;
       if (ok) {
+        // 32 columns of a warp's 32 rows at a time through shared memory (Q and the first K
+        // tiles, which every product has read by now), so that a store covers whole pieces
+        // of rows; a lane a row would touch 32 lines an instruction
+        unsigned char* stage = smem + L::OFF_Q + warp * 4096;
+        const int row0 = tile * kTile + 32 * (warp & 3);  // the warp's first row of the unit
 #pragma unroll 1
         for (int e = 0; e < DP / 64; ++e) {
           const int col = DP / 2 * half + 32 * e;
@@ -720,25 +751,40 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
-          if (live && a.part_o) {
-            float* po = a.part_o + slot * d.D + col;
+          if (a.part_o) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              if (col + j < d.D)
-                *reinterpret_cast<float4*>(po + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-          } else if (live) {
-            __nv_bfloat16* oo = a.o + out * d.D + col;
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                  make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (col + j < d.D)
-                *reinterpret_cast<uint4*>(oo + j) =
-                    make_uint4(pack_bf16(y[j], y[j + 1]), pack_bf16(y[j + 2], y[j + 3]),
-                               pack_bf16(y[j + 4], y[j + 5]), pack_bf16(y[j + 6], y[j + 7]));
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3), j = lane & 7;
+              const int to = __shfl_sync(0xffffffffu, out, rr);
+              if (row0 + rr < rows && col + 4 * j < d.D)
+                *reinterpret_cast<float4*>(a.part_o + (slot0 + to) * d.D + col + 4 * j) =
+                    *reinterpret_cast<const float4*>(stage + rr * 128 + ((j ^ (rr & 7)) << 4));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(pack_bf16(y[8 * j], y[8 * j + 1]), pack_bf16(y[8 * j + 2], y[8 * j + 3]),
+                             pack_bf16(y[8 * j + 4], y[8 * j + 5]), pack_bf16(y[8 * j + 6], y[8 * j + 7]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rr = 8 * i + (lane >> 2), j = lane & 3;
+              const int to = __shfl_sync(0xffffffffu, out, rr);
+              if (row0 + rr < rows && col + 8 * j < d.D)
+                *reinterpret_cast<uint4*>(a.o + (size_t)to * d.D + col + 8 * j) =
+                    *reinterpret_cast<const uint4*>(stage + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
+            }
           }
           __syncwarp();
         }
         // (either half may have seen them)
-        if (sPoison[lr] + sPoison[kTile + lr] != 0 && live)
+        if ((S->poison[tile][0][lr] | S->poison[tile][1][lr]) != 0 && live)
           add_nonfinite(a, out, slot, first, node, hk, DP / 2 * half, DP / 2 * (half + 1));
         if (live && half == 0) {
           const float z = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
@@ -845,7 +891,7 @@ size_t part_floats(const gdn_tree_attend_dims& d, const Plan& p) {
 }
 
 template <int DP>
-cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[4], long long blocks,
+cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[5], long long blocks,
                          cudaStream_t stream) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP>,
@@ -853,7 +899,7 @@ cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[4], long long
                                          Smem<DP>::kBytes);
   if (err != cudaSuccess) return err;
   attend_tc_kernel<DP><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
-      t, map[0], map[1], map[2], map[3], wait_hooks().limit_ns);
+      t, map[0], map[1], map[2], map[3], map[4], wait_hooks().limit_ns);
   return cudaGetLastError();
 }
 
@@ -891,7 +937,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     t.part_lse = t.part_o + part_floats(d, p);
   }
   // cache tiles by TMA where pages and tiles divide one another
-  CUtensorMap map[4];
+  CUtensorMap map[5];
   memset(map, 0, sizeof map);
   const int box = d.page_size < kTile ? d.page_size : kTile;
   const long long cache_rows = (long long)d.n_pages * d.page_size;
@@ -903,6 +949,9 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   t.own_box = d.D % 64 == 0 && a.k &&
               encode_head_rows_map(&map[2], a.k, d.T, d.Hkv, d.D, kTile) &&
               encode_head_rows_map(&map[3], a.v, d.T, d.Hkv, d.D, kTile);
+  const int G = d.Hq / d.Hkv;
+  t.q_box = d.D % 64 == 0 && kTile % G == 0 && a.scale >= 0.f &&
+            encode_q_map(&map[4], a.q, d.T, d.Hq, d.D, G, kTile / G);
   auto units = [&](const TcArgs& x, long long blocks) {
     return d.D <= 64 ? launch_units<64>(x, map, blocks, stream)
                      : launch_units<128>(x, map, blocks, stream);
@@ -915,9 +964,11 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits);
     if (err != cudaSuccess) return err;
   }
-  // sequences of few rows, with the prefix's parts added up on the spot
-  err = launch_attend_few(a, p.shared ? 0 : d.prefix_len, t.part_o, t.part_lse, p.prefix_splits,
-                          stream);
+  // sequences of few rows, with the prefix's parts added up on the spot (there are none where
+  // all have N rows, and N are many)
+  if (!p.many || d.T < (long long)d.B * d.N)
+    err = launch_attend_few(a, p.shared ? 0 : d.prefix_len, t.part_o, t.part_lse, p.prefix_splits,
+                            stream);
   if (err != cudaSuccess || !p.many) return err;
   t.prefix_units = false;
   t.with_prefix = !p.shared;

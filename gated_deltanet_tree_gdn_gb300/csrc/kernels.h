@@ -141,6 +141,9 @@ bool encode_state_map(CUtensorMap* map, const float* base, long long n_states);
 // boxes of 64 columns x one head x box_rows rows
 bool encode_head_rows_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
                           int box_rows);
+// the same with boxes of box_heads heads of each of box_rows rows, in that order
+bool encode_q_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
+                  int box_heads, int box_rows);
 
 bool verify_tc_supported(const gdn_tree_dims& d);
 cudaError_t launch_verify_tc(const VerifyArgs& a, cudaStream_t stream);

@@ -1234,17 +1234,27 @@ bool encode_state_map(CUtensorMap* map, const float* base, long long n_states) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_head_rows_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
-                          int box_rows) {
+static bool encode_rows(CUtensorMap* map, const void* base, long long rows, int heads, int width,
+                        int box_heads, int box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)heads * width * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_head_rows_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
+                          int box_rows) {
+  return encode_rows(map, base, rows, heads, width, 1, box_rows);
+}
+
+bool encode_q_map(CUtensorMap* map, const void* base, long long rows, int heads, int width,
+                  int box_heads, int box_rows) {
+  return encode_rows(map, base, rows, heads, width, box_heads, box_rows);
 }
 
 bool verify_tc_supported(const gdn_tree_dims& d) {
