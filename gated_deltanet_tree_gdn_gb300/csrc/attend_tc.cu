@@ -44,7 +44,7 @@ constexpr int kSoftmax = 512;             // softmax threads: two a row
 constexpr int kThreads = kSoftmax + 3 * 32;
 constexpr int kWarpK = kSoftmax / 32, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 constexpr int kHalf = kTile / 2;
-constexpr int kMaxSorted = 64;           // sequences that every warp may rank by length
+constexpr int kMaxSorted = 64;           // sequences that a unit may rank by length
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
@@ -90,6 +90,7 @@ struct Smem {
 struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], pvdone[2], lsum[2];
   uint64_t vraw, ready, qfull, drain;
+  int4 unit;  // the sequence, its first row and the one after its last, its context
   uint32_t tmem;
   int abort;
   float top[2][2][kTile];  // a row's maximum over each half of a tile; at the end its sums
@@ -130,34 +131,32 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
-// 64 consecutive fp32 columns of this warp's 32 lanes, in two loads and one wait
-__device__ __forceinline__ void tmem_ld_64(uint32_t taddr, float (&v)[2][32]) {
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=f"(v[e][0]), "=f"(v[e][1]), "=f"(v[e][2]), "=f"(v[e][3]), "=f"(v[e][4]),
-          "=f"(v[e][5]), "=f"(v[e][6]), "=f"(v[e][7]), "=f"(v[e][8]), "=f"(v[e][9]),
-          "=f"(v[e][10]), "=f"(v[e][11]), "=f"(v[e][12]), "=f"(v[e][13]), "=f"(v[e][14]),
-          "=f"(v[e][15]), "=f"(v[e][16]), "=f"(v[e][17]), "=f"(v[e][18]), "=f"(v[e][19]),
-          "=f"(v[e][20]), "=f"(v[e][21]), "=f"(v[e][22]), "=f"(v[e][23]), "=f"(v[e][24]),
-          "=f"(v[e][25]), "=f"(v[e][26]), "=f"(v[e][27]), "=f"(v[e][28]), "=f"(v[e][29]),
-          "=f"(v[e][30]), "=f"(v[e][31])
-        : "r"(taddr + 32 * e));
-  // (the values pass through the wait, so that nothing uses them before it)
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[e][0]), "+f"(v[e][1]), "+f"(v[e][2]), "+f"(v[e][3]), "+f"(v[e][4]),
-                   "+f"(v[e][5]), "+f"(v[e][6]), "+f"(v[e][7]), "+f"(v[e][8]), "+f"(v[e][9]),
-                   "+f"(v[e][10]), "+f"(v[e][11]), "+f"(v[e][12]), "+f"(v[e][13]),
-                   "+f"(v[e][14]), "+f"(v[e][15]), "+f"(v[e][16]), "+f"(v[e][17]),
-                   "+f"(v[e][18]), "+f"(v[e][19]), "+f"(v[e][20]), "+f"(v[e][21]),
-                   "+f"(v[e][22]), "+f"(v[e][23]), "+f"(v[e][24]), "+f"(v[e][25]),
-                   "+f"(v[e][26]), "+f"(v[e][27]), "+f"(v[e][28])
-                 :: "memory");
+// starts loading 32 consecutive fp32 columns of this warp's 32 lanes; tmem_ld_wait before use
+__device__ __forceinline__ void tmem_ld_start(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+// (the values pass through the wait, so that nothing uses them before it)
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14])
+               :: "memory");
+  asm volatile(""
+               : "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
+                 "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]),
+                 "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+               :: "memory");
+  asm volatile("" : "+f"(v[30]), "+f"(v[31])::"memory");
 }
 
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool take) {
@@ -201,9 +200,11 @@ template <bool kMasked>
 __device__ __forceinline__ void weights(uint32_t tS, float c, float base, const uint32_t (&w)[2],
                                         float& top, float& total, uint32_t (&pk)[2][16]) {
   float x[2][32], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-  tmem_ld_64(tS, x);
+  tmem_ld_start(tS, x[0]);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
+    tmem_ld_wait(x[e]);
+    if (e == 0) tmem_ld_start(tS + 32, x[1]);  // (comes while the first half is worked on)
 #pragma unroll
     for (int j = 0; j < 32; j += 2) fma2(x[e][j], x[e][j + 1], c, -base);
     if (kMasked) {
@@ -254,11 +255,15 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
 
 static_assert(sizeof(Bars) <= kBarBytes, "the barriers fit their place");
 
-// The sequence that comes `want`-th when the longest contexts come first (ties in order): each
-// warp ranks them for itself, two a lane.  Long units first, the SMs end closer together.
-__device__ __forceinline__ int ranked(const int32_t* ctx, int B, int want, int lane) {
+// The sequence that comes `want`-th when the longest contexts come first (ties in order), and
+// its rows and length: a warp ranks two a lane.  Long units first, the SMs end closer together.
+__device__ __forceinline__ int ranked(const int32_t* ctx, const int32_t* cu, int B, int want,
+                                      int lane, int& first, int& stop, int& len) {
   const int none = -2147483647 - 1;
-  const int x0 = lane < B ? ctx[lane] : none, x1 = lane + 32 < B ? ctx[lane + 32] : none;
+  const bool on0 = lane < B, on1 = lane + 32 < B;
+  const int f0 = on0 ? cu[lane] : 0, e0 = on0 ? cu[lane + 1] : 0;
+  const int f1 = on1 ? cu[lane + 32] : 0, e1 = on1 ? cu[lane + 33] : 0;
+  const int x0 = on0 ? ctx[lane] : none, x1 = on1 ? ctx[lane + 32] : none;
   int r0 = 0, r1 = 0;
 #pragma unroll 8
   for (int j = 0; j < 32; ++j) {
@@ -274,9 +279,13 @@ __device__ __forceinline__ int ranked(const int32_t* ctx, int B, int want, int l
       r1 += y > x1 || (y == x1 && j < lane);
     }
   }
-  const uint32_t m0 = __ballot_sync(0xffffffffu, lane < B && r0 == want);
-  const uint32_t m1 = __ballot_sync(0xffffffffu, lane + 32 < B && r1 == want);
-  return m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
+  const uint32_t m0 = __ballot_sync(0xffffffffu, on0 && r0 == want);
+  const uint32_t m1 = __ballot_sync(0xffffffffu, on1 && r1 == want);
+  const int at = (m0 ? __ffs(m0) : __ffs(m1)) - 1;
+  first = __shfl_sync(0xffffffffu, m0 ? f0 : f1, at);
+  stop = __shfl_sync(0xffffffffu, m0 ? e0 : e1, at);
+  len = __shfl_sync(0xffffffffu, m0 ? x0 : x1, at);
+  return m0 ? at : at + 32;
 }
 
 enum Segment { kPrefix = 0, kContext = 1, kOwn = 2 };
@@ -330,24 +339,62 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   const int t = u % a.tiles;
   u /= a.tiles;
   const int hk = u % d.Hkv;
-  int b = u / d.Hkv;  // (prefix units: 0)
-  if (a.by_length) b = ranked(a.ctx, d.B, b, lane);
-  int first = 0, n = 0, ctx = 0;
-  if (!a.prefix_units) {
-    const int stop = a.cu[b + 1];
-    first = a.cu[b];
-    n = stop - first;
-    ctx = a.ctx[b];
-    const long long cap = (long long)d.table_width * d.page_size;
-    if (first < 0 || n < 0 || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
-      if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
-      return;
+  // the sequence is found by one warp while others set up
+  if (warp == 0 && !a.prefix_units) {
+    int b = u / d.Hkv, first, stop, ctx;
+    if (a.by_length) {
+      b = ranked(a.ctx, a.cu, d.B, b, lane, first, stop, ctx);
+    } else {
+      stop = a.cu[b + 1];
+      first = a.cu[b];
+      ctx = a.ctx[b];
     }
-    if (n * G <= kAttendFewRows) return;  // (attend_few.cu's)
+    if (lane == 0) S->unit = make_int4(b, first, stop, ctx);
+  }
+  if (tid == 32) {
+    if (a.prefix_units) S->unit = make_int4(0, 0, 0, 0);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&S->kfull[s], 1);
+      mbar_init(&S->kempty[s], 1);
+      mbar_init(&S->vfull[s], 1);
+      mbar_init(&S->vempty[s], 1);
+      mbar_init(&S->sfull[s], 1);
+      mbar_init(&S->pready[s], kSoftmax / 64);  // (warps)
+      mbar_init(&S->pvdone[s], 1);
+      mbar_init(&S->lsum[s], kSoftmax / 64);
+    }
+    mbar_init(&S->vraw, 1);
+    mbar_init(&S->qfull, 1);
+    mbar_init(&S->ready, kSoftmax / 32);  // Q and the tree are in shared memory
+    mbar_init(&S->drain, 1);
+    S->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&S->tmem, 512);
+  // (attend_few.cu may start; it waits for this kernel's end before it reads its parts)
+  if (a.prefix_units) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = S->tmem;
+  constexpr uint32_t kStage = L::kKV;
+  const int b = S->unit.x, first = S->unit.y, n = S->unit.z - first, ctx = S->unit.w;
+  bool mine = true;  // the unit has rows, and they are this kernel's
+  if (!a.prefix_units) {
+    const long long cap = (long long)d.table_width * d.page_size;
+    if (first < 0 || n < 0 || S->unit.z > d.T || n > d.N || ctx < 0 || ctx > cap) {
+      if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+      mine = false;
+    } else {
+      mine = n * G > kAttendFewRows;  // (else attend_few.cu's)
+    }
   }
   const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
   const int r0 = first * G + t * 2 * kTile;
-  if (r0 >= rows_end) return;
+  if (!mine || r0 >= rows_end) {
+    if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    return;
+  }
   const int rows = min(2 * kTile, rows_end - r0);
   const bool two = rows > kTile;
   const bool own = a.k != nullptr && !a.prefix_units;
@@ -368,35 +415,6 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     else if (i < nP + nC) { seg = kContext; j0 = (i - nP) * kTile; len = ctx; }
     else { seg = kOwn; j0 = (all - 1 - i) * kTile; len = seen; }
   };
-
-  // (attend_few.cu may start; it waits for this kernel's end before it reads its parts)
-  if (a.prefix_units) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-  // ---- set up ------------------------------------------------------------------------
-  if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&S->kfull[s], 1);
-      mbar_init(&S->kempty[s], 1);
-      mbar_init(&S->vfull[s], 1);
-      mbar_init(&S->vempty[s], 1);
-      mbar_init(&S->sfull[s], 1);
-      mbar_init(&S->pready[s], kSoftmax / 64);  // (warps)
-      mbar_init(&S->pvdone[s], 1);
-      mbar_init(&S->lsum[s], kSoftmax / 64);
-    }
-    mbar_init(&S->vraw, 1);
-    mbar_init(&S->qfull, 1);
-    mbar_init(&S->ready, kSoftmax / 32);  // Q and the tree are in shared memory
-    mbar_init(&S->drain, 1);
-    S->abort = 0;
-    mbar_fence_init();
-  }
-  if (warp == kWarpMma) tmem_alloc(&S->tmem, 512);
-  tc_fence_before_sync();
-  __syncthreads();
-  tc_fence_after_sync();
-  const uint32_t tmem = S->tmem;
-  constexpr uint32_t kStage = L::kKV;
 
   if (warp == kWarpK || warp == kWarpV) {
     // ---- producers: K or V --------------------------------------------------------------
@@ -750,7 +768,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
             for (int j = 0; j < 32; ++j) y[j] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : y[j] * inv;
+          for (int j = 0; j < 32; ++j) y[j] *= inv;
           if (a.part_o) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
