@@ -32,8 +32,9 @@ namespace {
 
 constexpr int kRows = kAttendFewRows;
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kMaxCluster = 8;
-constexpr int kStages = 3;
+constexpr int kMaxCluster = 16;  // (over 8: not portable, asked for at the launch)
+constexpr int kPerSm = 3;
+constexpr int kStages = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -82,25 +83,32 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
 // before theirs.)
 __device__ __forceinline__ void prefix_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Where the 16 bytes `chunk` of a row of a K or V tile are: eight lanes that read at once, a
+// quarter of two rows (K) or two chunks of every other row (V), then find them in all banks.
+__device__ __forceinline__ int place(int row, int chunk) {
+  return 8 * (chunk ^ ((row & 6) ^ ((row & 1) << 2)));
+}
+
 template <int DP>
 struct Shared {
-  static constexpr int kLd = DP + 8;  // (rows 16 bytes apart in the banks)
   union {
-    __nv_bfloat16 ring[kWarps][kStages][2][16][kLd];  // K and V tiles
-    float O[kWarps][kRows][DP + 4];  // then the warps' sums; [0] then holds the CTA's
+    __nv_bfloat16 ring[kWarps][kStages][2][16][DP];  // K and V tiles (`place`)
+    struct {  // then
+      float O[kWarps][kRows][DP + 4];    // the warps' sums; [0] then holds the CTA's
+      float wp[kRows][kAttendMaxParts];  // weight of each part of the prefix in the result
+    };
   };
   uint4 q[DP / 32][2][32];         // Q as the MMAs take it: a lane's 16 bytes each
   float m[kWarps][kRows], l[kWarps][kRows];
   float cm[kRows], cl[kRows];      // the CTA's maximum and sum
   float w[kRows][kMaxCluster];     // weight of each CTA's sums in the result
-  float wp[kRows][kAttendMaxParts];  // and of each part of the prefix
   float scale[kRows];              // 1 / L
   uint32_t bad;                    // own nodes whose values hold infinities or NaN
   int32_t parent[kRows];
 };
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kPerSm)
 attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
                   const __nv_bfloat16* __restrict__ v, const int32_t* __restrict__ parent,
                   const int32_t* __restrict__ cu, const __nv_bfloat16* __restrict__ k_cache,
@@ -198,8 +206,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
         const int x = __shfl_sync(0xffffffffu, row, i + sub);
         const bool take = x >= 0 && 8 * ch < d.D;
         const size_t off = take ? x * stride : 0;
-        cp_async16_zfill(&S.ring[warp][stage][0][i + sub][8 * ch], take ? kb + off : kb, take);
-        cp_async16_zfill(&S.ring[warp][stage][1][i + sub][8 * ch], take ? vb + off : vb, take);
+        cp_async16_zfill(&S.ring[warp][stage][0][i + sub][place(i + sub, ch)], take ? kb + off : kb, take);
+        cp_async16_zfill(&S.ring[warp][stage][1][i + sub][place(i + sub, ch)], take ? vb + off : vb, take);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -239,8 +247,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
       there_of[kStages - 2] = __ballot_sync(0xffffffffu, row >= 0);
       fetch(ahead, row, stage == 0 ? kStages - 1 : stage - 1);
     }
-    const __nv_bfloat16(*kt)[Shared<DP>::kLd] = S.ring[warp][stage][0];
-    const __nv_bfloat16(*vt)[Shared<DP>::kLd] = S.ring[warp][stage][1];
+    const __nv_bfloat16(*kt)[DP] = S.ring[warp][stage][0];
+    const __nv_bfloat16(*vt)[DP] = S.ring[warp][stage][1];
     stage = stage == kStages - 1 ? 0 : stage + 1;
     float s[2][4] = {};
 #pragma unroll
@@ -248,7 +256,7 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
       const uint4 q0 = S.q[i][0][lane], q1 = S.q[i][1][lane];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint4 x = *reinterpret_cast<const uint4*>(&kt[r8 + 8 * e][32 * i + 8 * c]);
+        const uint4 x = *reinterpret_cast<const uint4*>(&kt[r8 + 8 * e][place(r8, 4 * i + c)]);
         mma_16816(s[e], q0, x.x, x.y);
         mma_16816(s[e], q1, x.z, x.w);
       }
@@ -258,12 +266,21 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = 8 * e + 2 * c + (i & 1);
-        const bool on = ((mine ? there & sees[i >> 1] : there) >> key) & 1u;
-        s[e][i] = on ? cs * s[e][i] : -INFINITY;
-        top[i >> 1] = fmaxf(top[i >> 1], s[e][i]);
-      }
+      for (int i = 0; i < 4; ++i) s[e][i] *= cs;
+    if (mine || there != 0xffffu) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = 8 * e + 2 * c + (i & 1);
+          const bool on = ((mine ? there & sees[i >> 1] : there) >> key) & 1u;
+          if (!on) s[e][i] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[e][i]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
@@ -301,7 +318,7 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int key = 2 * c + (e & 1) + 8 * (e >> 1);
-        x[e] = *reinterpret_cast<const uint4*>(&vt[key][64 * h + 8 * r8]);
+        x[e] = *reinterpret_cast<const uint4*>(&vt[key][place(key, 8 * h + r8)]);
         // own nodes are masked for some rows only: what is not finite is kept out of the
         // product (0 * inf) and added to the rows that see it at the end
         if (mine && n > 1 &&
@@ -467,6 +484,9 @@ cudaError_t launch_dp(const AttendArgs& a, int plen, const float* part_o, const 
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(Shared<DP>));
   if (err != cudaSuccess) return err;
+  if (cluster > 8)
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err != cudaSuccess) return err;
   const long long blocks = (long long)d.B * d.Hkv * cluster;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -493,17 +513,34 @@ cudaError_t launch_dp(const AttendArgs& a, int plen, const float* part_o, const 
 
 }  // namespace
 
+// How many CTAs take a sequence and key head, and about how long that takes in us.  The CTAs
+// run in rounds of kPerSm an SM.  64 keys (32 KB of 128-wide heads) take a CTA 1.3, 1.5 or
+// 2.4 us where 1, 2 or 3 of them share the SM, and its start and end about twice that.
+// Measured with 8 key heads and one of 4096 keys a sequence, in us by CTAs a unit: 16
+// sequences 1: 84, 2: 57, 4: 73, 8: 69; 32 sequences 97, 131, 113, 130; 64 sequences 234,
+// 205, 192, 238; one sequence of 8192 keys 150, 84, 45, 26, and 21 with 16.
+int attend_few_cluster(const gdn_tree_attend_dims& d, int prefix_len, float* us) {
+  constexpr float kUs[kPerSm + 1] = {0.f, 1.3f, 1.5f, 2.4f};
+  const long long sms = sm_count() > 0 ? sm_count() : 152, slots = kPerSm * sms;
+  const long long units = (long long)d.B * d.Hkv;
+  const long long keys = (long long)d.table_width * d.page_size + d.N + prefix_len;
+  int best = 1;
+  for (int C = 1; C <= kMaxCluster; C *= 2) {
+    const long long full = units * C / slots, rest = units * C - full * slots;
+    const long long rounds = (keys + 16 * kWarps * C - 1) / (16 * kWarps * C);
+    const float t = (full * kUs[kPerSm] + kUs[(rest + sms - 1) / sms]) * (rounds + 2);
+    if (C > 1 && t >= *us) continue;
+    best = C;
+    *us = t;
+  }
+  return best;
+}
+
 cudaError_t launch_attend_few(const AttendArgs& a, int prefix_len, const float* part_o,
                               const float* part_lse, int parts, cudaStream_t stream) {
   const gdn_tree_attend_dims& d = a.d;
-  // CTAs a sequence and key head: as many as run at once (two an SM; half as many again
-  // are let through), as long as a warp has 16 keys to take
-  const int sms = sm_count() > 0 ? sm_count() : 152;
-  const long long units = (long long)d.B * d.Hkv;
-  const long long keys = (long long)d.table_width * d.page_size + d.N + prefix_len;
-  int cluster = 1;
-  while (cluster < kMaxCluster && units * cluster * 2 <= 3 * sms && keys > 16 * kWarps * cluster)
-    cluster *= 2;
+  float us;
+  const int cluster = attend_few_cluster(d, prefix_len, &us);
   return d.D <= 64 ? launch_dp<64>(a, prefix_len, part_o, part_lse, parts, cluster, stream)
                    : launch_dp<128>(a, prefix_len, part_o, part_lse, parts, cluster, stream);
 }

@@ -874,30 +874,60 @@ struct Plan {
   int slots = 0;           // parts of a row (0: the kernel writes o itself)
 };
 
+// Which units there are, by an estimate of the time.  A unit takes about kTileUs for each key
+// tile and kEnds tiles for its start and end, and each SM has one at a time; a part's sums are
+// written and read again, and joined by a launch of its own.
+//  - Into how many parts a unit's keys are split: what makes the last round full, as long as
+//    the ends and the join do not eat it up.  Measured: 8 units of 33 tiles, in parts of 2, 4,
+//    8 and 16 tiles: 21.5, 21.7, 25.1, 30.4 us.
+//  - Whether the prefix has units of its own, with 256 rows from several sequences each, or
+//    every sequence reads it.  Measured (32 query and 8 key heads, 512 own rows; with / without):
+//    32 sequences of 1 row, prefix of 1024 rows 25 / 50 us, of 16384 rows 43 / 475 us; of 16
+//    nodes 60 / 51 and 152 / 384 us; of 64 nodes, whose units are full, 115 / 60 and 477 / 423
+//    us; 4 sequences of 16 nodes 30 / 18 and 45 / 61 us.
 Plan plan_of(const gdn_tree_attend_dims& d) {
+  constexpr float kTileUs = 1.6f, kJoinUs = 5.f, kPartBytesPerUs = 6e6f;
+  constexpr int kEnds = 5;
   Plan p;
   p.tc = d.dtype == GDN_TREE_BF16;
   if (!p.tc) return p;
   const int sms = sm_count() > 0 ? sm_count() : 152;
   const int G = d.Hq / d.Hkv;
-  const long long rows = (long long)d.T * G;  // of a key head
-  auto tiles = [](long long r) { return (int)((r + 2 * kTile - 1) / (2 * kTile)); };
-  // the prefix gets units of its own where the sequences' rows leave its tiles half empty
-  p.shared = d.prefix_len > 0 && d.B > 1 && rows < (long long)d.B * kTile;
-  p.seq_tiles = tiles((long long)d.N * G);
-  const long long units = (long long)d.B * d.Hkv * p.seq_tiles;
-  const long long keys = (long long)d.table_width * d.page_size + d.N + (p.shared ? 0 : d.prefix_len);
-  // parts of at least 4 key tiles, until every SM has a unit
-  auto splits = [&](long long n, long long k) {
-    const long long most = (k + 4 * kTile - 1) / (4 * kTile);
-    const long long want = n >= sms ? 1 : sms / n < kAttendMaxParts ? sms / n : kAttendMaxParts;
-    return (int)(want < most ? want : most < 1 ? 1 : most);
+  const float part_us = 8.f * d.T * d.Hq * d.D / kPartBytesPerUs;
+  auto row_tiles = [](long long r) { return (int)((r + 2 * kTile - 1) / (2 * kTile)); };
+  // n units of so many keys: the parts, and the time; joined: whether there are other parts
+  auto split = [&](long long n, long long keys, bool joined, int& parts) {
+    const long long tiles = (keys + kTile - 1) / kTile;
+    float best = 0.f;
+    parts = 1;
+    for (int s = 1; s <= kAttendMaxParts && (s == 1 || s <= tiles); ++s) {
+      const float us = (float)((n * s + sms - 1) / sms) * ((tiles + s - 1) / s + kEnds) * kTileUs +
+                       (s > 1 || joined ? s * part_us : 0.f) + (s > 1 && !joined ? kJoinUs : 0.f);
+      if (s > 1 && us >= best) continue;
+      best = us;
+      parts = s;
+    }
+    return best;
   };
   p.many = (long long)d.N * G > kAttendFewRows;
-  if (p.many) p.seq_splits = splits(units, keys);
-  if (p.shared) {
-    p.prefix_tiles = tiles(rows);
-    p.prefix_splits = splits((long long)d.Hkv * p.prefix_tiles, d.prefix_len);
+  p.seq_tiles = row_tiles((long long)d.N * G);
+  const long long units = (long long)d.B * d.Hkv * p.seq_tiles;
+  const long long own = (long long)d.table_width * d.page_size + d.N;
+  float us = 0.f;  // the sequences' units read the prefix too
+  if (p.many) us = split(units, own + d.prefix_len, false, p.seq_splits);
+  if (d.prefix_len > 0 && d.B > 1) {
+    if (!p.many) attend_few_cluster(d, d.prefix_len, &us);
+    int prefix_splits, seq_splits = 0;
+    const int prefix_tiles = row_tiles((long long)d.T * G);
+    float with = split((long long)d.Hkv * prefix_tiles, d.prefix_len, true, prefix_splits), rest;
+    if (p.many) rest = split(units, own, true, seq_splits) + kJoinUs;
+    else attend_few_cluster(d, 0, &rest);
+    if (with + rest < us) {
+      p.shared = true;
+      p.prefix_tiles = prefix_tiles;
+      p.prefix_splits = prefix_splits;
+      p.seq_splits = seq_splits;
+    }
   }
   p.slots = p.prefix_splits + p.seq_splits;
   if (!p.shared && p.seq_splits <= 1) p.slots = 0;

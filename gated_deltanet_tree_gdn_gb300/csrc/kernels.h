@@ -206,6 +206,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream);
 // of the rows' keys that other units took ([parts][T * Hq][D], [parts][T * Hq]) are added
 constexpr int kAttendFewRows = 16;
 constexpr int kAttendMaxParts = 64;  // of the shared prefix
+int attend_few_cluster(const gdn_tree_attend_dims& d, int prefix_len, float* us);
 cudaError_t launch_attend_few(const AttendArgs& a, int prefix_len, const float* part_o,
                               const float* part_lse, int parts, cudaStream_t stream);
 cudaError_t launch_attend_generic(const AttendArgs& a, cudaStream_t stream);
