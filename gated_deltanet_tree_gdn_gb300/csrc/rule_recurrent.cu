@@ -314,8 +314,11 @@ cudaError_t launch_recurrent(const RuleArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// The chunked kernels from kChunkedFrom tokens of the longest sequence on.  Below it their
-// two launches and the first chunk's chain cost more than the tokens one by one.
+// The chunked kernels from kChunkedFrom tokens of the longest sequence on.  Below it their two
+// launches and a whole chunk's work cost more than the tokens one by one.  Measured with 32
+// heads, chunked and one by one: 1 sequence of 8 tokens 16.2 and 9.3 us, of 16 15.6 and 15.7, of
+// 24 15.6 and 22.5, of 64 15.8 and 55; 4 sequences of 16 27 and 22, of 24 27 and 31; 16 sequences
+// of 16 80 and 66, of 24 81 and 95, of 64 83 and 251.
 constexpr int kChunkedFrom = 17;
 static bool chunked(const gdn_tree_dims& d, int32_t T) {
   return d.N >= kChunkedFrom && T > 0 && prefill_tc_supported(d);
@@ -331,11 +334,12 @@ cudaError_t launch_prefill(const RuleArgs& a, void* workspace, cudaStream_t stre
 }
 
 cudaError_t launch_decode_step(const RuleArgs& a, cudaStream_t stream) {
-  // a state a CTA once there are two for every SM; with fewer, four CTAs a state have it
-  // sooner
+  // A state a CTA by bulk copies where there are many rounds of them, else four CTAs a state,
+  // which have it sooner.  Measured with 32 heads: 16 sequences 17.2 and 14.3 us, 64 47.8 and
+  // 46.0, 96 68.6 and 68.2, 128 87.5 and 90.2, 192 127 and 138, 256 168 and 195.
   const gdn_tree_dims& d = a.d;
   const long long units = (long long)d.B * d.Hv;
-  if (d.dv == kMaxD && units >= 2 * (sm_count() > 0 ? sm_count() : 152) && units <= 0x7fffffffll)
+  if (d.dv == kMaxD && units >= 24 * (sm_count() > 0 ? sm_count() : 152) && units <= 0x7fffffffll)
     return d.dtype == GDN_TREE_BF16 ? launch_step_bulk<__nv_bfloat16>(a, stream)
                                     : launch_step_bulk<float>(a, stream);
   return launch_recurrent(a, stream);
