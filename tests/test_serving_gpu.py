@@ -210,6 +210,52 @@ def test_decode_step(B, Hqk, Hv, dk, dv, dtype, gates):
     assert torch.equal(again, pool)  # in place
 
 
+@pytest.mark.parametrize("B,Hqk,Hv,dk,dtype", [
+    (1850, 1, 2, 128, "bf16"), (3701, 1, 1, 16, "f32"), (1000, 2, 4, 48, "bf16")])
+def test_decode_step_of_thousands_of_states(B, Hqk, Hv, dk, dtype):
+    x = rule_inputs([1] * B, Hqk, Hv, dk, 128, dtype, seed=B, gates="reset")
+    status = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    slot = ints(x["slot"])
+    o, pool = gt.decode_step(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["pool"],
+                             state_slot=slot, dev_status=status)
+    assert (status == 0).all()
+    check_rule(o, pool, x)
+    again = x["pool"].clone()
+    gt.decode_step(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], again, state_slot=slot,
+                   pool_out=again)
+    assert torch.equal(again, pool)  # in place
+    slot[5] = B + 2  # no such state: reported, and nothing else changes
+    other = torch.full_like(o, 7.0)
+    gt.decode_step(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], x["pool"], state_slot=slot,
+                   o=other, dev_status=status)
+    assert status[5] == gt.STATUS_BAD_LAYOUT and (status != 0).sum() == 1
+    assert (other[5] == 7.0).all()
+    assert torch.equal(other[:5], o[:5]) and torch.equal(other[6:], o[6:])
+
+
+def test_prefill_in_several_segments():
+    """Batches whose tiles do not fit the workspace at once give what parts of them give."""
+    lens, Hqk, Hv = [20000, 130, 0, 5000, 64], 16, 32
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    normal = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    q, k = (torch.nn.functional.normalize(normal(T, Hqk, 128), dim=-1).bfloat16() for _ in range(2))
+    v, la, beta = normal(T, Hv, 128).bfloat16(), -normal(T, Hv).abs(), torch.sigmoid(normal(T, Hv))
+    pool = 0.1 * normal(len(lens), Hv, 128, 128)
+    cu = cu_of(lens)
+    dims = gt.Dims(len(lens), max(lens), Hqk, Hv, 128, 128, gt.BF16)
+    assert gt.prefill_workspace(dims, T) <= 512 << 20  # (all tiles at once would be over 600)
+    o, out = gt.prefill(q, k, v, la, beta, ints(cu), pool)
+    for b, n in enumerate(lens):
+        state, a = pool[b:b + 1].clone(), cu[b]
+        for lo in range(0, n, 2048):
+            hi = min(n, lo + 2048)
+            part = [x[a + lo:a + hi].contiguous() for x in (q, k, v, la, beta)]
+            got, _ = gt.prefill(*part, ints([0, hi - lo]), state, pool_out=state)
+            assert max_err(host(got), host(o[a + lo:a + hi])) <= EPS_BF16
+        assert max_err(host(state), host(out[b:b + 1])) <= TOL_F32
+
+
 def test_decode_step_bad_slot_is_reported():
     x = rule_inputs([1, 1], 1, 2, 128, 128, "bf16", seed=3)
     status = torch.empty(2, dtype=torch.int32, device="cuda")
