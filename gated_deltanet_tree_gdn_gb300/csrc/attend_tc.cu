@@ -962,7 +962,7 @@ size_t attend_workspace_bytes(const gdn_tree_attend_dims& d) {
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   const gdn_tree_attend_dims& d = a.d;
   const Plan p = plan_of(d);
-  if (!p.tc) return launch_attend_generic(a, stream);
+  if (!p.tc) return launch_attend_f32(a, stream);
   typedef const __nv_bfloat16* bf;
   TcArgs t{};
   t.q = static_cast<bf>(a.q);

@@ -67,6 +67,18 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// d += a * b and d *= w on two fp32 lanes
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5};\n"
+      "fma.rn.f32x2 x, y, z, x; mov.b64 {%0, %1}, x;}"
+      : "+f"(d.x), "+f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+}
+__device__ __forceinline__ void mul2(float2& d, float w) {
+  asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2};\n"
+      "mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+      : "+f"(d.x), "+f"(d.y) : "f"(w));
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);

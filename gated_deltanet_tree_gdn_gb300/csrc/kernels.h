@@ -209,7 +209,7 @@ constexpr int kAttendMaxParts = 64;  // of the shared prefix
 int attend_few_cluster(const gdn_tree_attend_dims& d, int prefix_len, float* us);
 cudaError_t launch_attend_few(const AttendArgs& a, int prefix_len, const float* part_o,
                               const float* part_lse, int parts, cudaStream_t stream);
-cudaError_t launch_attend_generic(const AttendArgs& a, cudaStream_t stream);
+cudaError_t launch_attend_f32(const AttendArgs& a, cudaStream_t stream);
 
 // rows of accepted paths (or all rows) into the pages of a cache
 struct AppendArgs {

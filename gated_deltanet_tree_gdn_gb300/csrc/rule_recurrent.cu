@@ -24,18 +24,6 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
                    (uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
-// d += a * b, d *= w and d = a * w + d on two fp32 lanes
-__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
-  asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5};\n"
-      "fma.rn.f32x2 x, y, z, x; mov.b64 {%0, %1}, x;}"
-      : "+f"(d.x), "+f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-}
-__device__ __forceinline__ void mul2(float2& d, float w) {
-  asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2};\n"
-      "mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
-      : "+f"(d.x), "+f"(d.y) : "f"(w));
-}
-
 // four consecutive elements as fp32, in pairs
 __device__ __forceinline__ void load4(const float* p, float2& a, float2& b) {
   const float4 x = *reinterpret_cast<const float4*>(p);
