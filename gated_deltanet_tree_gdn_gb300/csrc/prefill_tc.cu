@@ -476,6 +476,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     // the tiles go to the workspace as they lie
     fence_proxy_async_smem();
     __syncthreads();
+    // (the second kernel may set up now, where its launch says so)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0 && ok) {
       bulk_store(out, sTZ, kTZBytes);
       bulk_commit_group();
@@ -623,6 +625,10 @@ __device__ __forceinline__ void load_sum(uint32_t taddr, float (&x)[16]) {
   }
 }
 
+// From here on the first kernel's results are there.  (Every CTA comes here, so that this
+// kernel never ends before that one.)
+__device__ __forceinline__ void prep_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int kChains>
 __global__ void __launch_bounds__(Scan<kChains>::kThreads, 1)
 prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
@@ -641,11 +647,15 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   const int n = lay.count(b, d.N), st = lay.state(b);
   if (n < 0 || st < 0) {
     if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    prep_done();
     return;
   }
   const int chunks = (n + kC - 1) / kC;
   const int c_end = min(chunks, seg.c0 + seg.span);
-  if (seg.c0 > 0 && c_end <= seg.c0) return;  // this sequence ended in an earlier segment
+  if (seg.c0 > 0 && c_end <= seg.c0) {  // this sequence ended in an earlier segment
+    prep_done();
+    return;
+  }
   const size_t row0 = (size_t)lay.cu[b];
 
   if (tid == 0) {
@@ -678,6 +688,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   const bool run = B->abort == 0;
 
   if (warp == L::kWarpLoad) {
+    prep_done();
     const unsigned char* tz = ws + (slot_of(seg, lay.cu, b, seg.c0) * d.Hv + h) * (size_t)kSlotBytes;
     for (int c = seg.c0; run && c < c_end; ++c) {
       const int i = c - seg.c0, s = i % kStages;
@@ -957,6 +968,11 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   const uint64_t limit = wait_hooks().limit_ns;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const int longest = (d.N + kC - 1) / kC;
+  // The second kernel starts beside the first one's last CTAs, unless the sequences are long.
+  // Measured with 32 heads, so and one after the other: 512 tokens 38.0 and 41.4 us, 4 times
+  // 512 105 and 109, 4096 200 and 203, 8192 380 and 384, but 16384 790 and 744, 32768 (two
+  // rounds) 1566 and 1486: the chains that start first then run slower to the end.
+  const int beside = longest > 0 && longest <= 128;
   for (s.c0 = 0; s.c0 == 0 || s.c0 < longest; s.c0 += s.span) {
     if (longest > 0) {
       prefill_prep_kernel<<<(unsigned)(slots * d.Hv), kPrepThreads, kPrepBytes, stream>>>(
@@ -964,13 +980,25 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
       if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
     auto run = [&](auto kernel, int threads, uint32_t bytes) {
-      kernel<<<(unsigned)scan, threads, bytes, stream>>>(
-          mapK, mapQ, mapV, static_cast<const __nv_bfloat16*>(a.v), a.pool_in, a.pool_out,
-          static_cast<__nv_bfloat16*>(a.o), d, a.lay, s, ws, a.dev_status, limit);
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)scan);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = bytes;
+      cfg.stream = stream;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = beside;
+      const cudaError_t e = cudaLaunchKernelEx(
+          &cfg, kernel, mapK, mapQ, mapV, static_cast<const __nv_bfloat16*>(a.v), a.pool_in,
+          a.pool_out, static_cast<__nv_bfloat16*>(a.o), d, a.lay, s,
+          static_cast<const unsigned char*>(ws), a.dev_status, limit);
+      return e != cudaSuccess ? e : cudaGetLastError();
     };
-    if (two) run(prefill_scan_kernel<2>, Scan<2>::kThreads, Scan<2>::kBytes);
-    else run(prefill_scan_kernel<1>, Scan<1>::kThreads, Scan<1>::kBytes);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    err = two ? run(prefill_scan_kernel<2>, Scan<2>::kThreads, Scan<2>::kBytes)
+              : run(prefill_scan_kernel<1>, Scan<1>::kThreads, Scan<1>::kBytes);
+    if (err != cudaSuccess) return err;
     if (s.span == 0) break;  // (no tokens at all: the states are copied)
   }
   return cudaSuccess;
