@@ -133,6 +133,9 @@ def _ptr(t):
 
 
 def _check(t: torch.Tensor, name: str, dtype=None, shape=None):
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
