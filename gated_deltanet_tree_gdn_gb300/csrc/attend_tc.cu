@@ -44,7 +44,6 @@ constexpr int kSoftmax = 512;             // softmax threads: two a row
 constexpr int kThreads = kSoftmax + 3 * 32;
 constexpr int kWarpK = kSoftmax / 32, kWarpV = kWarpK + 1, kWarpMma = kWarpK + 2;
 constexpr int kHalf = kTile / 2;
-constexpr int kMaxSorted = 64;           // sequences that a unit may rank by length
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;             // log2 of the growth that is left in P
@@ -70,7 +69,7 @@ struct TcArgs {
   int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
   bool own_box;        // the tree's own rows come by TMA
   bool q_box;          // Q too: G divides a tile, and the scale is not negative
-  bool by_length;      // units of long contexts first (more units than SMs, kMaxSorted sequences at most)
+  bool by_length;      // units of long contexts first (more units than SMs, kMaxRanked sequences at most)
 };
 
 constexpr uint32_t kBarBytes = 5120;
@@ -256,36 +255,18 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
 static_assert(sizeof(Bars) <= kBarBytes, "the barriers fit their place");
 
 // The sequence that comes `want`-th when the longest contexts come first (ties in order), and
-// its rows and length: a warp ranks two a lane.  Long units first, the SMs end closer together.
+// its rows and length.  Long units first, the SMs end closer together.
 __device__ __forceinline__ int ranked(const int32_t* ctx, const int32_t* cu, int B, int want,
                                       int lane, int& first, int& stop, int& len) {
-  const int none = -2147483647 - 1;
   const bool on0 = lane < B, on1 = lane + 32 < B;
   const int f0 = on0 ? cu[lane] : 0, e0 = on0 ? cu[lane + 1] : 0;
   const int f1 = on1 ? cu[lane + 32] : 0, e1 = on1 ? cu[lane + 33] : 0;
-  const int x0 = on0 ? ctx[lane] : none, x1 = on1 ? ctx[lane + 32] : none;
-  int r0 = 0, r1 = 0;
-#pragma unroll 8
-  for (int j = 0; j < 32; ++j) {
-    const int y = __shfl_sync(0xffffffffu, x0, j);
-    r0 += y > x0 || (y == x0 && j < lane);
-    r1 += y >= x1;
-  }
-  if (B > 32) {
-#pragma unroll 8
-    for (int j = 0; j < 32; ++j) {
-      const int y = __shfl_sync(0xffffffffu, x1, j);
-      r0 += y > x0;
-      r1 += y > x1 || (y == x1 && j < lane);
-    }
-  }
-  const uint32_t m0 = __ballot_sync(0xffffffffu, on0 && r0 == want);
-  const uint32_t m1 = __ballot_sync(0xffffffffu, on1 && r1 == want);
-  const int at = (m0 ? __ffs(m0) : __ffs(m1)) - 1;
-  first = __shfl_sync(0xffffffffu, m0 ? f0 : f1, at);
-  stop = __shfl_sync(0xffffffffu, m0 ? e0 : e1, at);
-  len = __shfl_sync(0xffffffffu, m0 ? x0 : x1, at);
-  return m0 ? at : at + 32;
+  const int x0 = on0 ? ctx[lane] : kNoRank, x1 = on1 ? ctx[lane + 32] : kNoRank;
+  const int at = nth_largest(x0, x1, B, want, lane), l = at & 31;
+  first = __shfl_sync(0xffffffffu, at < 32 ? f0 : f1, l);
+  stop = __shfl_sync(0xffffffffu, at < 32 ? e0 : e1, l);
+  len = __shfl_sync(0xffffffffu, at < 32 ? x0 : x1, l);
+  return at;
 }
 
 enum Segment { kPrefix = 0, kContext = 1, kOwn = 2 };
@@ -1023,7 +1004,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   t.slot0 = p.prefix_splits;
   t.splits = p.seq_splits;
   t.tiles = p.seq_tiles;
-  t.by_length = d.B > 1 && d.B <= kMaxSorted && p.seq_splits == 1 &&
+  t.by_length = d.B > 1 && d.B <= kMaxRanked && p.seq_splits == 1 &&
                 (long long)d.B * d.Hkv * p.seq_tiles > sm_count();
   err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits);
   if (err != cudaSuccess || !p.slots) return err;

@@ -67,6 +67,30 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// The index of the `want`-th largest of B <= 64 numbers (equal ones in order), of which a lane
+// of the warp holds two: number `lane` and number 32 + `lane`, kNoRank past B.
+constexpr int kMaxRanked = 64, kNoRank = -2147483647 - 1;
+__device__ __forceinline__ int nth_largest(int x0, int x1, int B, int want, int lane) {
+  int r0 = 0, r1 = 0;
+#pragma unroll 8
+  for (int j = 0; j < 32; ++j) {
+    const int y = __shfl_sync(0xffffffffu, x0, j);
+    r0 += y > x0 || (y == x0 && j < lane);
+    r1 += y >= x1;
+  }
+  if (B > 32) {
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) {
+      const int y = __shfl_sync(0xffffffffu, x1, j);
+      r0 += y > x0;
+      r1 += y > x1 || (y == x1 && j < lane);
+    }
+  }
+  const uint32_t m0 = __ballot_sync(0xffffffffu, lane < B && r0 == want);
+  const uint32_t m1 = __ballot_sync(0xffffffffu, lane + 32 < B && r1 == want);
+  return m0 ? __ffs(m0) - 1 : __ffs(m1) + 31;
+}
+
 // d += a * b and d *= w on two fp32 lanes
 __device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
   asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %5};\n"

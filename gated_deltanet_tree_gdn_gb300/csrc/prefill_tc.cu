@@ -55,6 +55,7 @@ constexpr int kMinSegment = 8;                     // chunks a launch pair, at l
 struct Segment {
   int c0, span;
   bool dense;
+  bool by_length = false;  // the second kernel takes the longest sequences first
 };
 
 __host__ __device__ inline long long dense_slots(long long T, long long B) { return T / kC + B + 1; }
@@ -517,6 +518,7 @@ struct ScanBars {
   ChainBars chain[2];
   uint32_t tmem;
   int abort;
+  int unit;  // the sequence
 };
 static_assert(sizeof(ScanBars) <= 256, "the barriers fit their place");
 
@@ -642,8 +644,19 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slice = blockIdx.x % L::kSlices;
-  const int h = (blockIdx.x / L::kSlices) % d.Hv, b = blockIdx.x / L::kSlices / d.Hv;
+  const int h = (blockIdx.x / L::kSlices) % d.Hv;
   const int hq = h / (d.Hv / d.Hqk);
+  int b = blockIdx.x / L::kSlices / d.Hv;
+  if (seg.by_length) {  // (found by one warp)
+    if (warp == 0) {
+      const int x0 = lane < d.B ? lay.cu[lane + 1] - lay.cu[lane] : kNoRank;
+      const int x1 = lane + 32 < d.B ? lay.cu[lane + 33] - lay.cu[lane + 32] : kNoRank;
+      b = nth_largest(x0, x1, d.B, b, lane);
+      if (lane == 0) B->unit = b;
+    }
+    __syncthreads();
+    b = B->unit;
+  }
   const int n = lay.count(b, d.N), st = lay.state(b);
   if (n < 0 || st < 0) {
     if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
@@ -965,6 +978,9 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   const bool two = (long long)d.B * d.Hv * Scan<1>::kSlices > sms;
   const long long scan = (long long)d.B * d.Hv * (two ? Scan<2>::kSlices : Scan<1>::kSlices);
   if (slots * d.Hv > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  // in more than a round of the SMs the long sequences go first, so that the SMs end closer
+  // together (16 ragged prompts 492 to 463 us)
+  s.by_length = scan > sms && d.B > 1 && d.B <= kMaxRanked;
   const uint64_t limit = wait_hooks().limit_ns;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const int longest = (d.N + kC - 1) / kC;
