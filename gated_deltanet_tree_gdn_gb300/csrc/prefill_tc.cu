@@ -155,6 +155,7 @@ __device__ __forceinline__ void load_kq(unsigned char* tile, const CUtensorMap* 
 // Z = Y T on the tensor cores.  Bound by the latency of these short steps: three CTAs an SM
 // hide it in one another (one array for X and T, and T over K and Q, make them fit).
 constexpr int kPrepThreads = 256;
+constexpr int kWarpTmem = 2;  // the warp that holds the TMEM columns
 constexpr int kAld = 68;  // floats a row (16-byte rows)
 
 struct PrepShared {
@@ -240,13 +241,23 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % d.Hv, slot = blockIdx.x / d.Hv;
   const int hq = h / (d.Hv / d.Hqk);
+  if (tid == 0) {
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapQ);
+    mbar_init(&P.bar, 1);
+    mbar_init(&P.mma, 1);
+    P.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == kWarpTmem) tmem_alloc(&P.tmem, 128);
   int b, c;
-  if (seg.dense) {  // the last sequence whose first slot is not past this one
-    int lo = 0, hi = d.B - 1;
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (lay.cu[m] / kC + m <= slot) lo = m;
-      else hi = m - 1;
+  if (seg.dense) {  // the last sequence whose first slot is not past this one, 32 a probe
+    int lo = 0, hi = d.B;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) >> 5, m = lo + lane * step;
+      const bool not_past = m < hi && lay.cu[m] / kC + m <= slot;
+      lo += max(__popc(__ballot_sync(0xffffffffu, not_past)) - 1, 0) * step;
+      hi = min(hi, lo + step);
     }
     b = lo;
     c = slot - (lay.cu[b] / kC + b);
@@ -255,35 +266,43 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     c = seg.c0 + slot % seg.span;
   }
   const int n = lay.count(b, d.N);
-  if (c < 0 || n <= c * kC) return;  // (an invalid sequence is reported by the second kernel)
+  if (c < 0 || n <= c * kC) {  // (an invalid sequence is reported by the second kernel)
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == kWarpTmem) tmem_dealloc(P.tmem, 128);
+    return;
+  }
   const int nc = min(kC, n - c * kC);
   const size_t row = (size_t)lay.cu[b] + (size_t)c * kC;
-
   if (tid == 0) {
-    mbar_init(&P.bar, 1);
-    mbar_init(&P.mma, 1);
-    P.abort = 0;
-    mbar_fence_init();
     mbar_arrive_expect_tx(&P.bar, kTileKQ);
     load_kq(sKQ, &mapK, &mapQ, &P.bar, hq, (int)row);
   }
-  if (warp == 0) tmem_alloc(&P.tmem, 128);
+  float la[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};  // the gates of rows 2 lane and 2 lane + 1
+  if (warp == 1) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * lane + e >= nc) continue;
+      // (past L1, where the lines of cu are to stay)
+      la[e] = __ldcg(log_alpha + (row + 2 * lane + e) * d.Hv + h);
+      be[e] = __ldcg(beta + (row + 2 * lane + e) * d.Hv + h);
+    }
+  }
+
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = P.tmem;
-  unsigned char* out = ws + (slot_of(seg, lay.cu, b, c) * d.Hv + h) * (size_t)kSlotBytes;
+  unsigned char* out = ws + ((size_t)slot * d.Hv + h) * kSlotBytes;
   if (warp == 1) {
     // g by a scan of pairs; -inf (alpha = 0) becomes -1e4: e^-1e4 is 0 as well, and
     // differences of sums stay defined
     df x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = 2 * lane + e;
-      float la = i < nc ? log_alpha[(row + i) * d.Hv + h] : 0.f;
-      if (la < -1e4f) la = -1e4f;
-      x[e] = df{la, 0.f};
-      P.beta[i] = i < nc ? beta[(row + i) * d.Hv + h] : 0.f;
+      x[e] = df{la[e] < -1e4f ? -1e4f : la[e], 0.f};
+      P.beta[2 * lane + e] = be[e];
     }
     x[1] = df_add(x[0], x[1]);
     df run = x[1];
@@ -313,7 +332,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
       const int i = 2 * lane + e;
       const df gi = e ? run : g0;
       aux[i] = ex2(kLog2e * df_value(gi));
-      aux[kC + i] = P.beta[i];
+      aux[kC + i] = be[e];
       aux[2 * kC + i] = i < nc ? decay(last, gi) : 0.f;
     }
     if (lane == 0) aux[3 * kC] = ex2(kLog2e * df_value(last));
@@ -441,6 +460,12 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     fence_proxy_async_smem();
     tc_fence_before_sync();
     __syncthreads();
+    // the tiles go to the workspace as they lie, T's rows now and Z's when they are there
+    if (tid == 32) {
+#pragma unroll
+      for (int p = 0; p < 3; ++p) bulk_store(out + p * kTileTZ, sTZ + p * kTileTZ, kTileTZ / 2);
+      bulk_commit_group();
+    }
     // Z = Y T: lanes 64-127 of [T; Y] T (T as an operand whose rows are the inner index)
     if (warp == 0) {
       tc_fence_after_sync();
@@ -474,15 +499,18 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
         store_tz(sTZ, ln, 4 * half + c8, y);
       }
     }
-    // the tiles go to the workspace as they lie
     fence_proxy_async_smem();
     __syncthreads();
     // (the second kernel may set up now, where its launch says so)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0 && ok) {
-      bulk_store(out, sTZ, kTZBytes);
-      bulk_commit_group();
-      bulk_wait_all();
+    if (tid == 32) {
+      if (ok) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          bulk_store(out + p * kTileTZ + kTileTZ / 2, sTZ + p * kTileTZ + kTileTZ / 2, kTileTZ / 2);
+        bulk_commit_group();
+      }
+      bulk_wait_read_all();  // (the kernel's end is what the reader waits for)
     }
   }
   // (after a timeout: the copies and MMAs in flight end, or their bounded waits do)
@@ -495,7 +523,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   __syncthreads();
   tc_fence_after_sync();
   if (tid == 0 && P.abort && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
-  if (warp == 0) tmem_dealloc(tmem, 128);
+  if (warp == kWarpTmem) tmem_dealloc(tmem, 128);
 }
 
 // ---- second kernel: the chunks of a sequence, 32 value columns a chain ---------------------
