@@ -25,8 +25,8 @@
 //
 // What bounds it: the chain of dependent steps (MMA, TMEM to registers, split, shared
 // memory, MMA), not bytes or tensor rate.  One sequence of 32768 tokens with 32 heads takes
-// 1.48 ms (0.95 TB/s of inputs and outputs), 1.0 ms of it in the second kernel's chains and
-// the rest in the first kernel; 16 ragged prompts of 17 to 2048 tokens 500 us.
+// 1.39 ms (0.59 TB/s of inputs and outputs), 1.0 ms of it in the second kernel's chains and
+// the rest in the first kernel; 16 ragged prompts of 17 to 2048 tokens 416 us.
 #include <string.h>
 
 #include "common.cuh"
@@ -152,17 +152,19 @@ __device__ __forceinline__ void load_kq(unsigned char* tile, const CUtensorMap* 
 // ---- first kernel: T and Z of every chunk and head --------------------------------------
 // T = (I + X)^-1 by blocks: the four 16 x 16 blocks of the diagonal column by column, then
 // twice the block below the diagonal of a pair, T21 = -T22 X21 T11 (16, then 32 rows).
-// Z = Y T on the tensor cores.  Bound by the latency of these short steps: three CTAs an SM
-// hide it in one another (one array for X and T, and T over K and Q, make them fit).
+// Z = Y T on the tensor cores.  Bound by shared memory reads and the latency of these short
+// steps: three CTAs an SM hide it in one another (one array for X and T, and T over K and Q,
+// make them fit).  About 9 us a CTA of which the copies in take 2, the inverse 3; 8192 chunks
+// and heads 210 us.
 constexpr int kPrepThreads = 256;
 constexpr int kWarpTmem = 2;  // the warp that holds the TMEM columns
-constexpr int kAld = 68;  // floats a row (16-byte rows)
+constexpr int kAld = 72;  // floats a row (8 of a row and 4 rows lie in all banks)
 
 struct PrepShared {
   // below and on the diagonal T, above it X^T (X[t][s] at [s][t]); a diagonal block that is
   // done holds T^T above its diagonal
   float A[kC][kAld];
-  float P[kC / 2][kC / 2 + 4];  // a product of blocks on its way
+  float P[kC / 2][kC / 2 + 8];  // a product of blocks on its way
   df g[kC];
   float beta[kC], up[kC], down[kC];  // e^{g - g_mid}, e^{g_mid - g}
   uint64_t bar, mma;
@@ -172,58 +174,53 @@ struct PrepShared {
 constexpr uint32_t kPrepTiles = kTZBytes > kTileKQ ? kTZBytes : kTileKQ;  // [K; Q], then [T; Z]
 constexpr uint32_t kPrepBytes = kPrepTiles + sizeof(PrepShared) + 1024;
 
-// (a, b) += x (c, d), two fp32 lanes an instruction
-__device__ __forceinline__ void fma2(float& a, float& b, float x, float c, float d) {
-  asm("{\n\t.reg .b64 p, q, r;\n\t"
-      "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %4};\n\t"
-      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(x), "f"(c), "f"(d));
+// x as the sum of two numbers of 11 significant bits (and the rest, below 2^-22 of it)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;  // (the product drops the last 13)
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4],
+                                         const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// T21 = -T22 X21 T11 for the pair of n x n blocks at `o`: a thread takes row i and columns
-// j .. j + kCols of P = X21 T11, then (kSecond) of -T22 P.  T11 and T22 are triangular: k
-// runs from j in the first product, to i in the second.
-template <int n, int kCols, bool kSecond>
-__device__ __forceinline__ void block_product(PrepShared& S, int o, int po, int i, int j,
-                                              float (&acc)[kCols]) {
+// T21 = -T22 X21 T11 for the pair of n x n blocks at `o`: a warp's 16 rows and 8 columns of
+// P = X21 T11, then (kSecond) of T22 P, with d[0], d[1] at row lane / 4 and columns 2 (lane %
+// 4), + 1, and d[2], d[3] 8 rows below.  The operands are two parts each and three of their
+// four products are kept (2^-22 of a term; fp32 sums).  Shared memory reads bound this
+// kernel, and CUDA cores needed three times as many.
+template <int n, bool kSecond>
+__device__ __forceinline__ void block_product(const PrepShared& S, int o, int po, int mt, int nt,
+                                              int lane, float (&d)[4]) {
+  const int g = lane >> 2, t = lane & 3, j = 8 * nt + g;
 #pragma unroll
-  for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-  if (!kSecond) {
+  for (int e = 0; e < 4; ++e) d[e] = 0.f;
 #pragma unroll
-    for (int k = j; k < j + kCols; ++k) {
-      const float x = S.A[o + k][o + n + i];
+  for (int s = 0; s < n / 8; ++s) {
+    // T11 and T22 are triangular
+    if (kSecond ? 8 * s > 16 * mt + 15 : 8 * s + 7 < 8 * nt) continue;
+    uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
-      for (int e = 0; e < kCols; ++e)
-        if (j + e <= k) acc[e] = fmaf(x, S.A[o + k][o + j + e], acc[e]);
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * mt + g + 8 * (e & 1), k = 8 * s + t + 4 * (e >> 1);
+      float x = kSecond ? S.A[o + n + k][o + n + i] : S.A[o + k][o + n + i];
+      if (kSecond && k > i) x = 0.f;
+      split_tf32(x, ah[e], al[e]);
     }
-#pragma unroll 4
-    for (int k = j + kCols; k < n; ++k) {
-      const float x = S.A[o + k][o + n + i];
-      const float* y = &S.A[o + k][o + j];
-      if (kCols == 4) {
-        const float4 z = *reinterpret_cast<const float4*>(y);
-        fma2(acc[0], acc[1], x, z.x, z.y);
-        fma2(acc[kCols - 2], acc[kCols - 1], x, z.z, z.w);
-      } else {
-        const float2 z = *reinterpret_cast<const float2*>(y);
-        fma2(acc[0], acc[1], x, z.x, z.y);
-      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 8 * s + t + 4 * e;
+      float x = kSecond ? S.P[po + k][j] : S.A[o + k][o + j];
+      if (!kSecond && j > k) x = 0.f;
+      split_tf32(x, bh[e], bl[e]);
     }
-  } else {
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float x = k <= i ? -S.A[o + n + k][o + n + i] : 0.f;
-      const float* y = &S.P[po + k][j];
-      if (kCols == 4) {
-        const float4 z = *reinterpret_cast<const float4*>(y);
-        fma2(acc[0], acc[1], x, z.x, z.y);
-        fma2(acc[kCols - 2], acc[kCols - 1], x, z.z, z.w);
-      } else {
-        const float2 z = *reinterpret_cast<const float2*>(y);
-        fma2(acc[0], acc[1], x, z.x, z.y);
-      }
-    }
+    mma_tf32(d, al, bh);
+    mma_tf32(d, ah, bl);
+    mma_tf32(d, ah, bh);
   }
 }
 
@@ -421,29 +418,36 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
         if (i >= j) P.A[o + i][o + j] = P.A[o + j][o + i] = u[i];
     }
     __syncthreads();
-    {  // pairs of 16-row blocks: threads (pair, row i, 2 columns)
-      const int pr = tid >> 7, i = tid & 15, jq = (tid >> 4) & 7, o = 32 * pr;
-      float acc[2];
-      block_product<16, 2, false>(P, o, 16 * pr, i, 2 * jq, acc);
-      P.P[16 * pr + i][2 * jq] = acc[0];
-      P.P[16 * pr + i][2 * jq + 1] = acc[1];
+    {  // pairs of 16-row blocks: two warps a pair
+      const int pr = warp >> 1, nt = warp & 1, o = 32 * pr, i = lane >> 2, j = 8 * nt + 2 * (lane & 3);
+      float x[4];
+      if (warp < 4) {
+        block_product<16, false>(P, o, 16 * pr, 0, nt, lane, x);
+        *reinterpret_cast<float2*>(&P.P[16 * pr + i][j]) = make_float2(x[0], x[1]);
+        *reinterpret_cast<float2*>(&P.P[16 * pr + i + 8][j]) = make_float2(x[2], x[3]);
+      }
       __syncthreads();
-      block_product<16, 2, true>(P, o, 16 * pr, i, 2 * jq, acc);
+      if (warp < 4) {
+        block_product<16, true>(P, o, 16 * pr, 0, nt, lane, x);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        P.A[o + 16 + i][o + 2 * jq + e] = acc[e];
-        if (pr == 1) P.A[o + 2 * jq + e][o + 16 + i] = acc[e];
+        for (int e = 0; e < 4; ++e) {
+          const int ie = i + 8 * (e >> 1), je = j + (e & 1);
+          P.A[o + 16 + ie][o + je] = -x[e];
+          if (pr == 1) P.A[o + je][o + 16 + ie] = -x[e];
+        }
       }
     }
     __syncthreads();
-    {  // the pair of 32-row blocks: threads (row i, 4 columns)
-      const int i = tid & 31, jq = tid >> 5;
-      float acc[4];
-      block_product<32, 4, false>(P, 0, 0, i, 4 * jq, acc);
-      *reinterpret_cast<float4*>(&P.P[i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    {  // the pair of 32-row blocks
+      const int mt = warp & 1, nt = warp >> 1, i = 16 * mt + (lane >> 2), j = 8 * nt + 2 * (lane & 3);
+      float x[4];
+      block_product<32, false>(P, 0, 0, mt, nt, lane, x);
+      *reinterpret_cast<float2*>(&P.P[i][j]) = make_float2(x[0], x[1]);
+      *reinterpret_cast<float2*>(&P.P[i + 8][j]) = make_float2(x[2], x[3]);
       __syncthreads();
-      block_product<32, 4, true>(P, 0, 0, i, 4 * jq, acc);
-      *reinterpret_cast<float4*>(&P.A[32 + i][4 * jq]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      block_product<32, true>(P, 0, 0, mt, nt, lane, x);
+      *reinterpret_cast<float2*>(&P.A[32 + i][j]) = make_float2(-x[0], -x[1]);
+      *reinterpret_cast<float2*>(&P.A[32 + i + 8][j]) = make_float2(-x[2], -x[3]);
     }
     __syncthreads();
     // T in rows 0-63 of the tiles
