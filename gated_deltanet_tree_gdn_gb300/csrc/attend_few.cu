@@ -519,20 +519,30 @@ cudaError_t launch_dp(const AttendArgs& a, int plen, const float* part_o, const 
 // Measured with 8 key heads and one of 4096 keys a sequence, in us by CTAs a unit: 16
 // sequences 1: 84, 2: 57, 4: 73, 8: 69; 32 sequences 97, 131, 113, 130; 64 sequences 234,
 // 205, 192, 238; one sequence of 8192 keys 150, 84, 45, 26, and 21 with 16.
+// That is for the longest contexts that the page table holds.  They are rarely all that long,
+// and then the longest one is what is waited for; so more CTAs a unit are taken where they
+// would cost no more than 1.3 times as much, in three rounds at most and with 8 times 64 keys
+// each at least.  Measured with 256 to 8192 keys a sequence: 16 sequences 155, 91, 60, 51 us,
+// 32 sequences 163, 99, 79, 90.
 int attend_few_cluster(const gdn_tree_attend_dims& d, int prefix_len, float* us) {
-  constexpr float kUs[kPerSm + 1] = {0.f, 1.3f, 1.5f, 2.4f};
+  constexpr float kUs[kPerSm + 1] = {0.f, 1.3f, 1.5f, 2.4f}, kMore = 1.3f;
   const long long sms = sm_count() > 0 ? sm_count() : 152, slots = kPerSm * sms;
   const long long units = (long long)d.B * d.Hkv;
   const long long keys = (long long)d.table_width * d.page_size + d.N + prefix_len;
+  float least = 0.f;
   int best = 1;
-  for (int C = 1; C <= kMaxCluster; C *= 2) {
-    const long long full = units * C / slots, rest = units * C - full * slots;
-    const long long rounds = (keys + 16 * kWarps * C - 1) / (16 * kWarps * C);
-    const float t = (full * kUs[kPerSm] + kUs[(rest + sms - 1) / sms]) * (rounds + 2);
-    if (C > 1 && t >= *us) continue;
-    best = C;
-    *us = t;
-  }
+  for (int more = 0; more < 2; ++more)
+    for (int C = 1; C <= kMaxCluster; C *= 2) {
+      const long long full = units * C / slots, rest = units * C - full * slots;
+      const long long rounds = (keys + 16 * kWarps * C - 1) / (16 * kWarps * C);
+      const float t = (full * kUs[kPerSm] + kUs[(rest + sms - 1) / sms]) * (rounds + 2);
+      const bool take = !more ? C == 1 || t < least
+                              : C > best && t <= kMore * least && rounds >= 8 && units * C <= 3 * slots;
+      if (!take) continue;
+      best = C;
+      *us = t;
+      if (!more) least = t;
+    }
   return best;
 }
 
