@@ -628,7 +628,8 @@ def attend(q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len,
     gdn_tree_attend).  Returns (o, lse).
 
     q [T,Hq,D] and the rows' own k, v [T,Hkv,D] (both None: the rows see the cache alone);
-    parent [T] int32 (None: every sequence's rows are a chain, causal attention); cu_nodes
+    parent [T] int32, trees of up to 1024 rows (None: every sequence's rows are a chain of
+    any length, causal attention); cu_nodes
     [B+1]; k_cache, v_cache [n_pages,page_size,Hkv,D]; page_table [B,width] int32 and
     context_len [B] int32: each sequence's own context; prefix_pages [ceil(prefix_len /
     page_size)] int32: the rows that every sequence sees before its own.  scale defaults to

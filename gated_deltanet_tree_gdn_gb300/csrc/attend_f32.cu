@@ -79,7 +79,7 @@ attend_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int unit = blockIdx.x / C;
-  const int tile = unit % tiles;
+  const int tile = tiles - 1 - unit % tiles;  // (a chain's last rows see the most keys)
   const int hk = (unit / tiles) % d.Hkv;
   const int b = unit / tiles / d.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

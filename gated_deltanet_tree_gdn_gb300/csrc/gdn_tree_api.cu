@@ -504,7 +504,7 @@ int gdn_tree_attend(const void* q, const void* k, const void* v, const int32_t* 
                     size_t workspace_bytes, void* stream) {
   const int rc = check_attend_dims(dims);
   if (rc != GDN_TREE_OK) return rc;
-  if (dims.N > gdn::kMaxNLongHost) return GDN_TREE_EUNSUPPORTED;
+  if (parent && dims.N > gdn::kMaxNLongHost) return GDN_TREE_EUNSUPPORTED;
   if (dims.B == 0 || dims.T == 0 || dims.N == 0) return GDN_TREE_OK;  // nothing to do
   if ((k == nullptr) != (v == nullptr)) return GDN_TREE_EINVAL;
   const void* need[] = {q, o};

@@ -86,14 +86,14 @@ def attend_dims(**kw):
 
 
 def attend(lib, dims=None, k=P(1), v=P(2), q=P(0), table=P(6), prefix=P(8), cache=P(5), ctx=P(7),
-           ws=P(12), ws_bytes=1 << 60):
-    return lib.gdn_tree_attend(q, k, v, None, P(4), cache, cache, table, ctx, prefix, 1.0, P(10),
+           ws=P(12), ws_bytes=1 << 60, parent=None):
+    return lib.gdn_tree_attend(q, k, v, parent, P(4), cache, cache, table, ctx, prefix, 1.0, P(10),
                                P(11), dims or attend_dims(), None, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(D=24), gt.EUNSUPPORTED), (dict(D=256), gt.EUNSUPPORTED), (dict(dtype=2), gt.EUNSUPPORTED),
-    (dict(N=1025), gt.EUNSUPPORTED), (dict(Hq=7), gt.EINVAL), (dict(Hkv=0), gt.EINVAL),
+    (dict(Hq=7), gt.EINVAL), (dict(Hkv=0), gt.EINVAL),
     (dict(page_size=0), gt.EINVAL), (dict(prefix_len=-1), gt.EINVAL), (dict(T=-1), gt.EINVAL),
     (dict(table_width=1 << 28), gt.EUNSUPPORTED), (dict(B=70000), gt.EUNSUPPORTED),
     (dict(n_pages=-1), gt.EINVAL), (dict(table_width=-1), gt.EINVAL)])
@@ -110,6 +110,7 @@ def test_attend_arguments(lib):
     assert attend(lib, prefix=None) == gt.EINVAL     # a prefix without its pages
     assert attend(lib, cache=None) == gt.EINVAL
     assert attend(lib, ctx=None) == gt.EINVAL
+    assert attend(lib, attend_dims(N=1025), parent=P(3)) == gt.EUNSUPPORTED  # (a chain may be longer)
     assert attend(lib, attend_dims(B=0), q=None) == gt.OK
     assert attend(lib, attend_dims(T=0), q=None) == gt.OK
     d = attend_dims()

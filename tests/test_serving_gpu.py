@@ -387,6 +387,29 @@ def test_attend_cache_alone(case):
     check_attend(o, lse, x)
 
 
+LONG = [
+    # long chains; long contexts, which are split over CTAs and into parts; full prefix units
+    ([1500, 3], [10, 700], 200, 4, 2, 128, 64, "bf16"),
+    ([2100], [0], 0, 2, 1, 64, 16, "bf16"),
+    ([1100, 40], [30, 0], 50, 2, 1, 64, 16, "f32"),
+    ([1, 3], [9000, 30], 0, 8, 2, 128, 16, "bf16"),
+    ([1] * 16, [300 * (i + 1) for i in range(16)], 0, 8, 4, 64, 64, "bf16"),
+    ([60], [5000], 0, 4, 1, 128, 64, "bf16"),
+    ([20] * 12, [40] * 12, 6000, 8, 2, 128, 64, "bf16"),
+    ([1] * 30, [5] * 30, 4000, 16, 4, 128, 128, "bf16"),
+    ([1, 2], [2500, 100], 300, 4, 2, 128, 24, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)).replace(" ", "")[:60])
+def test_attend_long(case):
+    x = attend_inputs(*case, seed=len(case[0]) + case[2], tree="chain")
+    status = torch.full((len(case[0]),), -7, dtype=torch.int32, device="cuda")
+    o, lse = run_attend(x, chain=True, dev_status=status)
+    assert (status == 0).all()
+    check_attend(o, lse, x, chain=True)
+
+
 @pytest.mark.parametrize("size,scale", [(6.0, 1.0), (1.0, 0.0), (1.0, -0.3), (30.0, None)])
 def test_attend_scales_and_sharp_rows(size, scale):
     """Scores of thousands (one key takes the whole weight), a scale of zero (a mean) and a
