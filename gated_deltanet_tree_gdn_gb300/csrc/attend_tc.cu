@@ -317,12 +317,12 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   // ---- the unit: rows [r0, r1) of key head hk, key tiles [i0, i1) -------------------
   const int split = blockIdx.x % a.splits;
   int u = blockIdx.x / a.splits;
-  const int t = a.tiles - 1 - u % a.tiles;  // (a chain's last rows see the most keys)
-  u /= a.tiles;
   const int hk = u % d.Hkv;
+  u /= d.Hkv;
+  const int t = a.tiles - 1 - u % a.tiles;  // (a chain's last rows see the most keys)
   // the sequence is found by one warp while others set up
   if (warp == 0 && !a.prefix_units) {
-    int b = u / d.Hkv, first, stop, ctx;
+    int b = u / a.tiles, first, stop, ctx;
     if (a.by_length) {
       b = ranked(a.ctx, a.cu, d.B, b, lane, first, stop, ctx);
     } else {
