@@ -63,7 +63,6 @@ struct TcArgs {
   int slot0;        // first slot of this launch's parts
   int splits;       // parts of a row's keys in this launch
   int tiles;        // 256-row blocks a sequence (a batch, for prefix units)
-  int min_rows;     // sequences of fewer rows are not this kernel's
   bool prefix_units;   // units of the shared prefix over the whole batch
   bool with_prefix;    // a sequence's units include the prefix
   int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
