@@ -13,6 +13,7 @@
 //   - the prefix's: 256 rows of the whole batch, whatever sequence they are of, against
 //     the shared prefix, which is then read once for every 256 rows of the batch and not
 //     once for every sequence.
+// A unit of one row tile (kFork) lends the other's warps and columns to every second key tile.
 //
 // Roles (19 warps): warps 0-7 and 8-15 the softmax of row tile 0 and 1, two threads a row
 // (one for keys 0-63 of a tile, one for 64-127); warp 16 brings K tiles, warp 17 V tiles;
@@ -78,7 +79,7 @@ struct TcArgs {
   bool by_length;      // units of long contexts first (more units than SMs, kMaxRanked sequences at most)
 };
 
-constexpr uint32_t kBarBytes = 5120;
+constexpr uint32_t kBarBytes = 6144;
 
 template <int DP>
 struct Smem {
@@ -99,6 +100,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
   float top[2][2][kTile];  // a row's maximum over each half of a tile; at the end its sums
+  float mref[2][kTile];     // at the end: what a row's sums are over
   int poison[2][2][kTile];  // whether the half saw values that are not finite
   uint32_t badv[2][4];  // own rows of a V tile that hold infinities or NaN (by stage)
 };
@@ -303,7 +305,7 @@ __device__ __noinline__ void add_nonfinite(const TcArgs& a, size_t out, size_t s
   }
 }
 
-template <int DP>
+template <int DP, bool kFork>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapV,
@@ -383,7 +385,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     return;
   }
   const int rows = min(2 * kTile, rows_end - r0);
-  const bool two = rows > kTile;
+  const bool two = !kFork && rows > kTile;
   const bool own = a.k != nullptr && !a.prefix_units;
   const bool tree = own && a.parent != nullptr;
   const int plen = a.prefix_units || a.with_prefix ? d.prefix_len : 0;
@@ -395,6 +397,9 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   const int i0 = (int)((long long)all * split / a.splits);
   const int i1 = (int)((long long)all * (split + 1) / a.splits);
   const int ntiles = i1 - i0;
+  // rows for one tile only: the two groups of softmax warps take its key tiles by turns, with
+  // sums of their own (S and O of row tile 1), which are added up at the end
+  const bool fork = kFork && ntiles > 1;
   // key tile i: its segment, first key and keys (own tiles from the last to the first, so
   // that a row follows its path upwards once)
   auto tile_of = [&](int i, int& seg, int& j0, int& len) {
@@ -533,7 +538,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       auto issue_s = [&](int tile, int st, bool last_of_k) {
         if (elect_one()) {
           const uint32_t to = tmem + tile * kTile;
-          const uint64_t q = dQ + tile * (L::kQ >> 4), k = dK + st * (kStage >> 4);
+          const uint64_t q = dQ + (fork ? 0 : tile) * (L::kQ >> 4), k = dK + st * (kStage >> 4);
 #pragma unroll
           for (int s = 0; s < DP / 16; ++s) {
             const uint32_t off = ((s >> 2) * kSw128TileBytes + (s & 3) * 32) >> 4;
@@ -567,7 +572,35 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       }
       // (both tiles written out: a loop over them takes the descriptors out of the uniform
       // registers, and 8 % longer)
-      for (int at = 0; ok && at < ntiles; ++at) {
+      if (fork) {
+        ok = ok && wait_warp(&S->kfull[1], 0, S, limit_ns);
+        if (ok) issue_s(1, 1, true);
+        // (key tiles at and at + 1, written out as well)
+        for (int at = 0; ok && at < ntiles; at += 2) {
+          const uint32_t ph = (at >> 1) & 1;
+          ok = wait_warp(&S->vfull[0], ph, S, limit_ns) && wait_warp(&S->pready[0], ph, S, limit_ns);
+          if (!ok) break;
+          tc_fence_after_sync();
+          issue_pv(0, 0, at == 0, true);
+          if (at + 2 < ntiles) {
+            ok = wait_warp(&S->kfull[0], ph ^ 1, S, limit_ns);
+            if (!ok) break;
+            issue_s(0, 0, true);
+          }
+          if (at + 1 < ntiles) {
+            ok = wait_warp(&S->vfull[1], ph, S, limit_ns) && wait_warp(&S->pready[1], ph, S, limit_ns);
+            if (!ok) break;
+            tc_fence_after_sync();
+            issue_pv(1, 1, at == 0, true);
+          }
+          if (at + 3 < ntiles) {
+            ok = wait_warp(&S->kfull[1], ph ^ 1, S, limit_ns);
+            if (!ok) break;
+            issue_s(1, 1, true);
+          }
+        }
+      }
+      for (int at = 0; !fork && ok && at < ntiles; ++at) {
         const int st = at & 1, nx = (at + 1) & 1;
         const bool more = at + 1 < ntiles;
         ok = wait_warp(&S->vfull[st], (at >> 1) & 1, S, limit_ns) &&
@@ -622,7 +655,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     bool ok = wait_warp(&S->ready, 0, S, limit_ns);
     // ---- softmax: two threads a row --------------------------------------------------------
     const int tile = warp >> 3, half = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
-    const int r = tile * kTile + lr;
+    const int r = fork ? lr : tile * kTile + lr;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = tl + tile * kTile + kHalf * half, tO = tl + 2 * kTile + tile * kTile;
     // The two warps of a row, w and w + 4, meet at a named barrier (an mbarrier, with its
@@ -637,9 +670,11 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     int walk = node;                   // the next node of the path that is not yet masked
     float mref = -INFINITY, l = 0.f;   // of c s; l: this half's
     bool poison = false;
-    if (tile == 0 || two) {
-      for (int i = i0; i < i1; ++i) {
-        const int at = i - i0;
+    if (tile == 0 || two || fork) {
+      const int step = fork ? 2 : 1;
+      const int mine_of = fork ? (ntiles + 1 - tile) >> 1 : ntiles;  // this group's key tiles
+      for (int at = 0; at < mine_of; ++at) {
+        const int i = i0 + (fork ? tile : 0) + step * at;
         int seg, j0, len;
         tile_of(i, seg, j0, len);
         ok = wait_warp(&S->sfull[tile], at & 1, S, limit_ns) && ok;
@@ -717,24 +752,39 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         l += sum;
         if (seg == kOwn) {
           // (the V tile is read behind its barrier: its bits are written by then)
-          ok = wait_warp(&S->vfull[at & 1], (at >> 1) & 1, S, limit_ns) && ok;
+          const int st = (i - i0) & 1;
+          ok = wait_warp(&S->vfull[st], ((i - i0) >> 1) & 1, S, limit_ns) && ok;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) poison |= (w[e] & S->badv[at & 1][2 * half + e]) != 0u;
+          for (int e = 0; e < 2; ++e) poison |= (w[e] & S->badv[st][2 * half + e]) != 0u;
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before_sync();
         mbar_arrive_warp(&S->pready[tile]);
       }
       if (ok && ntiles > 0) {
-        ok = wait_warp(&S->pvdone[tile], (ntiles - 1) & 1, S, limit_ns);
+        ok = wait_warp(&S->pvdone[tile], (mine_of - 1) & 1, S, limit_ns);
         tc_fence_after_sync();
       }
       // the row's sum: both halves'
       S->top[tile][half][lr] = l;
       S->poison[tile][half][lr] = poison;
+      if (half == 0) S->mref[tile][lr] = mref;
       mbar_arrive_warp(&S->lsum[tile]);
       ok = wait_warp(&S->lsum[tile], 0, S, limit_ns) && ok;
       l = S->top[tile][0][lr] + S->top[tile][1][lr];
+      // both groups' sums, over the larger maximum: weights f of O and f2 of the other group's
+      float f = 1.f, f2 = 0.f;
+      if (fork) {
+        ok = wait_warp(&S->lsum[tile ^ 1], 0, S, limit_ns) && ok;
+        // (its last product as well)
+        ok = wait_warp(&S->pvdone[tile ^ 1], (((ntiles + tile) >> 1) - 1) & 1, S, limit_ns) && ok;
+        tc_fence_after_sync();
+        const float m2 = S->mref[tile ^ 1][lr], top = fmaxf(mref, m2);
+        f = mref == -INFINITY ? 0.f : ex2(mref - top);
+        f2 = m2 == -INFINITY ? 0.f : ex2(m2 - top);
+        l = f * l + f2 * (S->top[tile ^ 1][0][lr] + S->top[tile ^ 1][1][lr]);
+        mref = top;
+      }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (l NaN: kept)
       const int out = tok * d.Hq + hk * G + (rho - tok * G);
       const size_t slot0 = (size_t)(a.slot0 + split) * d.T * d.Hq, slot = slot0 + out;
@@ -743,12 +793,19 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
         // tiles, which every product has read by now), so that a store covers whole pieces
         // of rows; a lane a row would touch 32 lines an instruction
         unsigned char* stage = smem + L::OFF_Q + warp * 4096;
-        const int row0 = tile * kTile + 32 * (warp & 3);  // the warp's first row of the unit
+        const int row0 = (fork ? 0 : tile * kTile) + 32 * (warp & 3);  // the warp's first row of the unit
+        const int e0 = fork ? tile : 0, e1 = fork ? min(tile + 1, DP / 64) : DP / 64;
 #pragma unroll 1
-        for (int e = 0; e < DP / 64; ++e) {
+        for (int e = e0; e < e1; ++e) {
           const int col = DP / 2 * half + 32 * e;
           float y[32];
-          if (ntiles > 0) {
+          if (fork) {
+            float z[32];
+            tmem_ld_32cols(tO + col, y);
+            tmem_ld_32cols(tl + 2 * kTile + (tile ^ 1) * kTile + col, z);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = fmaf(f, y[j], f2 * z[j]);
+          } else if (ntiles > 0) {
             tmem_ld_32cols(tO + col, y);
           } else {
 #pragma unroll
@@ -789,9 +846,11 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
           __syncwarp();
         }
         // (either half may have seen them)
-        if ((S->poison[tile][0][lr] | S->poison[tile][1][lr]) != 0 && live)
-          add_nonfinite(a, out, slot, first, node, hk, DP / 2 * half, DP / 2 * (half + 1));
-        if (live && half == 0) {
+        int bad = S->poison[tile][0][lr] | S->poison[tile][1][lr];
+        if (fork) bad |= S->poison[tile ^ 1][0][lr] | S->poison[tile ^ 1][1][lr];
+        if (bad != 0 && live && e0 < e1)
+          add_nonfinite(a, out, slot, first, node, hk, DP / 2 * half + 32 * e0, DP / 2 * half + 32 * e1);
+        if (live && half == 0 && (tile == 0 || !fork)) {
           const float z = l == 0.f ? -INFINITY : (mref + log2f(l)) * kLn2;
           if (a.part_o) a.part_lse[slot] = z;
           else if (a.lse) a.lse[out] = z;
@@ -925,15 +984,15 @@ size_t part_floats(const gdn_tree_attend_dims& d, const Plan& p) {
   return (size_t)p.slots * d.T * d.Hq * d.D;
 }
 
-template <int DP>
+template <int DP, bool kFork>
 cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[5], long long blocks,
                          cudaStream_t stream) {
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP>,
+  cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<DP, kFork>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<DP>::kBytes);
   if (err != cudaSuccess) return err;
-  attend_tc_kernel<DP><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
+  attend_tc_kernel<DP, kFork><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
       t, map[0], map[1], map[2], map[3], map[4], wait_hooks().limit_ns);
   return cudaGetLastError();
 }
@@ -987,16 +1046,22 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   const int G = d.Hq / d.Hkv;
   t.q_box = d.D % 64 == 0 && kTile % G == 0 && a.scale >= 0.f &&
             encode_q_map(&map[4], a.q, d.T, d.Hq, d.D, G, kTile / G);
-  auto units = [&](const TcArgs& x, long long blocks) {
-    return d.D <= 64 ? launch_units<64>(x, map, blocks, stream)
-                     : launch_units<128>(x, map, blocks, stream);
+  // Units of at most 128 rows (`rows`: the most that one can have) have their key tiles taken by
+  // turns.  Measured against one group of warps for all: 32 trees of 32 nodes 68.6 and 78.1 us,
+  // 8 of them 37.5 and 45.0, 64-node trees with one query head a key head 70.1 and 73.9.
+  auto units = [&](const TcArgs& x, long long blocks, long long rows) {
+    if (rows <= kTile)
+      return d.D <= 64 ? launch_units<64, true>(x, map, blocks, stream)
+                       : launch_units<128, true>(x, map, blocks, stream);
+    return d.D <= 64 ? launch_units<64, false>(x, map, blocks, stream)
+                     : launch_units<128, false>(x, map, blocks, stream);
   };
   cudaError_t err = cudaSuccess;
   if (p.shared) {
     t.prefix_units = true;
     t.splits = p.prefix_splits;
     t.tiles = p.prefix_tiles;
-    err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits);
+    err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits, (long long)d.T * G);
     if (err != cudaSuccess) return err;
   }
   // sequences of few rows, with the prefix's parts added up on the spot (there are none where
@@ -1012,7 +1077,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   t.tiles = p.seq_tiles;
   t.by_length = d.B > 1 && d.B <= kMaxRanked && p.seq_splits == 1 &&
                 (long long)d.B * d.Hkv * p.seq_tiles > sm_count();
-  err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits);
+  err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits, (long long)d.N * G);
   if (err != cudaSuccess || !p.slots) return err;
   const int groups = (int)(((long long)d.N * d.Hq + 7) / 8);
   if ((long long)d.B * groups > 0x7fffffffll) return cudaErrorInvalidConfiguration;
