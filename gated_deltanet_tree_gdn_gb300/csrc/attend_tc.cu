@@ -920,20 +920,21 @@ struct Plan {
   int slots = 0;           // parts of a row (0: the kernel writes o itself)
 };
 
-// Which units there are, by an estimate of the time.  A unit takes about kTileUs for each key
-// tile and kEnds tiles for its start and end, and each SM has one at a time; a part's sums are
-// written and read again, and joined by a launch of its own.
+// Which units there are, by an estimate of the time.  A unit takes 1.6 us for each key tile,
+// 0.95 where it has at most 128 rows, and 8 for its start and end, and each SM has one at a
+// time; a part's sums are written and read again, and joined by a launch of its own.
 //  - Into how many parts a unit's keys are split: what makes the last round full, as long as
-//    the ends and the join do not eat it up.  Measured: 8 units of 33 tiles, in parts of 2, 4,
-//    8 and 16 tiles: 21.5, 21.7, 25.1, 30.4 us.
+//    the ends and the join do not eat it up.  Measured: 8 units of 33 tiles in 4, 8, 12 (taken),
+//    16 and 24 parts 27.7, 23.0, 21.2, 22.5 and 32.1 us.
 //  - Whether the prefix has units of its own, with 256 rows from several sequences each, or
-//    every sequence reads it.  Measured (32 query and 8 key heads, 512 own rows; with / without):
-//    32 sequences of 1 row, prefix of 1024 rows 25 / 50 us, of 16384 rows 43 / 475 us; of 16
-//    nodes 60 / 51 and 152 / 384 us; of 64 nodes, whose units are full, 115 / 60 and 477 / 423
-//    us; 4 sequences of 16 nodes 30 / 18 and 45 / 61 us.
+//    every sequence reads it.  Measured (32 query and 8 key heads, 512 own rows; with / without,
+//    the prefix of 1024, 4096 and 16384 rows): 32 sequences of 1 row 24 / 41, 35 / 106 and 44 /
+//    344 us; of 8 nodes 59 / 44, 69 / 88 and 106 / 262; of 31 nodes 79 / 46, 116 / 90 and 263 /
+//    264; of 64 nodes, whose units are full, 115 / 61, 188 / 134 and 481 / 429; 4 sequences of
+//    8 nodes 25 / 16, 29 / 22 and 40 / 46, of 31 nodes 28 / 18, 34 / 24 and 56 / 48.
 Plan plan_of(const gdn_tree_attend_dims& d) {
-  constexpr float kTileUs = 1.6f, kJoinUs = 5.f, kPartBytesPerUs = 6e6f;
-  constexpr int kEnds = 5;
+  constexpr float kTileUs = 1.6f, kTileUs1 = 0.95f, kEndsUs = 8.f, kJoinUs = 5.f;
+  constexpr float kPartBytesPerUs = 6e6f;
   Plan p;
   p.tc = d.dtype == GDN_TREE_BF16;
   if (!p.tc) return p;
@@ -941,13 +942,14 @@ Plan plan_of(const gdn_tree_attend_dims& d) {
   const int G = d.Hq / d.Hkv;
   const float part_us = 8.f * d.T * d.Hq * d.D / kPartBytesPerUs;
   auto row_tiles = [](long long r) { return (int)((r + 2 * kTile - 1) / (2 * kTile)); };
-  // n units of so many keys: the parts, and the time; joined: whether there are other parts
-  auto split = [&](long long n, long long keys, bool joined, int& parts) {
+  // n units of so many rows and keys: the parts, and the time; joined: whether there are others
+  auto split = [&](long long n, long long rows, long long keys, bool joined, int& parts) {
+    const float tile_us = rows <= kTile ? kTileUs1 : kTileUs;
     const long long tiles = (keys + kTile - 1) / kTile;
     float best = 0.f;
     parts = 1;
     for (int s = 1; s <= kAttendMaxParts && (s == 1 || s <= tiles); ++s) {
-      const float us = (float)((n * s + sms - 1) / sms) * ((tiles + s - 1) / s + kEnds) * kTileUs +
+      const float us = (float)((n * s + sms - 1) / sms) * ((tiles + s - 1) / s * tile_us + kEndsUs) +
                        (s > 1 || joined ? s * part_us : 0.f) + (s > 1 && !joined ? kJoinUs : 0.f);
       if (s > 1 && us >= best) continue;
       best = us;
@@ -960,13 +962,14 @@ Plan plan_of(const gdn_tree_attend_dims& d) {
   const long long units = (long long)d.B * d.Hkv * p.seq_tiles;
   const long long own = (long long)d.table_width * d.page_size + d.N;
   float us = 0.f;  // the sequences' units read the prefix too
-  if (p.many) us = split(units, own + d.prefix_len, false, p.seq_splits);
+  if (p.many) us = split(units, (long long)d.N * G, own + d.prefix_len, false, p.seq_splits);
   if (d.prefix_len > 0 && d.B > 1) {
     if (!p.many) attend_few_cluster(d, d.prefix_len, &us);
     int prefix_splits, seq_splits = 0;
     const int prefix_tiles = row_tiles((long long)d.T * G);
-    float with = split((long long)d.Hkv * prefix_tiles, d.prefix_len, true, prefix_splits), rest;
-    if (p.many) rest = split(units, own, true, seq_splits) + kJoinUs;
+    float with = split((long long)d.Hkv * prefix_tiles, (long long)d.T * G, d.prefix_len, true,
+                       prefix_splits), rest;
+    if (p.many) rest = split(units, (long long)d.N * G, own, true, seq_splits) + kJoinUs;
     else attend_few_cluster(d, 0, &rest);
     if (with + rest < us) {
       p.shared = true;
