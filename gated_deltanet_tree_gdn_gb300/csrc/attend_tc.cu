@@ -77,6 +77,9 @@ struct TcArgs {
   bool own_box;        // the tree's own rows come by TMA
   bool q_box;          // Q too: G divides a tile, and the scale is not negative
   bool by_length;      // units of long contexts first (more units than SMs, kMaxRanked sequences at most)
+  int rank0;           // then the first sequence of this launch, by length
+  bool before_rest;    // a launch of the other sequences follows, and may start
+  bool rest;           // this is that launch
 };
 
 constexpr uint32_t kBarBytes = 6144;
@@ -332,7 +335,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   if (warp == 0 && !a.prefix_units) {
     int b = u / a.tiles, first, stop, ctx;
     if (a.by_length) {
-      b = ranked(a.ctx, a.cu, d.B, b, lane, first, stop, ctx);
+      b = ranked(a.ctx, a.cu, d.B, a.rank0 + b, lane, first, stop, ctx);
     } else {
       stop = a.cu[b + 1];
       first = a.cu[b];
@@ -360,8 +363,9 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     mbar_fence_init();
   }
   if (warp == kWarpMma) tmem_alloc(&S->tmem, 512);
-  // (attend_few.cu may start; it waits for this kernel's end before it reads its parts)
-  if (a.prefix_units) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (attend_few.cu may start; it waits for this kernel's end before it reads its parts.  So may
+  // the launch of the rest, one CTA of which waits for this one's end before its own)
+  if (a.prefix_units || a.before_rest) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
@@ -379,12 +383,14 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
     }
   }
   const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
-  const int r0 = first * G + t * 2 * kTile;
+  constexpr int kUnitRows = kFork ? kTile : 2 * kTile;
+  const int r0 = first * G + t * kUnitRows;
   if (!mine || r0 >= rows_end) {
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+    if (a.rest && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  const int rows = min(2 * kTile, rows_end - r0);
+  const int rows = min(kUnitRows, rows_end - r0);
   const bool two = !kFork && rows > kTile;
   const bool own = a.k != nullptr && !a.prefix_units;
   const bool tree = own && a.parent != nullptr;
@@ -862,6 +868,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   __syncthreads();
   tc_fence_after_sync();
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (a.rest && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && S->abort && a.dev_status) {
     if (a.prefix_units)
       for (int bb = 0; bb < d.B; ++bb) atomicMax(a.dev_status + bb, GDN_TREE_STATUS_TIMEOUT);
@@ -995,9 +1002,19 @@ cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[5], long long
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Smem<DP>::kBytes);
   if (err != cudaSuccess) return err;
-  attend_tc_kernel<DP, kFork><<<(unsigned)blocks, kThreads, Smem<DP>::kBytes, stream>>>(
-      t, map[0], map[1], map[2], map[3], map[4], wait_hooks().limit_ns);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<DP>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = t.rest ? 1 : 0;
+  err = cudaLaunchKernelEx(&cfg, attend_tc_kernel<DP, kFork>, t, map[0], map[1], map[2], map[3],
+                           map[4], wait_hooks().limit_ns);
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
@@ -1080,7 +1097,26 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   t.tiles = p.seq_tiles;
   t.by_length = d.B > 1 && d.B <= kMaxRanked && p.seq_splits == 1 &&
                 (long long)d.B * d.Hkv * p.seq_tiles > sm_count();
-  err = units(t, (long long)d.B * d.Hkv * p.seq_tiles * p.seq_splits, (long long)d.N * G);
+  // What a last round of the SMs would be too few for goes in units of half the rows, beside
+  // the others' last ones: 32 trees of 128 nodes (512 units, 56 in the last round) 164.8 to
+  // 161.5 us, with 4096 own rows each 290 to 273 us.
+  const long long each = (long long)d.Hkv * p.seq_tiles, sms = sm_count() > 0 ? sm_count() : 152;
+  const long long half_tiles = ((long long)d.N * G + kTile - 1) / kTile;
+  int halved = 0;
+  if (t.by_length && half_tiles > 1) {
+    const long long left = d.B * each % sms;
+    halved = (int)((left + each - 1) / each);
+    if (halved * d.Hkv * half_tiles > sms) halved = 0;
+  }
+  t.before_rest = halved > 0;
+  err = units(t, (d.B - halved) * each * p.seq_splits, (long long)d.N * G);
+  if (err == cudaSuccess && halved > 0) {
+    t.before_rest = false;
+    t.rest = true;
+    t.rank0 = d.B - halved;
+    t.tiles = (int)half_tiles;
+    err = units(t, halved * d.Hkv * half_tiles, kTile);
+  }
   if (err != cudaSuccess || !p.slots) return err;
   const int groups = (int)(((long long)d.N * d.Hq + 7) / 8);
   if ((long long)d.B * groups > 0x7fffffffll) return cudaErrorInvalidConfiguration;

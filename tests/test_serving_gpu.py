@@ -330,13 +330,13 @@ def run_attend(x, chain=False, **kw):
                      prefix_len=x["prefix"], **kw)
 
 
-def check_attend(o, lse, x, chain=False, scale=None):
+def check_attend(o, lse, x, chain=False, scale=None, rows=slice(None)):
     opt = lambda t: None if t is None else host(t)  # noqa: E731
     ro, rl, ra = ref.attend(host(x["q"]), opt(x["k"]), opt(x["v"]), None if chain else x["parent"],
                             x["cu"], host(x["k_cache"]), host(x["v_cache"]), x["table"], x["ctx"],
                             x["prefix_pages"], x["prefix"],
                             x["q"].shape[2] ** -0.5 if scale is None else scale)
-    o, lse = host(o), host(lse)
+    o, lse, ro, rl, ra = (t[rows] for t in (host(o), host(lse), ro, rl, ra))
     bf16 = x["q"].dtype == torch.bfloat16
     top = np.max(np.abs(ra)) if ra.size else 0.0
     bound = (EPS_BF16 * (np.abs(ro) + ra) if bf16 else 0.0) + TOL_F32 * top
@@ -399,6 +399,31 @@ LONG = [
     ([1] * 30, [5] * 30, 4000, 16, 4, 128, 128, "bf16"),
     ([1, 2], [2500, 100], 300, 4, 2, 128, 24, "f32"),
 ]
+
+
+MANY = [
+    # more units than SMs, and a last round of few: the shortest contexts in smaller units
+    ([70] * 20, [37 * (i * 7 % 20) for i in range(20)], 40, 16, 4, 128, 64, "bf16"),
+    ([70, 3, 1, 40] * 5 + [66], [11 * (i * 5 % 21) for i in range(21)], 0, 16, 4, 64, 16, "bf16"),
+    ([150] * 10, [0] * 9 + [200], 0, 8, 8, 128, 32, "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=["equal", "ragged", "one-head"])
+@pytest.mark.parametrize("tree", ["random", "chain"])
+def test_attend_many_units(case, tree):
+    x = attend_inputs(*case, seed=len(case[0]) + case[2], tree=tree)
+    status = torch.full((len(case[0]),), -7, dtype=torch.int32, device="cuda")
+    o, lse = run_attend(x, chain=tree == "chain", dev_status=status)
+    assert (status == 0).all()
+    check_attend(o, lse, x, chain=tree == "chain")
+    # sequences with a length that cannot be are reported, and no other's rows change
+    bad = np.arange(len(x["ctx"])) % 6 == 5
+    o, lse = run_attend(dict(x, ctx=np.where(bad, -1, x["ctx"])), chain=tree == "chain",
+                        dev_status=status)
+    assert (status.cpu().numpy() == np.where(bad, gt.STATUS_BAD_LAYOUT, 0)).all()
+    check_attend(o, lse, dict(x, ctx=np.where(bad, 0, x["ctx"])), chain=tree == "chain",
+                 rows=np.flatnonzero(np.repeat(~bad, np.diff(x["cu"]))))
 
 
 @pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)).replace(" ", "")[:60])
