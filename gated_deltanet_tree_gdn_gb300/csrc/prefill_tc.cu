@@ -533,9 +533,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
 // ---- second kernel: the chunks of a sequence, 32 value columns a chain ---------------------
 // A CTA runs one chain of dependent steps (3800 cycles a chunk, of which its MMAs are 1250),
 // or two, over the same keys, queries and [T; Z], whose steps fill one another's waits (6300
-// cycles for both): two where one a CTA would take more than a round of the SMs.  Measured,
-// one and two a CTA: 2048 tokens of 32 heads (128 chains) 103 and 149 us, of 40 heads (160)
-// 176 and 162, of 64 heads 198 and 180; 16 ragged prompts of 32 heads 538 and 498.
+// cycles for both): two where that takes the SMs fewer cycles in all.  Measured, one and two a
+// CTA: 2048 tokens of 32 heads (128 chains) 103 and 149 us, of 40 heads (160) 167 and 150.
 constexpr int kChainThreads = 256;   // two threads a TMEM lane, 16 columns each
 constexpr int kStages = 2;
 // right-hand operands: rows of 3 x 32 bf16 (hi, mid | lo, unused) in two 64-column atoms; S
@@ -1005,9 +1004,19 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   if (err != cudaSuccess) return err;
   Segment s = plan(d, a.lay.T);
   const long long slots = s.dense ? dense_slots(a.lay.T, d.B) : (long long)s.span * d.B;
-  // one chain a CTA while there is an SM for each
+  // One chain a CTA or two: the rounds of the SMs, as if the rows were T / N sequences of the
+  // longest's length, times 3800 or 6300 cycles a chunk.  Sequences of one length take whole
+  // rounds; others, the longest first, fill them up.  Measured, one and two, with 32 heads: 2 and
+  // 3 sequences of 1000 tokens 101 and 88, 148 and 152 us, 16 of them 677 and 587; 16 of 17 to
+  // 2048 496 and 421; 8 of 17 to 4096 243 and 282; 4 of 627 to 3354 441 and 402; with 16 heads 3
+  // of 4 to 12220 468 and 711.
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  const bool two = (long long)d.B * d.Hv * Scan<1>::kSlices > sms;
+  const float full = d.N > 0 ? fminf((float)a.lay.T / d.N, (float)d.B) : (float)d.B;
+  auto rounds = [&](int slices) {
+    const float x = full * d.Hv * slices / sms;
+    return full >= 0.9f * d.B ? ceilf(x) : fmaxf(x, 1.f);
+  };
+  const bool two = 63.f * rounds(Scan<2>::kSlices) < 38.f * rounds(Scan<1>::kSlices);
   const long long scan = (long long)d.B * d.Hv * (two ? Scan<2>::kSlices : Scan<1>::kSlices);
   if (slots * d.Hv > 0x7fffffffll || scan > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   // in more than a round of the SMs the long sequences go first, so that the SMs end closer
