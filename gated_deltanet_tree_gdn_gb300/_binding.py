@@ -509,6 +509,19 @@ def _workspace(given, need, device):
         need, dtype=torch.uint8, device=device)
 
 
+_struct_cache: dict = {}
+
+
+def _struct(kind, *key):
+    """kind(*key), kept by its values to save the rebuild."""
+    d = _struct_cache.get((kind, key))
+    if d is None:
+        d = kind(*key)
+        if len(_struct_cache) < 256:
+            _struct_cache[kind, key] = d
+    return d
+
+
 _prefill_cache: dict = {}
 
 
@@ -597,7 +610,7 @@ def decode_step(q, k, v, log_alpha, beta, state_pool, *, state_slot=None, pool_o
         _check(dev_status, "dev_status", torch.int32, (B,))
     rc = load().gdn_tree_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                      _ptr(state_pool), _ptr(pool_out), _ptr(state_slot), n_slots,
-                                     _ptr(o), Dims(B, 1, Hqk, Hv, dk, dv, code),
+                                     _ptr(o), _struct(Dims, B, 1, Hqk, Hv, dk, dv, code),
                                      _ptr(dev_status), _stream(stream))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_decode_step")
@@ -716,7 +729,7 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
     _check(new_len, "new_len", torch.int32, (B,))
     if dev_status is not None:
         _check(dev_status, "dev_status", torch.int32, (B,))
-    d = AttendDims(B, T, N_max, Hkv, Hkv, D, code, page, n_pages, width, 0)
+    d = _struct(AttendDims, B, T, N_max, Hkv, Hkv, D, code, page, n_pages, width, 0)
     rc = load().gdn_tree_cache_append(_ptr(k), _ptr(v), _ptr(path), _ptr(path_len), Lmax,
                                       _ptr(cu_nodes), _ptr(k_cache), _ptr(v_cache),
                                       _ptr(page_table), _ptr(context_len), _ptr(new_len), d,
