@@ -44,7 +44,8 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2& a, float2&
 // the 16 before are computed.  Row 32 i + 4 (row group) + e: a warp's reads of k and q are
 // consecutive.  (Two columns a lane: with one, reading k and q takes as long as the chain.)
 // 0.21 us a token (fp32, 128 x 128 states, 4 heads); 16 sequences of 500 tokens with 32 heads
-// take 0.99 ms, 20 TFLOP/s.  One barrier a token and 32 columns over a CTA took twice as long.
+// take 0.99 ms, 20 TFLOP/s.  One barrier a token and 32 columns over a CTA took twice as long;
+// two tokens a turn, with one round of shuffles for both, 0.26 us a token and 1.14 ms.
 constexpr int kStage = 16;
 
 template <typename T, int kI, int kWarps>  // dk <= 32 kI
@@ -364,9 +365,9 @@ cudaError_t launch_recurrent(const RuleArgs& a, bool step, cudaStream_t stream) 
 
 // The chunked kernels from kChunkedFrom tokens of the longest sequence on.  Below it their two
 // launches and a whole chunk's work cost more than the tokens one by one.  Measured with 32
-// heads, chunked and one by one, in us: 1 sequence of 16 tokens 15.7 and 7.8, of 32 15.7 and
-// 12.1, of 64 15.9 and 20.5; 4 sequences of 32 26.9 and 26.0, of 40 26.9 and 31.6; 16
-// sequences of 16 80 and 45, of 32 81 and 80, of 40 83 and 98.
+// heads, chunked and one by one, in us: 1 sequence of 16 tokens 13 and 7.8, of 32 13 and 12.1,
+// of 64 13.1 and 20.5; 4 sequences of 32 27 and 26, of 48 27 and 37; 16 sequences of 16 78
+// and 45, of 32 78 and 80, of 48 79 and 117.
 constexpr int kChunkedFrom = 33;
 static bool chunked(const gdn_tree_dims& d, int32_t T) {
   return d.N >= kChunkedFrom && T > 0 && prefill_tc_supported(d);
