@@ -56,6 +56,7 @@ struct Segment {
   int c0, span;
   bool dense;
   bool by_length = false;  // the second kernel takes the longest sequences first
+  bool ahead = false;      // the next segment's first kernel runs beside this one's second
 };
 
 __host__ __device__ inline long long dense_slots(long long T, long long B) { return T / kC + B + 1; }
@@ -224,6 +225,12 @@ __device__ __forceinline__ void block_product(const PrepShared& S, int o, int po
   }
 }
 
+// One CTA of a first kernel that began beside the second kernel of the segment before waits for
+// that one's end, so that whatever follows this kernel follows both.
+__device__ __forceinline__ void scan_done(const Segment& seg) {
+  if (seg.ahead && seg.c0 > 0 && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 __global__ void __launch_bounds__(kPrepThreads, 3)
 prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapQ, const float* __restrict__ log_alpha,
@@ -268,6 +275,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     __syncthreads();
     tc_fence_after_sync();
     if (warp == kWarpTmem) tmem_dealloc(P.tmem, 128);
+    scan_done(seg);
     return;
   }
   const int nc = min(kC, n - c * kC);
@@ -528,6 +536,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   tc_fence_after_sync();
   if (tid == 0 && P.abort && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
   if (warp == kWarpTmem) tmem_dealloc(tmem, 128);
+  scan_done(seg);
 }
 
 // ---- second kernel: the chunks of a sequence, 32 value columns a chain ---------------------
@@ -671,6 +680,8 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
                     gdn_tree_dims d, SeqLayout lay, Segment seg, const unsigned char* ws,
                     int32_t* dev_status, uint64_t limit_ns) {
   using L = Scan<kChains>;
+  // (the next segment's T and Z go to the other half of the workspace)
+  if (seg.ahead) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -957,10 +968,23 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
   if (warp == L::kWarpMma) tmem_dealloc(tmem0, L::kTmemColumns);
 }
 
-// the segments for these dims: chunks a launch pair, and whether one pair does for all
+// The segments for these dims: chunks a launch pair, and whether one pair does for all.  Where
+// the second kernel leaves SMs idle and runs for long, its segments are short, so that the next
+// one's T and Z are computed on those SMs meanwhile, in the other half of the workspace.
+// Measured with 32 heads (24 SMs idle), so and in as few segments as fit: 32768 tokens FIG1 and
+// FIG2 us, 16384 FIG3 and FIG4.
+constexpr int kAheadChunks = 128;
 Segment plan(const gdn_tree_dims& d, long long T) {
   const size_t head = (size_t)d.Hv * kSlotBytes;
   const long long longest = ((long long)d.N + kC - 1) / kC;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  if ((long long)d.B * d.Hv * Scan<1>::kSlices <= sms - 8 && longest >= 2 * kAheadChunks &&
+      2 * kAheadChunks * d.B * head <= kWorkspaceTarget) {
+    const long long count = (longest + kAheadChunks - 1) / kAheadChunks;
+    Segment s{0, (int)((longest + count - 1) / count), false};
+    s.ahead = true;
+    return s;
+  }
   if (dense_slots(T, d.B) * head <= kWorkspaceTarget) return Segment{0, (int)longest, true};
   long long span = (long long)(kWorkspaceTarget / head) / d.B;
   if (span < kMinSegment) span = kMinSegment;
@@ -983,7 +1007,8 @@ bool prefill_tc_supported(const gdn_tree_dims& d) {
 
 size_t prefill_tc_workspace_bytes(const gdn_tree_dims& d, int32_t T) {
   const Segment s = plan(d, T);
-  return (size_t)(s.dense ? dense_slots(T, d.B) : (long long)s.span * d.B) * d.Hv * kSlotBytes;
+  return (size_t)(s.dense ? dense_slots(T, d.B) : (long long)s.span * d.B * (s.ahead ? 2 : 1)) *
+         d.Hv * kSlotBytes;
 }
 
 cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t stream) {
@@ -1032,9 +1057,19 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   const int beside = longest > 0 && longest <= 128;
   for (s.c0 = 0; s.c0 == 0 || s.c0 < longest; s.c0 += s.span) {
     if (longest > 0) {
-      prefill_prep_kernel<<<(unsigned)(slots * d.Hv), kPrepThreads, kPrepBytes, stream>>>(
-          mapK, mapQ, a.log_alpha, a.beta, d, a.lay, s, ws, a.dev_status, limit);
-      if ((err = cudaGetLastError()) != cudaSuccess) return err;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(slots * d.Hv));
+      cfg.blockDim = dim3(kPrepThreads);
+      cfg.dynamicSmemBytes = kPrepBytes;
+      cfg.stream = stream;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = s.ahead && s.c0 > 0;
+      err = cudaLaunchKernelEx(&cfg, prefill_prep_kernel, mapK, mapQ, a.log_alpha, a.beta, d, a.lay,
+                               s, ws, a.dev_status, limit);
+      if (err != cudaSuccess || (err = cudaGetLastError()) != cudaSuccess) return err;
     }
     auto run = [&](auto kernel, int threads, uint32_t bytes) {
       cudaLaunchConfig_t cfg = {};
@@ -1056,6 +1091,9 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
     err = two ? run(prefill_scan_kernel<2>, Scan<2>::kThreads, Scan<2>::kBytes)
               : run(prefill_scan_kernel<1>, Scan<1>::kThreads, Scan<1>::kBytes);
     if (err != cudaSuccess) return err;
+    if (s.ahead)  // the halves by turns
+      ws = static_cast<unsigned char*>(workspace) +
+           (ws == workspace ? (size_t)slots * d.Hv * kSlotBytes : 0);
     if (s.span == 0) break;  // (no tokens at all: the states are copied)
   }
   return cudaSuccess;

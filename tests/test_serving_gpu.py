@@ -233,9 +233,11 @@ def test_decode_step_of_thousands_of_states(B, Hqk, Hv, dk, dtype):
     assert torch.equal(other[:5], o[:5]) and torch.equal(other[6:], o[6:])
 
 
-def test_prefill_in_several_segments():
-    """Batches whose tiles do not fit the workspace at once give what parts of them give."""
-    lens, Hqk, Hv = [20000, 130, 0, 5000, 64], 16, 32
+@pytest.mark.parametrize("lens,Hqk,Hv", [
+    ([20000, 130, 0, 5000, 64], 16, 32),  # all tiles at once would be over 600 MB
+    ([16500], 2, 4), ([100, 17000, 0, 9000], 2, 4)], ids=["batch", "one", "few-heads"])
+def test_prefill_in_several_segments(lens, Hqk, Hv):
+    """Long batches, whose tiles are made in parts, give what parts of them give."""
     T = sum(lens)
     gen = torch.Generator(device="cuda").manual_seed(1)
     normal = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
@@ -244,7 +246,7 @@ def test_prefill_in_several_segments():
     pool = 0.1 * normal(len(lens), Hv, 128, 128)
     cu = cu_of(lens)
     dims = gt.Dims(len(lens), max(lens), Hqk, Hv, 128, 128, gt.BF16)
-    assert gt.prefill_workspace(dims, T) <= 512 << 20  # (all tiles at once would be over 600)
+    assert gt.prefill_workspace(dims, T) <= 512 << 20
     o, out = gt.prefill(q, k, v, la, beta, ints(cu), pool)
     for b, n in enumerate(lens):
         state, a = pool[b:b + 1].clone(), cu[b]
