@@ -25,8 +25,8 @@
 //
 // What bounds it: the chain of dependent steps (MMA, TMEM to registers, split, shared
 // memory, MMA), not bytes or tensor rate.  One sequence of 32768 tokens with 32 heads takes
-// 1.39 ms (0.59 TB/s of inputs and outputs), 1.0 ms of it in the second kernel's chains and
-// the rest in the first kernel; 16 ragged prompts of 17 to 2048 tokens 416 us.
+// 1.27 ms (0.64 TB/s of inputs and outputs), 1.0 ms of it in the second kernel's chains and
+// the rest in what of the first kernel does not fit beside them; 16 ragged prompts of 17 to 2048 tokens 416 us.
 #include <string.h>
 
 #include "common.cuh"
@@ -971,16 +971,18 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
 // The segments for these dims: chunks a launch pair, and whether one pair does for all.  Where
 // the second kernel leaves SMs idle and runs for long, its segments are short, so that the next
 // one's T and Z are computed on those SMs meanwhile, in the other half of the workspace.
-// Measured with 32 heads (24 SMs idle), so and in as few segments as fit: 32768 tokens FIG1 and
-// FIG2 us, 16384 FIG3 and FIG4.
+// Measured with 32 heads (24 SMs idle), so and in as few segments as fit: 32768 tokens 1273 and
+// 1377 us, 16384 660 and 688, 8192 342 and 353; with 2 heads, where the chains are all, 16384
+// tokens 519 and 518.  Segments of 64 chunks 1301 us (32768 tokens), of 32 1376.
 constexpr int kAheadChunks = 128;
 Segment plan(const gdn_tree_dims& d, long long T) {
   const size_t head = (size_t)d.Hv * kSlotBytes;
   const long long longest = ((long long)d.N + kC - 1) / kC;
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  if ((long long)d.B * d.Hv * Scan<1>::kSlices <= sms - 8 && longest >= 2 * kAheadChunks &&
+  if ((long long)d.B * d.Hv * Scan<1>::kSlices <= sms - 8 && longest >= kAheadChunks &&
       2 * kAheadChunks * d.B * head <= kWorkspaceTarget) {
-    const long long count = (longest + kAheadChunks - 1) / kAheadChunks;
+    long long count = (longest + kAheadChunks - 1) / kAheadChunks;
+    if (count < 2) count = 2;
     Segment s{0, (int)((longest + count - 1) / count), false};
     s.ahead = true;
     return s;
@@ -1052,9 +1054,10 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   const int longest = (d.N + kC - 1) / kC;
   // The second kernel starts beside the first one's last CTAs, unless the sequences are long.
   // Measured with 32 heads, so and one after the other: 512 tokens 38.0 and 41.4 us, 4 times
-  // 512 105 and 109, 4096 200 and 203, 8192 380 and 384, but 16384 790 and 744, 32768 (two
-  // rounds) 1566 and 1486: the chains that start first then run slower to the end.
-  const int beside = longest > 0 && longest <= 128;
+  // 512 105 and 109, 4096 200 and 203, but 16384 790 and 744, 32768 1566 and 1486: the chains
+  // that start first then run slower to the end.  (Not with segments made ahead: the states
+  // that it reads first are then the second kernel's of the segment before, which may run.)
+  const int beside = longest > 0 && longest <= kAheadChunks && !s.ahead;
   for (s.c0 = 0; s.c0 == 0 || s.c0 < longest; s.c0 += s.span) {
     if (longest > 0) {
       cudaLaunchConfig_t cfg = {};

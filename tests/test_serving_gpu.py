@@ -235,7 +235,8 @@ def test_decode_step_of_thousands_of_states(B, Hqk, Hv, dk, dtype):
 
 @pytest.mark.parametrize("lens,Hqk,Hv", [
     ([20000, 130, 0, 5000, 64], 16, 32),  # all tiles at once would be over 600 MB
-    ([16500], 2, 4), ([100, 17000, 0, 9000], 2, 4)], ids=["batch", "one", "few-heads"])
+    ([16500], 2, 4), ([8200], 4, 4), ([100, 17000, 0, 9000], 2, 4)],
+    ids=["batch", "one", "two-halves", "few-heads"])
 def test_prefill_in_several_segments(lens, Hqk, Hv):
     """Long batches, whose tiles are made in parts, give what parts of them give."""
     T = sum(lens)
