@@ -228,8 +228,8 @@ __device__ __forceinline__ void block_product(const PrepShared& S, int o, int po
 
 // One CTA of a first kernel that began beside the second kernel of the segment before waits for
 // that one's end, so that whatever follows this kernel follows both.
-__device__ __forceinline__ void scan_done(const Segment& seg) {
-  if (seg.ahead && seg.c0 > 0 && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void scan_done() {
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kPrepThreads, 3)
@@ -276,7 +276,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     __syncthreads();
     tc_fence_after_sync();
     if (warp == kWarpTmem) tmem_dealloc(P.tmem, 128);
-    scan_done(seg);
+    scan_done();
     return;
   }
   const int nc = min(kC, n - c * kC);
@@ -537,7 +537,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   tc_fence_after_sync();
   if (tid == 0 && P.abort && dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_TIMEOUT);
   if (warp == kWarpTmem) tmem_dealloc(tmem, 128);
-  scan_done(seg);
+  scan_done();
 }
 
 // ---- second kernel: the chunks of a sequence, 32 value columns a chain ---------------------
@@ -681,8 +681,6 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
                     gdn_tree_dims d, SeqLayout lay, Segment seg, const unsigned char* ws,
                     int32_t* dev_status, uint64_t limit_ns) {
   using L = Scan<kChains>;
-  // (the next segment's T and Z go to the other half of the workspace)
-  if (seg.ahead) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem[];
   ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -745,6 +743,8 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
 
   if (warp == L::kWarpLoad) {
     prep_done();
+    // (the next segment's first kernel, where its launch asks for it, may start now)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const unsigned char* tz = ws + (slot_of(seg, lay.cu, b, seg.c0) * d.Hv + h) * (size_t)kSlotBytes;
     for (int c = seg.c0; run && c < c_end; ++c) {
       const int i = c - seg.c0, s = i % kStages;
@@ -972,7 +972,7 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
 // The segments for these dims: chunks a launch pair, and whether one pair does for all.  Where
 // the second kernel leaves SMs idle and runs for long, its segments are short, so that the next
 // one's T and Z are computed on those SMs meanwhile, in the other half of the workspace.
-// Measured with 32 heads (24 SMs idle), so and in as few segments as fit: 32768 tokens 1273 and
+// Measured with 32 heads (24 SMs idle), so and in as few segments as fit: 32768 tokens 1266 and
 // 1377 us, 16384 660 and 688, 8192 342 and 353; with 2 heads, where the chains are all, 16384
 // tokens 519 and 518.  Segments of 64 chunks 1301 us (32768 tokens), of 32 1376.
 constexpr int kAheadChunks = 128;
