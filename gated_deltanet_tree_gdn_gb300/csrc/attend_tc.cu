@@ -73,6 +73,7 @@ struct TcArgs {
   int tiles;        // 256-row blocks a sequence (a batch, for prefix units)
   bool prefix_units;   // units of the shared prefix over the whole batch
   bool with_prefix;    // a sequence's units include the prefix
+  bool few;            // sequences of at most kAttendFewRows rows are attend_few.cu's
   int box_rows;        // rows of a TMA box of the cache (0: cache rows come by cp.async)
   bool own_box;        // the tree's own rows come by TMA
   bool q_box;          // Q too: G divides a tile, and the scale is not negative
@@ -379,7 +380,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
       mine = false;
     } else {
-      mine = n * G > kAttendFewRows;  // (else attend_few.cu's)
+      mine = !a.few || n * G > kAttendFewRows;  // (else attend_few.cu's)
     }
   }
   const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
@@ -880,14 +881,14 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
 // ---- joining the parts: a warp a row (node * Hq + h of sequence b) -----------------------
 __global__ void __launch_bounds__(256)
 attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse, int slots,
-                   const int32_t* __restrict__ cu, gdn_tree_attend_dims d, int groups,
+                   const int32_t* __restrict__ cu, gdn_tree_attend_dims d, int groups, bool few,
                    __nv_bfloat16* __restrict__ o, float* __restrict__ lse) {
   const int b = blockIdx.x / groups, lane = threadIdx.x & 31, D = d.D;
   const int first = cu[b], stop = cu[b + 1];
   const long long at = (long long)(blockIdx.x % groups) * 8 + (threadIdx.x >> 5);
   // (a sequence whose rows are out of range was reported, and has no parts)
   if (first < 0 || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq ||
-      (stop - first) * (d.Hq / d.Hkv) <= kAttendFewRows)  // (attend_few.cu adds those up itself)
+      (few && (stop - first) * (d.Hq / d.Hkv) <= kAttendFewRows))  // (attend_few.cu adds those up itself)
     return;
   const size_t rows = (size_t)d.T * d.Hq, row = (size_t)first * d.Hq + at;
   float top = -INFINITY;
@@ -1084,9 +1085,11 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
     err = units(t, (long long)d.Hkv * p.prefix_tiles * p.prefix_splits, (long long)d.T * G);
     if (err != cudaSuccess) return err;
   }
-  // sequences of few rows, with the prefix's parts added up on the spot (there are none where
-  // all have N rows, and N are many)
-  if (!p.many || d.T < (long long)d.B * d.N)
+  // Sequences of few rows, with the prefix's parts added up on the spot.  Where there are as many
+  // rows as a batch of N each has, that launch is saved and the units take all sequences:
+  // then all have N rows, which are many, or the arrays are larger than what is in them.
+  t.few = !p.many || d.T != (long long)d.B * d.N;
+  if (t.few)
     err = launch_attend_few(a, p.shared ? 0 : d.prefix_len, t.part_o, t.part_lse, p.prefix_splits,
                             stream);
   if (err != cudaSuccess || !p.many) return err;
@@ -1121,7 +1124,7 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t stream) {
   const int groups = (int)(((long long)d.N * d.Hq + 7) / 8);
   if ((long long)d.B * groups > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   attend_join_kernel<<<(unsigned)(d.B * groups), 256, 0, stream>>>(
-      t.part_o, t.part_lse, p.slots, t.cu, d, groups, t.o, t.lse);
+      t.part_o, t.part_lse, p.slots, t.cu, d, groups, t.few, t.o, t.lse);
   return cudaGetLastError();
 }
 
