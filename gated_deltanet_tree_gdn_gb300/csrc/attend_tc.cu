@@ -383,14 +383,16 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       mine = !a.few || n * G > kAttendFewRows;  // (else attend_few.cu's)
     }
   }
-  const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
   constexpr int kUnitRows = kFork ? kTile : 2 * kTile;
-  const int r0 = first * G + t * kUnitRows;
-  if (!mine || r0 >= rows_end) {
+  // (units past the sequence's rows, whose row numbers may be past 32 bits)
+  const long long unit0 = (long long)t * kUnitRows;
+  if (!mine || unit0 >= (long long)(a.prefix_units ? d.T : n) * G) {
     if (warp == kWarpMma) tmem_dealloc(tmem, 512);
     if (a.rest && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+  const int rows_end = a.prefix_units ? d.T * G : (first + n) * G;
+  const int r0 = first * G + (int)unit0;
   const int rows = min(kUnitRows, rows_end - r0);
   const bool two = !kFork && rows > kTile;
   const bool own = a.k != nullptr && !a.prefix_units;

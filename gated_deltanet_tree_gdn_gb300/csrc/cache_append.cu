@@ -7,6 +7,8 @@
 // kThreads / lanes rows of one sequence, as many lanes a row (a power of two, a warp at most)
 // as it has 16-byte pieces, k and v together.  16 prompts of 17 to 4096 rows of 8 heads of 128
 // bf16 take 32 us (5.8 TB/s read and written); 32 paths of up to 24 rows 3 us.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -76,10 +78,13 @@ cache_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
   const gdn_tree_attend_dims& d = a.d;
   const int vecs = d.Hkv * d.D * (d.dtype == GDN_TREE_BF16 ? 2 : 4) / 16;
-  const int most = a.path ? a.Lmax : d.N;
+  // (the first row past the last page is reported for all of them: what lies behind it is not
+  // looked at, however long the paths may be)
+  const long long room = (long long)d.table_width * d.page_size + 1;
+  const long long most = std::min<long long>(a.path ? a.Lmax : d.N, room);
   int lanes = 1;
   while (lanes < 32 && lanes < vecs) lanes *= 2;
-  const int groups = most > 0 ? (int)(((long long)most * lanes + kThreads - 1) / kThreads) : 1;
+  const int groups = most > 0 ? (int)((most * lanes + kThreads - 1) / kThreads) : 1;
   const long long blocks = (long long)d.B * groups;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cache_append_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(

@@ -69,6 +69,10 @@ int check_rule_dims(gdn_tree_dims d) {
   return check_dims(d);
 }
 
+// N, the most rows of a sequence, is a promise of any size: no more than all T rows count, and
+// what is worked out from it then fits its types and no unit lies past the rows
+int bounded_rows(int N, int T) { return N < T ? N : T; }
+
 int check_attend_dims(const gdn_tree_attend_dims& d) {
   if (d.B < 0 || d.T < 0 || d.N < 0 || d.Hq <= 0 || d.Hkv <= 0 || d.D <= 0 || d.page_size < 1 ||
       d.n_pages < 0 || d.table_width < 0 || d.prefix_len < 0)
@@ -464,12 +468,14 @@ int gdn_tree_prefill(const void* q, const void* k, const void* v, const float* l
   rc = check_packed(cu_tokens, T, state_slot, n_slots, dims.B, &lay);
   if (rc != GDN_TREE_OK) return rc;
   if (dims.B == 0) return GDN_TREE_OK;  // nothing to do
+  dims.N = bounded_rows(dims.N, T);
   return rule_call(q, k, v, log_alpha, beta, pool_in, pool_out, o, dims, lay, T, dev_status,
                    false, workspace, workspace_bytes, stream);
 }
 
 size_t gdn_tree_prefill_workspace(gdn_tree_dims dims, int32_t T) {
   if (check_rule_dims(dims) != GDN_TREE_OK || dims.B == 0 || T <= 0) return 0;
+  dims.N = bounded_rows(dims.N, T);
   return gdn::prefill_workspace_bytes(dims, T);
 }
 
@@ -493,6 +499,7 @@ int gdn_tree_decode_step(const void* q, const void* k, const void* v, const floa
 size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims) {
   if (check_attend_dims(dims) != GDN_TREE_OK || dims.B == 0 || dims.T == 0 || dims.N == 0)
     return 0;
+  dims.N = bounded_rows(dims.N, dims.T);
   return gdn::attend_workspace_bytes(dims);
 }
 
@@ -506,6 +513,7 @@ int gdn_tree_attend(const void* q, const void* k, const void* v, const int32_t* 
   if (rc != GDN_TREE_OK) return rc;
   if (parent && dims.N > gdn::kMaxNLongHost) return GDN_TREE_EUNSUPPORTED;
   if (dims.B == 0 || dims.T == 0 || dims.N == 0) return GDN_TREE_OK;  // nothing to do
+  dims.N = bounded_rows(dims.N, dims.T);
   if ((k == nullptr) != (v == nullptr)) return GDN_TREE_EINVAL;
   const void* need[] = {q, o};
   for (const void* p : need)
@@ -549,6 +557,7 @@ int gdn_tree_cache_append(const void* k, const void* v, const int32_t* path,
     return GDN_TREE_EINVAL;
   if (path_len != nullptr && Lmax < 0) return GDN_TREE_EINVAL;
   if (dims.B == 0) return GDN_TREE_OK;
+  dims.N = bounded_rows(dims.N, dims.T);
   const bool rows = dims.T > 0 && dims.table_width > 0 && dims.n_pages > 0;
   const void* data[] = {k, v, k_cache, v_cache};
   for (const void* p : data)

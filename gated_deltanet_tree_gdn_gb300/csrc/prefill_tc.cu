@@ -1052,7 +1052,7 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   s.by_length = scan > sms && d.B > 1 && d.B <= kMaxRanked;
   const uint64_t limit = wait_hooks().limit_ns;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  const int longest = (d.N + kC - 1) / kC;
+  const int longest = (int)(((long long)d.N + kC - 1) / kC);
   // The second kernel starts beside the first one's last CTAs, unless the sequences are long.
   // Measured with 32 heads, so and one after the other: 512 tokens 38.0 and 41.4 us, 4 times
   // 512 105 and 109, 4096 200 and 203, but 16384 790 and 744, 32768 1566 and 1486: the chains

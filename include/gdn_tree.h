@@ -320,7 +320,7 @@ int gdn_tree_build_topw(const float *cand_logp, int32_t B, int32_t N, int32_t c,
  *               aligned (NULL when that is 0); its contents are not kept
  * A sequence whose rows or slot are out of range gets GDN_TREE_STATUS_BAD_LAYOUT
  * and its outputs are left unwritten (where cu_tokens decreases, the sequences after
- * are unspecified too).  dims.N has no upper limit here.  bf16 with dk = dv = 128 is
+ * are unspecified too).  dims.N has no upper limit here (no more than T count).  bf16 with dk = dv = 128 is
  * computed in chunks of 64 tokens: an infinity or NaN in a token's inputs may reach the
  * outputs of the tokens before it in its chunk, not only those after it.
  */
@@ -383,8 +383,8 @@ typedef struct {
  *                aligned (NULL when that is 0); its contents are not kept
  * A row that sees nothing (no context, k and v NULL) gives o = 0, lse = -inf.
  * Cache rows past a length are not used, whatever they hold.
- * Limits: 1 <= N, and N <= 1024 where parent is given; D in {16, 32, ..., 128};
- * B <= 65535.
+ * Limits: 1 <= N (no more than T count), and N <= 1024 where parent is given; D in
+ * {16, 32, ..., 128}; B <= 65535.
  * dev_status[b]: GDN_TREE_STATUS_BAD_TREE (a parent out of range) or
  * GDN_TREE_STATUS_BAD_LAYOUT (rows, length or page out of range: nothing outside the
  * arrays is read) or GDN_TREE_STATUS_TIMEOUT; that sequence's o and lse are then
@@ -410,7 +410,8 @@ size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims);
  *   path_len     [B] int32, 0 <= path_len[b] <= Lmax
  *   new_len      [B] int32 or NULL; must not overlap context_len
  * page_table must already hold the pages that the new rows fall into.  Other shapes
- * as for gdn_tree_attend (dims.Hq and prefix_len are ignored; N has no upper limit).
+ * as for gdn_tree_attend (dims.Hq and prefix_len are ignored; N has no upper limit, and no
+ * more than T count).
  * The pages written must belong to one sequence each.
  * dev_status[b]: GDN_TREE_STATUS_BAD_PATH or GDN_TREE_STATUS_BAD_LAYOUT; the rows at
  * fault are not written, and with an invalid cu_nodes, path_len or context_len none

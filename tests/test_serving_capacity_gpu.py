@@ -9,7 +9,9 @@ import pytest
 import torch
 
 import gated_deltanet_tree_gdn_gb300 as gt
-from tests.test_serving_gpu import attend_inputs, check_attend, run_attend
+from oracle import serving as ref
+from tests.test_serving_gpu import (append_inputs, attend_inputs, check_attend, check_rule, host,
+                                    ints, rule_inputs, run_append, run_attend)
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +55,48 @@ def test_attend_rows_of_a_full_capacity(nodes, ctx, prefix, own, spare, tree):
     assert (status == 0).all()
     check_attend(o[:used], lse[:used], x, chain=tree == "chain")
     assert (o[used:] == 7.0).all() and (lse[used:] == 7.0).all()
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("N", [1 << 20, INT_MAX])
+def test_a_promise_past_the_rows_changes_nothing(N):
+    """N_max is a bound, however loose: results and workspaces are those of min(N_max, T)."""
+    x = rule_inputs([100, 0, 70], 2, 4, 128, 128, "bf16", seed=21)
+    dims = lambda n: gt.Dims(3, n, 2, 4, 128, 128, gt.BF16)  # noqa: E731
+    assert gt.prefill_workspace(dims(N), 170) == gt.prefill_workspace(dims(170), 170) > 0
+    o, pool = gt.prefill(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], ints(x["cu"]),
+                         x["pool"], state_slot=ints(x["slot"]), N_max=N)
+    check_rule(o, pool, x)
+    for case in (([1, 40, 3], [10, 130, 0], 77, 8, 2, 64, 16, "bf16"),
+                 ([1, 40, 3], [10, 130, 0], 77, 6, 2, 64, 24, "f32"),
+                 ([1], [300], 0, 32, 8, 128, 16, "bf16"),
+                 ([1, 2], [0, 9], 0, 4, 4, 16, 16, "f32")):
+        y = attend_inputs(*case, seed=22, tree="chain")
+        status = torch.full((len(case[0]),), -7, dtype=torch.int32, device="cuda")
+        o, lse = run_attend(y, chain=True, N_max=N, dev_status=status)
+        assert (status == 0).all()
+        check_attend(o, lse, y, chain=True)
+    for Lmax in (None, 24):
+        z = append_inputs([64, 3, 0], [0, 100, 7], 2, 64, 16, "bf16", seed=23, Lmax=Lmax)
+        want = ref.cache_append(host(z["k"]), host(z["v"]), z["cu"], host(z["k_cache"]),
+                                host(z["v_cache"]), z["table"], z["ctx"], z["path"], z["path_len"])
+        new_len = run_append(z, N_max=N)
+        assert np.array_equal(host(z["k_cache"]), want[0])
+        assert np.array_equal(host(z["v_cache"]), want[1])
+        assert new_len.tolist() == want[2].tolist()
+
+
+def test_a_prompt_past_its_pages_is_reported():
+    """More rows than the page table has room for: those that fit are written."""
+    z = append_inputs([40, 5], [0, 3], 2, 64, 16, "bf16", seed=24)
+    table = z["table"][:, :2].copy()  # room for 32 rows each
+    before = z["k_cache"].clone()
+    status = torch.empty(2, dtype=torch.int32, device="cuda")
+    run_append(dict(z, table=table), dev_status=status)
+    assert status.tolist() == [gt.STATUS_BAD_LAYOUT, 0]
+    for j in range(32):
+        assert torch.equal(z["k_cache"][table[0, j // 16], j % 16], z["k"][j])
+    third = int(z["table"][0, 2])
+    assert torch.equal(z["k_cache"][third], before[third])

@@ -183,3 +183,18 @@ def test_attend_definition_closed_forms():
     for i in range(2):
         assert np.allclose(o[i, 0], np.concatenate([rows, v[i]]).mean(0))
     assert np.allclose(lse, np.log(9))
+
+
+INT_MAX = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(prefix_len=0), dict(B=32, T=4096, Hq=32, Hkv=8, table_width=256),
+    dict(B=1, T=1, table_width=600), dict(B=40, T=40, prefix_len=4000), dict(B=3, T=700, Hkv=8)])
+def test_attend_plan_knows_the_rows(lib, kw):
+    """A promised N past the rows there are promises no more than those rows: the parts (whose
+    place is the workspace) are planned for min(N, T)."""
+    T = kw.get("T", 20)
+    need = lib.gdn_tree_attend_workspace(attend_dims(**kw, N=T))
+    for N in (T + 1, 1 << 20, INT_MAX):
+        assert lib.gdn_tree_attend_workspace(attend_dims(**kw, N=N)) == need
