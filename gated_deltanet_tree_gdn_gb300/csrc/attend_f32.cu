@@ -88,7 +88,8 @@ attend_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
 
   const int first = cu[b], stop = cu[b + 1], n = stop - first, ctx = context_len[b];
   const long long cap = (long long)d.table_width * d.page_size;
-  if (first < 0 || n < 0 || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
+  // (stop < first, not n < 0: of two numbers far apart the difference may wrap)
+  if (first < 0 || stop < first || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
     if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     return;  // (every CTA of the cluster)
   }

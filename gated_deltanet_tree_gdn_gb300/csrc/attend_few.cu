@@ -130,7 +130,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
 
   const int first = cu[b], stop = cu[b + 1], n = stop - first, ctx = context_len[b];
   const long long cap = (long long)d.table_width * d.page_size;
-  if (first < 0 || n < 0 || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
+  // (stop < first, not n < 0: of two numbers far apart the difference may wrap)
+  if (first < 0 || stop < first || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
     if (dev_status && tid == 0) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     prefix_done();
     return;  // (every CTA of the cluster)

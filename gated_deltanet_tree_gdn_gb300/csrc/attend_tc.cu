@@ -372,11 +372,12 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   tc_fence_after_sync();
   const uint32_t tmem = S->tmem;
   constexpr uint32_t kStage = L::kKV;
-  const int b = S->unit.x, first = S->unit.y, n = S->unit.z - first, ctx = S->unit.w;
+  const int b = S->unit.x, first = S->unit.y, stop = S->unit.z, n = stop - first, ctx = S->unit.w;
   bool mine = true;  // the unit has rows, and they are this kernel's
   if (!a.prefix_units) {
     const long long cap = (long long)d.table_width * d.page_size;
-    if (first < 0 || n < 0 || S->unit.z > d.T || n > d.N || ctx < 0 || ctx > cap) {
+    // (stop < first, not n < 0: of two numbers far apart the difference may wrap)
+    if (first < 0 || stop < first || stop > d.T || n > d.N || ctx < 0 || ctx > cap) {
       if (a.dev_status && tid == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
       mine = false;
     } else {
@@ -889,7 +890,7 @@ attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
   const int first = cu[b], stop = cu[b + 1];
   const long long at = (long long)(blockIdx.x % groups) * 8 + (threadIdx.x >> 5);
   // (a sequence whose rows are out of range was reported, and has no parts)
-  if (first < 0 || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq ||
+  if (first < 0 || stop < first || stop > d.T || stop - first > d.N || at >= (long long)(stop - first) * d.Hq ||
       (few && (stop - first) * (d.Hq / d.Hkv) <= kAttendFewRows))  // (attend_few.cu adds those up itself)
     return;
   const size_t rows = (size_t)d.T * d.Hq, row = (size_t)first * d.Hq + at;

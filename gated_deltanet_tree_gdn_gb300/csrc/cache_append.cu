@@ -31,7 +31,8 @@ cache_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
   const int len = path_len ? path_len[b] : rows;
   const long long cap = (long long)d.table_width * d.page_size;
   int bad = GDN_TREE_STATUS_OK;
-  if (first < 0 || rows < 0 || stop > d.T || rows > d.N || ctx < 0 || ctx > cap)
+  // (stop < first, not rows < 0: of two numbers far apart the difference may wrap)
+  if (first < 0 || stop < first || stop > d.T || rows > d.N || ctx < 0 || ctx > cap)
     bad = GDN_TREE_STATUS_BAD_LAYOUT;
   else if (path_len && (len < 0 || len > Lmax))
     bad = GDN_TREE_STATUS_BAD_PATH;

@@ -271,7 +271,8 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
     c = seg.c0 + slot % seg.span;
   }
   const int n = lay.count(b, d.N);
-  if (c < 0 || n <= c * kC) {  // (an invalid sequence is reported by the second kernel)
+  // (an invalid sequence is reported by the second kernel; its offset may give any c)
+  if (n < 0 || c < 0 || n <= (long long)c * kC) {
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();

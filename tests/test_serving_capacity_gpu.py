@@ -100,3 +100,37 @@ def test_a_prompt_past_its_pages_is_reported():
         assert torch.equal(z["k_cache"][table[0, j // 16], j % 16], z["k"][j])
     third = int(z["table"][0, 2])
     assert torch.equal(z["k_cache"][third], before[third])
+
+
+def test_row_offsets_that_wrap_are_reported():
+    """Offsets whose 32-bit difference wraps to a small number are no sequence's rows."""
+    cu = ints([0, INT_MAX, -2 ** 31, 7, 12])
+    bad = [gt.STATUS_BAD_LAYOUT] * 3 + [0]
+    for case in (([3, 3, 1, 5], [10, 5, 0, 20], 70, 8, 2, 64, 16, "bf16"),
+                 ([30, 30, 10, 50], [10, 5, 0, 20], 70, 8, 2, 64, 16, "bf16"),
+                 ([3, 3, 1, 5], [10, 5, 0, 20], 70, 8, 2, 64, 16, "f32")):
+        x = attend_inputs(*case, seed=25, tree="chain")
+        T = sum(case[0])
+        offsets = ints([0, INT_MAX, -2 ** 31, T - case[0][-1], T])
+        status = torch.full((4,), -7, dtype=torch.int32, device="cuda")
+        o = torch.full_like(x["q"], 7.0)
+        gt.attend(x["q"], x["k"], x["v"], None, offsets, x["k_cache"], x["v_cache"],
+                  ints(x["table"]), ints(x["ctx"]), prefix_pages=ints(x["prefix_pages"]),
+                  prefix_len=x["prefix"], N_max=T, o=o, dev_status=status)
+        assert status.tolist() == bad
+        assert (o[:T - case[0][-1]] == 7.0).all()
+        assert (o[T - case[0][-1]:] != 7.0).any()
+    z = append_inputs([3, 3, 1, 5], [0, 9, 7, 2], 2, 64, 16, "bf16", seed=26)
+    before, status = z["k_cache"].clone(), torch.empty(4, dtype=torch.int32, device="cuda")
+    new_len = gt.cache_append(z["k"], z["v"], cu, z["k_cache"], z["v_cache"], ints(z["table"]),
+                              ints(z["ctx"]), N_max=12, dev_status=status)
+    assert status.tolist() == bad and new_len.tolist() == [0, 9, 7, 7]
+    changed = (z["k_cache"] != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert changed == [int(z["table"][3, 0])]
+    x = rule_inputs([40, 100, 10], 1, 2, 128, 128, "bf16", seed=27)
+    status = torch.empty(3, dtype=torch.int32, device="cuda")
+    o = torch.full_like(x["v"], 7.0)
+    gt.prefill(x["q"], x["k"], x["v"], x["log_alpha"], x["beta"], ints([0, -2 ** 31, 140, 150]),
+               x["pool"], state_slot=ints(x["slot"]), N_max=100, o=o, dev_status=status)
+    assert status.tolist() == [gt.STATUS_BAD_LAYOUT] * 2 + [0]
+    assert (o[:140] == 7.0).all() and (o[140:] != 7.0).any()
