@@ -4,6 +4,10 @@ Argument marshalling only: dtype/shape/contiguity checks on torch tensors,
 then device pointers and the current CUDA stream go straight to the C entry
 points; every step of the computation runs in the library's kernels.  There
 is no fallback: if the library is not built, every call raises.
+
+A call runs on torch's current stream, or, with `stream=` (a torch.cuda.Stream or
+ExternalStream), as it would under torch.cuda.stream(stream): its inputs must be
+ready on that stream, and the tensors that it allocates belong to it.
 """
 
 from __future__ import annotations
@@ -153,12 +157,18 @@ def _check(t: torch.Tensor, name: str, dtype=None, shape=None):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
+def _stream() -> int:
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _on(stream, call, args):
+    """The call with these arguments under torch.cuda.stream(stream): what is allocated, copied or
+    read on the way then belongs to the stream that the kernels run on.  (A block of the current
+    stream could be handed out again, and a copy made, while they run.)"""
+    with torch.cuda.stream(stream):
+        return call(**dict(args, stream=None))
 
 
 _dims_cache: dict = {}
@@ -199,6 +209,8 @@ def verify_recurrent(q, k, v, log_alpha, beta, parent, S0, *, o=None, U=None, de
 
 
 def _verify(symbol, q, k, v, log_alpha, beta, parent, S0, o, U, dev_status, stream):
+    if stream is not None:
+        return _on(stream, _verify, locals())
     B, N, Hqk, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     dt = q.dtype
@@ -219,7 +231,7 @@ def _verify(symbol, q, k, v, log_alpha, beta, parent, S0, o, U, dev_status, stre
         _check(dev_status, "dev_status", torch.int32, (B,))
     rc = getattr(load(), symbol)(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                  _ptr(parent), _ptr(S0), _ptr(o), _ptr(U), dims_of(q, v),
-                                 _ptr(dev_status), _stream(stream))
+                                 _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, symbol)
     return o, U
@@ -234,6 +246,8 @@ def commit(path, path_len, U, k, log_alpha, S0, *, S1=None, parent=None, dev_sta
     allocated when not given; pass S1=S0 for an in-place commit.  parent
     (optional) enables the chain check of the path.
     """
+    if stream is not None:
+        return _on(stream, commit, locals())
     B, N, Hqk, dk = k.shape
     Hv, dv = S0.shape[1], S0.shape[3]
     _check(path, "path", torch.int32)
@@ -253,7 +267,7 @@ def commit(path, path_len, U, k, log_alpha, S0, *, S1=None, parent=None, dev_sta
     d = Dims(B, N, Hqk, Hv, dk, dv, _dtype_code(k))
     rc = load().gdn_tree_commit(_ptr(path), _ptr(path_len), _ptr(parent), _ptr(U), _ptr(k),
                                 _ptr(log_alpha), _ptr(S0), _ptr(S1), d, Lmax,
-                                _ptr(dev_status), _stream(stream))
+                                _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_commit")
     return S1
@@ -265,6 +279,8 @@ def commit_verify(prev_path, prev_path_len, prev_U, prev_k, prev_log_alpha, S_pr
     """One decoding iteration (C ABI gdn_tree_commit_verify): commit the previous
     tree's accepted path into S1, then verify the next tree from S1.
     Returns (S1, o, U).  S1=S_prev commits in place; U=prev_U reuses the buffer."""
+    if stream is not None:
+        return _on(stream, commit_verify, locals())
     B, N, Hqk, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     dt = q.dtype
@@ -300,7 +316,7 @@ def commit_verify(prev_path, prev_path_len, prev_U, prev_k, prev_log_alpha, S_pr
         _ptr(prev_path), _ptr(prev_path_len), _ptr(prev_parent), _ptr(prev_U), _ptr(prev_k),
         _ptr(prev_log_alpha), Np, Lmax, _ptr(S_prev), _ptr(S1), _ptr(q), _ptr(k), _ptr(v),
         _ptr(log_alpha), _ptr(beta), _ptr(parent), _ptr(o), _ptr(U), dims_of(q, v),
-        _ptr(commit_status), _ptr(verify_status), _stream(stream))
+        _ptr(commit_status), _ptr(verify_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_commit_verify")
     return S1, o, U
@@ -330,6 +346,8 @@ def verify_packed(q, k, v, log_alpha, beta, parent, cu_nodes, state_pool, *, sta
     state_pool [n_slots,Hv,dk,dv] fp32 with state_slot [B] (None: slot b).
     N_max is the largest tree (computed from cu_nodes on the host if None).
     o [T,Hv,dv] and U [Hv,T,dv] are allocated when not given."""
+    if stream is not None:
+        return _on(stream, verify_packed, locals())
     T, Hqk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = cu_nodes.shape[0] - 1
@@ -357,7 +375,7 @@ def verify_packed(q, k, v, log_alpha, beta, parent, cu_nodes, state_pool, *, sta
     rc = load().gdn_tree_verify_packed(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                        _ptr(parent), _ptr(cu_nodes), T, _ptr(state_pool),
                                        _ptr(state_slot), n_slots, _ptr(o), _ptr(U), d,
-                                       _ptr(dev_status), _stream(stream))
+                                       _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_verify_packed")
     return o, U
@@ -369,6 +387,8 @@ def commit_packed(path, path_len, U, k, log_alpha, cu_nodes, pool_in, *, pool_ou
     pool_out[state_slot[b]] = the state after sequence b's accepted path.  Returns
     pool_out (pool_out=pool_in commits in place; a new pool starts as a copy of
     pool_in, so that untouched slots keep their states)."""
+    if stream is not None:
+        return _on(stream, commit_packed, locals())
     T, Hqk, dk = k.shape
     Hv, dv = pool_in.shape[1], pool_in.shape[3]
     B = cu_nodes.shape[0] - 1
@@ -394,7 +414,7 @@ def commit_packed(path, path_len, U, k, log_alpha, cu_nodes, pool_in, *, pool_ou
     rc = load().gdn_tree_commit_packed(_ptr(path), _ptr(path_len), _ptr(parent), _ptr(cu_nodes),
                                        T, _ptr(U), _ptr(k), _ptr(log_alpha), _ptr(pool_in),
                                        _ptr(pool_out), _ptr(state_slot), n_slots, d, Lmax,
-                                       _ptr(dev_status), _stream(stream))
+                                       _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_commit_packed")
     return pool_out
@@ -406,6 +426,8 @@ def commit_verify_packed(prev_path, prev_path_len, prev_U, prev_k, prev_log_alph
                          U=None, commit_status=None, verify_status=None, stream=None):
     """One decoding iteration of a packed batch (C ABI gdn_tree_commit_verify_packed).
     Returns (pool_out, o, U); pool_out=pool_in commits in place."""
+    if stream is not None:
+        return _on(stream, commit_verify_packed, locals())
     T, Hqk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     Tp = prev_k.shape[0]
@@ -451,7 +473,7 @@ def commit_verify_packed(prev_path, prev_path_len, prev_U, prev_k, prev_log_alph
         _ptr(prev_U), _ptr(prev_k), _ptr(prev_log_alpha), prev_N_max, Lmax, _ptr(pool_in),
         _ptr(pool_out), _ptr(state_slot), n_slots, _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha),
         _ptr(beta), _ptr(parent), _ptr(cu_nodes), T, _ptr(o), _ptr(U), d, _ptr(commit_status),
-        _ptr(verify_status), _stream(stream))
+        _ptr(verify_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_commit_verify_packed")
     return pool_out, o, U
@@ -468,6 +490,8 @@ def build_topw(cand_logp, w: int, max_depth: int, *, parent=None, cand_index=Non
     cand_logp [B, N, c] fp32: the log-probabilities of each node's c candidate
     children.  Returns (parent [B, N] int32, cand_index [B, N] int32, score [B, N]
     fp32, n_built [B] int32); outputs are allocated when not given."""
+    if stream is not None:
+        return _on(stream, build_topw, locals())
     _check(cand_logp, "cand_logp", torch.float32)
     B, N, c = cand_logp.shape
     dev = cand_logp.device
@@ -485,7 +509,7 @@ def build_topw(cand_logp, w: int, max_depth: int, *, parent=None, cand_index=Non
     _check(n_built, "n_built", torch.int32, (B,))
     rc = load().gdn_tree_build_topw(_ptr(cand_logp), B, N, c, w, max_depth, _ptr(parent),
                                     _ptr(cand_index), _ptr(score), _ptr(n_built),
-                                    _stream(stream))
+                                    _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_build_topw")
     return parent, cand_index, score, n_built
@@ -540,6 +564,8 @@ def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None,
     b) holds the state each sequence starts from.  o [T,Hv,dv] is allocated when not given;
     pool_out=state_pool updates in place, a new pool starts as a copy of state_pool.
     workspace (``prefill_workspace`` bytes, uint8) is allocated when not given.  N_max is the longest sequence (computed from cu_tokens on the host if None)."""
+    if stream is not None:
+        return _on(stream, prefill, locals())
     T, Hqk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = cu_tokens.shape[0] - 1
@@ -575,7 +601,7 @@ def prefill(q, k, v, log_alpha, beta, cu_tokens, state_pool, *, state_slot=None,
     rc = load().gdn_tree_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                  _ptr(cu_tokens), T, _ptr(state_pool), _ptr(pool_out),
                                  _ptr(state_slot), n_slots, _ptr(o), d, _ptr(dev_status),
-                                 _ptr(workspace), need, _stream(stream))
+                                 _ptr(workspace), need, _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_prefill")
     return o, pool_out
@@ -589,6 +615,8 @@ def decode_step(q, k, v, log_alpha, beta, state_pool, *, state_slot=None, pool_o
     q, k [B,Hqk,dk], v [B,Hv,dv] (bf16 or fp32); log_alpha, beta [B,Hv] fp32; state_pool
     [n_slots,Hv,dk,dv] fp32 with state_slot [B] (None: slot b).  pool_out=state_pool steps
     in place; a new pool starts as a copy of state_pool."""
+    if stream is not None:
+        return _on(stream, decode_step, locals())
     B, Hqk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     dt = q.dtype
@@ -611,7 +639,7 @@ def decode_step(q, k, v, log_alpha, beta, state_pool, *, state_slot=None, pool_o
     rc = load().gdn_tree_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta),
                                      _ptr(state_pool), _ptr(pool_out), _ptr(state_slot), n_slots,
                                      _ptr(o), _struct(Dims, B, 1, Hqk, Hv, dk, dv, code),
-                                     _ptr(dev_status), _stream(stream))
+                                     _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_decode_step")
     return o, pool_out
@@ -649,6 +677,8 @@ def attend(q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len,
     1/sqrt(D).  o [T,Hq,D], lse [T,Hq] fp32 and workspace (``attend_workspace`` bytes, uint8)
     are allocated when not given.  N_max is the most rows of one sequence (computed from
     cu_nodes on the host if None)."""
+    if stream is not None:
+        return _on(stream, attend, locals())
     T, Hq, D = q.shape
     B = cu_nodes.shape[0] - 1
     Hkv = k_cache.shape[2]
@@ -691,7 +721,7 @@ def attend(q, k, v, parent, cu_nodes, k_cache, v_cache, page_table, context_len,
                              _ptr(prefix_pages) if prefix_len else None,
                              D ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), d,
                              _ptr(dev_status), _ptr(workspace), need,
-                             _stream(stream))
+                             _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_attend")
     return o, lse
@@ -707,6 +737,8 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
     tree, else all rows of each sequence.  k_cache, v_cache [n_pages,page_size,Hkv,D] are
     written in place at rows context_len[b] .. of the pages that page_table [B,width]
     already holds.  context_len itself is not changed."""
+    if stream is not None:
+        return _on(stream, cache_append, locals())
     T, Hkv, D = k.shape
     B = cu_nodes.shape[0] - 1
     dt = k.dtype
@@ -733,7 +765,7 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
     rc = load().gdn_tree_cache_append(_ptr(k), _ptr(v), _ptr(path), _ptr(path_len), Lmax,
                                       _ptr(cu_nodes), _ptr(k_cache), _ptr(v_cache),
                                       _ptr(page_table), _ptr(context_len), _ptr(new_len), d,
-                                      _ptr(dev_status), _stream(stream))
+                                      _ptr(dev_status), _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_cache_append")
     return new_len
