@@ -315,8 +315,9 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapV,
                  const __grid_constant__ CUtensorMap mapKo,
                  const __grid_constant__ CUtensorMap mapVo,
-                 const __grid_constant__ CUtensorMap mapQ, uint64_t limit_ns) {
+                 const __grid_constant__ CUtensorMap mapQ, WaitHooks hooks) {
   using L = Smem<DP>;
+  const uint64_t limit_ns = hooks.limit_ns;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -661,7 +662,8 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
       }
     fence_proxy_async_smem();
     __syncwarp();
-    mbar_arrive_warp(&S->ready);
+    if (!(b * d.Hkv + hk == hooks.withhold_unit && warp == hooks.withhold_node))
+      mbar_arrive_warp(&S->ready);
     bool ok = wait_warp(&S->ready, 0, S, limit_ns);
     // ---- softmax: two threads a row --------------------------------------------------------
     const int tile = warp >> 3, half = (warp >> 2) & 1, lr = (warp & 3) * 32 + lane;
@@ -871,6 +873,20 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  if (S->abort) {
+    // the tiles still on their way arrive (or these bounded waits end) before the CTA, and with
+    // it the place that they are written to, goes: both phases of each barrier, as the one that
+    // is open is not known
+    constexpr uint64_t kArrivalNs = 1000000;
+    for (uint32_t ph = 0; ph < 2; ++ph) {
+      for (int s = 0; s < 2; ++s)
+        if (warp == kWarpK) mbar_wait(&S->kfull[s], ph, kArrivalNs);
+        else if (warp == kWarpV) mbar_wait(&S->vfull[s], ph, kArrivalNs);
+      if (warp == kWarpV) mbar_wait(&S->vraw, ph, kArrivalNs);
+      if (warp == kWarpMma) mbar_wait(&S->qfull, ph, kArrivalNs);
+    }
+    __syncthreads();
+  }
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
   if (a.rest && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && S->abort && a.dev_status) {
@@ -1017,7 +1033,7 @@ cudaError_t launch_units(const TcArgs& t, const CUtensorMap (&map)[5], long long
   cfg.attrs = attr;
   cfg.numAttrs = t.rest ? 1 : 0;
   err = cudaLaunchKernelEx(&cfg, attend_tc_kernel<DP, kFork>, t, map[0], map[1], map[2], map[3],
-                           map[4], wait_hooks().limit_ns);
+                           map[4], wait_hooks());
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 

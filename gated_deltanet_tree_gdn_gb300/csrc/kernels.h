@@ -100,7 +100,9 @@ struct CommitVerifyArgs {
 //       tensor-core chunk-pass verifications of unit (b * Hv + h) never arrive on
 //       that node's solve barrier, so the waits of its descendants (in its chunk,
 //       for the chunk pass) run out (thread arrivals only: no copy or MMA is left
-//       in flight)
+//       in flight); in the attention on the tensor cores, warp <node> of the units
+//       (b * Hkv + key head; 0 for b in the shared prefix's) never says that Q and the
+//       tree are in place
 //   GDN_TREE_TEST_WITHHOLD_COPY=<b>        the tensor-core commit of sequence b
 //       expects its state copy but never issues it, so the wait for it runs out
 struct WaitHooks {
