@@ -102,9 +102,11 @@ struct CommitVerifyArgs {
 //       for the chunk pass) run out (thread arrivals only: no copy or MMA is left
 //       in flight); in the attention on the tensor cores, warp <node> of the units
 //       (b * Hkv + key head; 0 for b in the shared prefix's) never says that Q and the
-//       tree are in place
+//       tree are in place; in the prefill in chunks, warp <node> of the chains of
+//       (b * Hv + h) that its part of the first state is
 //   GDN_TREE_TEST_WITHHOLD_COPY=<b>        the tensor-core commit of sequence b
-//       expects its state copy but never issues it, so the wait for it runs out
+//       expects its state copy but never issues it, so the wait for it runs out; the
+//       prefill's first kernel does so with the keys and queries of b's chunks
 struct WaitHooks {
   uint64_t limit_ns = 2000000000ull;
   int withhold_unit = -1, withhold_node = -1;

@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
 prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapQ, const float* __restrict__ log_alpha,
                     const float* __restrict__ beta, gdn_tree_dims d, SeqLayout lay, Segment seg,
-                    unsigned char* ws, int32_t* dev_status, uint64_t limit_ns) {
+                    unsigned char* ws, int32_t* dev_status, WaitHooks hooks) {
+  const uint64_t limit_ns = hooks.limit_ns;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -284,7 +285,7 @@ prefill_prep_kernel(const __grid_constant__ CUtensorMap mapK,
   const size_t row = (size_t)lay.cu[b] + (size_t)c * kC;
   if (tid == 0) {
     mbar_arrive_expect_tx(&P.bar, kTileKQ);
-    load_kq(sKQ, &mapK, &mapQ, &P.bar, hq, (int)row);
+    if (b != hooks.withhold_copy_seq) load_kq(sKQ, &mapK, &mapQ, &P.bar, hq, (int)row);
   }
   float la[2] = {0.f, 0.f}, be[2] = {0.f, 0.f};  // the gates of rows 2 lane and 2 lane + 1
   if (warp == 1) {
@@ -680,8 +681,9 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
                     const __grid_constant__ CUtensorMap mapV, const __nv_bfloat16* __restrict__ v,
                     const float* pool_in, float* pool_out, __nv_bfloat16* __restrict__ o,
                     gdn_tree_dims d, SeqLayout lay, Segment seg, const unsigned char* ws,
-                    int32_t* dev_status, uint64_t limit_ns) {
+                    int32_t* dev_status, WaitHooks hooks) {
   using L = Scan<kChains>;
+  const uint64_t limit_ns = hooks.limit_ns;
   extern __shared__ __align__(1024) unsigned char smem[];
   ScanBars* B = reinterpret_cast<ScanBars*>(smem + L::OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -866,7 +868,8 @@ prefill_scan_kernel(const __grid_constant__ CUtensorMap mapK,
     bool ok = run;
     if (seg.c0 < c_end) {
       store_parts(to_s, S);
-      mbar_arrive_warp(&C.s_ready);
+      if (!(b * d.Hv + h == hooks.withhold_unit && warp == hooks.withhold_node))
+        mbar_arrive_warp(&C.s_ready);
     }
     // this token's v (16 columns) and weights, a chunk ahead (the pointers go along: nothing
     // is looked up on the way)
@@ -1051,7 +1054,7 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
   // in more than a round of the SMs the long sequences go first, so that the SMs end closer
   // together (16 ragged prompts 492 to 463 us)
   s.by_length = scan > sms && d.B > 1 && d.B <= kMaxRanked;
-  const uint64_t limit = wait_hooks().limit_ns;
+  const WaitHooks hooks = wait_hooks();
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const int longest = (int)(((long long)d.N + kC - 1) / kC);
   // The second kernel starts beside the first one's last CTAs, unless the sequences are long.
@@ -1073,7 +1076,7 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
       cfg.attrs = attr;
       cfg.numAttrs = s.ahead && s.c0 > 0;
       err = cudaLaunchKernelEx(&cfg, prefill_prep_kernel, mapK, mapQ, a.log_alpha, a.beta, d, a.lay,
-                               s, ws, a.dev_status, limit);
+                               s, ws, a.dev_status, hooks);
       if (err != cudaSuccess || (err = cudaGetLastError()) != cudaSuccess) return err;
     }
     auto run = [&](auto kernel, int threads, uint32_t bytes) {
@@ -1090,7 +1093,7 @@ cudaError_t launch_prefill_tc(const RuleArgs& a, void* workspace, cudaStream_t s
       const cudaError_t e = cudaLaunchKernelEx(
           &cfg, kernel, mapK, mapQ, mapV, static_cast<const __nv_bfloat16*>(a.v), a.pool_in,
           a.pool_out, static_cast<__nv_bfloat16*>(a.o), d, a.lay, s,
-          static_cast<const unsigned char*>(ws), a.dev_status, limit);
+          static_cast<const unsigned char*>(ws), a.dev_status, hooks);
       return e != cudaSuccess ? e : cudaGetLastError();
     };
     err = two ? run(prefill_scan_kernel<2>, Scan<2>::kThreads, Scan<2>::kBytes)

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import gated_deltanet_tree_gdn_gb300 as gt
-from tests.test_serving_gpu import attend_inputs, check_attend, run_attend
+from tests.test_serving_gpu import (EPS_BF16, TOL_F32, attend_inputs, check_attend, check_rule,
+                                    host, ints, max_err, rule_inputs, rule_ref, run_attend)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,35 @@ def test_shared_prefix_wait_runs_out(short_waits):
     o, lse = run_attend(x, dev_status=status)
     assert status.tolist() == [0] * 30
     check_attend(o, lse, x)
+
+
+@pytest.mark.parametrize("what", ["copy", "arrival"])
+@pytest.mark.parametrize("lens,Hqk,Hv", [([200, 130, 64], 2, 4), ([200] * 5, 16, 32)],
+                         ids=["one-chain", "two-chains"])
+def test_prefill_wait_runs_out(short_waits, what, lens, Hqk, Hv):
+    x = rule_inputs(lens, Hqk, Hv, 128, 128, "bf16", seed=43)
+    B, b = len(lens), 1
+    if what == "copy":
+        short_waits.setenv("GDN_TREE_TEST_WITHHOLD_COPY", str(b))
+    else:
+        short_waits.setenv("GDN_TREE_TEST_WITHHOLD_NODE", f"{b * Hv + 3}:5")
+    args = [x[n] for n in ("q", "k", "v", "log_alpha", "beta")] + [ints(x["cu"]), x["pool"]]
+    status = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    out = x["pool"].clone()
+    o, pool = gt.prefill(*args, state_slot=ints(x["slot"]), pool_out=out, dev_status=status)
+    assert status.tolist() == [gt.STATUS_TIMEOUT if i == b else 0 for i in range(B)]
+    ro, rp = rule_ref(x)
+    o, pool = host(o), host(pool)
+    for i in range(B):
+        if i == b:
+            continue
+        rows, slot = slice(x["cu"][i], x["cu"][i + 1]), x["slot"][i]
+        assert max_err(pool[slot], rp[slot]) <= TOL_F32
+        assert (np.abs(o[rows] - ro[rows]) <= EPS_BF16 * np.abs(ro[rows])
+                + TOL_F32 * np.abs(ro).max()).all()
+    if what == "arrival":  # the state of the head is left unwritten
+        assert (pool[x["slot"][b], 3] == host(x["pool"])[x["slot"][b], 3]).all()
+    short_waits.undo()
+    o, pool = gt.prefill(*args, state_slot=ints(x["slot"]), dev_status=status)
+    assert (status == 0).all()
+    check_rule(o, pool, x)
