@@ -347,7 +347,8 @@ template <int DP>
 cudaError_t launch_dp(const AttendArgs& a, cudaStream_t stream) {
   using L = Shared<DP>;
   const gdn_tree_attend_dims& d = a.d;
-  const int tiles = (int)(((long long)d.N * (d.Hq / d.Hkv) + kM - 1) / kM);
+  // (N = 0: one, that reports the sequences with rows all the same)
+  const int tiles = d.N > 0 ? (int)(((long long)d.N * (d.Hq / d.Hkv) + kM - 1) / kM) : 1;
   const long long units = (long long)d.B * d.Hkv * tiles;
   const size_t bytes = sizeof(L) + (a.parent ? sizeof(int32_t) * (size_t)d.N : 0);
   cudaError_t err = cudaFuncSetAttribute(attend_f32_kernel<DP>,

@@ -497,8 +497,7 @@ int gdn_tree_decode_step(const void* q, const void* k, const void* v, const floa
 }
 
 size_t gdn_tree_attend_workspace(gdn_tree_attend_dims dims) {
-  if (check_attend_dims(dims) != GDN_TREE_OK || dims.B == 0 || dims.T == 0 || dims.N == 0)
-    return 0;
+  if (check_attend_dims(dims) != GDN_TREE_OK || dims.B == 0 || dims.T == 0) return 0;
   dims.N = bounded_rows(dims.N, dims.T);
   return gdn::attend_workspace_bytes(dims);
 }
@@ -512,7 +511,12 @@ int gdn_tree_attend(const void* q, const void* k, const void* v, const int32_t* 
   const int rc = check_attend_dims(dims);
   if (rc != GDN_TREE_OK) return rc;
   if (parent && dims.N > gdn::kMaxNLongHost) return GDN_TREE_EUNSUPPORTED;
-  if (dims.B == 0 || dims.T == 0 || dims.N == 0) return GDN_TREE_OK;  // nothing to do
+  if (dims.B == 0) return GDN_TREE_OK;  // nothing to do
+  if (dev_status && !aligned4(dev_status)) return GDN_TREE_EINVAL;
+  if (dims.T == 0)  // nothing but the statuses
+    return clear_status(dev_status, dims.B, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_TREE_OK
+               : GDN_TREE_ECUDA;
   dims.N = bounded_rows(dims.N, dims.T);
   if ((k == nullptr) != (v == nullptr)) return GDN_TREE_EINVAL;
   const void* need[] = {q, o};
@@ -527,7 +531,7 @@ int gdn_tree_attend(const void* q, const void* k, const void* v, const int32_t* 
   const void* ints[] = {cu_nodes, context_len};
   for (const void* p : ints)
     if (p == nullptr || !aligned4(p)) return GDN_TREE_EINVAL;
-  const void* opt[] = {parent, page_table, prefix_pages, lse, dev_status};
+  const void* opt[] = {parent, page_table, prefix_pages, lse};
   for (const void* p : opt)
     if (!aligned4(p)) return GDN_TREE_EINVAL;
   if ((dims.table_width > 0 && page_table == nullptr) ||

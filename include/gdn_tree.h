@@ -383,7 +383,8 @@ typedef struct {
  *                aligned (NULL when that is 0); its contents are not kept
  * A row that sees nothing (no context, k and v NULL) gives o = 0, lse = -inf.
  * Cache rows past a length are not used, whatever they hold.
- * Limits: 1 <= N (no more than T count), and N <= 1024 where parent is given; D in
+ * With T = 0 nothing but dev_status is written.
+ * Limits: 0 <= N (no more than T count), and N <= 1024 where parent is given; D in
  * {16, 32, ..., 128}; B <= 65535.
  * dev_status[b]: GDN_TREE_STATUS_BAD_TREE (a parent out of range) or
  * GDN_TREE_STATUS_BAD_LAYOUT (rows, length or page out of range: nothing outside the

@@ -134,3 +134,22 @@ def test_row_offsets_that_wrap_are_reported():
                x["pool"], state_slot=ints(x["slot"]), N_max=100, o=o, dev_status=status)
     assert status.tolist() == [gt.STATUS_BAD_LAYOUT] * 2 + [0]
     assert (o[:140] == 7.0).all() and (o[140:] != 7.0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_status_of_a_batch_without_rows(dtype):
+    """The statuses of a call are its own, also where it has nothing to compute; a promise of no
+    rows that the offsets break is reported like any other."""
+    x = attend_inputs([0, 0], [3, 200], 40, 8, 2, 64, 16, dtype, seed=28)
+    status = torch.full((2,), -7, dtype=torch.int32, device="cuda")
+    run_attend(x, N_max=1, dev_status=status)
+    assert status.tolist() == [0, 0]
+    y = attend_inputs([2, 0], [3, 200], 40, 8, 2, 64, 16, dtype, seed=29)
+    o = torch.full_like(y["q"], 7.0)
+    status.fill_(-7)
+    run_attend(y, N_max=0, o=o, dev_status=status)
+    assert status.tolist() == [gt.STATUS_BAD_LAYOUT, 0]
+    assert (o == 7.0).all()
+    run_attend(dict(y, cu=np.zeros(3, dtype=np.int32)), N_max=0, o=o, dev_status=status)
+    assert status.tolist() == [0, 0]
+    assert (o == 7.0).all()
