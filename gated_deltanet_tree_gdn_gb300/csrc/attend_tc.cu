@@ -915,8 +915,10 @@ attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   float sum = 0.f;
-  if (top > -INFINITY)
-    for (int s = lane; s < slots; s += 32) sum += expf(part_lse[s * rows + row] - top);
+  for (int s = lane; s < slots; s += 32) {
+    const float z = part_lse[s * rows + row];
+    if (z != -INFINITY) sum += expf(z - top);  // (a NaN is kept, which fmaxf drops)
+  }
   sum = warp_sum(sum);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -934,7 +936,7 @@ attend_join_kernel(const float* __restrict__ part_o, const float* __restrict__ p
   if (4 * lane < D)
     *reinterpret_cast<uint2*>(o + row * D + 4 * lane) =
         make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
-  if (lse && lane == 0) lse[row] = sum > 0.f ? top + logf(sum) : (top == -INFINITY ? -INFINITY : sum);
+  if (lse && lane == 0) lse[row] = sum > 0.f ? top + logf(sum) : (sum == 0.f ? -INFINITY : sum);
 }
 
 // ---- the plan: what runs for these dims --------------------------------------------------

@@ -153,3 +153,19 @@ def test_status_of_a_batch_without_rows(dtype):
     run_attend(dict(y, cu=np.zeros(3, dtype=np.int32)), N_max=0, o=o, dev_status=status)
     assert status.tolist() == [0, 0]
     assert (o == 7.0).all()
+
+
+@pytest.mark.parametrize("nodes,ctx,prefix,dtype", [
+    ([60], [5000], 0, "bf16"),                        # keys in parts
+    ([20, 1] * 6, [40] * 12, 6000, "bf16"),           # the prefix by units of its own
+    ([60, 2], [300, 10], 0, "bf16"), ([2], [5000], 0, "bf16"), ([60], [500], 40, "f32")])
+def test_rows_whose_query_is_nan(nodes, ctx, prefix, dtype):
+    """All scores of such a row are NaN, in every part: so are its o and its lse."""
+    x = attend_inputs(nodes, ctx, prefix, 8, 2, 128, 64, dtype, seed=30)
+    good = run_attend(x)
+    bad = [0, sum(nodes) - 1]
+    x["q"][bad] = float("nan")
+    o, lse = run_attend(x)
+    rest = np.setdiff1d(np.arange(sum(nodes)), bad)
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(o[rest], good[0][rest]) and torch.equal(lse[rest], good[1][rest])
