@@ -113,7 +113,11 @@ attend_f32_kernel(const float* __restrict__ q, const float* __restrict__ k,
     const int pi = j / d.page_size;
     const int pg = pre ? prefix_pages[pi] : table[(size_t)b * d.table_width + pi];
     if (pg >= 0 && pg < d.n_pages) return pg * d.page_size + (j - pi * d.page_size);
-    if (dev_status) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    if (dev_status) {  // a bad page of the prefix is every sequence's error
+      if (!pre) atomicMax(dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+      else
+        for (int i = 0; i < d.B; ++i) atomicMax(dev_status + i, GDN_TREE_STATUS_BAD_LAYOUT);
+    }
     return -1;
   };
   constexpr int kChunks = DP / 4, kAtOnce = 32 / kChunks;

@@ -169,3 +169,14 @@ def test_rows_whose_query_is_nan(nodes, ctx, prefix, dtype):
     rest = np.setdiff1d(np.arange(sum(nodes)), bad)
     assert torch.isnan(o[bad]).all() and torch.isnan(lse[bad]).all()
     assert torch.equal(o[rest], good[0][rest]) and torch.equal(lse[rest], good[1][rest])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [[0, 3, 1], [0, 40, 30]])
+def test_a_bad_page_of_the_prefix_is_told_to_all(nodes, dtype):
+    x = attend_inputs(nodes, [9, 0, 20], 70, 8, 2, 64, 16, dtype, seed=34)
+    pages = x["prefix_pages"].copy()
+    pages[2] = -1
+    status = torch.full((3,), -7, dtype=torch.int32, device="cuda")
+    run_attend(dict(x, prefix_pages=pages), dev_status=status)
+    assert status.tolist() == [gt.STATUS_BAD_LAYOUT] * 3
