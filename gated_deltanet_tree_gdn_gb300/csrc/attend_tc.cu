@@ -309,6 +309,21 @@ __device__ __noinline__ void add_nonfinite(const TcArgs& a, size_t out, size_t s
   }
 }
 
+// After a wait that ran out: the tiles still on their way arrive (or these bounded waits end)
+// before the CTA, and with it the place that they are written to, goes.  Both phases of each
+// barrier, as the one that is open is not known.  All threads come here.
+__device__ __noinline__ void await_tiles(Bars* S, int warp) {
+  constexpr uint64_t kArrivalNs = 1000000;
+  for (uint32_t ph = 0; ph < 2; ++ph) {
+    for (int s = 0; s < 2; ++s)
+      if (warp == kWarpK) mbar_wait(&S->kfull[s], ph, kArrivalNs);
+      else if (warp == kWarpV) mbar_wait(&S->vfull[s], ph, kArrivalNs);
+    if (warp == kWarpV) mbar_wait(&S->vraw, ph, kArrivalNs);
+    if (warp == kWarpMma) mbar_wait(&S->qfull, ph, kArrivalNs);
+  }
+  __syncthreads();
+}
+
 template <int DP, bool kFork>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
@@ -873,20 +888,7 @@ attend_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mapK,
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (S->abort) {
-    // the tiles still on their way arrive (or these bounded waits end) before the CTA, and with
-    // it the place that they are written to, goes: both phases of each barrier, as the one that
-    // is open is not known
-    constexpr uint64_t kArrivalNs = 1000000;
-    for (uint32_t ph = 0; ph < 2; ++ph) {
-      for (int s = 0; s < 2; ++s)
-        if (warp == kWarpK) mbar_wait(&S->kfull[s], ph, kArrivalNs);
-        else if (warp == kWarpV) mbar_wait(&S->vfull[s], ph, kArrivalNs);
-      if (warp == kWarpV) mbar_wait(&S->vraw, ph, kArrivalNs);
-      if (warp == kWarpMma) mbar_wait(&S->qfull, ph, kArrivalNs);
-    }
-    __syncthreads();
-  }
+  if (S->abort) await_tiles(S, warp);
   if (warp == kWarpMma) tmem_dealloc(tmem, 512);
   if (a.rest && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0 && S->abort && a.dev_status) {
