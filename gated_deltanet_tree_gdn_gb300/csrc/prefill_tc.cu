@@ -47,11 +47,16 @@ constexpr uint32_t kTZBytes = 3 * kTileTZ;
 constexpr uint32_t kAuxBytes = 1024;               // e^g, beta, e^{gC - g} [64] each, e^gC
 constexpr uint32_t kSlotBytes = kTZBytes + kAuxBytes;
 constexpr uint32_t kTileKQ = 2 * 128 * 128;        // [K; Q]: 128 rows x 128, two 64-column blocks
+// What the workspace is kept to where a segment of at least kMinSegment chunks of every sequence
+// fits.  It is a target, not a limit: with 32 heads 41 sequences fit; of more, a segment is
+// kMinSegment chunks of each (12.8 MB a sequence), or all chunks packed where that is less.
+// Shorter segments would read and write the states too often (64 KB each way a sequence and
+// head, against 50 KB of tiles a chunk).
 constexpr size_t kWorkspaceTarget = (size_t)512 << 20;
 constexpr int kMinSegment = 8;                     // chunks a launch pair, at least
 
-// Chunks [c0, c0 + span) of every sequence are one segment; where all chunks fit the
-// workspace there is one, with slots packed by row position (dense = true), else
+// Chunks [c0, c0 + span) of every sequence are one segment; where all chunks fit the target
+// there is one, with slots packed by row position (dense = true), else
 // slot = b * span + c - c0.
 struct Segment {
   int c0, span;

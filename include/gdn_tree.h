@@ -317,12 +317,17 @@ int gdn_tree_build_topw(const float *cand_logp, int32_t B, int32_t N, int32_t c,
  *               (in place), any other overlap is refused.  Slots must be distinct.
  *   log_alpha   any value <= 0, -inf (alpha = 0, the state is forgotten) included
  *   workspace   gdn_tree_prefill_workspace(dims, T) bytes of device memory, 16-byte
- *               aligned (NULL when that is 0); its contents are not kept
+ *               aligned (NULL when that is 0); its contents are not kept.  At most 512 MB,
+ *               or Hv * 50176 * min(8 B, T / 64 + B + 1) bytes where that is more (with 32
+ *               heads, from 42 sequences on)
  * A sequence whose rows or slot are out of range gets GDN_TREE_STATUS_BAD_LAYOUT
  * and its outputs are left unwritten (where cu_tokens decreases, the sequences after
  * are unspecified too).  dims.N has no upper limit here (no more than T count).  bf16 with dk = dv = 128 is
  * computed in chunks of 64 tokens: an infinity or NaN in a token's inputs may reach the
- * outputs of the tokens before it in its chunk, not only those after it.
+ * outputs of the tokens before it in its chunk, not only those after it.  States and sums
+ * are fp32 everywhere; in chunks, the operands of the products are held in parts of 22 bits
+ * (the inverse of a chunk's system) or more, which leaves the states within about 3e-7 of
+ * the exact rule (the rule token by token in fp32: the same).
  */
 int gdn_tree_prefill(const void *q, const void *k, const void *v, const float *log_alpha,
                      const float *beta, const int32_t *cu_tokens, int32_t T,
@@ -382,6 +387,10 @@ typedef struct {
  *   workspace    gdn_tree_attend_workspace(dims) bytes of device memory, 16-byte
  *                aligned (NULL when that is 0); its contents are not kept
  * A row that sees nothing (no context, k and v NULL) gives o = 0, lse = -inf.
+ * Scores, the softmax's maximum and sum, and the sums over rows are fp32.  In bf16 the
+ * weights p are rounded to bf16 for the second product (at most 2^-8 of each, so at most
+ * 2^-8 sum_j p_ij |v_j| of o, beside o's own rounding); lse is made of the weights before
+ * that.  In fp32 nothing is rounded below fp32.
  * Cache rows past a length are not used, whatever they hold.
  * With T = 0 nothing but dev_status is written.
  * Limits: 0 <= N (no more than T count), and N <= 1024 where parent is given; D in

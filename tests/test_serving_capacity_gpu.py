@@ -180,3 +180,14 @@ def test_a_bad_page_of_the_prefix_is_told_to_all(nodes, dtype):
     status = torch.full((3,), -7, dtype=torch.int32, device="cuda")
     run_attend(dict(x, prefix_pages=pages), dev_status=status)
     assert status.tolist() == [gt.STATUS_BAD_LAYOUT] * 3
+
+
+@pytest.mark.parametrize("B,N,avg,Hv", [(1, 32768, 32768, 32), (16, 2048, 700, 32), (64, 512, 512, 32),
+                                        (256, 512, 512, 32), (256, 2048, 2048, 32),
+                                        (1024, 2048, 100, 32), (4096, 4096, 4096, 32),
+                                        (300, 32768, 600, 32), (4096, 33, 33, 64), (1, 64, 64, 128)])
+def test_prefill_workspace_is_bounded(B, N, avg, Hv):
+    """512 MB, or what eight chunks of every sequence (fewer, where all have fewer) take."""
+    T, head = B * avg, Hv * 50176
+    need = gt.prefill_workspace(gt.Dims(B, N, Hv, Hv, 128, 128, gt.BF16), T)
+    assert 0 < need <= max(512 << 20, head * min(8 * B, T // 64 + B + 1))
