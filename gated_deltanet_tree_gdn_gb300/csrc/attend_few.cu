@@ -310,7 +310,8 @@ attend_few_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __re
         s[e][i] = ex2(s[e][i] - (m[i >> 1] == -INFINITY ? 0.f : m[i >> 1]));
         l[i >> 1] += s[e][i];  // (this lane's keys; the four lanes of a row add up at the end)
       }
-    // P as the A operand: its inner index is the key
+    // P as the A operand: its inner index is the key.  (bf16 as V is, at most 2^-8 of a weight;
+    // l above is the fp32 weights')
     const uint4 pa = make_uint4(pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]),
                                 pack_bf16(s[1][0], s[1][1]), pack_bf16(s[1][2], s[1][3]));
 #pragma unroll

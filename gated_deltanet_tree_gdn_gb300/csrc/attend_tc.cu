@@ -30,9 +30,8 @@
 // softmax: the 16 warps then share the issue slots (193 us for 32 trees of 128 nodes, against
 // 166), although a unit of one row tile gained by it (112 to 94 us for 20 smaller trees).
 //
-// Measured: those 32 trees over 256 to 4096 rows and a prefix of 1024, 32 heads of 128: 166 us,
-// 1.1 PFLOP/s; causal prompts of 4096, 8192 and 16384 rows 204, 690 and 2530 us, 0.67, 0.80 and
-// 0.87 PFLOP/s.
+// Measured: those 32 trees over 256 to 4096 rows and a prefix of 1024, 32 heads of 128: 159 us,
+// 1.2 PFLOP/s; causal prompts of 4096 and 16384 rows 180 and 2373 us, 0.77 and 0.93 PFLOP/s.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one its
 // sums use (exact either way: P and l stay far below the overflow of their types).
@@ -206,7 +205,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // One thread's 64 weights of a tile: exp2(c s - base) of 64 TMEM columns as bf16 pairs in
 // pk, their fp32 sum, and the largest c s - base.  192 instructions where nothing is
 // masked (the masked form, 64 selections more, is a branch of its own: folded into one by
-// the compiler the selections would run for every tile).
+// the compiler the selections would run for every tile).  bf16, because the product's other
+// operand, V, is and the MMA takes one type: at most 2^-8 of a weight, 2^-8 sum_j p_j |v_j|
+// of o.  A second part a weight would take that away for twice the products of P V and half
+// as many stores again; o is rounded to bf16 anyhow.
 template <bool kMasked>
 __device__ __forceinline__ void weights(uint32_t tS, float c, float base, const uint32_t (&w)[2],
                                         float& top, float& total, uint32_t (&pk)[2][16]) {
