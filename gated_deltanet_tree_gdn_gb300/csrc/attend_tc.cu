@@ -31,7 +31,7 @@
 // 166), although a unit of one row tile gained by it (112 to 94 us for 20 smaller trees).
 //
 // Measured: those 32 trees over 256 to 4096 rows and a prefix of 1024, 32 heads of 128: 159 us,
-// 1.2 PFLOP/s; causal prompts of 4096 and 16384 rows 180 and 2373 us, 0.77 and 0.93 PFLOP/s.
+// 1.1 PFLOP/s; causal prompts of 4096 and 16384 rows 180 and 2373 us, 0.77 and 0.93 PFLOP/s.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one its
 // sums use (exact either way: P and l stay far below the overflow of their types).
