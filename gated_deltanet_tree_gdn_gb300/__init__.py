@@ -17,6 +17,13 @@ Serving a hybrid model around it (ragged batches, states in a pool, a paged cach
     o, lse = attend(...)            # trees or tokens over a paged cache with a shared prefix
     new_len = cache_append(...)     # accepted rows (or a prompt's) join the cache
 
+In front of the attention:
+
+    freq, scale = rope_frequencies(...)      # a model's rotary frequencies, once
+    positions = tree_positions(...)          # of draft trees' nodes, or of prompts' rows
+    q, k = norm_rope(...)                    # heads normalised and rotated in one pass
+    q, new_len = cache_append_rope(...)      # rows normalised and rotated into the cache
+
 Build the library first with ``python -m gated_deltanet_tree_gdn_gb300.build``.
 """
 
@@ -25,7 +32,8 @@ from ._binding import (  # noqa: F401
     STATUS_BAD_PATH, STATUS_TIMEOUT, SYMBOLS, Dims, GdnTreeError, commit, commit_verify,
     library_path, load, strerror, verify, verify_recurrent, verify_packed, commit_packed,
     commit_verify_packed, STATUS_BAD_LAYOUT, build_topw, AttendDims, prefill,
-    prefill_workspace, decode_step, attend, attend_workspace, cache_append,
+    prefill_workspace, decode_step, attend, attend_workspace, cache_append, tree_positions,
+    norm_rope, cache_append_rope, rope_frequencies,
 )
 from .build import build_library  # noqa: F401
 

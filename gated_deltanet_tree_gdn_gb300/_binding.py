@@ -27,7 +27,9 @@ SYMBOLS = ("gdn_tree_verify", "gdn_tree_commit", "gdn_tree_commit_verify",
            "gdn_tree_verify_recurrent", "gdn_tree_verify_packed", "gdn_tree_commit_packed",
            "gdn_tree_commit_verify_packed", "gdn_tree_build_topw", "gdn_tree_prefill", "gdn_tree_prefill_workspace",
            "gdn_tree_decode_step", "gdn_tree_attend", "gdn_tree_attend_workspace",
-           "gdn_tree_cache_append", "gdn_tree_strerror", "gdn_tree_version")
+           "gdn_tree_cache_append", "gdn_tree_norm_rope", "gdn_tree_cache_append_rope",
+           "gdn_tree_positions", "gdn_tree_rope_frequencies", "gdn_tree_strerror",
+           "gdn_tree_version")
 
 
 class Dims(ctypes.Structure):
@@ -38,6 +40,29 @@ class AttendDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "N", "Hq", "Hkv", "D", "dtype",
                                               "page_size", "n_pages", "table_width",
                                               "prefix_len")]
+
+
+NORMS = {None: 0, "rms": 1, "unit": 2}
+STRETCHES = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rotary_dim", "interleaved", "norm")] + [
+        (n, ctypes.c_float) for n in ("scale", "eps")]
+
+
+class RopeStretch(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("factor", "trained_len", "fast", "slow")]
+
+
+class Strides(ctypes.Structure):
+    _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    _names = ("q", "k", "v", "q_out", "k_out", "v_out")
+    _fields_ = [(n, ctypes.c_void_p) for n in _names] + [(n + "_strides", Strides) for n in _names]
 
 
 class GdnTreeError(RuntimeError):
@@ -103,6 +128,16 @@ def load(path: str | None = None):
     lib.gdn_tree_cache_append.argtypes = [vp, vp, ip, ip, i32, ip, vp, vp, ip, ip, ip, AttendDims,
                                           ip, vp]
     lib.gdn_tree_cache_append.restype = ctypes.c_int
+    lib.gdn_tree_norm_rope.argtypes = [vp, Strides, vp, Strides, ip, vp, fp, fp, vp, Strides, vp,
+                                       Strides, AttendDims, Rope, vp]
+    lib.gdn_tree_norm_rope.restype = ctypes.c_int
+    lib.gdn_tree_cache_append_rope.argtypes = [Heads, vp, fp, fp, ip, vp, vp, ip, ip, ip,
+                                               AttendDims, Rope, ip, vp]
+    lib.gdn_tree_cache_append_rope.restype = ctypes.c_int
+    lib.gdn_tree_positions.argtypes = [ip, ip, ip, i32, ip, i32, i32, i32, ip, vp]
+    lib.gdn_tree_positions.restype = ctypes.c_int
+    lib.gdn_tree_rope_frequencies.argtypes = [i32, ctypes.c_double, RopeStretch, vp, vp]
+    lib.gdn_tree_rope_frequencies.restype = ctypes.c_int
     lib.gdn_tree_strerror.argtypes = [ctypes.c_int]
     lib.gdn_tree_strerror.restype = ctypes.c_char_p
     lib.gdn_tree_version.argtypes = []
@@ -769,3 +804,235 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_cache_append")
     return new_len
+
+
+# ---------------------------------------------------------------------------
+# in front of the attention: positions, norms and rotation
+# ---------------------------------------------------------------------------
+
+def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, N_max=None,
+                   positions=None, dev_status=None, stream=None):
+    """The positions of draft trees' nodes, or of chains' rows (C ABI gdn_tree_positions):
+    prefix_len + context_len[b] + the node's depth.  Returns positions [T] int32.
+
+    parent [T] int32, trees of up to 1024 rows (None: every sequence's rows are a chain of any
+    length; T or positions then says how many rows there are); cu_nodes [B+1]; context_len [B]
+    int32 (None: 0).  positions is allocated when not given; rows of no sequence are left as
+    they are."""
+    if stream is not None:
+        return _on(stream, tree_positions, locals())
+    B = cu_nodes.shape[0] - 1
+    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+    _check_device(cu_nodes, "cu_nodes")
+    if parent is not None:
+        rows = parent.shape[0]
+    elif positions is not None:
+        rows = positions.shape[0]
+    elif T is not None:
+        rows = T
+    else:
+        raise ValueError("without parent, T or positions says how many rows there are")
+    if T is not None and T != rows:
+        raise ValueError(f"T is {T}, but there are {rows} rows")
+    if parent is not None:
+        _check(parent, "parent", torch.int32, (rows,))
+        _check_device(parent, "parent")
+    if context_len is not None:
+        _check(context_len, "context_len", torch.int32, (B,))
+        _check_device(context_len, "context_len")
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
+    if positions is None:
+        positions = torch.empty((rows,), dtype=torch.int32, device=cu_nodes.device)
+    _check(positions, "positions", torch.int32, (rows,))
+    _check_device(positions, "positions")
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+        _check_device(dev_status, "dev_status")
+    rc = load().gdn_tree_positions(_ptr(parent), _ptr(cu_nodes), _ptr(context_len), prefix_len,
+                                   _ptr(positions), B, rows, N_max, _ptr(dev_status), _stream())
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_positions")
+    return positions
+
+
+def rope_frequencies(rotary_dim, base=10000.0, *, stretch=None, factor=1.0, trained_len=0.0,
+                     fast=32.0, slow=1.0, device="cuda"):
+    """A model's rotary frequencies (C ABI gdn_tree_rope_frequencies), made once.  Returns
+    (freq [rotary_dim / 2] int64, rope_scale), as ``norm_rope`` takes them: freq is turns a
+    position in units of 2^-64.
+
+    stretch, for positions past those of the training: None, "linear" (slower by factor), "ntk"
+    (a larger base), "yarn" or "bands" (pairs that turn `slow` times or less in trained_len
+    positions are slower by factor, those that turn `fast` times or more keep their speed)."""
+    if stretch not in STRETCHES:
+        raise ValueError(f"stretch must be one of {list(STRETCHES)}, got {stretch!r}")
+    freq = (ctypes.c_uint64 * max(int(rotary_dim) // 2, 1))()
+    scale = ctypes.c_float()
+    rc = load().gdn_tree_rope_frequencies(
+        rotary_dim, base, RopeStretch(STRETCHES[stretch], factor, trained_len, fast, slow), freq,
+        ctypes.byref(scale))
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_rope_frequencies")
+    # (all below 2^63)
+    return torch.tensor(list(freq), dtype=torch.int64, device=device), scale.value
+
+
+def _check_device(t, name):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on another device than the current one")
+
+
+def _heads(t, name, dtype, shape):
+    """The strides of an array of heads [T, H, D] whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    row, head, one = t.stride()
+    if one != 1 and t.numel():
+        raise ValueError(f"{name}'s heads must be contiguous")
+    _check_device(t, name)
+    return row, head
+
+
+_NO_STRIDES = (0, 0)
+
+
+def _rope(D, freq, interleaved, rope_scale, norm, eps, weights):
+    """(rotary_dim, Rope) of the arguments that the calls below share."""
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
+    R = 0
+    if freq is not None:
+        R = 2 * freq.shape[0]
+        _check(freq, "freq", torch.int64, (R // 2,))
+        _check_device(freq, "freq")
+    for name, w in weights:
+        if w is not None:
+            _check(w, name, torch.float32, (D,))
+            _check_device(w, name)
+    return R, _struct(Rope, R, int(bool(interleaved)), NORMS[norm], float(rope_scale), float(eps))
+
+
+def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_scale=1.0,
+              norm=None, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None,
+              stream=None):
+    """Queries and keys normalised for each head and rotated by their rows' positions, in one
+    pass (C ABI gdn_tree_norm_rope).  Returns (q_out, k_out), None for one that is not given.
+
+    q [T,Hq,D], k [T,Hkv,D] (bf16 or fp32; either may be None), heads contiguous, rows and heads
+    with any strides of whole 16 bytes: columns of a projection's output need no copy.  norm:
+    None, "rms" (with q_weight, k_weight [D] fp32, or without) or "unit".  positions [T] int32
+    and freq [R/2] (``rope_frequencies``) rotate the first R elements of each head, element i
+    with i + R/2 or, interleaved, 2 i with 2 i + 1; both None: no rotation.  q_out, k_out are
+    allocated when not given; q_out=q and k_out=k work in place."""
+    if stream is not None:
+        return _on(stream, norm_rope, locals())
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    T, _, D = x.shape
+    dt = x.dtype
+    code = _dtype_code(x)
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq are given together or not at all")
+    Hq = Hkv = 0
+    qs = ks = qo = ko = _NO_STRIDES
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _heads(q, "q", dt, (T, Hq, D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        qo = _heads(q_out, "q_out", dt, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError("q_out is given with q")
+    if k is not None:
+        Hkv = k.shape[1]
+        ks = _heads(k, "k", dt, (T, Hkv, D))
+        if k_out is None:
+            k_out = torch.empty((T, Hkv, D), dtype=dt, device=k.device)
+        ko = _heads(k_out, "k_out", dt, (T, Hkv, D))
+    elif k_out is not None:
+        raise ValueError("k_out is given with k")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (T,))
+        _check_device(positions, "positions")
+    _, rope = _rope(D, freq, interleaved, rope_scale, norm, eps,
+                    (("q_weight", q_weight), ("k_weight", k_weight)))
+    rc = load().gdn_tree_norm_rope(
+        _ptr(q), _struct(Strides, *qs), _ptr(k), _struct(Strides, *ks), _ptr(positions),
+        _ptr(freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _struct(Strides, *qo),
+        _ptr(k_out), _struct(Strides, *ko),
+        _struct(AttendDims, 0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), rope, _stream())
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_norm_rope")
+    return q_out, k_out
+
+
+def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_len, freq=None, *,
+                      prefix_len=0, interleaved=False, rope_scale=1.0, norm=None, q_weight=None,
+                      k_weight=None, eps=1e-6, q_out=None, k_out=None, v_out=None, N_max=None,
+                      new_len=None, dev_status=None, stream=None):
+    """All rows of each sequence join its paged cache, keys normalised and rotated on the way
+    (C ABI gdn_tree_cache_append_rope).  Returns (q_out, new_len).
+
+    Row j of sequence b stands at position prefix_len + context_len[b] + j.  k, v [T,Hkv,D] and
+    q [T,Hq,D] (None: keys and values alone) with strides as for ``norm_rope``, whose freq,
+    interleaved, rope_scale, norm, weights and eps these are.  k_cache, v_cache
+    [n_pages,page_size,Hkv,D] are written in place, as by ``cache_append``.  q_out (the queries
+    normalised and rotated) is allocated when not given; k_out and v_out, where given, get the
+    rows' keys and values too (what ``attend`` takes beside the cache).  context_len itself is
+    not changed: new_len [B] int32 holds the lengths after the call."""
+    if stream is not None:
+        return _on(stream, cache_append_rope, locals())
+    T, Hkv, D = k.shape
+    B = cu_nodes.shape[0] - 1
+    dt = k.dtype
+    code = _dtype_code(k)
+    Hq = 0
+    qs = qo = ko = vo = _NO_STRIDES
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _heads(q, "q", dt, (T, Hq, D))
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=k.device)
+        qo = _heads(q_out, "q_out", dt, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError("q_out is given with q")
+    ks = _heads(k, "k", dt, (T, Hkv, D))
+    vs = _heads(v, "v", dt, (T, Hkv, D))
+    if k_out is not None:
+        ko = _heads(k_out, "k_out", dt, (T, Hkv, D))
+    if v_out is not None:
+        vo = _heads(v_out, "v_out", dt, (T, Hkv, D))
+    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
+    n_pages, page, width = _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt)
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
+    if new_len is None:
+        new_len = torch.empty((B,), dtype=torch.int32, device=k.device)
+    _check(new_len, "new_len", torch.int32, (B,))
+    for name, t in (("cu_nodes", cu_nodes), ("k_cache", k_cache), ("v_cache", v_cache),
+                    ("page_table", page_table), ("context_len", context_len),
+                    ("new_len", new_len)):
+        _check_device(t, name)
+    if dev_status is not None:
+        _check(dev_status, "dev_status", torch.int32, (B,))
+        _check_device(dev_status, "dev_status")
+    _, rope = _rope(D, freq, interleaved, rope_scale, norm, eps,
+                    (("q_weight", q_weight), ("k_weight", k_weight)))
+    heads = Heads(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out), _ptr(v_out),
+                  qs, ks, vs, qo, ko, vo)
+    rc = load().gdn_tree_cache_append_rope(
+        heads, _ptr(freq), _ptr(q_weight), _ptr(k_weight), _ptr(cu_nodes), _ptr(k_cache),
+        _ptr(v_cache), _ptr(page_table), _ptr(context_len), _ptr(new_len),
+        _struct(AttendDims, B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len), rope,
+        _ptr(dev_status), _stream())
+    if rc != OK:
+        raise GdnTreeError(rc, "gdn_tree_cache_append_rope")
+    return q_out, new_len

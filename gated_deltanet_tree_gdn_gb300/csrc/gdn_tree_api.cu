@@ -4,6 +4,7 @@
 // before anything is enqueued; the kernels only check what depends on device
 // data (tree and path validity) and report it through dev_status.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -89,6 +90,99 @@ int check_attend_dims(const gdn_tree_attend_dims& d) {
     return GDN_TREE_EUNSUPPORTED;
   return GDN_TREE_OK;
 }
+
+// T rows of H heads of `width` bytes, `row` and `head` bytes apart
+struct HeadRows {
+  const char* p;
+  long long row, head, T, H, width;
+
+  bool any() const { return p != nullptr && T > 0 && H > 0; }
+  long long span() const { return (H - 1) * head + width; }  // of a row
+  bool same(const HeadRows& o) const {
+    return p == o.p && row == o.row && head == o.head && T == o.T && H == o.H;
+  }
+  size_t extent() const { return any() ? (size_t)((T - 1) * row + span()) : 0; }
+  // no two heads of it share a byte
+  bool apart() const {
+    return T * H <= 1 || (head >= width && (T == 1 || row >= span())) || (H == 1 && row >= width) ||
+           (row >= width && head >= (T - 1) * row + width);
+  }
+};
+
+// two arrays of heads share no byte (as far as their extents, or equal strides, tell)
+bool disjoint(const HeadRows& a, const HeadRows& b) {
+  if (!a.any() || !b.any() || !any_overlap(a.p, a.extent(), b.p, b.extent())) return true;
+  const auto beside = [](long long off, long long period, long long wa, long long wb) {
+    off = ((off % period) + period) % period;
+    return off >= wa && off + wb <= period;
+  };
+  const long long off = b.p - a.p;
+  // columns of the same rows
+  const bool rows = a.T > 1 && b.T > 1;
+  if (rows && a.row == b.row && a.span() <= a.row && b.span() <= a.row &&
+      beside(off, a.row, a.span(), b.span()))
+    return true;
+  // columns of the same heads (of one row, or of rows of whole heads)
+  return a.H > 1 && b.H > 1 && a.head == b.head && a.head > 0 &&
+         (a.T == 1 || a.row % a.head == 0) && (b.T == 1 || b.row % a.head == 0) &&
+         beside(off, a.head, a.width, b.width);
+}
+
+// fills `out` from a pointer and strides in elements; strides that step over a single row or
+// head do not count.  Misaligned or negative ones, or strides out of range, are refused.
+int check_heads(const void* p, gdn_tree_strides* s, int T, int H, int D, int dtype,
+                HeadRows* out) {
+  const long long es = dtype == GDN_TREE_BF16 ? 2 : 4;
+  if (T <= 1) s->row = 0;
+  if (H <= 1) s->head = 0;
+  if (!aligned16(p) || s->row < 0 || s->head < 0 || s->row % (16 / es) || s->head % (16 / es))
+    return GDN_TREE_EINVAL;
+  // (offsets, in bytes, stay within 63 bits)
+  if (s->row > (1ll << 60) / (T > 0 ? T : 1) / es || s->head > (1ll << 60) / (H > 0 ? H : 1) / es)
+    return GDN_TREE_EUNSUPPORTED;
+  *out = HeadRows{static_cast<const char*>(p), s->row * es, s->head * es, T, H, D * es};
+  return GDN_TREE_OK;
+}
+
+int check_rope(const gdn_tree_attend_dims& d, const gdn_tree_rope& r, const uint64_t* freq,
+               const float* q_weight, const float* k_weight) {
+  if (d.T < 0) return GDN_TREE_EINVAL;
+  if (d.dtype != GDN_TREE_BF16 && d.dtype != GDN_TREE_F32) return GDN_TREE_EUNSUPPORTED;
+  if (!supported_head_dim(d.D)) return GDN_TREE_EUNSUPPORTED;
+  if (r.rotary_dim < 0 || r.rotary_dim > d.D || r.rotary_dim % 2 || r.interleaved < 0 ||
+      r.interleaved > 1 || r.norm < GDN_TREE_NORM_NONE || r.norm > GDN_TREE_NORM_UNIT)
+    return GDN_TREE_EINVAL;
+  if (r.norm != GDN_TREE_NORM_NONE && !(r.eps >= 0.f && r.eps <= 3e38f)) return GDN_TREE_EINVAL;
+  if (r.norm == GDN_TREE_NORM_NONE && (q_weight || k_weight)) return GDN_TREE_EINVAL;
+  if (r.rotary_dim > 0 && freq == nullptr) return GDN_TREE_EINVAL;
+  if (!aligned16(freq) || !aligned16(q_weight) || !aligned16(k_weight)) return GDN_TREE_EINVAL;
+  return GDN_TREE_OK;
+}
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+
+// outputs out[i] of inputs in[i] (in place, or apart from every array of the call)
+int check_apart(const HeadRows* in, const HeadRows* out, int n, const Range* others, int m) {
+  for (int i = 0; i < n; ++i) {
+    if (!out[i].any()) continue;
+    if (!out[i].apart()) return GDN_TREE_EINVAL;
+    for (int j = 0; j < n; ++j) {
+      if (!(i == j && out[i].same(in[j])) && !disjoint(out[i], in[j])) return GDN_TREE_EINVAL;
+      if (i < j && !disjoint(out[i], out[j])) return GDN_TREE_EINVAL;
+    }
+    for (int j = 0; j < m; ++j)
+      if (others[j].p && any_overlap(out[i].p, out[i].extent(), others[j].p, others[j].bytes))
+        return GDN_TREE_EINVAL;
+  }
+  return GDN_TREE_OK;
+}
+
+// heads of a row of the calls in front of the attention (a warp's share of them is counted in
+// 32 bits, and no model has more)
+constexpr int kMostHeads = 1 << 20;
 
 // Per-sequence status words start at GDN_TREE_STATUS_OK; the kernels raise
 // them with atomicMax, so that no unit's report can be lost to another's.
@@ -581,6 +675,189 @@ int gdn_tree_cache_append(const void* k, const void* v, const int32_t* path,
                           context_len, new_len, dims, dev_status};
   const cudaError_t err = gdn::launch_cache_append(a, st);
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_norm_rope(const void* q, gdn_tree_strides q_strides, const void* k,
+                       gdn_tree_strides k_strides, const int32_t* positions,
+                       const uint64_t* freq, const float* q_weight, const float* k_weight,
+                       void* q_out, gdn_tree_strides q_out_strides, void* k_out,
+                       gdn_tree_strides k_out_strides, gdn_tree_attend_dims dims,
+                       gdn_tree_rope rope, void* stream) {
+  if (q == nullptr) dims.Hq = 0, q_weight = nullptr, q_out = nullptr;
+  if (k == nullptr) dims.Hkv = 0, k_weight = nullptr, k_out = nullptr;
+  int rc = check_rope(dims, rope, freq, q_weight, k_weight);
+  if (rc != GDN_TREE_OK) return rc;
+  if ((q != nullptr && dims.Hq <= 0) || (k != nullptr && dims.Hkv <= 0)) return GDN_TREE_EINVAL;
+  if (dims.Hq + (long long)dims.Hkv > kMostHeads) return GDN_TREE_EUNSUPPORTED;
+  if (!aligned4(positions)) return GDN_TREE_EINVAL;
+  if (dims.T == 0) return GDN_TREE_OK;
+  if (q == nullptr && k == nullptr) return GDN_TREE_EINVAL;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
+      (rope.rotary_dim > 0 && positions == nullptr))
+    return GDN_TREE_EINVAL;
+  HeadRows in[2], out[2];
+  const int T = dims.T, D = dims.D, dt = dims.dtype;
+  if ((rc = check_heads(q, &q_strides, T, dims.Hq, D, dt, &in[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k, &k_strides, T, dims.Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
+      (rc = check_heads(q_out, &q_out_strides, T, dims.Hq, D, dt, &out[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k_out, &k_out_strides, T, dims.Hkv, D, dt, &out[1])) != GDN_TREE_OK)
+    return rc;
+  const Range others[] = {{positions, rope.rotary_dim ? (size_t)T * 4 : 0},
+                          {freq, (size_t)rope.rotary_dim * 4},
+                          {q_weight, (size_t)D * 4},
+                          {k_weight, (size_t)D * 4}};
+  rc = check_apart(in, out, 2, others, 4);
+  if (rc != GDN_TREE_OK) return rc;
+  gdn::RopeArgs a{};
+  a.x = gdn_tree_heads{q, k, nullptr, q_out, k_out, nullptr, q_strides, k_strides,
+                       gdn_tree_strides{}, q_out_strides, k_out_strides, gdn_tree_strides{}};
+  a.positions = positions;
+  a.freq = freq;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.d = dims;
+  a.rope = rope;
+  const cudaError_t err = gdn::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_cache_append_rope(gdn_tree_heads x, const uint64_t* freq, const float* q_weight,
+                               const float* k_weight, const int32_t* cu_nodes, void* k_cache,
+                               void* v_cache, const int32_t* page_table,
+                               const int32_t* context_len, int32_t* new_len,
+                               gdn_tree_attend_dims dims, gdn_tree_rope rope,
+                               int32_t* dev_status, void* stream) {
+  const int Hq = x.q ? dims.Hq : 0;
+  if (x.q == nullptr) q_weight = nullptr, x.q_out = nullptr;
+  if (Hq < 0 || (x.q != nullptr && Hq == 0)) return GDN_TREE_EINVAL;
+  dims.Hq = dims.Hkv;  // (no multiple of Hkv is wanted here)
+  int rc = check_attend_dims(dims);
+  if (rc != GDN_TREE_OK) return rc;
+  dims.Hq = Hq;
+  rc = check_rope(dims, rope, freq, q_weight, k_weight);
+  if (rc != GDN_TREE_OK) return rc;
+  if (dims.Hq + 2ll * dims.Hkv > kMostHeads) return GDN_TREE_EUNSUPPORTED;
+  if (dims.B == 0) return GDN_TREE_OK;
+  dims.N = bounded_rows(dims.N, dims.T);
+  const bool rows = dims.T > 0, paged = rows && dims.table_width > 0 && dims.n_pages > 0;
+  if (rows && (x.k == nullptr || x.v == nullptr)) return GDN_TREE_EINVAL;
+  if (rows && (x.q == nullptr) != (x.q_out == nullptr)) return GDN_TREE_EINVAL;
+  void* const cache[] = {k_cache, v_cache};
+  for (const void* p : cache)
+    if ((paged && p == nullptr) || !aligned16(p)) return GDN_TREE_EINVAL;
+  const void* ints[] = {cu_nodes, context_len};
+  for (const void* p : ints)
+    if (p == nullptr || !aligned4(p)) return GDN_TREE_EINVAL;
+  const void* opt[] = {page_table, new_len, dev_status};
+  for (const void* p : opt)
+    if (!aligned4(p)) return GDN_TREE_EINVAL;
+  if (dims.table_width > 0 && page_table == nullptr) return GDN_TREE_EINVAL;
+  HeadRows in[3], out[3];
+  const int T = dims.T, Hkv = dims.Hkv, D = dims.D, dt = dims.dtype;
+  if ((rc = check_heads(x.q, &x.q_strides, T, Hq, D, dt, &in[0])) != GDN_TREE_OK ||
+      (rc = check_heads(x.k, &x.k_strides, T, Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
+      (rc = check_heads(x.v, &x.v_strides, T, Hkv, D, dt, &in[2])) != GDN_TREE_OK ||
+      (rc = check_heads(x.q_out, &x.q_out_strides, T, Hq, D, dt, &out[0])) != GDN_TREE_OK ||
+      (rc = check_heads(x.k_out, &x.k_out_strides, T, Hkv, D, dt, &out[1])) != GDN_TREE_OK ||
+      (rc = check_heads(x.v_out, &x.v_out_strides, T, Hkv, D, dt, &out[2])) != GDN_TREE_OK)
+    return rc;
+  const size_t one = (size_t)Hkv * D * (dt == GDN_TREE_BF16 ? 2 : 4);
+  const size_t held = (size_t)dims.n_pages * dims.page_size * one, B4 = (size_t)dims.B * 4;
+  const Range others[] = {{freq, (size_t)rope.rotary_dim * 4},
+                          {q_weight, (size_t)D * 4},
+                          {k_weight, (size_t)D * 4},
+                          {cu_nodes, B4 + 4},
+                          {context_len, B4},
+                          {page_table, B4 * dims.table_width},
+                          {dev_status, B4},
+                          {new_len, B4},
+                          {v_cache, held},
+                          {k_cache, held}};
+  constexpr int kOthers = sizeof(others) / sizeof(others[0]);
+  rc = check_apart(in, out, 3, others, kOthers);
+  if (rc != GDN_TREE_OK) return rc;
+  // what else is written: the caches, new_len and dev_status
+  for (int w = kOthers - 4; w < kOthers; ++w) {
+    if (others[w].p == nullptr) continue;
+    for (int j = 0; j < w; ++j)
+      if (others[j].p && any_overlap(others[w].p, others[w].bytes, others[j].p, others[j].bytes))
+        return GDN_TREE_EINVAL;
+    for (const HeadRows& i : in)
+      if (any_overlap(others[w].p, others[w].bytes, i.p, i.extent())) return GDN_TREE_EINVAL;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
+  const gdn::RopeArgs a{x, nullptr, freq, q_weight, k_weight, dims, rope, cu_nodes, page_table,
+                        context_len, k_cache, v_cache, new_len, dev_status};
+  const cudaError_t err = gdn::launch_cache_append_rope(a, st);
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_positions(const int32_t* parent, const int32_t* cu_nodes,
+                       const int32_t* context_len, int32_t prefix_len, int32_t* positions,
+                       int32_t B, int32_t T, int32_t N, int32_t* dev_status, void* stream) {
+  if (B < 0 || T < 0 || N < 0 || prefix_len < 0) return GDN_TREE_EINVAL;
+  if (B > 65535 || (parent && N > gdn::kMaxNLongHost)) return GDN_TREE_EUNSUPPORTED;
+  if (B == 0) return GDN_TREE_OK;
+  if (cu_nodes == nullptr || (T > 0 && positions == nullptr)) return GDN_TREE_EINVAL;
+  const void* ints[] = {parent, cu_nodes, context_len, positions, dev_status};
+  for (const void* p : ints)
+    if (!aligned4(p)) return GDN_TREE_EINVAL;
+  const size_t T4 = (size_t)T * 4, B4 = (size_t)B * 4;
+  const Range others[] = {{parent, T4}, {cu_nodes, B4 + 4}, {context_len, B4}};
+  for (const Range& o : others)
+    if (o.p && ((positions && any_overlap(positions, T4, o.p, o.bytes)) ||
+                (dev_status && any_overlap(dev_status, B4, o.p, o.bytes))))
+      return GDN_TREE_EINVAL;
+  if (positions && dev_status && any_overlap(positions, T4, dev_status, B4))
+    return GDN_TREE_EINVAL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (clear_status(dev_status, B, st) != cudaSuccess) return GDN_TREE_ECUDA;
+  const gdn::PositionArgs a{parent, cu_nodes, context_len, prefix_len, positions, B, T,
+                            bounded_rows(N, T), dev_status};
+  const cudaError_t err = gdn::launch_tree_positions(a, st);
+  return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
+}
+
+int gdn_tree_rope_frequencies(int32_t rotary_dim, double base, gdn_tree_rope_stretch stretch,
+                              uint64_t* freq, float* scale) {
+  const int R = rotary_dim;
+  const gdn_tree_rope_stretch& s = stretch;
+  const bool bands = s.kind == GDN_TREE_STRETCH_YARN || s.kind == GDN_TREE_STRETCH_BANDS;
+  if (R < 2 || R % 2 || !(base > 1.0) || !isfinite(base) || freq == nullptr || scale == nullptr)
+    return GDN_TREE_EINVAL;
+  if (R > gdn::kMaxDHost || s.kind < GDN_TREE_STRETCH_NONE || s.kind > GDN_TREE_STRETCH_BANDS)
+    return GDN_TREE_EUNSUPPORTED;
+  if (s.kind != GDN_TREE_STRETCH_NONE && !(s.factor >= 1.0 && isfinite(s.factor)))
+    return GDN_TREE_EINVAL;
+  if (s.kind == GDN_TREE_STRETCH_NTK && R == 2) return GDN_TREE_EINVAL;
+  if (bands && !(s.trained_len > 0.0 && isfinite(s.trained_len) && s.slow > 0.0 &&
+                 s.fast > s.slow && isfinite(s.fast)))
+    return GDN_TREE_EINVAL;
+  const double kTurn = 6.283185307179586476925;  // 2 pi
+  if (s.kind == GDN_TREE_STRETCH_NTK) base *= pow(s.factor, (double)R / (R - 2));
+  // the number of the pair that turns `turns` times within the trained length
+  const auto pair_of = [&](double turns) {
+    return R * log(s.trained_len / (kTurn * turns)) / (2.0 * log(base));
+  };
+  double lo = 0.0, hi = 0.0;
+  if (s.kind == GDN_TREE_STRETCH_YARN) {
+    lo = fmax(floor(pair_of(s.fast)), 0.0);
+    hi = fmin(ceil(pair_of(s.slow)), R - 1.0);
+  }
+  for (int i = 0; i < R / 2; ++i) {
+    double f = pow(base, -2.0 * i / R);
+    double slow = s.kind == GDN_TREE_STRETCH_LINEAR ? 1.0 : 0.0;  // how much of it is slowed down
+    if (s.kind == GDN_TREE_STRETCH_YARN)
+      slow = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+    if (s.kind == GDN_TREE_STRETCH_BANDS)
+      slow = 1.0 - fmin(fmax((s.trained_len * f / kTurn - s.slow) / (s.fast - s.slow), 0.0), 1.0);
+    if (slow > 0.0) f = f * (1.0 - slow) + f / s.factor * slow;
+    // (below 2^63: f is at most 1, a sixth of a turn)
+    freq[i] = (uint64_t)llround(ldexp(f / kTurn, 64));
+  }
+  *scale = s.kind == GDN_TREE_STRETCH_YARN ? (float)(0.1 * log(s.factor) + 1.0) : 1.f;
+  return GDN_TREE_OK;
 }
 
 const char* gdn_tree_strerror(int code) {

@@ -229,6 +229,33 @@ struct AppendArgs {
 };
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 
+// heads normalised and rotated (norm_rope), and rows that join the cache on the way
+// (append: cu, page_table and the fields below them are set, positions is not)
+struct RopeArgs {
+  gdn_tree_heads x;
+  const int32_t* positions;
+  const uint64_t* freq;
+  const float *q_weight, *k_weight;
+  gdn_tree_attend_dims d;
+  gdn_tree_rope rope;
+  const int32_t *cu, *page_table, *context_len;
+  void *k_cache, *v_cache;
+  int32_t* new_len;
+  int32_t* dev_status;
+};
+cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_append_rope(const RopeArgs& a, cudaStream_t stream);
+
+// positions of tree nodes or of chains
+struct PositionArgs {
+  const int32_t *parent, *cu, *context_len;
+  int32_t prefix_len;
+  int32_t* positions;
+  int32_t B, T, N;
+  int32_t* dev_status;
+};
+cudaError_t launch_tree_positions(const PositionArgs& a, cudaStream_t stream);
+
 bool commit_verify_tc_supported(const gdn_tree_dims& d, int prev_N, int Lmax);
 cudaError_t launch_commit_verify_tc(const CommitVerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_commit_verify(const CommitVerifyArgs& a, cudaStream_t stream);

@@ -433,6 +433,143 @@ int gdn_tree_cache_append(const void *k, const void *v, const int32_t *path,
                           const int32_t *context_len, int32_t *new_len,
                           gdn_tree_attend_dims dims, int32_t *dev_status, void *stream);
 
+/*
+ * In front of the attention
+ * -------------------------
+ * What a layer's projection gives becomes what the calls above take: heads normalised,
+ * rotated by their rows' positions, and (for rows that join the cache) written to their
+ * pages on the way.
+ */
+
+/* norms of a head's row x of D elements, with weights w (all 1 where absent) */
+#define GDN_TREE_NORM_NONE 0
+#define GDN_TREE_NORM_RMS 1  /* x_i w_i / sqrt(sum x^2 / D + eps) */
+#define GDN_TREE_NORM_UNIT 2 /* x_i w_i / sqrt(sum x^2 + eps): unit length, for the delta rule */
+
+/*
+ * The rotation of the first rotary_dim = R elements of a head (the others pass): pair i of
+ * R / 2 is turned by the angle a = p f_i at position p,
+ *     (x, y) -> scale (x cos a - y sin a,  y cos a + x sin a),
+ * where pair i is elements i and i + R / 2 (interleaved 0) or 2 i and 2 i + 1 (interleaved 1).
+ * The norm, if any, comes first.  freq[i] is f_i as turns a position in units of 2^-64,
+ * round(f_i / (2 pi) 2^64) mod 2^64 (gdn_tree_rope_frequencies makes them): p freq[i] mod 2^64
+ * is then the angle's fraction of a turn, as exact at far positions as at near ones.
+ */
+typedef struct {
+  int32_t rotary_dim;  /* R: even, 0 .. D; 0: no rotation                     */
+  int32_t interleaved; /* 0 or 1                                              */
+  int32_t norm;        /* GDN_TREE_NORM_*                                     */
+  float scale;         /* of the rotated elements (1 unless the frequencies want another) */
+  float eps;           /* of the norm, >= 0                                   */
+} gdn_tree_rope;
+
+/* Where row t and head h of an array of heads start: t * row + h * head elements after its
+ * first (a head's D elements are contiguous).  Multiples of 16 bytes and not negative; what
+ * steps over a single row or head does not count.  An output's rows and heads must not
+ * overlap one another. */
+typedef struct {
+  int64_t row, head;
+} gdn_tree_strides;
+
+/*
+ * gdn_tree_norm_rope -- queries and keys normalised for each head and rotated, in one pass.
+ *
+ *   q, q_out     T rows of Hq heads of D;  k, k_out: of Hkv heads.  q or k may be NULL (its
+ *                output, weights, heads and strides then do not count).  An output may be its
+ *                own input (same pointer, same strides); any other overlap of an output with
+ *                an array of the call is refused.
+ *   positions    [T] int32, any value (NULL where rotary_dim is 0)
+ *   freq         [rotary_dim / 2] uint64, device (NULL where rotary_dim is 0)
+ *   q_weight, k_weight  [D] fp32 or NULL; NULL where there is no norm
+ *   dims         T, Hq, Hkv, D, dtype; the others are ignored.  D: 16, 32, ..., 128; Hq and
+ *                Hkv need not be multiples of one another.
+ * Sums, norms and rotations are fp32 and rounded once, to the output's type.  (Squares past
+ * the range of fp32, of elements past 1e19, overflow: the row's norm is then infinite.)
+ */
+int gdn_tree_norm_rope(const void *q, gdn_tree_strides q_strides, const void *k,
+                       gdn_tree_strides k_strides, const int32_t *positions,
+                       const uint64_t *freq, const float *q_weight, const float *k_weight,
+                       void *q_out, gdn_tree_strides q_out_strides, void *k_out,
+                       gdn_tree_strides k_out_strides, gdn_tree_attend_dims dims,
+                       gdn_tree_rope rope, void *stream);
+
+/* the arrays of heads of gdn_tree_cache_append_rope and their strides */
+typedef struct {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_out;
+  gdn_tree_strides q_strides, k_strides, v_strides, q_out_strides, k_out_strides, v_out_strides;
+} gdn_tree_heads;
+
+/*
+ * gdn_tree_cache_append_rope -- all rows of each sequence join its cache in order (prompts,
+ * parts of prompts, single tokens), normalised and rotated on the way.  For each sequence b
+ * and its row j, at position p = prefix_len + context_len[b] + j,
+ *     k row of the cache, context_len[b] + j  <-  norm and rotation at p of k's row,
+ *     v row of the cache, context_len[b] + j  <-  v's row,
+ *     q_out, k_out, v_out  <-  the same of q, k and v, in the rows' own order,
+ * and new_len[b] = context_len[b] + its rows.
+ *
+ *   heads        k, v: rows of Hkv heads.  q with q_out: of Hq heads, or both NULL.  k_out and
+ *                v_out (what gdn_tree_attend takes as the rows' own keys and values): NULL
+ *                where they are not wanted; they may be k and v themselves, q_out may be q.
+ *                Any other overlap of an output with an array of the call is refused.
+ *   cu_nodes, page_table, context_len, k_cache, v_cache, new_len: as for
+ *                gdn_tree_cache_append; dims.prefix_len: the rows that come before every
+ *                sequence's own (they need not be in a cache)
+ *   freq, q_weight, k_weight, rope: as for gdn_tree_norm_rope
+ * With the cache's rows rotated, gdn_tree_attend without k and v and with new_len attends to
+ * a single token's own row too.
+ * dev_status[b]: GDN_TREE_STATUS_BAD_LAYOUT.  Rows without a place in the cache (a bad page, or
+ * past the table) are not written there, their outputs are; of a sequence whose cu_nodes or
+ * context_len is invalid nothing is written and new_len[b] = context_len[b].  Where cu_nodes
+ * decreases, the other sequences are unspecified too (nothing outside the arrays is touched).
+ */
+int gdn_tree_cache_append_rope(gdn_tree_heads heads, const uint64_t *freq, const float *q_weight,
+                               const float *k_weight, const int32_t *cu_nodes, void *k_cache,
+                               void *v_cache, const int32_t *page_table,
+                               const int32_t *context_len, int32_t *new_len,
+                               gdn_tree_attend_dims dims, gdn_tree_rope rope,
+                               int32_t *dev_status, void *stream);
+
+/*
+ * gdn_tree_positions -- the positions of a draft tree's nodes (or of a prompt's rows):
+ *     positions[cu_nodes[b] + t] = prefix_len + context_len[b] + depth(t),
+ * where a root's depth is 0 and another node's is its parent's plus 1.
+ *
+ *   parent       [T] int32 as for gdn_tree_attend, N <= 1024; NULL: chains of any length
+ *                (depth(t) = t)
+ *   context_len  [B] int32, >= 0, or NULL: 0
+ *   positions    [T] int32; rows of no sequence are left as they are
+ * B sequences of at most N of T rows.  dev_status[b] (or NULL): GDN_TREE_STATUS_BAD_TREE, or
+ * GDN_TREE_STATUS_BAD_LAYOUT (cu_nodes, context_len, or a position that 32 bits do not hold);
+ * that sequence's positions are then left as they are.  positions overlaps no other array.
+ */
+int gdn_tree_positions(const int32_t *parent, const int32_t *cu_nodes,
+                       const int32_t *context_len, int32_t prefix_len, int32_t *positions,
+                       int32_t B, int32_t T, int32_t N, int32_t *dev_status, void *stream);
+
+/* How the frequencies base^(-2 i / R) are changed for positions past the training's. */
+#define GDN_TREE_STRETCH_NONE 0
+#define GDN_TREE_STRETCH_LINEAR 1 /* f / factor */
+#define GDN_TREE_STRETCH_NTK 2    /* base * factor^(R / (R - 2)) in place of base (R > 2) */
+#define GDN_TREE_STRETCH_YARN 3   /* f for pairs that turn `fast` times or more in trained_len
+                                     positions, f / factor for those that turn `slow` times or
+                                     less, blended by the pair's number between (Peng et al.,
+                                     "YaRN"); scale = 0.1 ln(factor) + 1 */
+#define GDN_TREE_STRETCH_BANDS 4  /* the same bands, blended by the number of turns; scale 1 */
+
+typedef struct {
+  int32_t kind;        /* GDN_TREE_STRETCH_*; the fields below are read where it uses them */
+  double factor;       /* >= 1 */
+  double trained_len;  /* > 0 */
+  double fast, slow;   /* 0 < slow < fast */
+} gdn_tree_rope_stretch;
+
+/* A model's frequencies, on the HOST: freq[rotary_dim / 2] as gdn_tree_rope says, to be copied
+ * to the device once, and its scale.  rotary_dim: even, 2 .. 128; base > 1. */
+int gdn_tree_rope_frequencies(int32_t rotary_dim, double base, gdn_tree_rope_stretch stretch,
+                              uint64_t *freq, float *scale);
+
 /* Human-readable text for a return code or a device status code. */
 const char *gdn_tree_strerror(int code);
 
