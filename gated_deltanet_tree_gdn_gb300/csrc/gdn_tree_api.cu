@@ -149,6 +149,7 @@ int check_rope(const gdn_tree_attend_dims& d, const gdn_tree_rope& r, const uint
   if (d.T < 0) return GDN_TREE_EINVAL;
   if (d.dtype != GDN_TREE_BF16 && d.dtype != GDN_TREE_F32) return GDN_TREE_EUNSUPPORTED;
   if (!supported_head_dim(d.D)) return GDN_TREE_EUNSUPPORTED;
+  if (d.T > 0x7fffffff - 4096) return GDN_TREE_EUNSUPPORTED;  // (a unit's number fits 32 bits)
   if (r.rotary_dim < 0 || r.rotary_dim > d.D || r.rotary_dim % 2 || r.interleaved < 0 ||
       r.interleaved > 1 || r.norm < GDN_TREE_NORM_NONE || r.norm > GDN_TREE_NORM_UNIT)
     return GDN_TREE_EINVAL;
