@@ -60,9 +60,8 @@ class Strides(ctypes.Structure):
     _fields_ = [("row", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
-class Heads(ctypes.Structure):
-    _names = ("q", "k", "v", "q_out", "k_out", "v_out")
-    _fields_ = [(n, ctypes.c_void_p) for n in _names] + [(n + "_strides", Strides) for n in _names]
+class HeadStrides(ctypes.Structure):
+    _fields_ = [(n, Strides) for n in ("q", "k", "v", "q_out", "k_out", "v_out")]
 
 
 class GdnTreeError(RuntimeError):
@@ -128,11 +127,11 @@ def load(path: str | None = None):
     lib.gdn_tree_cache_append.argtypes = [vp, vp, ip, ip, i32, ip, vp, vp, ip, ip, ip, AttendDims,
                                           ip, vp]
     lib.gdn_tree_cache_append.restype = ctypes.c_int
-    lib.gdn_tree_norm_rope.argtypes = [vp, Strides, vp, Strides, ip, vp, fp, fp, vp, Strides, vp,
-                                       Strides, AttendDims, Rope, vp]
+    lib.gdn_tree_norm_rope.argtypes = [vp, vp, ip, vp, fp, fp, vp, vp, HeadStrides, AttendDims,
+                                       Rope, vp]
     lib.gdn_tree_norm_rope.restype = ctypes.c_int
-    lib.gdn_tree_cache_append_rope.argtypes = [Heads, vp, fp, fp, ip, vp, vp, ip, ip, ip,
-                                               AttendDims, Rope, ip, vp]
+    lib.gdn_tree_cache_append_rope.argtypes = [vp, vp, vp, vp, fp, fp, ip, vp, vp, vp, vp, vp, ip,
+                                               ip, ip, HeadStrides, AttendDims, Rope, ip, vp]
     lib.gdn_tree_cache_append_rope.restype = ctypes.c_int
     lib.gdn_tree_positions.argtypes = [ip, ip, ip, i32, ip, i32, i32, i32, ip, vp]
     lib.gdn_tree_positions.restype = ctypes.c_int
@@ -810,6 +809,72 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
 # in front of the attention: positions, norms and rotation
 # ---------------------------------------------------------------------------
 
+# (These take 4 to 18 tensors ahead of a launch of 2 microseconds: a tensor is looked at once, and
+# what the call needs of the shapes is made once for each set of them.)
+
+def _flat(t, name, dtype, shape, dev):
+    """The address of a dense tensor of this type and shape on the current device."""
+    if not (type(t) is torch.Tensor and t.get_device() == dev and t.dtype is dtype
+            and t.is_contiguous() and t.shape == shape):
+        _check(t, name, dtype, shape)
+        _check_device(t, name, dev)
+    return t.data_ptr()
+
+
+def _check_device(t, name, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device than the current one")
+
+
+def _device(t, name):
+    """The current device, which t is on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    _check_device(t, name, dev)
+    return dev
+
+
+def _heads(t, name, dtype, shape, dev):
+    """The strides of an array of heads [T, H, D] whose heads are contiguous."""
+    if type(t) is torch.Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == shape:
+        strides = t.stride()
+        if strides[2] == 1:
+            return strides
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name}'s heads must be contiguous")
+    _check_device(t, name, dev)
+    return t.stride()
+
+
+_NO_STRIDES = (0, 0, 0)
+_rope_cache: dict = {}
+
+
+def _rope_structs(strides, dims, interleaved, norm, rope_scale, eps, R):
+    """The structs of a call: HeadStrides, AttendDims and Rope."""
+    key = (strides, dims, interleaved, norm, rope_scale, eps, R)
+    known = _rope_cache.get(key)
+    if known is None:
+        if norm not in NORMS:
+            raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
+        known = (HeadStrides(*(Strides(*s[:2]) for s in strides)), AttendDims(*dims),
+                 Rope(R, int(bool(interleaved)), NORMS[norm], rope_scale, eps))
+        if len(_rope_cache) < 256:
+            _rope_cache[key] = known
+    return known
+
+
 def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, N_max=None,
                    positions=None, dev_status=None, stream=None):
     """The positions of draft trees' nodes, or of chains' rows (C ABI gdn_tree_positions):
@@ -821,9 +886,9 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
     they are."""
     if stream is not None:
         return _on(stream, tree_positions, locals())
+    dev = _device(cu_nodes, "cu_nodes")
     B = cu_nodes.shape[0] - 1
-    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
-    _check_device(cu_nodes, "cu_nodes")
+    cu = _flat(cu_nodes, "cu_nodes", torch.int32, (B + 1,), dev)
     if parent is not None:
         rows = parent.shape[0]
     elif positions is not None:
@@ -834,23 +899,16 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
         raise ValueError("without parent, T or positions says how many rows there are")
     if T is not None and T != rows:
         raise ValueError(f"T is {T}, but there are {rows} rows")
-    if parent is not None:
-        _check(parent, "parent", torch.int32, (rows,))
-        _check_device(parent, "parent")
-    if context_len is not None:
-        _check(context_len, "context_len", torch.int32, (B,))
-        _check_device(context_len, "context_len")
     if N_max is None:
         N_max = _most_rows(cu_nodes)
     if positions is None:
         positions = torch.empty((rows,), dtype=torch.int32, device=cu_nodes.device)
-    _check(positions, "positions", torch.int32, (rows,))
-    _check_device(positions, "positions")
-    if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (B,))
-        _check_device(dev_status, "dev_status")
-    rc = load().gdn_tree_positions(_ptr(parent), _ptr(cu_nodes), _ptr(context_len), prefix_len,
-                                   _ptr(positions), B, rows, N_max, _ptr(dev_status), _stream())
+    rc = load().gdn_tree_positions(
+        None if parent is None else _flat(parent, "parent", torch.int32, (rows,), dev), cu,
+        None if context_len is None else _flat(context_len, "context_len", torch.int32, (B,), dev),
+        prefix_len, _flat(positions, "positions", torch.int32, (rows,), dev), B, rows, N_max,
+        None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, (B,), dev),
+        _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_positions")
     return positions
@@ -878,47 +936,6 @@ def rope_frequencies(rotary_dim, base=10000.0, *, stretch=None, factor=1.0, trai
     return torch.tensor(list(freq), dtype=torch.int64, device=device), scale.value
 
 
-def _check_device(t, name):
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on another device than the current one")
-
-
-def _heads(t, name, dtype, shape):
-    """The strides of an array of heads [T, H, D] whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    row, head, one = t.stride()
-    if one != 1 and t.numel():
-        raise ValueError(f"{name}'s heads must be contiguous")
-    _check_device(t, name)
-    return row, head
-
-
-_NO_STRIDES = (0, 0)
-
-
-def _rope(D, freq, interleaved, rope_scale, norm, eps, weights):
-    """(rotary_dim, Rope) of the arguments that the calls below share."""
-    if norm not in NORMS:
-        raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
-    R = 0
-    if freq is not None:
-        R = 2 * freq.shape[0]
-        _check(freq, "freq", torch.int64, (R // 2,))
-        _check_device(freq, "freq")
-    for name, w in weights:
-        if w is not None:
-            _check(w, name, torch.float32, (D,))
-            _check_device(w, name)
-    return R, _struct(Rope, R, int(bool(interleaved)), NORMS[norm], float(rope_scale), float(eps))
-
-
 def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_scale=1.0,
               norm=None, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None,
               stream=None):
@@ -936,39 +953,48 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
+    if (positions is None) != (freq is None):
+        raise ValueError("positions and freq are given together or not at all")
     T, _, D = x.shape
     dt = x.dtype
     code = _dtype_code(x)
-    if (positions is None) != (freq is None):
-        raise ValueError("positions and freq are given together or not at all")
-    Hq = Hkv = 0
+    dev = _device(x, "q" if x is q else "k")
+    Hq = Hkv = R = 0
     qs = ks = qo = ko = _NO_STRIDES
+    qp = kp = qop = kop = pp = fp = wq = wk = None
     if q is not None:
-        Hq = q.shape[1]
-        qs = _heads(q, "q", dt, (T, Hq, D))
+        shape = q.shape
+        Hq = shape[1]
+        qs = _heads(q, "q", dt, (T, Hq, D), dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-        qo = _heads(q_out, "q_out", dt, (T, Hq, D))
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        qo = _heads(q_out, "q_out", dt, shape, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        if q_weight is not None:
+            wq = _flat(q_weight, "q_weight", torch.float32, (D,), dev)
     elif q_out is not None:
         raise ValueError("q_out is given with q")
     if k is not None:
-        Hkv = k.shape[1]
-        ks = _heads(k, "k", dt, (T, Hkv, D))
+        shape = k.shape
+        Hkv = shape[1]
+        ks = _heads(k, "k", dt, (T, Hkv, D), dev)
         if k_out is None:
-            k_out = torch.empty((T, Hkv, D), dtype=dt, device=k.device)
-        ko = _heads(k_out, "k_out", dt, (T, Hkv, D))
+            k_out = torch.empty(shape, dtype=dt, device=k.device)
+        ko = _heads(k_out, "k_out", dt, shape, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        if k_weight is not None:
+            wk = _flat(k_weight, "k_weight", torch.float32, (D,), dev)
     elif k_out is not None:
         raise ValueError("k_out is given with k")
-    if positions is not None:
-        _check(positions, "positions", torch.int32, (T,))
-        _check_device(positions, "positions")
-    _, rope = _rope(D, freq, interleaved, rope_scale, norm, eps,
-                    (("q_weight", q_weight), ("k_weight", k_weight)))
-    rc = load().gdn_tree_norm_rope(
-        _ptr(q), _struct(Strides, *qs), _ptr(k), _struct(Strides, *ks), _ptr(positions),
-        _ptr(freq), _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _struct(Strides, *qo),
-        _ptr(k_out), _struct(Strides, *ko),
-        _struct(AttendDims, 0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), rope, _stream())
+    if freq is not None:
+        half = freq.shape[0]
+        R = 2 * half
+        fp = _flat(freq, "freq", torch.int64, (half,), dev)
+        pp = _flat(positions, "positions", torch.int32, (T,), dev)
+    strides, dims, rope = _rope_structs((qs, ks, _NO_STRIDES, qo, ko),
+                                        (0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), interleaved, norm,
+                                        rope_scale, eps, R)
+    rc = load().gdn_tree_norm_rope(qp, kp, pp, fp, wq, wk, qop, kop, strides, dims, rope, _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_norm_rope")
     return q_out, k_out
@@ -990,49 +1016,61 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
     not changed: new_len [B] int32 holds the lengths after the call."""
     if stream is not None:
         return _on(stream, cache_append_rope, locals())
-    T, Hkv, D = k.shape
+    shape = k.shape
+    T, Hkv, D = shape
     B = cu_nodes.shape[0] - 1
     dt = k.dtype
     code = _dtype_code(k)
-    Hq = 0
+    dev = _device(k, "k")
+    Hq = R = 0
     qs = qo = ko = vo = _NO_STRIDES
+    qp = qop = kop = vop = fp = wq = wk = sp = None
+    ks = _heads(k, "k", dt, shape, dev)
+    vs = _heads(v, "v", dt, shape, dev)
     if q is not None:
         Hq = q.shape[1]
-        qs = _heads(q, "q", dt, (T, Hq, D))
+        qs = _heads(q, "q", dt, (T, Hq, D), dev)
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=dt, device=k.device)
-        qo = _heads(q_out, "q_out", dt, (T, Hq, D))
+        qo = _heads(q_out, "q_out", dt, (T, Hq, D), dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+        if q_weight is not None:
+            wq = _flat(q_weight, "q_weight", torch.float32, (D,), dev)
     elif q_out is not None:
         raise ValueError("q_out is given with q")
-    ks = _heads(k, "k", dt, (T, Hkv, D))
-    vs = _heads(v, "v", dt, (T, Hkv, D))
     if k_out is not None:
-        ko = _heads(k_out, "k_out", dt, (T, Hkv, D))
+        ko = _heads(k_out, "k_out", dt, shape, dev)
+        kop = k_out.data_ptr()
     if v_out is not None:
-        vo = _heads(v_out, "v_out", dt, (T, Hkv, D))
-    _check(cu_nodes, "cu_nodes", torch.int32, (B + 1,))
-    n_pages, page, width = _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt)
+        vo = _heads(v_out, "v_out", dt, shape, dev)
+        vop = v_out.data_ptr()
+    if k_weight is not None:
+        wk = _flat(k_weight, "k_weight", torch.float32, (D,), dev)
+    if freq is not None:
+        half = freq.shape[0]
+        R = 2 * half
+        fp = _flat(freq, "freq", torch.int64, (half,), dev)
+    cu = _flat(cu_nodes, "cu_nodes", torch.int32, (B + 1,), dev)
+    n_pages, page = k_cache.shape[:2]
+    cache = (n_pages, page, Hkv, D)
+    kc = _flat(k_cache, "k_cache", dt, cache, dev)
+    vc = _flat(v_cache, "v_cache", dt, cache, dev)
+    width = page_table.shape[1]
+    table = _flat(page_table, "page_table", torch.int32, (B, width), dev)
+    ctx = _flat(context_len, "context_len", torch.int32, (B,), dev)
     if N_max is None:
         N_max = _most_rows(cu_nodes)
     if new_len is None:
         new_len = torch.empty((B,), dtype=torch.int32, device=k.device)
-    _check(new_len, "new_len", torch.int32, (B,))
-    for name, t in (("cu_nodes", cu_nodes), ("k_cache", k_cache), ("v_cache", v_cache),
-                    ("page_table", page_table), ("context_len", context_len),
-                    ("new_len", new_len)):
-        _check_device(t, name)
+    nl = _flat(new_len, "new_len", torch.int32, (B,), dev)
     if dev_status is not None:
-        _check(dev_status, "dev_status", torch.int32, (B,))
-        _check_device(dev_status, "dev_status")
-    _, rope = _rope(D, freq, interleaved, rope_scale, norm, eps,
-                    (("q_weight", q_weight), ("k_weight", k_weight)))
-    heads = Heads(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out), _ptr(v_out),
-                  qs, ks, vs, qo, ko, vo)
-    rc = load().gdn_tree_cache_append_rope(
-        heads, _ptr(freq), _ptr(q_weight), _ptr(k_weight), _ptr(cu_nodes), _ptr(k_cache),
-        _ptr(v_cache), _ptr(page_table), _ptr(context_len), _ptr(new_len),
-        _struct(AttendDims, B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len), rope,
-        _ptr(dev_status), _stream())
+        sp = _flat(dev_status, "dev_status", torch.int32, (B,), dev)
+    strides, dims, rope = _rope_structs(
+        (qs, ks, vs, qo, ko, vo), (B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len),
+        interleaved, norm, rope_scale, eps, R)
+    rc = load().gdn_tree_cache_append_rope(qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu, qop, kop,
+                                           vop, kc, vc, table, ctx, nl, strides, dims, rope, sp,
+                                           _stream())
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_cache_append_rope")
     return q_out, new_len

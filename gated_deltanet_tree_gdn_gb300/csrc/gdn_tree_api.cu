@@ -678,12 +678,10 @@ int gdn_tree_cache_append(const void* k, const void* v, const int32_t* path,
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
 }
 
-int gdn_tree_norm_rope(const void* q, gdn_tree_strides q_strides, const void* k,
-                       gdn_tree_strides k_strides, const int32_t* positions,
+int gdn_tree_norm_rope(const void* q, const void* k, const int32_t* positions,
                        const uint64_t* freq, const float* q_weight, const float* k_weight,
-                       void* q_out, gdn_tree_strides q_out_strides, void* k_out,
-                       gdn_tree_strides k_out_strides, gdn_tree_attend_dims dims,
-                       gdn_tree_rope rope, void* stream) {
+                       void* q_out, void* k_out, gdn_tree_head_strides strides,
+                       gdn_tree_attend_dims dims, gdn_tree_rope rope, void* stream) {
   if (q == nullptr) dims.Hq = 0, q_weight = nullptr, q_out = nullptr;
   if (k == nullptr) dims.Hkv = 0, k_weight = nullptr, k_out = nullptr;
   int rc = check_rope(dims, rope, freq, q_weight, k_weight);
@@ -698,10 +696,10 @@ int gdn_tree_norm_rope(const void* q, gdn_tree_strides q_strides, const void* k,
     return GDN_TREE_EINVAL;
   HeadRows in[2], out[2];
   const int T = dims.T, D = dims.D, dt = dims.dtype;
-  if ((rc = check_heads(q, &q_strides, T, dims.Hq, D, dt, &in[0])) != GDN_TREE_OK ||
-      (rc = check_heads(k, &k_strides, T, dims.Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
-      (rc = check_heads(q_out, &q_out_strides, T, dims.Hq, D, dt, &out[0])) != GDN_TREE_OK ||
-      (rc = check_heads(k_out, &k_out_strides, T, dims.Hkv, D, dt, &out[1])) != GDN_TREE_OK)
+  if ((rc = check_heads(q, &strides.q, T, dims.Hq, D, dt, &in[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k, &strides.k, T, dims.Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
+      (rc = check_heads(q_out, &strides.q_out, T, dims.Hq, D, dt, &out[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k_out, &strides.k_out, T, dims.Hkv, D, dt, &out[1])) != GDN_TREE_OK)
     return rc;
   const Range others[] = {{positions, rope.rotary_dim ? (size_t)T * 4 : 0},
                           {freq, (size_t)rope.rotary_dim * 4},
@@ -710,8 +708,8 @@ int gdn_tree_norm_rope(const void* q, gdn_tree_strides q_strides, const void* k,
   rc = check_apart(in, out, 2, others, 4);
   if (rc != GDN_TREE_OK) return rc;
   gdn::RopeArgs a{};
-  a.x = gdn_tree_heads{q, k, nullptr, q_out, k_out, nullptr, q_strides, k_strides,
-                       gdn_tree_strides{}, q_out_strides, k_out_strides, gdn_tree_strides{}};
+  a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out;
+  a.s = strides;
   a.positions = positions;
   a.freq = freq;
   a.q_weight = q_weight;
@@ -722,15 +720,16 @@ int gdn_tree_norm_rope(const void* q, gdn_tree_strides q_strides, const void* k,
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;
 }
 
-int gdn_tree_cache_append_rope(gdn_tree_heads x, const uint64_t* freq, const float* q_weight,
-                               const float* k_weight, const int32_t* cu_nodes, void* k_cache,
-                               void* v_cache, const int32_t* page_table,
+int gdn_tree_cache_append_rope(const void* q, const void* k, const void* v, const uint64_t* freq,
+                               const float* q_weight, const float* k_weight,
+                               const int32_t* cu_nodes, void* q_out, void* k_out, void* v_out,
+                               void* k_cache, void* v_cache, const int32_t* page_table,
                                const int32_t* context_len, int32_t* new_len,
-                               gdn_tree_attend_dims dims, gdn_tree_rope rope,
-                               int32_t* dev_status, void* stream) {
-  const int Hq = x.q ? dims.Hq : 0;
-  if (x.q == nullptr) q_weight = nullptr, x.q_out = nullptr;
-  if (Hq < 0 || (x.q != nullptr && Hq == 0)) return GDN_TREE_EINVAL;
+                               gdn_tree_head_strides strides, gdn_tree_attend_dims dims,
+                               gdn_tree_rope rope, int32_t* dev_status, void* stream) {
+  const int Hq = q ? dims.Hq : 0;
+  if (q == nullptr) q_weight = nullptr, q_out = nullptr;
+  if (Hq < 0 || (q != nullptr && Hq == 0)) return GDN_TREE_EINVAL;
   dims.Hq = dims.Hkv;  // (no multiple of Hkv is wanted here)
   int rc = check_attend_dims(dims);
   if (rc != GDN_TREE_OK) return rc;
@@ -741,8 +740,8 @@ int gdn_tree_cache_append_rope(gdn_tree_heads x, const uint64_t* freq, const flo
   if (dims.B == 0) return GDN_TREE_OK;
   dims.N = bounded_rows(dims.N, dims.T);
   const bool rows = dims.T > 0, paged = rows && dims.table_width > 0 && dims.n_pages > 0;
-  if (rows && (x.k == nullptr || x.v == nullptr)) return GDN_TREE_EINVAL;
-  if (rows && (x.q == nullptr) != (x.q_out == nullptr)) return GDN_TREE_EINVAL;
+  if (rows && (k == nullptr || v == nullptr)) return GDN_TREE_EINVAL;
+  if (rows && (q == nullptr) != (q_out == nullptr)) return GDN_TREE_EINVAL;
   void* const cache[] = {k_cache, v_cache};
   for (const void* p : cache)
     if ((paged && p == nullptr) || !aligned16(p)) return GDN_TREE_EINVAL;
@@ -755,12 +754,12 @@ int gdn_tree_cache_append_rope(gdn_tree_heads x, const uint64_t* freq, const flo
   if (dims.table_width > 0 && page_table == nullptr) return GDN_TREE_EINVAL;
   HeadRows in[3], out[3];
   const int T = dims.T, Hkv = dims.Hkv, D = dims.D, dt = dims.dtype;
-  if ((rc = check_heads(x.q, &x.q_strides, T, Hq, D, dt, &in[0])) != GDN_TREE_OK ||
-      (rc = check_heads(x.k, &x.k_strides, T, Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
-      (rc = check_heads(x.v, &x.v_strides, T, Hkv, D, dt, &in[2])) != GDN_TREE_OK ||
-      (rc = check_heads(x.q_out, &x.q_out_strides, T, Hq, D, dt, &out[0])) != GDN_TREE_OK ||
-      (rc = check_heads(x.k_out, &x.k_out_strides, T, Hkv, D, dt, &out[1])) != GDN_TREE_OK ||
-      (rc = check_heads(x.v_out, &x.v_out_strides, T, Hkv, D, dt, &out[2])) != GDN_TREE_OK)
+  if ((rc = check_heads(q, &strides.q, T, Hq, D, dt, &in[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k, &strides.k, T, Hkv, D, dt, &in[1])) != GDN_TREE_OK ||
+      (rc = check_heads(v, &strides.v, T, Hkv, D, dt, &in[2])) != GDN_TREE_OK ||
+      (rc = check_heads(q_out, &strides.q_out, T, Hq, D, dt, &out[0])) != GDN_TREE_OK ||
+      (rc = check_heads(k_out, &strides.k_out, T, Hkv, D, dt, &out[1])) != GDN_TREE_OK ||
+      (rc = check_heads(v_out, &strides.v_out, T, Hkv, D, dt, &out[2])) != GDN_TREE_OK)
     return rc;
   const size_t one = (size_t)Hkv * D * (dt == GDN_TREE_BF16 ? 2 : 4);
   const size_t held = (size_t)dims.n_pages * dims.page_size * one, B4 = (size_t)dims.B * 4;
@@ -788,7 +787,7 @@ int gdn_tree_cache_append_rope(gdn_tree_heads x, const uint64_t* freq, const flo
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (clear_status(dev_status, dims.B, st) != cudaSuccess) return GDN_TREE_ECUDA;
-  const gdn::RopeArgs a{x, nullptr, freq, q_weight, k_weight, dims, rope, cu_nodes, page_table,
+  const gdn::RopeArgs a{q, k, v, q_out, k_out, v_out, strides, nullptr, freq, q_weight, k_weight, dims, rope, cu_nodes, page_table,
                         context_len, k_cache, v_cache, new_len, dev_status};
   const cudaError_t err = gdn::launch_cache_append_rope(a, st);
   return err == cudaSuccess ? GDN_TREE_OK : GDN_TREE_ECUDA;

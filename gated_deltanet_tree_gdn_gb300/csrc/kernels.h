@@ -232,7 +232,9 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 // heads normalised and rotated (norm_rope), and rows that join the cache on the way
 // (append: cu, page_table and the fields below them are set, positions is not)
 struct RopeArgs {
-  gdn_tree_heads x;
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_out;
+  gdn_tree_head_strides s;
   const int32_t* positions;
   const uint64_t* freq;
   const float *q_weight, *k_weight;

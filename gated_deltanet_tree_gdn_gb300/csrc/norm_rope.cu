@@ -129,14 +129,14 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
   const int va = kPairs == kHalves && c >= nr ? c + nr : c;
   const int vb = kPairs != kHalves ? c + nv : c < nr ? c + nr : va + nv - nr;
 
-  const T* const q = static_cast<const T*>(a.x.q) + t * a.x.q_strides.row;
-  const T* const k = static_cast<const T*>(a.x.k) + t * a.x.k_strides.row;
-  const T* const v = static_cast<const T*>(a.x.v) + (kAppend ? t * a.x.v_strides.row : 0);
+  const T* const q = static_cast<const T*>(a.q) + t * a.s.q.row;
+  const T* const k = static_cast<const T*>(a.k) + t * a.s.k.row;
+  const T* const v = static_cast<const T*>(a.v) + (kAppend ? t * a.s.v.row : 0);
   const auto fetch = [&](int h, uint4* x) {
     if (!has || h >= h1) return;
-    const T* p = h < Hq ? q + h * a.x.q_strides.head
-                 : !kAppend || h < Hq + Hkv ? k + (h - Hq) * a.x.k_strides.head
-                                            : v + (h - Hq - Hkv) * a.x.v_strides.head;
+    const T* p = h < Hq ? q + h * a.s.q.head
+                 : !kAppend || h < Hq + Hkv ? k + (h - Hq) * a.s.k.head
+                                            : v + (h - Hq - Hkv) * a.s.v.head;
     x[0] = __ldcs(reinterpret_cast<const uint4*>(p) + va);
     x[1] = __ldcs(reinterpret_cast<const uint4*>(p) + vb);
   };
@@ -279,16 +279,16 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
         reinterpret_cast<uint4*>(row)[vb] = yb;
       };
       if (hi < Hq) {
-        put(static_cast<T*>(a.x.q_out) + t * a.x.q_out_strides.row + hi * a.x.q_out_strides.head);
+        put(static_cast<T*>(a.q_out) + t * a.s.q_out.row + hi * a.s.q_out.head);
       } else if (!kAppend) {
-        put(static_cast<T*>(a.x.k_out) + t * a.x.k_out_strides.row +
-            (hi - Hq) * a.x.k_out_strides.head);
+        put(static_cast<T*>(a.k_out) + t * a.s.k_out.row +
+            (hi - Hq) * a.s.k_out.head);
       } else {
         const int n = hi - Hq - (value ? Hkv : 0);
         if (place >= 0)
           put(static_cast<T*>(value ? a.v_cache : a.k_cache) + (place * Hkv + n) * D);
-        T* const out = static_cast<T*>(value ? a.x.v_out : a.x.k_out);
-        const gdn_tree_strides s = value ? a.x.v_out_strides : a.x.k_out_strides;
+        T* const out = static_cast<T*>(value ? a.v_out : a.k_out);
+        const gdn_tree_strides s = value ? a.s.v_out : a.s.k_out;
         if (out) put(out + t * s.row + n * s.head);
       }
     }

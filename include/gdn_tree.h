@@ -471,11 +471,15 @@ typedef struct {
   int64_t row, head;
 } gdn_tree_strides;
 
+typedef struct {
+  gdn_tree_strides q, k, v, q_out, k_out, v_out;
+} gdn_tree_head_strides;
+
 /*
  * gdn_tree_norm_rope -- queries and keys normalised for each head and rotated, in one pass.
  *
  *   q, q_out     T rows of Hq heads of D;  k, k_out: of Hkv heads.  q or k may be NULL (its
- *                output, weights, heads and strides then do not count).  An output may be its
+ *                output, weight, heads and strides then do not count).  An output may be its
  *                own input (same pointer, same strides); any other overlap of an output with
  *                an array of the call is refused.
  *   positions    [T] int32, any value (NULL where rotary_dim is 0)
@@ -486,19 +490,10 @@ typedef struct {
  * Sums, norms and rotations are fp32 and rounded once, to the output's type.  (Squares past
  * the range of fp32, of elements past 1e19, overflow: the row's norm is then infinite.)
  */
-int gdn_tree_norm_rope(const void *q, gdn_tree_strides q_strides, const void *k,
-                       gdn_tree_strides k_strides, const int32_t *positions,
+int gdn_tree_norm_rope(const void *q, const void *k, const int32_t *positions,
                        const uint64_t *freq, const float *q_weight, const float *k_weight,
-                       void *q_out, gdn_tree_strides q_out_strides, void *k_out,
-                       gdn_tree_strides k_out_strides, gdn_tree_attend_dims dims,
-                       gdn_tree_rope rope, void *stream);
-
-/* the arrays of heads of gdn_tree_cache_append_rope and their strides */
-typedef struct {
-  const void *q, *k, *v;
-  void *q_out, *k_out, *v_out;
-  gdn_tree_strides q_strides, k_strides, v_strides, q_out_strides, k_out_strides, v_out_strides;
-} gdn_tree_heads;
+                       void *q_out, void *k_out, gdn_tree_head_strides strides,
+                       gdn_tree_attend_dims dims, gdn_tree_rope rope, void *stream);
 
 /*
  * gdn_tree_cache_append_rope -- all rows of each sequence join its cache in order (prompts,
@@ -509,7 +504,7 @@ typedef struct {
  *     q_out, k_out, v_out  <-  the same of q, k and v, in the rows' own order,
  * and new_len[b] = context_len[b] + its rows.
  *
- *   heads        k, v: rows of Hkv heads.  q with q_out: of Hq heads, or both NULL.  k_out and
+ *   k, v         T rows of Hkv heads.  q with q_out: of Hq heads, or both NULL.  k_out and
  *                v_out (what gdn_tree_attend takes as the rows' own keys and values): NULL
  *                where they are not wanted; they may be k and v themselves, q_out may be q.
  *                Any other overlap of an output with an array of the call is refused.
@@ -524,12 +519,13 @@ typedef struct {
  * context_len is invalid nothing is written and new_len[b] = context_len[b].  Where cu_nodes
  * decreases, the other sequences are unspecified too (nothing outside the arrays is touched).
  */
-int gdn_tree_cache_append_rope(gdn_tree_heads heads, const uint64_t *freq, const float *q_weight,
-                               const float *k_weight, const int32_t *cu_nodes, void *k_cache,
-                               void *v_cache, const int32_t *page_table,
+int gdn_tree_cache_append_rope(const void *q, const void *k, const void *v, const uint64_t *freq,
+                               const float *q_weight, const float *k_weight,
+                               const int32_t *cu_nodes, void *q_out, void *k_out, void *v_out,
+                               void *k_cache, void *v_cache, const int32_t *page_table,
                                const int32_t *context_len, int32_t *new_len,
-                               gdn_tree_attend_dims dims, gdn_tree_rope rope,
-                               int32_t *dev_status, void *stream);
+                               gdn_tree_head_strides strides, gdn_tree_attend_dims dims,
+                               gdn_tree_rope rope, int32_t *dev_status, void *stream);
 
 /*
  * gdn_tree_positions -- the positions of a draft tree's nodes (or of a prompt's rows):

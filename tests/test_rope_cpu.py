@@ -27,7 +27,7 @@ def P(i=0, off=0):
 
 
 T, HQ, HKV, D = 20, 8, 2, 64
-S = _binding.Strides
+S = _binding.HeadStrides
 
 
 def shape(**kw):
@@ -45,23 +45,24 @@ def turn(**kw):
 
 def norm_rope(lib, dims=None, rope=None, q=P(0), qs=(HQ * D, D), k=P(1), ks=(HKV * D, D), pos=P(2),
               freq=P(3), qw=P(4), kw=P(5), qo=P(6), qos=(HQ * D, D), ko=P(7), kos=(HKV * D, D)):
-    return lib.gdn_tree_norm_rope(q, S(*qs), k, S(*ks), pos, freq, qw, kw, qo, S(*qos), ko, S(*kos),
-                                  dims or shape(), rope or turn(), None)
+    return lib.gdn_tree_norm_rope(q, k, pos, freq, qw, kw, qo, ko,
+                                  S(q=qs, k=ks, q_out=qos, k_out=kos), dims or shape(),
+                                  rope or turn(), None)
 
 
 def append(lib, dims=None, rope=None, freq=P(3), cu=P(8), cache=P(9), v_cache=P(10), table=P(11),
            ctx=P(12), new=P(13), status=None, **kw):
     x = dict(q=P(0), k=P(1), v=P(2), q_out=P(6), k_out=None, v_out=None)
     strides = dict(q=(HQ * D, D), k=(HKV * D, D), v=(HKV * D, D))
-    strides.update({n + "_out": s for n, s in strides.items()})
+    strides.update({n + "_out": s for n, s in list(strides.items())})
     for n, v in kw.items():
         if n.endswith("_strides"):
             strides[n[:-8]] = v
         else:
             x[n] = v
-    heads = _binding.Heads(**x, **{n + "_strides": S(*s) for n, s in strides.items()})
-    return lib.gdn_tree_cache_append_rope(heads, freq, P(4), P(5), cu, cache, v_cache, table, ctx,
-                                          new, dims or shape(), rope or turn(), status, None)
+    return lib.gdn_tree_cache_append_rope(
+        x["q"], x["k"], x["v"], freq, P(4), P(5), cu, x["q_out"], x["k_out"], x["v_out"], cache,
+        v_cache, table, ctx, new, S(**strides), dims or shape(), rope or turn(), status, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -301,7 +302,8 @@ def test_everything_of_a_call_is_on_its_stream(monkeypatch, name, given):
     monkeypatch.setattr(torch.cuda, "stream", under)
     monkeypatch.setattr(_binding, "_check", lambda *a: None)
     monkeypatch.setattr(_binding, "_check_device", lambda *a: None)
-    monkeypatch.setattr(_binding, "_heads", lambda t, *a: t.stride()[:2])
+    monkeypatch.setattr(_binding, "_device", lambda *a: 0)
+    monkeypatch.setattr(_binding, "_heads", lambda t, *a: t.stride())
     monkeypatch.setattr(_binding, "load", lambda: Library(launched))
     monkeypatch.setattr(_binding, "_raw_stream", lambda device: current[-1])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
