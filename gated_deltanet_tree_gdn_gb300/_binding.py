@@ -812,9 +812,18 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
 # (These take 4 to 18 tensors ahead of a launch of 2 microseconds: a tensor is looked at once, and
 # what the call needs of the shapes is made once for each set of them.)
 
+_Tensor, _i32, _i64, _f32 = torch.Tensor, torch.int32, torch.int64, torch.float32
+# (asked only where there is a CUDA tensor: the runtime is up then)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream_of(dev) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _flat(t, name, dtype, shape, dev):
     """The address of a dense tensor of this type and shape on the current device."""
-    if not (type(t) is torch.Tensor and t.get_device() == dev and t.dtype is dtype
+    if not (type(t) is _Tensor and t.get_device() == dev and t.dtype is dtype
             and t.is_contiguous() and t.shape == shape):
         _check(t, name, dtype, shape)
         _check_device(t, name, dev)
@@ -828,18 +837,18 @@ def _check_device(t, name, dev):
 
 def _device(t, name):
     """The current device, which t is on."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     _check_device(t, name, dev)
     return dev
 
 
 def _heads(t, name, dtype, shape, dev):
     """The strides of an array of heads [T, H, D] whose heads are contiguous."""
-    if type(t) is torch.Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == shape:
+    if type(t) is _Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == shape:
         strides = t.stride()
         if strides[2] == 1:
             return strides
@@ -870,8 +879,9 @@ def _rope_structs(strides, dims, interleaved, norm, rope_scale, eps, R):
             raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
         known = (HeadStrides(*(Strides(*s[:2]) for s in strides)), AttendDims(*dims),
                  Rope(R, int(bool(interleaved)), NORMS[norm], rope_scale, eps))
-        if len(_rope_cache) < 256:
-            _rope_cache[key] = known
+        if len(_rope_cache) >= 256:  # (a server's rows differ from call to call)
+            _rope_cache.clear()
+        _rope_cache[key] = known
     return known
 
 
@@ -888,7 +898,7 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
         return _on(stream, tree_positions, locals())
     dev = _device(cu_nodes, "cu_nodes")
     B = cu_nodes.shape[0] - 1
-    cu = _flat(cu_nodes, "cu_nodes", torch.int32, (B + 1,), dev)
+    cu = _flat(cu_nodes, "cu_nodes", _i32, (B + 1,), dev)
     if parent is not None:
         rows = parent.shape[0]
     elif positions is not None:
@@ -904,11 +914,11 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
     if positions is None:
         positions = torch.empty((rows,), dtype=torch.int32, device=cu_nodes.device)
     rc = load().gdn_tree_positions(
-        None if parent is None else _flat(parent, "parent", torch.int32, (rows,), dev), cu,
-        None if context_len is None else _flat(context_len, "context_len", torch.int32, (B,), dev),
-        prefix_len, _flat(positions, "positions", torch.int32, (rows,), dev), B, rows, N_max,
-        None if dev_status is None else _flat(dev_status, "dev_status", torch.int32, (B,), dev),
-        _stream())
+        None if parent is None else _flat(parent, "parent", _i32, (rows,), dev), cu,
+        None if context_len is None else _flat(context_len, "context_len", _i32, (B,), dev),
+        prefix_len, _flat(positions, "positions", _i32, (rows,), dev), B, rows, N_max,
+        None if dev_status is None else _flat(dev_status, "dev_status", _i32, (B,), dev),
+        _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_positions")
     return positions
@@ -971,7 +981,7 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
         qo = _heads(q_out, "q_out", dt, shape, dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
         if q_weight is not None:
-            wq = _flat(q_weight, "q_weight", torch.float32, (D,), dev)
+            wq = _flat(q_weight, "q_weight", _f32, (D,), dev)
     elif q_out is not None:
         raise ValueError("q_out is given with q")
     if k is not None:
@@ -983,18 +993,19 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
         ko = _heads(k_out, "k_out", dt, shape, dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
         if k_weight is not None:
-            wk = _flat(k_weight, "k_weight", torch.float32, (D,), dev)
+            wk = _flat(k_weight, "k_weight", _f32, (D,), dev)
     elif k_out is not None:
         raise ValueError("k_out is given with k")
     if freq is not None:
         half = freq.shape[0]
         R = 2 * half
-        fp = _flat(freq, "freq", torch.int64, (half,), dev)
-        pp = _flat(positions, "positions", torch.int32, (T,), dev)
+        fp = _flat(freq, "freq", _i64, (half,), dev)
+        pp = _flat(positions, "positions", _i32, (T,), dev)
     strides, dims, rope = _rope_structs((qs, ks, _NO_STRIDES, qo, ko),
                                         (0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), interleaved, norm,
                                         rope_scale, eps, R)
-    rc = load().gdn_tree_norm_rope(qp, kp, pp, fp, wq, wk, qop, kop, strides, dims, rope, _stream())
+    rc = load().gdn_tree_norm_rope(qp, kp, pp, fp, wq, wk, qop, kop, strides, dims, rope,
+                                   _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_norm_rope")
     return q_out, k_out
@@ -1035,7 +1046,7 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
         qo = _heads(q_out, "q_out", dt, (T, Hq, D), dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
         if q_weight is not None:
-            wq = _flat(q_weight, "q_weight", torch.float32, (D,), dev)
+            wq = _flat(q_weight, "q_weight", _f32, (D,), dev)
     elif q_out is not None:
         raise ValueError("q_out is given with q")
     if k_out is not None:
@@ -1045,32 +1056,32 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
         vo = _heads(v_out, "v_out", dt, shape, dev)
         vop = v_out.data_ptr()
     if k_weight is not None:
-        wk = _flat(k_weight, "k_weight", torch.float32, (D,), dev)
+        wk = _flat(k_weight, "k_weight", _f32, (D,), dev)
     if freq is not None:
         half = freq.shape[0]
         R = 2 * half
-        fp = _flat(freq, "freq", torch.int64, (half,), dev)
-    cu = _flat(cu_nodes, "cu_nodes", torch.int32, (B + 1,), dev)
+        fp = _flat(freq, "freq", _i64, (half,), dev)
+    cu = _flat(cu_nodes, "cu_nodes", _i32, (B + 1,), dev)
     n_pages, page = k_cache.shape[:2]
     cache = (n_pages, page, Hkv, D)
     kc = _flat(k_cache, "k_cache", dt, cache, dev)
     vc = _flat(v_cache, "v_cache", dt, cache, dev)
     width = page_table.shape[1]
-    table = _flat(page_table, "page_table", torch.int32, (B, width), dev)
-    ctx = _flat(context_len, "context_len", torch.int32, (B,), dev)
+    table = _flat(page_table, "page_table", _i32, (B, width), dev)
+    ctx = _flat(context_len, "context_len", _i32, (B,), dev)
     if N_max is None:
         N_max = _most_rows(cu_nodes)
     if new_len is None:
         new_len = torch.empty((B,), dtype=torch.int32, device=k.device)
-    nl = _flat(new_len, "new_len", torch.int32, (B,), dev)
+    nl = _flat(new_len, "new_len", _i32, (B,), dev)
     if dev_status is not None:
-        sp = _flat(dev_status, "dev_status", torch.int32, (B,), dev)
+        sp = _flat(dev_status, "dev_status", _i32, (B,), dev)
     strides, dims, rope = _rope_structs(
         (qs, ks, vs, qo, ko, vo), (B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len),
         interleaved, norm, rope_scale, eps, R)
     rc = load().gdn_tree_cache_append_rope(qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu, qop, kop,
                                            vop, kc, vc, table, ctx, nl, strides, dims, rope, sp,
-                                           _stream())
+                                           _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_cache_append_rope")
     return q_out, new_len

@@ -19,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4, kBatch = 2;
+constexpr int kWarps = 4, kStages = 4;
 
 // How the pairs of a rotation lie in a lane's two vectors of E elements, number va and vb of the
 // head's D / E:
@@ -36,36 +36,58 @@ __device__ __forceinline__ float2 turn(long long p, uint64_t freq, float scale) 
   return {c * scale, s * scale};
 }
 
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// two elements at once: a * b and a * b + c
+__device__ __forceinline__ float2 mul(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// a 16-byte vector of E elements as E / 2 pairs of neighbours
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int kSize = 4;
-  static __device__ __forceinline__ void open(const uint4& v, float* x) {
-    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  static __device__ __forceinline__ void open(const uint4& v, float2* x) {
+    x[0] = {__uint_as_float(v.x), __uint_as_float(v.y)};
+    x[1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
   }
-  static __device__ __forceinline__ uint4 close(const float* x) {
-    return {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-            __float_as_uint(x[3])};
+  static __device__ __forceinline__ uint4 close(const float2* x) {
+    return {__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+            __float_as_uint(x[1].y)};
   }
 };
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kSize = 8;
-  static __device__ __forceinline__ void open(const uint4& v, float* x) {
+  static __device__ __forceinline__ void open(const uint4& v, float2* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      x[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
   }
-  static __device__ __forceinline__ uint4 close(const float* x) {
+  static __device__ __forceinline__ uint4 close(const float2* x) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x[i].x, x[i].y);
       w[i] = reinterpret_cast<const uint32_t&>(p);
     }
     return {w[0], w[1], w[2], w[3]};
@@ -101,12 +123,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, const int32_t* con
 }
 
 template <typename T, Pairs kPairs, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, kPairs == kCrossed ? 4 : 8)
 norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
-  constexpr int E = Vec<T>::kSize;
-  constexpr int kTurns = kPairs == kCrossed ? 2 * E : E;  // a lane's
+  constexpr int E = Vec<T>::kSize, P = E / 2;  // elements and pairs of neighbours of a vector
+  __shared__ uint4 ring[kWarps][kStages][2][32];  // vectors on their way, each lane's its own
+  __shared__ float4 turns[kWarps][kMaxD / 4];     // cos and sin of the row's pairs, two by two
   __shared__ float staged[kPairs == kCrossed ? kWarps : 1][kPairs == kCrossed ? 64 * E : 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int Hq = a.d.Hq, Hkv = a.d.Hkv, D = a.d.D, R = a.rope.rotary_dim;
   if (kAppend) {
     const int b = blockIdx.x * (32 * kWarps) + threadIdx.x;
@@ -119,42 +142,52 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
   }
   const int unit = blockIdx.x * kWarps + warp, t = unit / splits;
   if (t >= a.d.T) return;
-  // heads: a warp takes 32 / lanes at a time, q's, then k's, then v's
+  // A pass takes `each` heads of q, of k or of v; the warp takes passes i0 .. i1 - 1 of the row.
   const int each = 32 / lanes, g = lane / lanes, c = lane & (lanes - 1);
-  const int H = Hq + (kAppend ? 2 : 1) * Hkv;
-  const int h0 = (unit - t * splits) * per * each + g;
-  const int h1 = min(H, (unit - t * splits + 1) * per * each);
+  const int of_q = (Hq + each - 1) / each, of_k = (Hkv + each - 1) / each;
+  const int passes = of_q + (kAppend ? 2 : 1) * of_k;
+  const int i0 = (unit - t * splits) * per, i1 = min(i0 + per, passes);
   const int nv = D / (2 * E), nr = R / (2 * E);
-  const bool has = c < nv;
   const int va = kPairs == kHalves && c >= nr ? c + nr : c;
   const int vb = kPairs != kHalves ? c + nv : c < nr ? c + nr : va + nv - nr;
-
-  const T* const q = static_cast<const T*>(a.q) + t * a.s.q.row;
-  const T* const k = static_cast<const T*>(a.k) + t * a.s.k.row;
-  const T* const v = static_cast<const T*>(a.v) + (kAppend ? t * a.s.v.row : 0);
-  const auto fetch = [&](int h, uint4* x) {
-    if (!has || h >= h1) return;
-    const T* p = h < Hq ? q + h * a.s.q.head
-                 : !kAppend || h < Hq + Hkv ? k + (h - Hq) * a.s.k.head
-                                            : v + (h - Hq - Hkv) * a.s.v.head;
-    x[0] = __ldcs(reinterpret_cast<const uint4*>(p) + va);
-    x[1] = __ldcs(reinterpret_cast<const uint4*>(p) + vb);
+  // (lanes past the head, where D is no power of two, have no head)
+  const auto head_of = [&](int i, int* of) {
+    const int first = i < of_q ? 0 : !kAppend || i < of_q + of_k ? of_q : of_q + of_k;
+    *of = c < nv ? (i < of_q ? Hq : Hkv) : 0;
+    return (i - first) * each + g;
   };
-  uint4 next[kBatch][2];
+  // the vectors of pass i, copied to its stage of the ring (one group a pass, empty or not)
+  const auto fetch = [&](int i) {
+    int of;
+    const int h = head_of(i, &of);
+    if (i < i1 && h < of) {
+      const void* from = i < of_q ? a.q : !kAppend || i < of_q + of_k ? a.k : a.v;
+      const gdn_tree_strides s = i < of_q ? a.s.q : !kAppend || i < of_q + of_k ? a.s.k : a.s.v;
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + t * s.row +
+                                                      h * s.head);
+      const uint32_t to = smem_u32(&ring[warp][(unsigned)(i - i0) % kStages][0][lane]);
+      copy16(to, p + va);
+      copy16(to + 32 * 16, p + vb);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i) fetch(h0 + i * each, next[i]);
+  for (int i = 0; i < kStages - 1; ++i) fetch(i0 + i);
 
   // the row's position, and its place in the cache (-1: none)
   long long p = 0, place = -1;
   if (kAppend) {
     int ctx;
     const int b = sequence_of(a.cu, a.context_len, a.d.B, t, lane, &ctx);
-    if (b < 0 || b >= a.d.B) return;
-    const int first = a.cu[b], stop = a.cu[b + 1];
-    if (!in_range(a.d, first, stop, ctx) || t < first || t >= stop) return;
+    const bool some = b >= 0 && b < a.d.B;
+    const int first = some ? a.cu[b] : 0, stop = some ? a.cu[b + 1] : 0;
+    if (!some || !in_range(a.d, first, stop, ctx) || t < first || t >= stop) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      return;
+    }
     const long long at = (long long)ctx + (t - first);
     p = a.d.prefix_len + at;
-    if (h1 > Hq) {
+    if (i1 > of_q) {
       if (at < (long long)a.d.table_width * a.d.page_size) {
         // (at fits 32 bits here)
         const unsigned entry = (unsigned)at / (unsigned)a.d.page_size;
@@ -169,139 +202,134 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     p = a.positions[t];
   }
 
-  // the row's cosines and sines, of the pairs of this lane
-  float co[kTurns], si[kTurns];
+  // The row's cosines and sines, each made by one lane; then those of this lane's elements:
+  // of x[j] for j < P as they are, and for kCrossed those of the second vector, and signed.
+  constexpr int kTurns = kPairs == kCrossed ? 2 * P : P;
+  float2 co[kTurns], si[kTurns];
+  if (R > 0) {
+    float2* const row = reinterpret_cast<float2*>(turns[warp]);
+    for (int i = lane; i < R / 2; i += 32) row[i] = turn(p, a.freq[i], a.rope.scale);
+    __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kTurns; ++i) {
-    co[i] = 1.f, si[i] = 0.f;
-    int pair;
-    bool turned;
-    if (kPairs == kHalves) {
-      pair = E * c + i, turned = c < nr;
-    } else if (kPairs == kNeighbours) {
-      pair = (E / 2) * (i < E / 2 ? va : vb) + (i & (E / 2 - 1)), turned = pair < R / 2;
-    } else {
-      const int e = E * (i < E ? va : vb) + (i & (E - 1));
-      pair = e < R / 2 ? e : e - R / 2, turned = e < R;
-    }
-    if (turned && has) {
-      const float2 cs = turn(p, a.freq[pair], a.rope.scale);
-      co[i] = cs.x, si[i] = cs.y;
+    for (int j = 0; j < kTurns; ++j) {
+      if constexpr (kPairs == kHalves) {
+        const float4 f = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
+        co[j] = {f.x, f.z}, si[j] = {f.y, f.w};
+      } else if constexpr (kPairs == kNeighbours) {
+        // (pairs j of both vectors, one after the other)
+        const int i = P * va + j, k = P * vb + j;
+        const float2 f = i < R / 2 ? row[i] : float2{1.f, 0.f};
+        const float2 h = k < R / 2 ? row[k] : float2{1.f, 0.f};
+        co[j] = {f.x, h.x}, si[j] = {f.y, h.y};
+      } else {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int e = E * (j < P ? va : vb) + 2 * (j & (P - 1)) + k;
+          const float2 f = e < R ? row[e < R / 2 ? e : e - R / 2] : float2{1.f, 0.f};
+          v[k] = f.x, v[2 + k] = e < R / 2 ? -f.y : f.y;
+        }
+        co[j] = {v[0], v[1]}, si[j] = {v[2], v[3]};
+      }
     }
   }
 
   const float share = a.rope.norm == GDN_TREE_NORM_RMS ? 1.f / D : 1.f;
-  for (int h = h0; h - g < h1; h += kBatch * each) {
-    uint4 raw[kBatch][2];
+  for (int i = i0; i < i1; ++i) {
+    const bool value = kAppend && i >= of_q + of_k;
+    int of;
+    const int h = head_of(i, &of);
+    float2 x[2 * P];
+    fetch(i + kStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    uint4 y[2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) raw[i][0] = next[i][0], raw[i][1] = next[i][1];
+    for (int j = 0; j < 2; ++j) y[j] = ring[warp][(unsigned)(i - i0) % kStages][j][lane];
+    Vec<T>::open(y[0], x);
+    Vec<T>::open(y[1], x + P);
+    if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
+      float2 two = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) fetch(h + (kBatch + i) * each, next[i]);
+      for (int j = 0; j < 2 * P; ++j) two = fma(x[j], x[j], two);
+      float square = h < of ? two.x + two.y : 0.f;
+      const float* const w = i < of_q ? a.q_weight : a.k_weight;
+      if (w && c < nv) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int hi = h + i * each;
-      if (hi - g >= h1) break;  // (the warp's)
-      const bool mine = has && hi < h1, value = kAppend && hi >= Hq + Hkv;
-      float x[2 * E];
-      if (mine) {
-        Vec<T>::open(raw[i][0], x);
-        Vec<T>::open(raw[i][1], x + E);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) x[e] = 0.f;
-      }
-      if (a.rope.norm != GDN_TREE_NORM_NONE) {
-        float square = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) square += x[e] * x[e];
-        for (int o = lanes / 2; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
-        if (mine && !value) {
-          const float r = __frsqrt_rn(square * share + a.rope.eps);
-          const float* const w = hi < Hq ? a.q_weight : a.k_weight;
-          if (w) {
-#pragma unroll
-            for (int e = 0; e < 2 * E; e += 4) {
-              const float4 f = __ldg(reinterpret_cast<const float4*>(w + E * (e < E ? va : vb) +
-                                                                     (e & (E - 1))));
-              x[e] *= r * f.x, x[e + 1] *= r * f.y, x[e + 2] *= r * f.z, x[e + 3] *= r * f.w;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2 * E; ++e) x[e] *= r;
-          }
+        for (int j = 0; j < 2 * P; j += 2) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(
+              w + E * (j < P ? va : vb) + 2 * (j & (P - 1))));
+          x[j] = mul(x[j], float2{v.x, v.y});
+          x[j + 1] = mul(x[j + 1], float2{v.z, v.w});
         }
       }
-      if (kPairs == kHalves) {
-        if (c < nr && !value) {
+      for (int o = lanes / 2; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
+      const float r = __frsqrt_rn(square * share + a.rope.eps);
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float u = x[e], w = x[E + e];
-            x[e] = u * co[e] - w * si[e];
-            x[E + e] = w * co[e] + u * si[e];
+      for (int j = 0; j < 2 * P; ++j) x[j] = mul(x[j], float2{r, r});
+    }
+    if (!value && R > 0) {
+      if constexpr (kPairs == kHalves) {
+        if (c < nr) {
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            const float2 u = x[j], v = x[P + j];
+            x[j] = fma(u, co[j], mul(v, float2{-si[j].x, -si[j].y}));
+            x[P + j] = fma(v, co[j], mul(u, si[j]));
           }
         }
-      } else if (kPairs == kNeighbours) {
+      } else if constexpr (kPairs == kNeighbours) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int j = 0; j < P; ++j) {
           // (what is not rotated is left alone, not turned by 0: its pair may not be finite)
-          const bool turned = (E / 2) * (e < E / 2 ? va : vb) + (e & (E / 2 - 1)) < R / 2;
-          const float u = x[2 * e], w = x[2 * e + 1];
-          if (turned && !value) {
-            x[2 * e] = u * co[e] - w * si[e];
-            x[2 * e + 1] = w * co[e] + u * si[e];
-          }
+          const float2 u = x[j], v = x[P + j];
+          if (P * va + j < R / 2)
+            x[j] = {u.x * co[j].x - u.y * si[j].x, u.y * co[j].x + u.x * si[j].x};
+          if (P * vb + j < R / 2)
+            x[P + j] = {v.x * co[j].y - v.y * si[j].y, v.y * co[j].y + v.x * si[j].y};
         }
       } else {
         float* const row = staged[warp] + g * D;
         __syncwarp();
-        if (has) {
+        if (c < nv) {
 #pragma unroll
-          for (int e = 0; e < 2 * E; e += 4)
-            *reinterpret_cast<float4*>(row + E * (e < E ? va : vb) + (e & (E - 1))) =
-                float4{x[e], x[e + 1], x[e + 2], x[e + 3]};
+          for (int j = 0; j < 2 * P; j += 2)
+            *reinterpret_cast<float4*>(row + E * (j < P ? va : vb) + 2 * (j & (P - 1))) =
+                float4{x[j].x, x[j].y, x[j + 1].x, x[j + 1].y};
         }
         __syncwarp();
-        if (has && !value) {
+        if (c < nv) {
 #pragma unroll
-          for (int e = 0; e < 2 * E; ++e) {
-            const int n = E * (e < E ? va : vb) + (e & (E - 1));
-            if (n < R) {
-              const float u = row[n < R / 2 ? n + R / 2 : n - R / 2];
-              x[e] = n < R / 2 ? x[e] * co[e] - u * si[e] : x[e] * co[e] + u * si[e];
-            }
+          for (int j = 0; j < 2 * P; ++j) {
+            const int e = E * (j < P ? va : vb) + 2 * (j & (P - 1));
+            if (e < R) x[j].x = x[j].x * co[j].x + row[e < R / 2 ? e + R / 2 : e - R / 2] * si[j].x;
+            if (e + 1 < R)
+              x[j].y = x[j].y * co[j].y + row[e + 1 < R / 2 ? e + 1 + R / 2 : e + 1 - R / 2] * si[j].y;
           }
         }
       }
-      if (!mine) continue;
-      const uint4 ya = Vec<T>::close(x), yb = Vec<T>::close(x + E);
-      const auto put = [&](T* row) {
-        reinterpret_cast<uint4*>(row)[va] = ya;
-        reinterpret_cast<uint4*>(row)[vb] = yb;
-      };
-      if (hi < Hq) {
-        put(static_cast<T*>(a.q_out) + t * a.s.q_out.row + hi * a.s.q_out.head);
-      } else if (!kAppend) {
-        put(static_cast<T*>(a.k_out) + t * a.s.k_out.row +
-            (hi - Hq) * a.s.k_out.head);
-      } else {
-        const int n = hi - Hq - (value ? Hkv : 0);
-        if (place >= 0)
-          put(static_cast<T*>(value ? a.v_cache : a.k_cache) + (place * Hkv + n) * D);
-        T* const out = static_cast<T*>(value ? a.v_out : a.k_out);
-        const gdn_tree_strides s = value ? a.s.v_out : a.s.k_out;
-        if (out) put(out + t * s.row + n * s.head);
-      }
     }
+    if (h >= of) continue;
+    if (!value) y[0] = Vec<T>::close(x), y[1] = Vec<T>::close(x + P);
+    const auto put = [&](T* row) {
+      reinterpret_cast<uint4*>(row)[va] = y[0];
+      reinterpret_cast<uint4*>(row)[vb] = y[1];
+    };
+    void* const out = i < of_q ? a.q_out : value ? a.v_out : a.k_out;
+    const gdn_tree_strides s = i < of_q ? a.s.q_out : value ? a.s.v_out : a.s.k_out;
+    if (!kAppend || out) put(static_cast<T*>(out) + t * s.row + h * s.head);
+    if (kAppend && i >= of_q && place >= 0)
+      put(static_cast<T*>(value ? a.v_cache : a.k_cache) + (place * Hkv + h) * D);
   }
 }
 
 template <bool kAppend>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const bool bf16 = a.d.dtype == GDN_TREE_BF16;
-  const int H = a.d.Hq + (kAppend ? 2 : 1) * a.d.Hkv, E = bf16 ? 8 : 4, R = a.rope.rotary_dim;
+  const int E = bf16 ? 8 : 4, R = a.rope.rotary_dim;
   int lanes = 1;
   while (lanes * 2 * E < a.d.D) lanes *= 2;
-  const int each = 32 / lanes, passes = (H + each - 1) / each;
+  const int each = 32 / lanes;
+  const int passes = (a.d.Hq + each - 1) / each + (kAppend ? 2 : 1) * ((a.d.Hkv + each - 1) / each);
   const int sms = sm_count();
   int splits = 1;
   if (a.d.T > 0 && (long long)a.d.T < 16ll * sms) splits = std::min(passes, 16 * sms / a.d.T + 1);
