@@ -19,13 +19,14 @@
 namespace gdn {
 namespace {
 
+// (3 to 6 stages take the same time within 2 %; 2 take 3 to 6 % more, 8 leave room for fewer warps)
 constexpr int kWarps = 4, kStages = 4;
 
 // How the pairs of a rotation lie in a lane's two vectors of E elements, number va and vb of the
 // head's D / E:
 //   kNeighbours  elements 2 i and 2 i + 1 are in the same vector
 //   kHalves      R a multiple of 2 E (0 included): vb = va + R / 2 E holds va's partners
-//   kCrossed     elements i and i + R / 2 for any other R: through shared memory
+//   kCrossed     elements i and i + R / 2 for any other R: rotated in the ring, a pair a lane
 enum Pairs { kNeighbours, kHalves, kCrossed };
 
 // cos and sin of the angle at position p of a pair of this frequency, times the scale
@@ -69,6 +70,10 @@ struct Vec<float> {
     x[0] = {__uint_as_float(v.x), __uint_as_float(v.y)};
     x[1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
   }
+  // the first n elements (even) of one vector, the others of another
+  static __device__ __forceinline__ uint4 mix(const uint4& a, const uint4& b, int n) {
+    return {a.x, a.y, n > 2 ? a.z : b.z, n > 2 ? a.w : b.w};
+  }
   static __device__ __forceinline__ uint4 close(const float2* x) {
     return {__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
             __float_as_uint(x[1].y)};
@@ -82,6 +87,9 @@ struct Vec<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       x[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+  }
+  static __device__ __forceinline__ uint4 mix(const uint4& a, const uint4& b, int n) {
+    return {a.x, n > 2 ? a.y : b.y, n > 4 ? a.z : b.z, n > 6 ? a.w : b.w};
   }
   static __device__ __forceinline__ uint4 close(const float2* x) {
     uint32_t w[4];
@@ -123,12 +131,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, const int32_t* con
 }
 
 template <typename T, Pairs kPairs, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps, kPairs == kCrossed ? 4 : 8)
+__global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7)
 norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
   constexpr int E = Vec<T>::kSize, P = E / 2;  // elements and pairs of neighbours of a vector
-  __shared__ uint4 ring[kWarps][kStages][2][32];  // vectors on their way, each lane's its own
+  // vectors on their way: each lane's its own, head by head for kCrossed
+  __shared__ uint4 ring[kWarps][kStages][64];
   __shared__ float4 turns[kWarps][kMaxD / 4];     // cos and sin of the row's pairs, two by two
-  __shared__ float staged[kPairs == kCrossed ? kWarps : 1][kPairs == kCrossed ? 64 * E : 1];
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int Hq = a.d.Hq, Hkv = a.d.Hkv, D = a.d.D, R = a.rope.rotary_dim;
   if (kAppend) {
@@ -156,6 +164,8 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     *of = c < nv ? (i < of_q ? Hq : Hkv) : 0;
     return (i - first) * each + g;
   };
+  const int slot_a = kPairs == kCrossed ? g * 2 * lanes + c : lane;
+  const int slot_b = kPairs == kCrossed ? slot_a + nv : lane + 32;
   // the vectors of pass i, copied to its stage of the ring (one group a pass, empty or not)
   const auto fetch = [&](int i) {
     int of;
@@ -165,14 +175,27 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
       const gdn_tree_strides s = i < of_q ? a.s.q : !kAppend || i < of_q + of_k ? a.s.k : a.s.v;
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + t * s.row +
                                                       h * s.head);
-      const uint32_t to = smem_u32(&ring[warp][(unsigned)(i - i0) % kStages][0][lane]);
-      copy16(to, p + va);
-      copy16(to + 32 * 16, p + vb);
+      uint4* const stage = ring[warp][(unsigned)(i - i0) % kStages];
+      copy16(smem_u32(stage + slot_a), p + va);
+      copy16(smem_u32(stage + slot_b), p + vb);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i0 + i);
+
+  // the weights of this lane's elements: of q's, then of k's
+  float2 w[2 * P];
+  const auto load_weights = [&](const float* from) {
+#pragma unroll
+    for (int j = 0; j < 2 * P; j += 2) {
+      const float4 v = from && c < nv ? __ldg(reinterpret_cast<const float4*>(
+                                            from + E * (j < P ? va : vb) + 2 * (j & (P - 1))))
+                                      : float4{1.f, 1.f, 1.f, 1.f};
+      w[j] = {v.x, v.y}, w[j + 1] = {v.z, v.w};
+    }
+  };
+  load_weights(i0 < of_q ? a.q_weight : a.k_weight);
 
   // the row's position, and its place in the cache (-1: none)
   long long p = 0, place = -1;
@@ -202,114 +225,126 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     p = a.positions[t];
   }
 
-  // The row's cosines and sines, each made by one lane; then those of this lane's elements:
-  // of x[j] for j < P as they are, and for kCrossed those of the second vector, and signed.
-  constexpr int kTurns = kPairs == kCrossed ? 2 * P : P;
-  float2 co[kTurns], si[kTurns];
-  if (R > 0) {
+  // The row's cosines and sines, each made by one lane; then those of this lane's pairs: of
+  // kNeighbours, pairs j of both vectors; of kCrossed, where `wide` lanes take a head, pairs
+  // `mine` and `mine` + 32.
+  constexpr int kMine = kPairs == kCrossed ? 1 : P;
+  float2 co[kMine], si[kMine];
+  const int wide = R > 32 ? 32 : R > 16 ? 16 : 8, mine = lane & (wide - 1);
+  if constexpr (kPairs == kCrossed) {
+    const float2 none = {1.f, 0.f};
+    const float2 f = mine < R / 2 ? turn(p, a.freq[mine], a.rope.scale) : none;
+    const float2 h = mine + 32 < R / 2 ? turn(p, a.freq[mine + 32], a.rope.scale) : none;
+    co[0] = {f.x, h.x}, si[0] = {f.y, h.y};
+  } else if (R > 0) {
     float2* const row = reinterpret_cast<float2*>(turns[warp]);
     for (int i = lane; i < R / 2; i += 32) row[i] = turn(p, a.freq[i], a.rope.scale);
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < kTurns; ++j) {
+    for (int j = 0; j < P; ++j) {
       if constexpr (kPairs == kHalves) {
-        const float4 f = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
-        co[j] = {f.x, f.z}, si[j] = {f.y, f.w};
-      } else if constexpr (kPairs == kNeighbours) {
-        // (pairs j of both vectors, one after the other)
-        const int i = P * va + j, k = P * vb + j;
-        const float2 f = i < R / 2 ? row[i] : float2{1.f, 0.f};
-        const float2 h = k < R / 2 ? row[k] : float2{1.f, 0.f};
-        co[j] = {f.x, h.x}, si[j] = {f.y, h.y};
+        const float4 two = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
+        co[j] = {two.x, two.z}, si[j] = {two.y, two.w};
       } else {
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int e = E * (j < P ? va : vb) + 2 * (j & (P - 1)) + k;
-          const float2 f = e < R ? row[e < R / 2 ? e : e - R / 2] : float2{1.f, 0.f};
-          v[k] = f.x, v[2 + k] = e < R / 2 ? -f.y : f.y;
-        }
-        co[j] = {v[0], v[1]}, si[j] = {v[2], v[3]};
+        const int m = P * va + j, n = P * vb + j;
+        const float2 f = m < R / 2 ? row[m] : float2{1.f, 0.f};
+        const float2 h = n < R / 2 ? row[n] : float2{1.f, 0.f};
+        co[j] = {f.x, h.x}, si[j] = {f.y, h.y};
       }
     }
   }
+  // the weights of kCrossed's pairs: of their first elements and of their second
+  float2 w1 = {1.f, 1.f}, w2 = {1.f, 1.f};
+  const auto cross_weights = [&](const float* from) {
+    if (kPairs != kCrossed || from == nullptr) return;
+    if (mine < R / 2) w1.x = from[mine], w2.x = from[mine + R / 2];
+    if (mine + 32 < R / 2) w1.y = from[mine + 32], w2.y = from[mine + 32 + R / 2];
+  };
+  cross_weights(i0 < of_q ? a.q_weight : a.k_weight);
 
   const float share = a.rope.norm == GDN_TREE_NORM_RMS ? 1.f / D : 1.f;
   for (int i = i0; i < i1; ++i) {
     const bool value = kAppend && i >= of_q + of_k;
     int of;
     const int h = head_of(i, &of);
-    float2 x[2 * P];
+    // (kCrossed: the stage that is filled next was read by other lanes, this one is)
+    if constexpr (kPairs == kCrossed) __syncwarp();
     fetch(i + kStages - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    uint4 y[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) y[j] = ring[warp][(unsigned)(i - i0) % kStages][j][lane];
+    if constexpr (kPairs == kCrossed) __syncwarp();
+    uint4* const stage = ring[warp][(unsigned)(i - i0) % kStages];
+    uint4 y[2] = {stage[slot_a], stage[slot_b]};
+    float2 x[2 * P];
     Vec<T>::open(y[0], x);
     Vec<T>::open(y[1], x + P);
-    if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
+    float r = 1.f;
+    if (a.rope.norm != GDN_TREE_NORM_NONE) {
       float2 two = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) two = fma(x[j], x[j], two);
       float square = h < of ? two.x + two.y : 0.f;
-      const float* const w = i < of_q ? a.q_weight : a.k_weight;
-      if (w && c < nv) {
-#pragma unroll
-        for (int j = 0; j < 2 * P; j += 2) {
-          const float4 v = __ldg(reinterpret_cast<const float4*>(
-              w + E * (j < P ? va : vb) + 2 * (j & (P - 1))));
-          x[j] = mul(x[j], float2{v.x, v.y});
-          x[j + 1] = mul(x[j + 1], float2{v.z, v.w});
-        }
-      }
       for (int o = lanes / 2; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
-      const float r = __frsqrt_rn(square * share + a.rope.eps);
-#pragma unroll
-      for (int j = 0; j < 2 * P; ++j) x[j] = mul(x[j], float2{r, r});
+      r = __frsqrt_rn(square * share + a.rope.eps);
     }
-    if (!value && R > 0) {
-      if constexpr (kPairs == kHalves) {
-        if (c < nr) {
+    if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
 #pragma unroll
-          for (int j = 0; j < P; ++j) {
-            const float2 u = x[j], v = x[P + j];
-            x[j] = fma(u, co[j], mul(v, float2{-si[j].x, -si[j].y}));
-            x[P + j] = fma(v, co[j], mul(u, si[j]));
-          }
-        }
-      } else if constexpr (kPairs == kNeighbours) {
+      for (int j = 0; j < 2 * P; ++j) x[j] = mul(x[j], mul(w[j], float2{r, r}));
+    }
+    if (kPairs == kHalves && !value && c < nr) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          // (what is not rotated is left alone, not turned by 0: its pair may not be finite)
-          const float2 u = x[j], v = x[P + j];
-          if (P * va + j < R / 2)
-            x[j] = {u.x * co[j].x - u.y * si[j].x, u.y * co[j].x + u.x * si[j].x};
-          if (P * vb + j < R / 2)
-            x[P + j] = {v.x * co[j].y - v.y * si[j].y, v.y * co[j].y + v.x * si[j].y};
-        }
-      } else {
-        float* const row = staged[warp] + g * D;
-        __syncwarp();
-        if (c < nv) {
+      for (int j = 0; j < P; ++j) {
+        const float2 u = x[j], v = x[P + j];
+        x[j] = fma(u, co[j], mul(v, float2{-si[j].x, -si[j].y}));
+        x[P + j] = fma(v, co[j], mul(u, si[j]));
+      }
+    }
+    if (kPairs == kNeighbours && !value && R > 0) {
 #pragma unroll
-          for (int j = 0; j < 2 * P; j += 2)
-            *reinterpret_cast<float4*>(row + E * (j < P ? va : vb) + 2 * (j & (P - 1))) =
-                float4{x[j].x, x[j].y, x[j + 1].x, x[j + 1].y};
-        }
-        __syncwarp();
-        if (c < nv) {
-#pragma unroll
-          for (int j = 0; j < 2 * P; ++j) {
-            const int e = E * (j < P ? va : vb) + 2 * (j & (P - 1));
-            if (e < R) x[j].x = x[j].x * co[j].x + row[e < R / 2 ? e + R / 2 : e - R / 2] * si[j].x;
-            if (e + 1 < R)
-              x[j].y = x[j].y * co[j].y + row[e + 1 < R / 2 ? e + 1 + R / 2 : e + 1 - R / 2] * si[j].y;
-          }
+      for (int j = 0; j < P; ++j) {
+        // (what is not rotated is left alone, not turned by 0: its pair may not be finite)
+        const float2 u = x[j], v = x[P + j];
+        if (P * va + j < R / 2)
+          x[j] = {u.x * co[j].x - u.y * si[j].x, u.y * co[j].x + u.x * si[j].x};
+        if (P * vb + j < R / 2)
+          x[P + j] = {v.x * co[j].y - v.y * si[j].y, v.y * co[j].y + v.x * si[j].y};
+      }
+    }
+    if (kPairs == kCrossed && !value) {
+      __syncwarp();  // (every lane has its vectors)
+      // (h - g is the pass's first head)
+      const int heads = min(each, (i < of_q ? Hq : Hkv) - (h - g));
+      for (int n0 = 0; n0 < heads; n0 += 32 / wide) {
+        const int n = min(n0 + lane / wide, heads - 1);
+        const float rn = __shfl_sync(0xffffffffu, r, n * lanes);
+        T* const head = reinterpret_cast<T*>(stage + n * 2 * lanes);
+        const auto cross = [&](int at, float first, float second, float cs, float sn) {
+          const float u = to_f32(head[at]) * (first * rn), v = to_f32(head[at + R / 2]) * (second * rn);
+          head[at] = from_f32<T>(u * cs - v * sn);
+          head[at + R / 2] = from_f32<T>(v * cs + u * sn);
+        };
+        if (n0 + lane / wide < heads) {
+          if (mine < R / 2) cross(mine, w1.x, w2.x, co[0].x, si[0].x);
+          if (mine + 32 < R / 2) cross(mine + 32, w1.y, w2.y, co[0].y, si[0].y);
         }
       }
+      __syncwarp();
+    }
+    if (i + 1 == of_q) {  // (ahead of the first pass that takes them)
+      load_weights(a.k_weight);
+      w1 = w2 = {1.f, 1.f};
+      cross_weights(a.k_weight);
     }
     if (h >= of) continue;
-    if (!value) y[0] = Vec<T>::close(x), y[1] = Vec<T>::close(x + P);
+    if (kPairs == kCrossed && !value) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int left = R - E * (j ? vb : va);  // rotated elements of the vector
+        const uint4 own = Vec<T>::close(x + j * P), turned = stage[j ? slot_b : slot_a];
+        y[j] = left >= E ? turned : left <= 0 ? own : Vec<T>::mix(turned, own, left);
+      }
+    } else if (!value) {
+      y[0] = Vec<T>::close(x), y[1] = Vec<T>::close(x + P);
+    }
     const auto put = [&](T* row) {
       reinterpret_cast<uint4*>(row)[va] = y[0];
       reinterpret_cast<uint4*>(row)[vb] = y[1];
@@ -331,8 +366,13 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int each = 32 / lanes;
   const int passes = (a.d.Hq + each - 1) / each + (kAppend ? 2 : 1) * ((a.d.Hkv + each - 1) / each);
   const int sms = sm_count();
+  // Warps a row: one where the rows alone fill the SMs (what a warp makes once for its row is then
+  // made once), more where they do not (a warp's passes follow one another).  Measured with 32 + 8
+  // heads of 128 in bf16, a warp a row against this rule: 1 row 6.5 and 2.5 us, 256 rows 6.8 and
+  // 3.9, 1024 rows 8.6 and 7.8; four warps a row at 4096 rows 22 us against 17.4.
+  const int want = 12 * sms;
   int splits = 1;
-  if (a.d.T > 0 && (long long)a.d.T < 16ll * sms) splits = std::min(passes, 16 * sms / a.d.T + 1);
+  if (a.d.T > 0 && a.d.T <= want) splits = std::min(passes, want / a.d.T + 1);
   const int per = (passes + splits - 1) / splits;
   splits = (passes + per - 1) / per;
   long long blocks = ((long long)a.d.T * splits + kWarps - 1) / kWarps;

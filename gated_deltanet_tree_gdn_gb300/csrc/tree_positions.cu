@@ -32,35 +32,50 @@ __global__ void __launch_bounds__(kThreads) chain_positions_kernel(const Positio
   if (j < stop - first) a.positions[first + j] = (int)(start + j);
 }
 
+// a barrier of the first `threads` threads, and whether x holds for any of them
+__device__ __forceinline__ bool sync_any(int threads, bool x) {
+  uint32_t any;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.u32 q, %1, 0;\n"
+      "barrier.red.or.pred p, 1, %2, q; selp.u32 %0, 1, 0, p;}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(threads)
+      : "memory");
+  return any != 0;
+}
+
 __global__ void __launch_bounds__(kMaxNLong) tree_positions_kernel(const PositionArgs a) {
-  __shared__ int up[kMaxNLong], depth[kMaxNLong];
+  // a node's count so far (high half) and the ancestor it points at, plus 1 (low half), of the
+  // last round and of this one
+  __shared__ uint32_t nodes[2][kMaxNLong];
   const int b = blockIdx.x, t = threadIdx.x;
   const int first = a.cu[b], stop = a.cu[b + 1], ctx = a.context_len ? a.context_len[b] : 0;
   if (!in_range(a, first, stop, ctx)) {
     if (a.dev_status && t == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     return;
   }
-  const int n = stop - first;
-  int p = t < n ? a.parent[first + t] : -1;
-  if (__syncthreads_or(p < -1 || p >= t)) {
+  // (the warps of a smaller tree's missing nodes leave)
+  const int n = stop - first, threads = (n + 31) / 32 * 32;
+  if (t >= threads) return;
+  int up = t < n ? a.parent[first + t] : -1;
+  uint32_t depth = up >= 0;
+  const bool bad = up < -1 || up >= t;
+  nodes[0][t] = bad ? 0u : depth << 16 | (uint32_t)(up + 1);
+  if (sync_any(threads, bad)) {
     if (a.dev_status && t == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_TREE);
     return;
   }
-  int d = p >= 0;
-  up[t] = p;
-  depth[t] = d;
-  // (every round at least halves the longest way to a root)
-  while (__syncthreads_or(p >= 0)) {
-    int dp = 0, pp = -1;
-    if (p >= 0) dp = depth[p], pp = up[p];
-    __syncthreads();
-    d += dp;
-    p = pp;
-    up[t] = p;
-    depth[t] = d;
+  // (a round at least halves the longest way to a root, and reads what the one before wrote)
+  for (int now = 0; sync_any(threads, up >= 0); now ^= 1) {
+    if (up >= 0) {
+      const uint32_t next = nodes[now][up];
+      depth += next >> 16;
+      up = (int)(next & 0xffffu) - 1;
+    }
+    nodes[now ^ 1][t] = depth << 16 | (uint32_t)(up + 1);
   }
-  const long long at = (long long)a.prefix_len + ctx + d;
-  if (__syncthreads_or(t < n && at > 0x7fffffffll)) {
+  const long long at = (long long)a.prefix_len + ctx + depth;
+  if (sync_any(threads, t < n && at > 0x7fffffffll)) {
     if (a.dev_status && t == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     return;
   }
