@@ -130,9 +130,25 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, const int32_t* con
   return lo;
 }
 
+// How a row is divided: 2^lane_bits lanes a head, 32 >> lane_bits heads of q, of k or of v a pass,
+// of_q and of_k passes; `splits` warps a row of `per` passes each.
+struct Plan {
+  int lane_bits, of_q, of_k, splits, per;
+};
+
+// A lane's way through the heads of a row that its passes take: the address of its own, how far it
+// is to the one of the next pass, the head and how many there are.
+struct Walk {
+  char* at;
+  long long step;
+  int h, of;
+  __device__ __forceinline__ void next(int each) { at += step, h += each; }
+  __device__ __forceinline__ bool on() const { return h < of; }
+};
+
 template <typename T, Pairs kPairs, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7)
-norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
+__global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : kPairs == kCrossed ? 6 : 7)
+norm_rope_kernel(const RopeArgs a, const Plan plan) {
   constexpr int E = Vec<T>::kSize, P = E / 2;  // elements and pairs of neighbours of a vector
   // vectors on their way: each lane's its own, head by head for kCrossed
   __shared__ uint4 ring[kWarps][kStages][64];
@@ -148,41 +164,59 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
       if (!ok && a.dev_status) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     }
   }
-  const int unit = blockIdx.x * kWarps + warp, t = unit / splits;
+  int t = blockIdx.x * kWarps + warp, i0 = 0;
+  if (plan.splits > 1) {
+    const int unit = t;
+    t = unit / plan.splits;
+    i0 = (unit - t * plan.splits) * plan.per;
+  }
   if (t >= a.d.T) return;
-  // A pass takes `each` heads of q, of k or of v; the warp takes passes i0 .. i1 - 1 of the row.
-  const int each = 32 / lanes, g = lane / lanes, c = lane & (lanes - 1);
-  const int of_q = (Hq + each - 1) / each, of_k = (Hkv + each - 1) / each;
-  const int passes = of_q + (kAppend ? 2 : 1) * of_k;
-  const int i0 = (unit - t * splits) * per, i1 = min(i0 + per, passes);
+  const int lanes = 1 << plan.lane_bits, each = 32 >> plan.lane_bits;
+  const int g = lane >> plan.lane_bits, c = lane & (lanes - 1);
+  const int k0 = plan.of_q, v0 = k0 + plan.of_k;  // the first passes of k and of v
+  const int i1 = min(i0 + plan.per, kAppend ? v0 + plan.of_k : v0);
   const int nv = D / (2 * E), nr = R / (2 * E);
   const int va = kPairs == kHalves && c >= nr ? c + nr : c;
   const int vb = kPairs != kHalves ? c + nv : c < nr ? c + nr : va + nv - nr;
-  // (lanes past the head, where D is no power of two, have no head)
-  const auto head_of = [&](int i, int* of) {
-    const int first = i < of_q ? 0 : !kAppend || i < of_q + of_k ? of_q : of_q + of_k;
-    *of = c < nv ? (i < of_q ? Hq : Hkv) : 0;
-    return (i - first) * each + g;
+  const int to_b = (vb - va) * 16;  // bytes
+  // the way of pass i and the ones after it of the same kind (lanes past the head, where D is no
+  // power of two, have none)
+  const auto walk = [&](int i, const void* q, const void* k, const void* v,
+                        const gdn_tree_strides& sq, const gdn_tree_strides& sk,
+                        const gdn_tree_strides& sv) {
+    const bool is_q = i < k0, is_k = !kAppend || i < v0;
+    const char* from = static_cast<const char*>(is_q ? q : is_k ? k : v);
+    const gdn_tree_strides s = is_q ? sq : is_k ? sk : sv;
+    const int h = (i - (is_q ? 0 : is_k ? k0 : v0)) * each + g;
+    return Walk{const_cast<char*>(from) + (t * s.row + h * s.head) * (long long)sizeof(T) + va * 16,
+                s.head * each * (long long)sizeof(T), h, c < nv ? (is_q ? Hq : Hkv) : 0};
   };
   const int slot_a = kPairs == kCrossed ? g * 2 * lanes + c : lane;
   const int slot_b = kPairs == kCrossed ? slot_a + nv : lane + 32;
-  // the vectors of pass i, copied to its stage of the ring (one group a pass, empty or not)
-  const auto fetch = [&](int i) {
-    int of;
-    const int h = head_of(i, &of);
-    if (i < i1 && h < of) {
-      const void* from = i < of_q ? a.q : !kAppend || i < of_q + of_k ? a.k : a.v;
-      const gdn_tree_strides s = i < of_q ? a.s.q : !kAppend || i < of_q + of_k ? a.s.k : a.s.v;
-      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const T*>(from) + t * s.row +
-                                                      h * s.head);
-      uint4* const stage = ring[warp][(unsigned)(i - i0) % kStages];
-      copy16(smem_u32(stage + slot_a), p + va);
-      copy16(smem_u32(stage + slot_b), p + vb);
+  // The vectors of passes i0, i0 + 1, ... are copied to the stages of the ring in turn (one group
+  // a pass, empty or not).
+  constexpr int kStage = sizeof(ring[0][0]);
+  const uint32_t ring_a = smem_u32(&ring[warp][0][slot_a]);
+  const uint32_t ring_b = smem_u32(&ring[warp][0][slot_b]);
+  Walk in = walk(i0, a.q, a.k, a.v, a.s.q, a.s.k, a.s.v);
+  int coming = i0;  // the pass that is copied next
+  uint32_t stage_in = 0;
+  const auto fetch = [&] {
+    if (coming < i1) {
+      if (in.on()) {
+        copy16(ring_a + stage_in, in.at);
+        copy16(ring_b + stage_in, in.at + to_b);
+      }
+      in.next(each);
+      ++coming;
+      if (coming == k0 || (kAppend && coming == v0))
+        in = walk(coming, a.q, a.k, a.v, a.s.q, a.s.k, a.s.v);
+      stage_in = stage_in + kStage == kStages * kStage ? 0 : stage_in + kStage;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i0 + i);
+  for (int i = 0; i < kStages - 1; ++i) fetch();
 
   // the weights of this lane's elements: of q's, then of k's
   float2 w[2 * P];
@@ -195,7 +229,7 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
       w[j] = {v.x, v.y}, w[j + 1] = {v.z, v.w};
     }
   };
-  load_weights(i0 < of_q ? a.q_weight : a.k_weight);
+  load_weights(i0 < k0 ? a.q_weight : a.k_weight);
 
   // the row's position, and its place in the cache (-1: none)
   long long p = 0, place = -1;
@@ -210,7 +244,7 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     }
     const long long at = (long long)ctx + (t - first);
     p = a.d.prefix_len + at;
-    if (i1 > of_q) {
+    if (i1 > k0) {
       if (at < (long long)a.d.table_width * a.d.page_size) {
         // (at fits 32 bits here)
         const unsigned entry = (unsigned)at / (unsigned)a.d.page_size;
@@ -260,19 +294,33 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     if (mine < R / 2) w1.x = from[mine], w2.x = from[mine + R / 2];
     if (mine + 32 < R / 2) w1.y = from[mine + 32], w2.y = from[mine + 32 + R / 2];
   };
-  cross_weights(i0 < of_q ? a.q_weight : a.k_weight);
+  cross_weights(i0 < k0 ? a.q_weight : a.k_weight);
 
   const float share = a.rope.norm == GDN_TREE_NORM_RMS ? 1.f / D : 1.f;
+  // where a pass's heads go: an output's (at NULL: none), and the cache's
+  const auto walk_out = [&](int i) {
+    Walk w = walk(i, a.q_out, a.k_out, a.v_out, a.s.q_out, a.s.k_out, a.s.v_out);
+    if (kAppend && (i < k0 ? a.q_out : i < v0 ? a.k_out : a.v_out) == nullptr) w.at = nullptr;
+    return w;
+  };
+  const auto walk_cache = [&](int i) {
+    if (!kAppend || i < k0 || place < 0) return static_cast<char*>(nullptr);
+    const int h = (i - (i < v0 ? k0 : v0)) * each + g;
+    return static_cast<char*>(i < v0 ? a.k_cache : a.v_cache) +
+           (place * Hkv + h) * D * (long long)sizeof(T) + va * 16;
+  };
+  Walk out = walk_out(i0);
+  char* cached = walk_cache(i0);
+  int now = 0;  // the stage
   for (int i = i0; i < i1; ++i) {
-    const bool value = kAppend && i >= of_q + of_k;
-    int of;
-    const int h = head_of(i, &of);
+    const bool value = kAppend && i >= v0;
     // (kCrossed: the stage that is filled next was read by other lanes, this one is)
     if constexpr (kPairs == kCrossed) __syncwarp();
-    fetch(i + kStages - 1);
+    fetch();
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     if constexpr (kPairs == kCrossed) __syncwarp();
-    uint4* const stage = ring[warp][(unsigned)(i - i0) % kStages];
+    uint4* const stage = ring[warp][now];
+    now = now + 1 == kStages ? 0 : now + 1;
     uint4 y[2] = {stage[slot_a], stage[slot_b]};
     float2 x[2 * P];
     Vec<T>::open(y[0], x);
@@ -282,7 +330,7 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
       float2 two = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) two = fma(x[j], x[j], two);
-      float square = h < of ? two.x + two.y : 0.f;
+      float square = out.on() ? two.x + two.y : 0.f;
       for (int o = lanes / 2; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
       r = __frsqrt_rn(square * share + a.rope.eps);
     }
@@ -311,8 +359,8 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
     }
     if (kPairs == kCrossed && !value) {
       __syncwarp();  // (every lane has its vectors)
-      // (h - g is the pass's first head)
-      const int heads = min(each, (i < of_q ? Hq : Hkv) - (h - g));
+      // (out.h - g is the pass's first head)
+      const int heads = min(each, (i < k0 ? Hq : Hkv) - (out.h - g));
       for (int n0 = 0; n0 < heads; n0 += 32 / wide) {
         const int n = min(n0 + lane / wide, heads - 1);
         const float rn = __shfl_sync(0xffffffffu, r, n * lanes);
@@ -329,31 +377,39 @@ norm_rope_kernel(const RopeArgs a, int lanes, int splits, int per) {
       }
       __syncwarp();
     }
-    if (i + 1 == of_q) {  // (ahead of the first pass that takes them)
+    if (i + 1 == k0) {  // (ahead of the first pass that takes them)
       load_weights(a.k_weight);
       w1 = w2 = {1.f, 1.f};
       cross_weights(a.k_weight);
     }
-    if (h >= of) continue;
-    if (kPairs == kCrossed && !value) {
+    if (out.on()) {
+      if (kPairs == kCrossed && !value) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int left = R - E * (j ? vb : va);  // rotated elements of the vector
-        const uint4 own = Vec<T>::close(x + j * P), turned = stage[j ? slot_b : slot_a];
-        y[j] = left >= E ? turned : left <= 0 ? own : Vec<T>::mix(turned, own, left);
+        for (int j = 0; j < 2; ++j) {
+          const int left = R - E * (j ? vb : va);  // rotated elements of the vector
+          const uint4 own = Vec<T>::close(x + j * P), turned = stage[j ? slot_b : slot_a];
+          y[j] = left >= E ? turned : left <= 0 ? own : Vec<T>::mix(turned, own, left);
+        }
+      } else if (!value) {
+        y[0] = Vec<T>::close(x), y[1] = Vec<T>::close(x + P);
       }
-    } else if (!value) {
-      y[0] = Vec<T>::close(x), y[1] = Vec<T>::close(x + P);
+      if (!kAppend || out.at) {
+        *reinterpret_cast<uint4*>(out.at) = y[0];
+        *reinterpret_cast<uint4*>(out.at + to_b) = y[1];
+      }
+      if (kAppend && cached) {
+        *reinterpret_cast<uint4*>(cached) = y[0];
+        *reinterpret_cast<uint4*>(cached + to_b) = y[1];
+      }
     }
-    const auto put = [&](T* row) {
-      reinterpret_cast<uint4*>(row)[va] = y[0];
-      reinterpret_cast<uint4*>(row)[vb] = y[1];
-    };
-    void* const out = i < of_q ? a.q_out : value ? a.v_out : a.k_out;
-    const gdn_tree_strides s = i < of_q ? a.s.q_out : value ? a.s.v_out : a.s.k_out;
-    if (!kAppend || out) put(static_cast<T*>(out) + t * s.row + h * s.head);
-    if (kAppend && i >= of_q && place >= 0)
-      put(static_cast<T*>(value ? a.v_cache : a.k_cache) + (place * Hkv + h) * D);
+    if (i + 1 == k0 || (kAppend && i + 1 == v0)) {
+      out = walk_out(i + 1);
+      cached = walk_cache(i + 1);
+    } else {
+      if (!kAppend || out.at) out.at += out.step;
+      out.h += each;
+      if (kAppend && cached) cached += each * D * (int)sizeof(T);
+    }
   }
 }
 
@@ -361,10 +417,12 @@ template <bool kAppend>
 cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const bool bf16 = a.d.dtype == GDN_TREE_BF16;
   const int E = bf16 ? 8 : 4, R = a.rope.rotary_dim;
-  int lanes = 1;
-  while (lanes * 2 * E < a.d.D) lanes *= 2;
-  const int each = 32 / lanes;
-  const int passes = (a.d.Hq + each - 1) / each + (kAppend ? 2 : 1) * ((a.d.Hkv + each - 1) / each);
+  Plan plan{};
+  while ((2 * E << plan.lane_bits) < a.d.D) ++plan.lane_bits;
+  const int each = 32 >> plan.lane_bits;
+  plan.of_q = (a.d.Hq + each - 1) / each;
+  plan.of_k = (a.d.Hkv + each - 1) / each;
+  const int passes = plan.of_q + (kAppend ? 2 : 1) * plan.of_k;
   const int sms = sm_count();
   // Warps a row: one where the rows alone fill the SMs (what a warp makes once for its row is then
   // made once), more where they do not (a warp's passes follow one another).  Measured with 32 + 8
@@ -373,14 +431,14 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int want = 12 * sms;
   int splits = 1;
   if (a.d.T > 0 && a.d.T <= want) splits = std::min(passes, want / a.d.T + 1);
-  const int per = (passes + splits - 1) / splits;
-  splits = (passes + per - 1) / per;
-  long long blocks = ((long long)a.d.T * splits + kWarps - 1) / kWarps;
+  plan.per = (passes + splits - 1) / splits;
+  plan.splits = (passes + plan.per - 1) / plan.per;
+  long long blocks = ((long long)a.d.T * plan.splits + kWarps - 1) / kWarps;
   if (kAppend) blocks = std::max(blocks, ((long long)a.d.B + 32 * kWarps - 1) / (32 * kWarps));
   if (blocks == 0) return cudaSuccess;
   const auto go = [&](auto type, auto pairs) {
     norm_rope_kernel<decltype(type), decltype(pairs)::value, kAppend>
-        <<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a, lanes, splits, per);
+        <<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a, plan);
   };
   const auto by_pairs = [&](auto type) {
     if (a.rope.interleaved) go(type, std::integral_constant<Pairs, kNeighbours>());
