@@ -130,10 +130,10 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, const int32_t* con
   return lo;
 }
 
-// How a row is divided: 2^lane_bits lanes a head, 32 >> lane_bits heads of q, of k or of v a pass,
-// of_q and of_k passes; `splits` warps a row of `per` passes each.
+// How a row is divided: 2^kBits lanes a head, 32 >> kBits heads of q, of k or of v a pass, of_q and
+// of_k passes; `splits` warps a row of `per` passes each.
 struct Plan {
-  int lane_bits, of_q, of_k, splits, per;
+  int of_q, of_k, splits, per;
 };
 
 // A lane's way through the heads of a row that its passes take: the address of its own, how far it
@@ -142,11 +142,10 @@ struct Walk {
   char* at;
   long long step;
   int h, of;
-  __device__ __forceinline__ void next(int each) { at += step, h += each; }
   __device__ __forceinline__ bool on() const { return h < of; }
 };
 
-template <typename T, Pairs kPairs, bool kAppend>
+template <typename T, int kBits, Pairs kPairs, bool kAppend>
 __global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : kPairs == kCrossed ? 6 : 7)
 norm_rope_kernel(const RopeArgs a, const Plan plan) {
   constexpr int E = Vec<T>::kSize, P = E / 2;  // elements and pairs of neighbours of a vector
@@ -171,8 +170,8 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
     i0 = (unit - t * plan.splits) * plan.per;
   }
   if (t >= a.d.T) return;
-  const int lanes = 1 << plan.lane_bits, each = 32 >> plan.lane_bits;
-  const int g = lane >> plan.lane_bits, c = lane & (lanes - 1);
+  constexpr int lanes = 1 << kBits, each = 32 >> kBits;
+  const int g = lane >> kBits, c = lane & (lanes - 1);
   const int k0 = plan.of_q, v0 = k0 + plan.of_k;  // the first passes of k and of v
   const int i1 = min(i0 + plan.per, kAppend ? v0 + plan.of_k : v0);
   const int nv = D / (2 * E), nr = R / (2 * E);
@@ -207,7 +206,7 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
         copy16(ring_a + stage_in, in.at);
         copy16(ring_b + stage_in, in.at + to_b);
       }
-      in.next(each);
+      in.at += in.step, in.h += each;
       ++coming;
       if (coming == k0 || (kAppend && coming == v0))
         in = walk(coming, a.q, a.k, a.v, a.s.q, a.s.k, a.s.v);
@@ -331,8 +330,9 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) two = fma(x[j], x[j], two);
       float square = out.on() ? two.x + two.y : 0.f;
+#pragma unroll
       for (int o = lanes / 2; o > 0; o >>= 1) square += __shfl_xor_sync(0xffffffffu, square, o);
-      r = __frsqrt_rn(square * share + a.rope.eps);
+      r = rsqrtf(square * share + a.rope.eps);
     }
     if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
 #pragma unroll
@@ -418,8 +418,9 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const bool bf16 = a.d.dtype == GDN_TREE_BF16;
   const int E = bf16 ? 8 : 4, R = a.rope.rotary_dim;
   Plan plan{};
-  while ((2 * E << plan.lane_bits) < a.d.D) ++plan.lane_bits;
-  const int each = 32 >> plan.lane_bits;
+  int bits = 0;
+  while ((2 * E << bits) < a.d.D) ++bits;
+  const int each = 32 >> bits;
   plan.of_q = (a.d.Hq + each - 1) / each;
   plan.of_k = (a.d.Hkv + each - 1) / each;
   const int passes = plan.of_q + (kAppend ? 2 : 1) * plan.of_k;
@@ -436,17 +437,25 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   long long blocks = ((long long)a.d.T * plan.splits + kWarps - 1) / kWarps;
   if (kAppend) blocks = std::max(blocks, ((long long)a.d.B + 32 * kWarps - 1) / (32 * kWarps));
   if (blocks == 0) return cudaSuccess;
-  const auto go = [&](auto type, auto pairs) {
-    norm_rope_kernel<decltype(type), decltype(pairs)::value, kAppend>
+  const auto go = [&](auto type, auto lane_bits, auto pairs) {
+    norm_rope_kernel<decltype(type), decltype(lane_bits)::value, decltype(pairs)::value, kAppend>
         <<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a, plan);
   };
-  const auto by_pairs = [&](auto type) {
-    if (a.rope.interleaved) go(type, std::integral_constant<Pairs, kNeighbours>());
-    else if (R % (2 * E) == 0) go(type, std::integral_constant<Pairs, kHalves>());
-    else go(type, std::integral_constant<Pairs, kCrossed>());
+  const auto by_pairs = [&](auto type, auto lane_bits) {
+    if (a.rope.interleaved) go(type, lane_bits, std::integral_constant<Pairs, kNeighbours>());
+    else if (R % (2 * E) == 0) go(type, lane_bits, std::integral_constant<Pairs, kHalves>());
+    else go(type, lane_bits, std::integral_constant<Pairs, kCrossed>());
   };
-  if (bf16) by_pairs(__nv_bfloat16());
-  else by_pairs(float());
+  // (heads of 16 to 128 elements: 1 to 8 lanes in bf16, 2 to 16 in fp32)
+  const auto by_lanes = [&](auto type, auto least) {
+    constexpr int kLeast = decltype(least)::value;
+    if (bits == kLeast) by_pairs(type, std::integral_constant<int, kLeast>());
+    else if (bits == kLeast + 1) by_pairs(type, std::integral_constant<int, kLeast + 1>());
+    else if (bits == kLeast + 2) by_pairs(type, std::integral_constant<int, kLeast + 2>());
+    else by_pairs(type, std::integral_constant<int, kLeast + 3>());
+  };
+  if (bf16) by_lanes(__nv_bfloat16(), std::integral_constant<int, 0>());
+  else by_lanes(float(), std::integral_constant<int, 1>());
   return cudaGetLastError();
 }
 
