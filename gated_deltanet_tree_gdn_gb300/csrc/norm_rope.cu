@@ -70,6 +70,12 @@ struct Vec<float> {
     x[0] = {__uint_as_float(v.x), __uint_as_float(v.y)};
     x[1] = {__uint_as_float(v.z), __uint_as_float(v.w)};
   }
+  static __device__ __forceinline__ float2 two(const float* p) {
+    return *reinterpret_cast<const float2*>(p);
+  }
+  static __device__ __forceinline__ void put(float* p, float2 x) {
+    *reinterpret_cast<float2*>(p) = x;
+  }
   // the first n elements (even) of one vector, the others of another
   static __device__ __forceinline__ uint4 mix(const uint4& a, const uint4& b, int n) {
     return {a.x, a.y, n > 2 ? a.z : b.z, n > 2 ? a.w : b.w};
@@ -87,6 +93,12 @@ struct Vec<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       x[i] = {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+  }
+  static __device__ __forceinline__ float2 two(const __nv_bfloat16* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+  }
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, float2 x) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x.x, x.y);
   }
   static __device__ __forceinline__ uint4 mix(const uint4& a, const uint4& b, int n) {
     return {a.x, n > 2 ? a.y : b.y, n > 4 ? a.z : b.z, n > 6 ? a.w : b.w};
@@ -146,7 +158,7 @@ struct Walk {
 };
 
 template <typename T, int kBits, Pairs kPairs, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : kPairs == kCrossed ? 6 : 7)
+__global__ void __launch_bounds__(32 * kWarps, kAppend || kPairs == kCrossed ? 5 : 7)
 norm_rope_kernel(const RopeArgs a, const Plan plan) {
   constexpr int E = Vec<T>::kSize, P = E / 2;  // elements and pairs of neighbours of a vector
   // vectors on their way: each lane's its own, head by head for kCrossed
@@ -259,15 +271,17 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   }
 
   // The row's cosines and sines, each made by one lane; then those of this lane's pairs: of
-  // kNeighbours, pairs j of both vectors; of kCrossed, where `wide` lanes take a head, pairs
-  // `mine` and `mine` + 32.
+  // kNeighbours, pairs j of both vectors; of kCrossed, where `wide` lanes take a head, the two
+  // pairs m0 and m1: neighbours where R / 2 is even, so that they are read and written together.
   constexpr int kMine = kPairs == kCrossed ? 1 : P;
   float2 co[kMine], si[kMine];
-  const int wide = R > 32 ? 32 : R > 16 ? 16 : 8, mine = lane & (wide - 1);
+  const bool even = R % 4 == 0;
+  const int need = even ? R / 4 : R / 2, wide = need > 16 ? 32 : need > 8 ? 16 : 8;
+  const int m0 = (lane & (wide - 1)) << even, m1 = even ? m0 + 1 : m0 + 32;
   if constexpr (kPairs == kCrossed) {
     const float2 none = {1.f, 0.f};
-    const float2 f = mine < R / 2 ? turn(p, a.freq[mine], a.rope.scale) : none;
-    const float2 h = mine + 32 < R / 2 ? turn(p, a.freq[mine + 32], a.rope.scale) : none;
+    const float2 f = m0 < R / 2 ? turn(p, a.freq[m0], a.rope.scale) : none;
+    const float2 h = m1 < R / 2 ? turn(p, a.freq[m1], a.rope.scale) : none;
     co[0] = {f.x, h.x}, si[0] = {f.y, h.y};
   } else if (R > 0) {
     float2* const row = reinterpret_cast<float2*>(turns[warp]);
@@ -276,12 +290,12 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       if constexpr (kPairs == kHalves) {
-        const float4 two = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
+        [[maybe_unused]] const float4 two = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
         co[j] = {two.x, two.z}, si[j] = {two.y, two.w};
       } else {
         const int m = P * va + j, n = P * vb + j;
         const float2 f = m < R / 2 ? row[m] : float2{1.f, 0.f};
-        const float2 h = n < R / 2 ? row[n] : float2{1.f, 0.f};
+        [[maybe_unused]] const float2 h = n < R / 2 ? row[n] : float2{1.f, 0.f};
         co[j] = {f.x, h.x}, si[j] = {f.y, h.y};
       }
     }
@@ -290,8 +304,8 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   float2 w1 = {1.f, 1.f}, w2 = {1.f, 1.f};
   const auto cross_weights = [&](const float* from) {
     if (kPairs != kCrossed || from == nullptr) return;
-    if (mine < R / 2) w1.x = from[mine], w2.x = from[mine + R / 2];
-    if (mine + 32 < R / 2) w1.y = from[mine + 32], w2.y = from[mine + 32 + R / 2];
+    if (m0 < R / 2) w1.x = from[m0], w2.x = from[m0 + R / 2];
+    if (m1 < R / 2) w1.y = from[m1], w2.y = from[m1 + R / 2];
   };
   cross_weights(i0 < k0 ? a.q_weight : a.k_weight);
 
@@ -365,14 +379,26 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
         const int n = min(n0 + lane / wide, heads - 1);
         const float rn = __shfl_sync(0xffffffffu, r, n * lanes);
         T* const head = reinterpret_cast<T*>(stage + n * 2 * lanes);
-        const auto cross = [&](int at, float first, float second, float cs, float sn) {
-          const float u = to_f32(head[at]) * (first * rn), v = to_f32(head[at + R / 2]) * (second * rn);
-          head[at] = from_f32<T>(u * cs - v * sn);
-          head[at + R / 2] = from_f32<T>(v * cs + u * sn);
-        };
-        if (n0 + lane / wide < heads) {
-          if (mine < R / 2) cross(mine, w1.x, w2.x, co[0].x, si[0].x);
-          if (mine + 32 < R / 2) cross(mine + 32, w1.y, w2.y, co[0].y, si[0].y);
+        if (n0 + lane / wide < heads && m0 < R / 2) {
+          const auto cross = [&](float2& u, float2& v) {
+            u = mul(u, mul(w1, float2{rn, rn})), v = mul(v, mul(w2, float2{rn, rn}));
+            const float2 t = u;
+            u = fma(u, co[0], mul(v, float2{-si[0].x, -si[0].y}));
+            v = fma(v, co[0], mul(t, si[0]));
+          };
+          if (even) {
+            float2 u = Vec<T>::two(head + m0), v = Vec<T>::two(head + m0 + R / 2);
+            cross(u, v);
+            Vec<T>::put(head + m0, u), Vec<T>::put(head + m0 + R / 2, v);
+          } else {
+            const bool both = m1 < R / 2;
+            const int m = both ? m1 : m0;
+            float2 u = {to_f32(head[m0]), to_f32(head[m])};
+            float2 v = {to_f32(head[m0 + R / 2]), to_f32(head[m + R / 2])};
+            cross(u, v);
+            head[m0] = from_f32<T>(u.x), head[m0 + R / 2] = from_f32<T>(v.x);
+            if (both) head[m1] = from_f32<T>(u.y), head[m1 + R / 2] = from_f32<T>(v.y);
+          }
         }
       }
       __syncwarp();
