@@ -812,7 +812,7 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
 # (These take 4 to 18 tensors ahead of a launch of 2 microseconds: a tensor is looked at once, and
 # what the call needs of the shapes is made once for each set of them.)
 
-_Tensor, _i32, _i64, _f32 = torch.Tensor, torch.int32, torch.int64, torch.float32
+_i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
 # (asked only where there is a CUDA tensor: the runtime is up then)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -823,10 +823,14 @@ def _stream_of(dev) -> int:
 
 def _flat(t, name, dtype, shape, dev):
     """The address of a dense tensor of this type and shape on the current device."""
-    if not (type(t) is _Tensor and t.get_device() == dev and t.dtype is dtype
-            and t.is_contiguous() and t.shape == shape):
-        _check(t, name, dtype, shape)
-        _check_device(t, name, dev)
+    try:
+        if (t.get_device() == dev and t.dtype is dtype and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:  # (no tensor)
+        pass
+    _check(t, name, dtype, shape)
+    _check_device(t, name, dev)
     return t.data_ptr()
 
 
@@ -837,7 +841,7 @@ def _check_device(t, name, dev):
 
 def _device(t, name):
     """The current device, which t is on."""
-    if not isinstance(t, _Tensor):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -848,10 +852,13 @@ def _device(t, name):
 
 def _heads(t, name, dtype, shape, dev):
     """The strides of an array of heads [T, H, D] whose heads are contiguous."""
-    if type(t) is _Tensor and t.get_device() == dev and t.dtype is dtype and t.shape == shape:
-        strides = t.stride()
-        if strides[2] == 1:
-            return strides
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape:
+            strides = t.stride()
+            if strides[2] == 1:
+                return strides
+    except AttributeError:  # (no tensor)
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:

@@ -128,13 +128,14 @@ bool disjoint(const HeadRows& a, const HeadRows& b) {
          beside(off, a.head, a.width, b.width);
 }
 
-// fills `out` from a pointer and strides in elements; strides that step over a single row or
-// head do not count.  Misaligned or negative ones, or strides out of range, are refused.
+// fills `out` from a pointer and strides in elements; strides of no array, or that step over a
+// single row or head, do not count.  Misaligned or negative ones, or strides out of range, are
+// refused.
 int check_heads(const void* p, gdn_tree_strides* s, int T, int H, int D, int dtype,
                 HeadRows* out) {
   const long long es = dtype == GDN_TREE_BF16 ? 2 : 4;
-  if (T <= 1) s->row = 0;
-  if (H <= 1) s->head = 0;
+  if (T <= 1 || p == nullptr) s->row = 0;
+  if (H <= 1 || p == nullptr) s->head = 0;
   if (!aligned16(p) || s->row < 0 || s->head < 0 || s->row % (16 / es) || s->head % (16 / es))
     return GDN_TREE_EINVAL;
   // (offsets, in bytes, stay within 63 bits)

@@ -124,6 +124,8 @@ def test_strides(lib):
     for over in ((0, D), (HQ * D - 8, D), (HQ * D, 0), (HQ * D, D - 8), (D, D), (D, T * D - 8)):
         assert norm_rope(lib, qos=over) == gt.EINVAL
     assert norm_rope(lib, qs=(1 << 60, D)) == gt.EUNSUPPORTED
+    assert norm_rope(lib, q=None, qs=(3, -5), ks=(1 << 60, D)) == gt.EUNSUPPORTED  # (k's, not q's)
+    assert norm_rope(lib, q=None, qs=(3, -5), qos=(3, -5), ko=P(2)) == gt.EINVAL    # ko over positions
     # (a null freq is the last thing wrong: the strides before it were taken)
     assert norm_rope(lib, shape(Hq=1), qos=(D, 3), freq=None) == gt.EINVAL
     h = (1 << 60) * 8
