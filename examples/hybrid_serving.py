@@ -3,13 +3,13 @@
     python examples/hybrid_serving.py
 
 Every sequence shares a system prompt.  It is read once: `prefill` leaves its states, and
-`cache_append` its keys and values on pages that all sequences then see as their prefix.  The
-sequences' own prompts follow as one ragged batch.  After that a round drafts a tree of tokens
-below each sequence's next one (`build_topw`), runs it through the model (`verify_packed` and
-`attend`, which change nothing), and keeps the path that the model itself would have taken
-(`commit_packed` for the states, `cache_append` for the keys and values).  Every third round
-nothing is drafted, and the next token is run alone (`decode_step`, `attend` of one row,
-`cache_append`).
+`cache_append_rope` its keys (normalised and rotated) and values on pages that all sequences then
+see as their prefix.  The sequences' own prompts follow as one ragged batch.  After that a round
+drafts a tree of tokens below each sequence's next one (`build_topw`), runs it through the model
+at the nodes' positions (`tree_positions`, `norm_rope`, `verify_packed` and `attend`, which change
+nothing), and keeps the path that the model itself would have taken (`commit_packed` for the
+states, `cache_append` for the keys and values).  Every third round nothing is drafted, and the
+next token is run alone: `decode_step`, and `cache_append_rope` with `attend` to the cache.
 
 The weights are random.  At the end the kept tokens are run through the model from nothing, in
 one `prefill` and one causal `attend` a layer, and must give the same logits.
@@ -26,13 +26,17 @@ import gated_deltanet_tree_gdn_gb300 as gt  # noqa: E402
 
 VOCAB, WIDTH, LAYERS = 16, 256, 4          # even layers: Gated DeltaNet, odd: attention
 HQK, HV, DK = 2, 4, 128                    # its heads (dk = dv)
-HQ, HKV, D = 8, 2, 64                      # the attention's
+HQ, HKV, D, ROTATED = 8, 2, 64, 32         # the attention's, and how much of a head is rotated
 PAGE, PAGES_EACH = 16, 16                  # pages of a sequence's own context
 NODES, CANDIDATES, DEPTH = 24, 4, 6        # a draft tree
 
 
 def ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rows_like(x):
+    return torch.empty(x.shape, dtype=x.dtype, device="cuda")
 
 
 class Model:
@@ -47,6 +51,11 @@ class Model:
 
         self.embed = weight(VOCAB, WIDTH) * 4
         self.head = weight(WIDTH, VOCAB)
+        # the attention's rotary frequencies, and the weights of its heads' norms
+        freq, scale = gt.rope_frequencies(ROTATED, 1e4)
+        near_one = lambda: 1 + 0.1 * torch.randn(D, device="cuda", generator=gen)  # noqa: E731
+        self.rope = dict(freq=freq, rope_scale=scale, norm="rms", q_weight=near_one(),
+                         k_weight=near_one())
         self.layers = []
         for i in range(LAYERS):
             if i % 2 == 0:
@@ -63,15 +72,15 @@ class Model:
         T = x.shape[0]
         for i, (w_in, sizes, w_out) in enumerate(self.layers):
             y = torch.nn.functional.rms_norm(x, (WIDTH,)).bfloat16() @ w_in
-            y = [p.contiguous() for p in y.split(sizes, dim=1)]
+            y = y.split(sizes, dim=1)
+            heads = lambda z, n: z.unflatten(1, (n, -1))  # noqa: E731 (columns, no copy)
             if i % 2 == 0:
-                unit = lambda z: torch.nn.functional.normalize(  # noqa: E731
-                    z.view(T, HQK, DK).float(), dim=-1).bfloat16()
+                q, k = gt.norm_rope(heads(y[0], HQK), heads(y[1], HQK), norm="unit")
                 log_alpha = -0.2 * torch.nn.functional.softplus(y[3].float())
-                o = rule(i, unit(y[0]), unit(y[1]), y[2].view(T, HV, DK), log_alpha,
+                o = rule(i, q, k, heads(y[2], HV).contiguous(), log_alpha,
                          torch.sigmoid(y[4].float()))
             else:
-                o = attention(i, y[0].view(T, HQ, D), y[1].view(T, HKV, D), y[2].view(T, HKV, D))
+                o = attention(i, heads(y[0], HQ), heads(y[1], HKV), heads(y[2], HKV))
             x = x + (o.reshape(T, -1) @ w_out).float()
         return torch.nn.functional.rms_norm(x, (WIDTH,)).bfloat16().float() @ self.head.float()
 
@@ -88,9 +97,11 @@ class Server:
         self.prefix_pages = pages[:n_prefix].contiguous()
         self.table = pages[n_prefix:].view(batch, PAGES_EACH).contiguous()
         self.context_len = ints([0] * batch)
-        self.caches = {i: [torch.zeros(len(pages), PAGE, HKV, D, dtype=torch.bfloat16, device="cuda")
-                           for _ in range(2)] for i in range(1, LAYERS, 2)}
-        self.states = {i: torch.zeros(batch, HV, DK, DK, device="cuda") for i in range(0, LAYERS, 2)}
+        self.caches = {i: [torch.zeros(len(pages), PAGE, HKV, D, dtype=torch.bfloat16,
+                                       device="cuda") for _ in range(2)]
+                       for i in range(1, LAYERS, 2)}
+        self.states = {i: torch.zeros(batch, HV, DK, DK, device="cuda")
+                       for i in range(0, LAYERS, 2)}
         # the system prompt, once: sequence 0's state, given to all of them
         cu, none = ints([0, self.prefix_len]), ints([0])
 
@@ -98,22 +109,25 @@ class Server:
             return gt.prefill(*qkvab, cu, self.states[i], pool_out=self.states[i])[0]
 
         def attention(i, q, k, v):
-            o, _ = gt.attend(q, k, v, None, cu, *self.caches[i], self.prefix_pages[None], none)
-            gt.cache_append(k, v, cu, *self.caches[i], self.prefix_pages[None], none)
-            return o
+            own = dict(k_out=rows_like(k), v_out=rows_like(v))
+            q, _ = gt.cache_append_rope(q, k, v, cu, *self.caches[i], self.prefix_pages[None], none,
+                                        **own, **model.rope)
+            return gt.attend(q, *own.values(), None, cu, *self.caches[i], self.prefix_pages[None],
+                             none)[0]
 
         model.run(ints(system_prompt), rule, attention)
         for s in self.states.values():
             s[1:] = s[:1]
 
-    def attend(self, i, q, k, v, parent, cu, rows):
-        return gt.attend(q, k, v, parent, cu, *self.caches[i], self.table, self.context_len,
+    def attend(self, i, q, k, v, parent, cu, rows, context_len):
+        return gt.attend(q, k, v, parent, cu, *self.caches[i], self.table, context_len,
                          prefix_pages=self.prefix_pages, prefix_len=self.prefix_len,
                          N_max=rows)[0]
 
-    def append(self, i, k, v, cu, rows, **path):
-        return gt.cache_append(k, v, cu, *self.caches[i], self.table, self.context_len, N_max=rows,
-                               **path)
+    def append_rope(self, i, q, k, v, cu, rows, **own):
+        return gt.cache_append_rope(q, k, v, cu, *self.caches[i], self.table, self.context_len,
+                                    prefix_len=self.prefix_len, N_max=rows, **own,
+                                    **self.model.rope)
 
     def prompts(self, lists):
         """The sequences' prompts as one ragged batch; the logits behind each one's last token."""
@@ -125,9 +139,10 @@ class Server:
             return gt.prefill(*qkvab, cu, self.states[i], N_max=rows, pool_out=self.states[i])[0]
 
         def attention(i, q, k, v):
-            o = self.attend(i, q, k, v, None, cu, rows)
-            kept.append(self.append(i, k, v, cu, rows))
-            return o
+            own = dict(k_out=rows_like(k), v_out=rows_like(v))
+            q, after = self.append_rope(i, q, k, v, cu, rows, **own)
+            kept.append(after)
+            return self.attend(i, q, *own.values(), None, cu, rows, self.context_len)
 
         logits = self.model.run(ints(sum(lists, [])), rule, attention)
         self.context_len = kept[-1]
@@ -141,9 +156,10 @@ class Server:
             return gt.decode_step(*qkvab, self.states[i], pool_out=self.states[i])[0]
 
         def attention(i, q, k, v):
-            o = self.attend(i, q, k, v, None, cu, 1)
-            kept.append(self.append(i, k, v, cu, 1))
-            return o
+            # (the token's own row is the last of the cache)
+            q, after = self.append_rope(i, q, k, v, cu, 1)
+            kept.append(after)
+            return self.attend(i, q, None, None, None, cu, 1, after)
 
         logits = self.model.run(tokens, rule, attention)
         self.context_len = kept[-1]
@@ -177,9 +193,13 @@ class Server:
             rule_kept[i] = (U, k, log_alpha)
             return o
 
+        positions = gt.tree_positions(par, cu, context_len=self.context_len,
+                                      prefix_len=self.prefix_len, N_max=rows)
+
         def attention(i, q, k, v):
-            attn_kept[i] = (k, v)
-            return self.attend(i, q, k, v, par, cu, rows)
+            q, k = gt.norm_rope(q, k, positions, **self.model.rope)
+            attn_kept[i] = (k, v.contiguous())
+            return self.attend(i, q, *attn_kept[i], par, cu, rows, self.context_len)
 
         below = self.model.run(ints(tokens), rule, attention)
         # greedy: follow the model's own choice while the tree has it
@@ -202,7 +222,8 @@ class Server:
             gt.commit_packed(path, path_len, U, k, log_alpha, cu, self.states[i],
                              pool_out=self.states[i], parent=par, N_max=rows)
         for i, (k, v) in attn_kept.items():
-            kept = self.append(i, k, v, cu, rows, path=path, path_len=path_len)
+            kept = gt.cache_append(k, v, cu, *self.caches[i], self.table, self.context_len,
+                                   N_max=rows, path=path, path_len=path_len)
         self.context_len = kept
         return taken, last
 
@@ -217,8 +238,11 @@ def whole(model, lists):
     def rule(i, *qkvab):
         return gt.prefill(*qkvab, cu, torch.zeros(len(lists), HV, DK, DK, device="cuda"))[0]
 
+    positions = gt.tree_positions(None, cu, T=ends[-1])
+
     def attention(i, q, k, v):
-        return gt.attend(q, k, v, None, cu, no_cache, no_cache,
+        q, k = gt.norm_rope(q, k, positions, **model.rope)
+        return gt.attend(q, k, v.contiguous(), None, cu, no_cache, no_cache,
                          torch.zeros(len(lists), 1, dtype=torch.int32, device="cuda"),
                          ints([0] * len(lists)))[0]
 
