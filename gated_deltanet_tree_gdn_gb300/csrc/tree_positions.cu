@@ -12,24 +12,37 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// rows, and their positions, are in range
+// the rows and the context of a sequence are in range
 __device__ __forceinline__ bool in_range(const PositionArgs& a, int first, int stop, int ctx) {
   return first >= 0 && stop >= first && stop <= a.T && stop - first <= a.N && ctx >= 0;
 }
+__device__ __forceinline__ int context_of(const PositionArgs& a, int b) {
+  return a.context_len ? a.context_len[b] : 0;
+}
 
+// A thread a row, which looks its sequence up: a grid over the rows there are is right for batches
+// of any raggedness, and for any number of sequences.
 __global__ void __launch_bounds__(kThreads) chain_positions_kernel(const PositionArgs a) {
-  const int groups = gridDim.x / a.B, b = blockIdx.x / groups;
-  const int first = a.cu[b], stop = a.cu[b + 1], ctx = a.context_len ? a.context_len[b] : 0;
-  const int j0 = (blockIdx.x % groups) * kThreads;
-  const long long start = (long long)a.prefix_len + ctx;
-  if (!in_range(a, first, stop, ctx) || start + (stop - first) - 1 > 0x7fffffffll) {
-    if (a.dev_status && j0 == 0 && threadIdx.x == 0)
-      atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
-    return;
+  const long long x = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const auto fits = [&](int b, long long* start) {
+    const int first = a.cu[b], stop = a.cu[b + 1], ctx = context_of(a, b);
+    *start = (long long)a.prefix_len + ctx;
+    return in_range(a, first, stop, ctx) && *start + (stop - first) - 1 <= 0x7fffffffll;
+  };
+  long long start;
+  if (x < a.B && a.dev_status && !fits((int)x, &start))
+    atomicMax(a.dev_status + x, GDN_TREE_STATUS_BAD_LAYOUT);
+  if (x >= a.T) return;
+  const int t = (int)x;
+  int lo = -1, hi = a.B + 1;  // the last b with cu[b] <= t (whatever cu holds, within [-1, B])
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
   }
-  // (the grid has a CTA for each kThreads of the most rows there may be)
-  const int j = j0 + threadIdx.x;
-  if (j < stop - first) a.positions[first + j] = (int)(start + j);
+  if (lo < 0 || lo >= a.B || !fits(lo, &start)) return;
+  const int j = t - a.cu[lo];
+  if (t < a.cu[lo + 1]) a.positions[t] = (int)(start + j);
 }
 
 // a barrier of the first `threads` threads, and whether x holds for any of them
@@ -49,7 +62,7 @@ __global__ void __launch_bounds__(kMaxNLong) tree_positions_kernel(const Positio
   // last round and of this one
   __shared__ uint32_t nodes[2][kMaxNLong];
   const int b = blockIdx.x, t = threadIdx.x;
-  const int first = a.cu[b], stop = a.cu[b + 1], ctx = a.context_len ? a.context_len[b] : 0;
+  const int first = a.cu[b], stop = a.cu[b + 1], ctx = context_of(a, b);
   if (!in_range(a, first, stop, ctx)) {
     if (a.dev_status && t == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
     return;
@@ -90,9 +103,9 @@ cudaError_t launch_tree_positions(const PositionArgs& a, cudaStream_t stream) {
     tree_positions_kernel<<<a.B, threads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  const long long groups = a.N > kThreads ? ((long long)a.N + kThreads - 1) / kThreads : 1;
-  if (groups * a.B > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  chain_positions_kernel<<<(unsigned)(groups * a.B), kThreads, 0, stream>>>(a);
+  const long long threads = a.T > a.B ? a.T : a.B;
+  const unsigned blocks = (unsigned)((threads + kThreads - 1) / kThreads);
+  chain_positions_kernel<<<blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

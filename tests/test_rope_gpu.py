@@ -2,10 +2,11 @@
 GPU against their fp64 definitions.
 
 Tolerances, from the arithmetic, in units of u = 2^-24 (half a step of fp32, relative):
-  norm      the squares of a head's 128 elements and their sum: each term passes at most 16
-            products and additions in a lane and 5 additions between lanes, 21 u of the sum; its
-            factor and eps 2 u; a root halves that, 11.5 u; the root, the product with the weight
-            and the one with the element 1 u each (the root 2): 16 u of a normalised element
+  norm      the squares of a head's 128 elements and their sum: each term passes at most 9
+            products and additions in a lane and 4 additions between lanes, 13 u of the sum; its
+            factor and eps 2 u; a root halves that, 7.5 u; the root's reciprocal is within 2 steps,
+            4 u; its products with the weight and with the element 1 u each: under 16 u of a
+            normalised element
   rotation  the fraction of a turn is rounded to 24 bits, at most pi u as an angle; sine and
             cosine are within 2 steps, 4 u; their product with the scale 1 u; the two products and
             the sum 3 u: 12 u of scale (|x| + |y|), x and y being the pair
@@ -289,8 +290,9 @@ def append_inputs(lens, ctx, Hq, Hkv, D, R, page, dtype, rows, norm, seed, prefi
     held = [-(-(c + n) // page) for c, n in zip(ctx, lens)]
     order = r.permutation(sum(held) + 2).astype(np.int32)
     table = np.full((len(lens), max(held + [1])), 1 << 30, dtype=np.int32)
+    start = np.concatenate([[0], np.cumsum(held)])
     for b, h in enumerate(held):
-        table[b, :h] = order[sum(held[:b]):sum(held[:b]) + h]
+        table[b, :h] = order[start[b]:start[b] + h]
     t = lambda *s: torch.tensor(r.standard_normal(s), dtype=DT[dtype], device="cuda")  # noqa: E731
     x.update(cu=cu_of(lens), ctx=np.array(ctx, dtype=np.int32), table=table, prefix=prefix, T=T,
              k_cache=t(sum(held) + 2, page, Hkv, D), v_cache=t(sum(held) + 2, page, Hkv, D))
@@ -408,8 +410,8 @@ def test_append_bad_device_data_is_reported():
         allowed = {int(p) for b in (0, 1, 2, 5) for p in x["table"][b] if 0 <= p < len(cache)}
         assert set(touched) <= allowed
     # offsets that decrease, or run past the rows: reported, and nothing outside is touched
-    for cu in ([0, 20, 60, 40, 80, 100, 120], [0, 20, 40, 60, 80, 100, 10 ** 9], [-5, 20, 40, 60, 80, 100, 120],
-               [0, 20, 40, 60, -2 ** 31, 100, 2 ** 31 - 1]):
+    for cu in ([0, 20, 60, 40, 80, 100, 120], [0, 20, 40, 60, 80, 100, 10 ** 9],
+               [-5, 20, 40, 60, 80, 100, 120], [0, 20, 40, 60, -2 ** 31, 100, 2 ** 31 - 1]):
         y = append_inputs([20] * 6, [10] * 6, 4, 2, 64, 64, 16, "bf16", "dense", "rms", seed=1)
         y["cu"] = np.array(cu, dtype=np.int32)
         _, n = run_append(y, False, dev_status=status, N_max=30)
@@ -433,6 +435,47 @@ def test_append_past_the_table():
     x["table"] = x["table"][:, :0].copy()
     q3, _ = run_append(x, False, dev_status=status)
     assert status.tolist() == [gt.STATUS_BAD_LAYOUT] and torch.equal(q, q3)
+
+
+def test_very_many_sequences():
+    """The most sequences there may be, most of them empty: every row finds its own."""
+    r = np.random.default_rng(13)
+    B = 65535
+    lens = (r.random(B) < 0.03).astype(int) * r.integers(1, 4, B)
+    lens[[0, 31, 32, 1023, 1024, B - 1]] = 2
+    ctx = r.integers(0, 9, B)
+    x = append_inputs(list(lens), list(ctx), 2, 1, 16, 16, 4, "f32", "dense", None, seed=14, extra=5)
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    status = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    q, new_len = run_append(x, False, dev_status=status)
+    assert (status == 0).all()
+    check_append(x, False, before, q, new_len)
+    out = torch.full((x["T"],), -7, dtype=torch.int32, device="cuda")
+    gt.tree_positions(None, ints(x["cu"]), context_len=ints(ctx), prefix_len=3, positions=out,
+                      dev_status=status)
+    assert (status == 0).all()
+    assert out.tolist() == ref.tree_positions(None, x["cu"], ctx, 3, x["T"], fill=-7).tolist()
+
+
+def test_arrays_of_a_fixed_capacity():
+    """Arrays with room for more rows than there are, and a promise far above them: the rows of no
+    sequence and their outputs stay as they were."""
+    x = append_inputs([1, 3, 0, 2], [9, 0, 5, 31], 4, 2, 64, 32, 16, "bf16", "fused", "rms", seed=15,
+                      extra=250)
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    out = torch.full((256, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    q, new_len = run_append(x, False, N_max=2 ** 31 - 1, q_out=out)
+    check_append(x, False, before, q, new_len)
+    assert (out[6:] == 5.0).all()
+    par = ints([-1, -1, 0, 1, -1, 0] + [77] * 250)
+    pos = torch.full((256,), -7, dtype=torch.int32, device="cuda")
+    gt.tree_positions(par, ints(x["cu"]), context_len=ints(x["ctx"]), positions=pos, N_max=1024)
+    assert pos.tolist() == [9, 0, 1, 2, 31, 32] + [-7] * 250
+    # no rows at all, in arrays with room
+    none = dict(x, cu=np.zeros(5, dtype=np.int32))
+    keep = x["k_cache"].clone()
+    _, new_len = run_append(none, False)
+    assert new_len.tolist() == list(x["ctx"]) and torch.equal(x["k_cache"], keep)
 
 
 def test_append_cache_past_32_bit_offsets():
@@ -686,6 +729,39 @@ def test_a_call_on_a_given_stream_and_in_a_graph(name):
             assert torch.equal(a[touched], b[touched]) and touched.sum() == 137 * 2
         else:
             assert torch.equal(a, b)
+
+
+def test_two_graphs_in_turn():
+    """Two captured calls of different shapes, replayed in turn on changing inputs."""
+    x = [append_inputs([40, 7], [3, 60], 8, 2, 128, 128, 32, "bf16", "fused", "rms", seed=21),
+         append_inputs([5] * 9, [b for b in range(9)], 4, 4, 64, 20, 16, "f32", "dense", "unit", seed=22)]
+    held = [[ints(y[n]) for n in ("cu", "table", "ctx")] for y in x]
+    status = [torch.empty(len(y["ctx"]), dtype=torch.int32, device="cuda") for y in x]
+
+    def call(i, inter, **kw):
+        y, (cu, table, ctx) = x[i], held[i]
+        return gt.cache_append_rope(y["q"], y["k"], y["v"], cu, y["k_cache"], y["v_cache"], table, ctx,
+                                    y["freq"], prefix_len=11, norm=y["norm"], q_weight=y["wq"],
+                                    k_weight=y["wk"], rope_scale=y["scale"], interleaved=inter,
+                                    N_max=40, dev_status=status[i], **kw)
+
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(i, bool(i)))
+        graphs.append(g)
+    for turn in range(3):
+        for y in x:
+            for n in "qkv":
+                y[n].copy_(torch.randn(y[n].shape, device="cuda"))
+        before = [(y["k_cache"].clone(), y["v_cache"].clone()) for y in x]
+        for i in (0, 1) if turn % 2 else (1, 0):
+            status[i].fill_(-7)
+            graphs[i].replay()
+        for i, y in enumerate(x):
+            assert (status[i] == 0).all()
+            check_append(dict(y, prefix=11), bool(i), before[i], *outs[i])
 
 
 def test_two_calls_at_once():
