@@ -7,9 +7,25 @@
 // p f_i in floating point would need more bits than fp32 has (p = 10^6 leaves 2^-4 of a radian).
 //
 // Everything is read once and written once, so the call is bound by DRAM, or by latency where
-// there are few rows.  A warp takes some heads of one row: a head's elements lie over a few lanes
-// (8 for 128 of bf16), two 16-byte vectors a lane, and lane c of every head holds the same
-// elements, so that the cosines and sines of a row are made once for all heads that a warp takes.
+// there are few rows.  A warp takes the heads of one row, or some of them: a head's elements lie
+// over a few lanes (8 for 128 of bf16), two 16-byte vectors a lane, and lane c of every head holds
+// the same elements, so that the cosines and sines of a row are made once (a pair a lane, through
+// shared memory) for all heads that a warp takes, and a pair's elements are in one lane.
+//
+// Measured on one GB300, calls in a CUDA graph over inputs that do not fit the L2 (a plain copy
+// kernel over as many bytes in brackets): 32768 rows of 32 + 8 heads of 128 in bf16, every second
+// 128 elements read, 105 us, 6.4 TB/s (99); 16384 rows of 16 + 16 heads made unit vectors 43.8
+// (41.5); 8191 rows of 16 + 16 heads rotated 23.4 (22); 4096 rows of 32 + 8 heads 17.2 (14.2: they
+// are one round of the SMs, so that every warp's way from its first load to its last store counts);
+// 16 prompts of 17 to 4096 rows into the cache and beside it 85.5, 6.1 TB/s; one row 2.4, into the
+// cache 3.4.
+//
+// What that took, on the 32768 rows: vectors by plain loads, one or two passes ahead in registers,
+// 130 to 149 us (loads in flight then cost registers, and with them warps); by cp.async, three
+// passes ahead, 120; a lane's weights in registers and not from L1 in every pass, 106; fewer
+// instructions (packed fp32 arithmetic; addresses by steps; lanes a head known to the compiler)
+// 105, and more where heads are small: 16384 rows of 32 + 8 heads of 80 elements 56 to 43 us, of 64
+// 32.5 to 28.2.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,14 +35,14 @@
 namespace gdn {
 namespace {
 
-// (3 to 6 stages take the same time within 2 %; 2 take 3 to 6 % more, 8 leave room for fewer warps)
+// (32768 rows: 106 us with 4 stages, 108 to 110 with 2, 3 or 5; 8 leave room for fewer warps)
 constexpr int kWarps = 4, kStages = 4;
 
 // How the pairs of a rotation lie in a lane's two vectors of E elements, number va and vb of the
-// head's D / E:
+// head's D / E (16384 rows of 32 + 8 heads of 128 in bf16: 54 us, 54, and 59 to 80):
 //   kNeighbours  elements 2 i and 2 i + 1 are in the same vector
 //   kHalves      R a multiple of 2 E (0 included): vb = va + R / 2 E holds va's partners
-//   kCrossed     elements i and i + R / 2 for any other R: rotated in the ring, a pair a lane
+//   kCrossed     elements i and i + R / 2 for any other R: rotated in the ring, two pairs a lane
 enum Pairs { kNeighbours, kHalves, kCrossed };
 
 // cos and sin of the angle at position p of a pair of this frequency, times the scale
@@ -290,11 +306,12 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       if constexpr (kPairs == kHalves) {
-        [[maybe_unused]] const float4 two = c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
+        [[maybe_unused]] const float4 two =
+            c < nr ? turns[warp][P * c + j] : float4{1.f, 0.f, 1.f, 0.f};
         co[j] = {two.x, two.z}, si[j] = {two.y, two.w};
       } else {
         const int m = P * va + j, n = P * vb + j;
-        const float2 f = m < R / 2 ? row[m] : float2{1.f, 0.f};
+        [[maybe_unused]] const float2 f = m < R / 2 ? row[m] : float2{1.f, 0.f};
         [[maybe_unused]] const float2 h = n < R / 2 ? row[n] : float2{1.f, 0.f};
         co[j] = {f.x, h.x}, si[j] = {f.y, h.y};
       }

@@ -86,7 +86,10 @@ def frequencies(R, base, stretch=None, factor=1.0, trained_len=0.0, fast=32.0, s
         if stretch == "bands":
             keep = np.clip((turns - slow) / (L(fast) - L(slow)), 0, 1)
             return keep * f + (1 - keep) * f / factor, 1.0
-        pair = lambda n: R * math.log(trained_len / (2 * math.pi * n)) / (2 * math.log(base))  # noqa: E731
+
+        def pair(n):
+            return R * math.log(trained_len / (2 * math.pi * n)) / (2 * math.log(base))
+
         lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
         late = np.clip((i - lo) / max(hi - lo, 1e-3), 0, 1)
         return (1 - late) * f + late * f / factor, 0.1 * math.log(factor) + 1
