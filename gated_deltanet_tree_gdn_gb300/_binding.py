@@ -878,14 +878,16 @@ _rope_cache: dict = {}
 
 
 def _rope_structs(strides, dims, interleaved, norm, rope_scale, eps, R):
-    """The structs of a call: HeadStrides, AttendDims and Rope."""
+    """The structs of a call, HeadStrides, AttendDims and Rope, kept by their values (which are
+    plain numbers here: a tensor would be known by its identity)."""
+    interleaved = bool(interleaved)
     key = (strides, dims, interleaved, norm, rope_scale, eps, R)
     known = _rope_cache.get(key)
     if known is None:
         if norm not in NORMS:
             raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
         known = (HeadStrides(*(Strides(*s[:2]) for s in strides)), AttendDims(*dims),
-                 Rope(R, int(bool(interleaved)), NORMS[norm], rope_scale, eps))
+                 Rope(R, interleaved, NORMS[norm], rope_scale, eps))
         if len(_rope_cache) >= 256:  # (a server's rows differ from call to call)
             _rope_cache.clear()
         _rope_cache[key] = known
@@ -923,7 +925,7 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
     rc = load().gdn_tree_positions(
         None if parent is None else _flat(parent, "parent", _i32, (rows,), dev), cu,
         None if context_len is None else _flat(context_len, "context_len", _i32, (B,), dev),
-        prefix_len, _flat(positions, "positions", _i32, (rows,), dev), B, rows, N_max,
+        int(prefix_len), _flat(positions, "positions", _i32, (rows,), dev), B, rows, int(N_max),
         None if dev_status is None else _flat(dev_status, "dev_status", _i32, (B,), dev),
         _stream_of(dev))
     if rc != OK:
@@ -1010,7 +1012,7 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
         pp = _flat(positions, "positions", _i32, (T,), dev)
     strides, dims, rope = _rope_structs((qs, ks, _NO_STRIDES, qo, ko),
                                         (0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), interleaved, norm,
-                                        rope_scale, eps, R)
+                                        float(rope_scale), float(eps), R)
     rc = load().gdn_tree_norm_rope(qp, kp, pp, fp, wq, wk, qop, kop, strides, dims, rope,
                                    _stream_of(dev))
     if rc != OK:
@@ -1084,8 +1086,9 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
     if dev_status is not None:
         sp = _flat(dev_status, "dev_status", _i32, (B,), dev)
     strides, dims, rope = _rope_structs(
-        (qs, ks, vs, qo, ko, vo), (B, T, N_max, Hq, Hkv, D, code, page, n_pages, width, prefix_len),
-        interleaved, norm, rope_scale, eps, R)
+        (qs, ks, vs, qo, ko, vo),
+        (B, T, int(N_max), Hq, Hkv, D, code, page, n_pages, width, int(prefix_len)), interleaved,
+        norm, float(rope_scale), float(eps), R)
     rc = load().gdn_tree_cache_append_rope(qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu, qop, kop,
                                            vop, kc, vc, table, ctx, nl, strides, dims, rope, sp,
                                            _stream_of(dev))

@@ -157,7 +157,8 @@ int check_rope(const gdn_tree_attend_dims& d, const gdn_tree_rope& r, const uint
   if (r.norm != GDN_TREE_NORM_NONE && !(r.eps >= 0.f && r.eps <= 3e38f)) return GDN_TREE_EINVAL;
   if (r.norm == GDN_TREE_NORM_NONE && (q_weight || k_weight)) return GDN_TREE_EINVAL;
   if (r.rotary_dim > 0 && freq == nullptr) return GDN_TREE_EINVAL;
-  if (!aligned16(freq) || !aligned16(q_weight) || !aligned16(k_weight)) return GDN_TREE_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(freq) & 7u) || !aligned16(q_weight) || !aligned16(k_weight))
+    return GDN_TREE_EINVAL;
   return GDN_TREE_OK;
 }
 

@@ -483,12 +483,13 @@ typedef struct {
  *                own input (same pointer, same strides); any other overlap of an output with
  *                an array of the call is refused.
  *   positions    [T] int32, any value (NULL where rotary_dim is 0)
- *   freq         [rotary_dim / 2] uint64, device (NULL where rotary_dim is 0)
+ *   freq         [rotary_dim / 2] uint64, device, 8-byte aligned (NULL where rotary_dim is 0)
  *   q_weight, k_weight  [D] fp32 or NULL; NULL where there is no norm
  *   dims         T, Hq, Hkv, D, dtype; the others are ignored.  D: 16, 32, ..., 128; Hq and
  *                Hkv need not be multiples of one another.
- * Sums, norms and rotations are fp32 and rounded once, to the output's type.  (Squares past
- * the range of fp32, of elements past 1e19, overflow: the row's norm is then infinite.)
+ * Sums, norms and rotations are fp32 and rounded once, to the output's type.  (So are the
+ * squares: elements past 1e19 make a head's norm infinite and the head 0; with an eps of 0, a
+ * head whose elements are all below 1e-19 has no norm, as has one of zeros.)
  */
 int gdn_tree_norm_rope(const void *q, const void *k, const int32_t *positions,
                        const uint64_t *freq, const float *q_weight, const float *k_weight,

@@ -88,7 +88,7 @@ def test_pointers(lib):
         assert call(lib, q=P(0, 8)) == gt.EINVAL               # 8-byte aligned only
         assert call(lib, k=P(1, 2)) == gt.EINVAL
         assert call(lib, freq=None) == gt.EINVAL               # a rotation without frequencies
-        assert call(lib, freq=P(3, 8)) == gt.EINVAL
+        assert call(lib, freq=P(3, 4)) == gt.EINVAL
     assert norm_rope(lib, qo=None) == gt.EINVAL
     assert norm_rope(lib, ko=None) == gt.EINVAL
     assert norm_rope(lib, pos=None) == gt.EINVAL

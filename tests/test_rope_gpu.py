@@ -251,6 +251,34 @@ def test_large_and_tiny_elements():
     check(q, want(x, "q", False, eps=0.25), "f32")
 
 
+@pytest.mark.parametrize("norm", ["rms", "unit"])
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 128, 64), ("bf16", 96, 10), ("f32", 32, 0)])
+def test_weights_of_one_of_the_two(norm, dtype, D, R):
+    """Weights scale either norm, and may be given for queries or keys alone."""
+    for missing in ("wq", "wk", None):
+        x = inputs(40, 5, 3, D, R, dtype, "fused", seed=23, norm="rms")
+        x["norm"] = norm
+        if missing:
+            x[missing] = None
+        q, k = run(x, False)
+        check(q, want(x, "q", False), dtype)
+        check(k, want(x, "k", False), dtype)
+
+
+def test_values_of_a_call_are_read_when_it_is_made():
+    """Sizes and scales given as tensors count with the value that they have at the call."""
+    x = append_inputs([3, 5], [2, 0], 2, 1, 64, 64, 16, "f32", "dense", "rms", seed=24)
+    scale, most = torch.tensor(1.0), torch.tensor(5)
+    first, _ = run_append(x, False, rope_scale=scale, N_max=most)
+    scale.fill_(2.0)
+    second, _ = run_append(x, False, rope_scale=scale, N_max=most)
+    assert torch.allclose(second, 2 * first)
+    status = torch.empty(2, dtype=torch.int32, device="cuda")
+    most.fill_(4)
+    run_append(x, False, N_max=most, dev_status=status)
+    assert status.tolist() == [0, gt.STATUS_BAD_LAYOUT]
+
+
 def test_refused_on_the_gpu():
     x = inputs(6, 4, 2, 64, 64, "bf16", "dense", seed=10, norm="rms")
     with pytest.raises(ValueError, match="contiguous"):
@@ -366,6 +394,25 @@ def test_append_beside_the_rows_and_behind_the_last():
     assert torch.equal(y["k_cache"], x["k_cache"]) and torch.equal(y["v_cache"], x["v_cache"])
     for n, o in zip("qkv", out):
         assert torch.equal(y[n][:38], o[:38]) and torch.equal(y[n][38:], x[n][38:])
+
+
+def test_append_at_the_farthest_positions():
+    """Positions past 2^31: a prefix of the largest length, and the rows behind it."""
+    x = append_inputs([40, 3], [5000, 100], 2, 1, 64, 64, 16, "f32", "dense", None, seed=25,
+                      prefix=2 ** 31 - 4097)
+    x["freq"], x["scale"] = gt.rope_frequencies(64, 1e6)
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    q, new_len = run_append(x, True)
+    check_append(x, True, before, q, new_len)
+
+
+def test_append_with_one_of_the_outputs():
+    x = append_inputs([9, 4], [3, 20], 2, 2, 64, 64, 8, "bf16", "fused", "rms", seed=26)
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    k_out, v_out = (torch.empty(13, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, n = run_append(x, False, k_out=k_out)
+    run_append(x, False, v_out=v_out)
+    check_append(x, False, before, q, n, k_out, v_out)
 
 
 def test_append_is_norm_rope_and_cache_append():
