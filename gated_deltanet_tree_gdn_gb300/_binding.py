@@ -841,12 +841,11 @@ def _check_device(t, name, dev):
 
 def _device(t, name):
     """The current device, which t is on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = _current_device()
-    _check_device(t, name, dev)
+    if dev != _current_device():
+        raise ValueError(f"{name} is on another device than the current one")
     return dev
 
 

@@ -247,6 +247,7 @@ struct RopeArgs {
 };
 cudaError_t launch_norm_rope(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_append_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_f32(const RopeArgs& a, bool append, cudaStream_t stream);
 
 // positions of tree nodes or of chains
 struct PositionArgs {
