@@ -809,8 +809,10 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
 # in front of the attention: positions, norms and rotation
 # ---------------------------------------------------------------------------
 
-# (These take 4 to 18 tensors ahead of a launch of 2 microseconds: a tensor is looked at once, and
-# what the call needs of the shapes is made once for each set of them.)
+# (These take 4 to 18 tensors ahead of a launch of 2 microseconds.  So that a call costs little
+# where nothing is wrong, its tensors are looked at in one expression, each property read once;
+# where that finds a fault, or what it does not know, they are checked one by one, which says what
+# is wrong.  What the call needs of the shapes is made once for each set of them.)
 
 _i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
 # (asked only where there is a CUDA tensor: the runtime is up then)
@@ -821,22 +823,37 @@ def _stream_of(dev) -> int:
     return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
-def _flat(t, name, dtype, shape, dev):
-    """The address of a dense tensor of this type and shape on the current device."""
-    try:
-        if (t.get_device() == dev and t.dtype is dtype and t.shape == shape
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except AttributeError:  # (no tensor)
-        pass
-    _check(t, name, dtype, shape)
-    _check_device(t, name, dev)
-    return t.data_ptr()
-
-
 def _check_device(t, name, dev):
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device than the current one")
+
+
+def _check_flat(dev, *tensors):
+    """Dense tensors (tensor or None, name, type, shape) on the current device."""
+    for t, name, dtype, shape in tensors:
+        if t is not None:
+            _check(t, name, dtype, shape)
+            _check_device(t, name, dev)
+
+
+def _check_heads(dev, dtype, T, D, *tensors):
+    """Arrays of heads [T,H,D] (tensor or None, name, the tensor whose shape it has or None) whose
+    heads are contiguous."""
+    for t, name, like in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        H = t.shape[1] if like is None and t.dim() > 1 else "H" if like is None else like.shape[1]
+        if t.shape != (T, H, D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
+        if t.stride(2) != 1 and t.numel():
+            raise ValueError(f"{name}'s heads must be contiguous")
+        _check_device(t, name, dev)
 
 
 def _device(t, name):
@@ -847,29 +864,6 @@ def _device(t, name):
     if dev != _current_device():
         raise ValueError(f"{name} is on another device than the current one")
     return dev
-
-
-def _heads(t, name, dtype, shape, dev):
-    """The strides of an array of heads [T, H, D] whose heads are contiguous."""
-    try:
-        if t.get_device() == dev and t.dtype is dtype and t.shape == shape:
-            strides = t.stride()
-            if strides[2] == 1:
-                return strides
-    except AttributeError:  # (no tensor)
-        pass
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(2) != 1 and t.numel():
-        raise ValueError(f"{name}'s heads must be contiguous")
-    _check_device(t, name, dev)
-    return t.stride()
 
 
 _NO_STRIDES = (0, 0, 0)
@@ -906,7 +900,6 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
         return _on(stream, tree_positions, locals())
     dev = _device(cu_nodes, "cu_nodes")
     B = cu_nodes.shape[0] - 1
-    cu = _flat(cu_nodes, "cu_nodes", _i32, (B + 1,), dev)
     if parent is not None:
         rows = parent.shape[0]
     elif positions is not None:
@@ -917,16 +910,33 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
         raise ValueError("without parent, T or positions says how many rows there are")
     if T is not None and T != rows:
         raise ValueError(f"T is {T}, but there are {rows} rows")
-    if N_max is None:
-        N_max = _most_rows(cu_nodes)
     if positions is None:
         positions = torch.empty((rows,), dtype=torch.int32, device=cu_nodes.device)
+    try:
+        good = (cu_nodes.dtype is _i32 and cu_nodes.is_contiguous() and cu_nodes.dim() == 1
+                and positions.shape == (rows,) and positions.dtype is _i32
+                and positions.is_contiguous() and positions.get_device() == dev
+                and (parent is None or parent.dtype is _i32 and parent.is_contiguous()
+                     and parent.dim() == 1 and parent.get_device() == dev)
+                and (context_len is None or context_len.shape == (B,) and context_len.dtype is _i32
+                     and context_len.is_contiguous() and context_len.get_device() == dev)
+                and (dev_status is None or dev_status.shape == (B,) and dev_status.dtype is _i32
+                     and dev_status.is_contiguous() and dev_status.get_device() == dev))
+    except AttributeError:  # (no tensor)
+        good = False
+    if not good:
+        _check_flat(dev, (cu_nodes, "cu_nodes", torch.int32, (B + 1,)),
+                    (parent, "parent", torch.int32, (rows,)),
+                    (context_len, "context_len", torch.int32, (B,)),
+                    (positions, "positions", torch.int32, (rows,)),
+                    (dev_status, "dev_status", torch.int32, (B,)))
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
     rc = load().gdn_tree_positions(
-        None if parent is None else _flat(parent, "parent", _i32, (rows,), dev), cu,
-        None if context_len is None else _flat(context_len, "context_len", _i32, (B,), dev),
-        int(prefix_len), _flat(positions, "positions", _i32, (rows,), dev), B, rows, int(N_max),
-        None if dev_status is None else _flat(dev_status, "dev_status", _i32, (B,), dev),
-        _stream_of(dev))
+        None if parent is None else parent.data_ptr(), cu_nodes.data_ptr(),
+        None if context_len is None else context_len.data_ptr(), int(prefix_len),
+        positions.data_ptr(), B, rows, int(N_max),
+        None if dev_status is None else dev_status.data_ptr(), _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_positions")
     return positions
@@ -980,35 +990,53 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
     Hq = Hkv = R = 0
     qs = ks = qo = ko = _NO_STRIDES
     qp = kp = qop = kop = pp = fp = wq = wk = None
-    if q is not None:
-        shape = q.shape
-        Hq = shape[1]
-        qs = _heads(q, "q", dt, (T, Hq, D), dev)
-        if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=q.device)
-        qo = _heads(q_out, "q_out", dt, shape, dev)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-        if q_weight is not None:
-            wq = _flat(q_weight, "q_weight", _f32, (D,), dev)
-    elif q_out is not None:
-        raise ValueError("q_out is given with q")
-    if k is not None:
-        shape = k.shape
-        Hkv = shape[1]
-        ks = _heads(k, "k", dt, (T, Hkv, D), dev)
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=dt, device=k.device)
-        ko = _heads(k_out, "k_out", dt, shape, dev)
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-        if k_weight is not None:
-            wk = _flat(k_weight, "k_weight", _f32, (D,), dev)
-    elif k_out is not None:
-        raise ValueError("k_out is given with k")
-    if freq is not None:
-        half = freq.shape[0]
-        R = 2 * half
-        fp = _flat(freq, "freq", _i64, (half,), dev)
-        pp = _flat(positions, "positions", _i32, (T,), dev)
+    q_shape = k_shape = f_shape = None
+    good = True
+    try:
+        if q is not None:
+            q_shape = q.shape
+            if q_out is None:
+                q_out = torch.empty(q_shape, dtype=dt, device=q.device)
+            Hq, qs, qo = q_shape[1], q.stride(), q_out.stride()
+            good = (qs[2] == 1 and qo[2] == 1 and q_out.shape == q_shape and q_out.dtype is dt
+                    and q_out.get_device() == dev
+                    and (q_weight is None or q_weight.shape == (D,) and q_weight.dtype is _f32
+                         and q_weight.is_contiguous() and q_weight.get_device() == dev))
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+            wq = None if q_weight is None else q_weight.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out is given with q")
+        if k is not None:
+            k_shape = k.shape
+            if k_out is None:
+                k_out = torch.empty(k_shape, dtype=dt, device=k.device)
+            Hkv, ks, ko = k_shape[1], k.stride(), k_out.stride()
+            good = (good and k_shape == (T, Hkv, D) and k.dtype is dt and k.get_device() == dev
+                    and ks[2] == 1 and ko[2] == 1 and k_out.shape == k_shape
+                    and k_out.dtype is dt and k_out.get_device() == dev
+                    and (k_weight is None or k_weight.shape == (D,) and k_weight.dtype is _f32
+                         and k_weight.is_contiguous() and k_weight.get_device() == dev))
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+            wk = None if k_weight is None else k_weight.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out is given with k")
+        if freq is not None:
+            f_shape = freq.shape
+            R = 2 * f_shape[0]
+            good = (good and len(f_shape) == 1 and freq.dtype is _i64 and freq.is_contiguous()
+                    and freq.get_device() == dev and positions.shape == (T,)
+                    and positions.dtype is _i32 and positions.is_contiguous()
+                    and positions.get_device() == dev)
+            fp, pp = freq.data_ptr(), positions.data_ptr()
+    except (AttributeError, IndexError):  # (no tensor, or too few dimensions)
+        good = False
+    if not good:
+        _check_heads(dev, dt, T, D, (q, "q", None), (q_out, "q_out", q), (k, "k", None),
+                     (k_out, "k_out", k))
+        _check_flat(dev, (q_weight if q is not None else None, "q_weight", torch.float32, (D,)),
+                    (k_weight if k is not None else None, "k_weight", torch.float32, (D,)),
+                    (freq, "freq", torch.int64, (R // 2,)),
+                    (positions, "positions", torch.int32, (T,)))
     strides, dims, rope = _rope_structs((qs, ks, _NO_STRIDES, qo, ko),
                                         (0, T, 0, Hq, Hkv, D, code, 1, 0, 0, 0), interleaved, norm,
                                         float(rope_scale), float(eps), R)
@@ -1041,56 +1069,93 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
     dt = k.dtype
     code = _dtype_code(k)
     dev = _device(k, "k")
-    Hq = R = 0
-    qs = qo = ko = vo = _NO_STRIDES
-    qp = qop = kop = vop = fp = wq = wk = sp = None
-    ks = _heads(k, "k", dt, shape, dev)
-    vs = _heads(v, "v", dt, shape, dev)
-    if q is not None:
-        Hq = q.shape[1]
-        qs = _heads(q, "q", dt, (T, Hq, D), dev)
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=k.device)
-        qo = _heads(q_out, "q_out", dt, (T, Hq, D), dev)
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-        if q_weight is not None:
-            wq = _flat(q_weight, "q_weight", _f32, (D,), dev)
-    elif q_out is not None:
-        raise ValueError("q_out is given with q")
-    if k_out is not None:
-        ko = _heads(k_out, "k_out", dt, shape, dev)
-        kop = k_out.data_ptr()
-    if v_out is not None:
-        vo = _heads(v_out, "v_out", dt, shape, dev)
-        vop = v_out.data_ptr()
-    if k_weight is not None:
-        wk = _flat(k_weight, "k_weight", _f32, (D,), dev)
-    if freq is not None:
-        half = freq.shape[0]
-        R = 2 * half
-        fp = _flat(freq, "freq", _i64, (half,), dev)
-    cu = _flat(cu_nodes, "cu_nodes", _i32, (B + 1,), dev)
-    n_pages, page = k_cache.shape[:2]
-    cache = (n_pages, page, Hkv, D)
-    kc = _flat(k_cache, "k_cache", dt, cache, dev)
-    vc = _flat(v_cache, "v_cache", dt, cache, dev)
+    cache = k_cache.shape
+    n_pages, page = cache[:2]
     width = page_table.shape[1]
-    table = _flat(page_table, "page_table", _i32, (B, width), dev)
-    ctx = _flat(context_len, "context_len", _i32, (B,), dev)
-    if N_max is None:
-        N_max = _most_rows(cu_nodes)
     if new_len is None:
         new_len = torch.empty((B,), dtype=torch.int32, device=k.device)
-    nl = _flat(new_len, "new_len", _i32, (B,), dev)
-    if dev_status is not None:
-        sp = _flat(dev_status, "dev_status", _i32, (B,), dev)
+    Hq = R = 0
+    ks = vs = _NO_STRIDES
+    qs = qo = ko = vo = _NO_STRIDES
+    qp = qop = kop = vop = fp = wq = wk = sp = None
+    try:
+        ks, vs = k.stride(), v.stride()
+        good = (ks[2] == 1 and vs[2] == 1 and v.shape == shape and v.dtype is dt
+                and v.get_device() == dev and cu_nodes.dim() == 1 and cu_nodes.dtype is _i32
+                and cu_nodes.is_contiguous() and cu_nodes.get_device() == dev
+                and cache == (n_pages, page, Hkv, D) and k_cache.dtype is dt
+                and k_cache.is_contiguous() and k_cache.get_device() == dev
+                and v_cache.shape == cache and v_cache.dtype is dt and v_cache.is_contiguous()
+                and v_cache.get_device() == dev
+                and page_table.shape == (B, width) and page_table.dtype is _i32
+                and page_table.is_contiguous() and page_table.get_device() == dev
+                and context_len.shape == (B,) and context_len.dtype is _i32
+                and context_len.is_contiguous() and context_len.get_device() == dev
+                and new_len.shape == (B,) and new_len.dtype is _i32 and new_len.is_contiguous()
+                and new_len.get_device() == dev)
+        if q is not None:
+            q_shape = q.shape
+            if q_out is None:
+                q_out = torch.empty(q_shape, dtype=dt, device=k.device)
+            Hq, qs, qo = q_shape[1], q.stride(), q_out.stride()
+            good = (good and q_shape == (T, Hq, D) and q.dtype is dt and q.get_device() == dev
+                    and qs[2] == 1 and qo[2] == 1 and q_out.shape == q_shape
+                    and q_out.dtype is dt and q_out.get_device() == dev
+                    and (q_weight is None or q_weight.shape == (D,) and q_weight.dtype is _f32
+                         and q_weight.is_contiguous() and q_weight.get_device() == dev))
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+            wq = None if q_weight is None else q_weight.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out is given with q")
+        if k_out is not None:
+            ko = k_out.stride()
+            good = (good and ko[2] == 1 and k_out.shape == shape and k_out.dtype is dt
+                    and k_out.get_device() == dev)
+            kop = k_out.data_ptr()
+        if v_out is not None:
+            vo = v_out.stride()
+            good = (good and vo[2] == 1 and v_out.shape == shape and v_out.dtype is dt
+                    and v_out.get_device() == dev)
+            vop = v_out.data_ptr()
+        if k_weight is not None:
+            good = (good and k_weight.shape == (D,) and k_weight.dtype is _f32
+                    and k_weight.is_contiguous() and k_weight.get_device() == dev)
+            wk = k_weight.data_ptr()
+        if freq is not None:
+            f_shape = freq.shape
+            R = 2 * f_shape[0]
+            good = (good and len(f_shape) == 1 and freq.dtype is _i64 and freq.is_contiguous()
+                    and freq.get_device() == dev)
+            fp = freq.data_ptr()
+        if dev_status is not None:
+            good = (good and dev_status.shape == (B,) and dev_status.dtype is _i32
+                    and dev_status.is_contiguous() and dev_status.get_device() == dev)
+            sp = dev_status.data_ptr()
+    except (AttributeError, IndexError):  # (no tensor, or too few dimensions)
+        good = False
+    if not good:
+        _check_heads(dev, dt, T, D, (q, "q", None), (q_out, "q_out", q), (k, "k", None),
+                     (v, "v", k), (k_out, "k_out", k), (v_out, "v_out", k))
+        _check_cache(k_cache, v_cache, page_table, context_len, B, Hkv, D, dt)
+        _check_flat(dev, (cu_nodes, "cu_nodes", torch.int32, (B + 1,)),
+                    (k_cache, "k_cache", dt, cache), (v_cache, "v_cache", dt, cache),
+                    (page_table, "page_table", torch.int32, (B, width)),
+                    (context_len, "context_len", torch.int32, (B,)),
+                    (new_len, "new_len", torch.int32, (B,)),
+                    (dev_status, "dev_status", torch.int32, (B,)),
+                    (q_weight if q is not None else None, "q_weight", torch.float32, (D,)),
+                    (k_weight, "k_weight", torch.float32, (D,)),
+                    (freq, "freq", torch.int64, (R // 2,)))
+    if N_max is None:
+        N_max = _most_rows(cu_nodes)
     strides, dims, rope = _rope_structs(
         (qs, ks, vs, qo, ko, vo),
         (B, T, int(N_max), Hq, Hkv, D, code, page, n_pages, width, int(prefix_len)), interleaved,
         norm, float(rope_scale), float(eps), R)
-    rc = load().gdn_tree_cache_append_rope(qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu, qop, kop,
-                                           vop, kc, vc, table, ctx, nl, strides, dims, rope, sp,
-                                           _stream_of(dev))
+    rc = load().gdn_tree_cache_append_rope(
+        qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu_nodes.data_ptr(), qop, kop, vop,
+        k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), context_len.data_ptr(),
+        new_len.data_ptr(), strides, dims, rope, sp, _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_cache_append_rope")
     return q_out, new_len

@@ -293,6 +293,24 @@ def test_refused_on_the_gpu():
         run(dict(x, k=x["k"].float()), False)
     with pytest.raises(ValueError, match="norm"):
         run(x, False, norm="l1")
+    for kw in (dict(q_out=x["q"].flatten(1)), dict(q_out=x["q"][..., None]),
+               dict(k_out=x["k"].flatten(1)), dict(q_weight=x["wq"][None])):
+        with pytest.raises(ValueError, match="shape"):
+            run(x, False, **kw)
+    for kw in (dict(q_out=5), dict(k_weight=[1.0] * 64), dict(q_weight=np.ones(64))):
+        with pytest.raises(TypeError, match="torch.Tensor"):
+            run(x, False, **kw)
+    pos = ints(x["positions"])
+    for p, f, what in ((pos[:5], x["freq"], ValueError), (pos.long(), x["freq"], TypeError),
+                       (pos, x["freq"].int(), TypeError), (pos, x["freq"][None], ValueError),
+                       (pos, x["freq"][0], ValueError), (pos.cpu(), x["freq"], ValueError),
+                       (x["positions"], x["freq"], TypeError), (pos, [1, 2], TypeError),
+                       (torch.stack([pos, pos], 1)[:, 0], x["freq"], ValueError)):
+        with pytest.raises(what):
+            gt.norm_rope(x["q"], x["k"], p, f)
+    for k in (x["k"][:5], x["k"][..., :32], x["k"][..., None], x["k"].cpu()):
+        with pytest.raises(ValueError):
+            gt.norm_rope(x["q"], k, pos, x["freq"])
     one_row = torch.empty(1, 4, 64, dtype=torch.bfloat16, device="cuda").expand(6, 4, 64)
     for kw in (dict(q_out=one_row), dict(norm=None), dict(k_out=x["q"][:, 1:3])):
         with pytest.raises(gt.GdnTreeError) as e:
@@ -465,6 +483,31 @@ def test_append_bad_device_data_is_reported():
         bad = [not (0 <= a <= b <= 120 and b - a <= 30) for a, b in zip(cu, cu[1:])]
         assert [s == L for s in status.tolist()] == bad
         assert [int(v) for v in n] == [10 if w else 10 + b - a for a, b, w in zip(cu, cu[1:], bad)]
+
+
+def test_append_refused_on_the_gpu():
+    """Each argument of a wrong type, shape, layout or place is named; nothing is written."""
+    x = append_inputs([6, 3], [10, 0], 4, 2, 64, 64, 16, "bf16", "dense", "rms", seed=27)
+    good = dict(q=x["q"], k=x["k"], v=x["v"], cu_nodes=ints(x["cu"]), k_cache=x["k_cache"],
+                v_cache=x["v_cache"], page_table=ints(x["table"]), context_len=ints(x["ctx"]),
+                freq=x["freq"], norm="rms", q_weight=x["wq"], k_weight=x["wk"],
+                q_out=torch.empty_like(x["q"]), k_out=torch.empty_like(x["k"]),
+                v_out=torch.empty_like(x["v"]), new_len=ints([0, 0]), dev_status=ints([0, 0]), N_max=6)
+    gt.cache_append_rope(**good)
+    before = {n: t.clone() for n, t in good.items() if isinstance(t, torch.Tensor)}
+    for name, t in before.items():
+        names = [name]
+        bad = [t.cpu(), t[..., None] if name != "k" else t[:, :1], t.double(), "text"]
+        if t.dim() > 1 and name not in ("k", "v", "q", "k_out", "v_out", "q_out"):
+            bad.append(torch.stack([t, t], -1)[..., 0])
+        for b in bad:
+            if name == "k" and isinstance(b, str):
+                continue
+            with pytest.raises((TypeError, ValueError, AttributeError)) as e:
+                gt.cache_append_rope(**dict(good, **{name: b}))
+            if name not in ("k", "cu_nodes", "k_cache", "page_table") or not isinstance(b, str):
+                assert any(n in str(e.value) for n in names + (["v"] if name == "k" else [])), (name, b)
+    assert all(torch.equal(t, before[n]) for n, t in good.items() if n in before)
 
 
 def test_append_past_the_table():
