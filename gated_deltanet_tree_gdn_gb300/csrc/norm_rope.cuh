@@ -14,18 +14,18 @@
 //
 // Measured on one GB300, calls in a CUDA graph over inputs that do not fit the L2 (a plain copy
 // kernel over as many bytes in brackets): 32768 rows of 32 + 8 heads of 128 in bf16, every second
-// 128 elements read, 105 us, 6.4 TB/s (99); 16384 rows of 16 + 16 heads made unit vectors 43.8
-// (41.5); 8191 rows of 16 + 16 heads rotated 23.4 (22); 4096 rows of 32 + 8 heads 17.2 (14.2: they
+// 128 elements read, 104 us, 6.5 TB/s (99); 16384 rows of 16 + 16 heads made unit vectors 43.7
+// (41.5); 8191 rows of 16 + 16 heads rotated 22.9 (22); 4096 rows of 32 + 8 heads 16.3 (14.2: they
 // are one round of the SMs, so that every warp's way from its first load to its last store counts);
-// 16 prompts of 17 to 4096 rows into the cache and beside it 85.5, 6.1 TB/s; one row 2.4, into the
-// cache 3.4.
+// 16 prompts of 17 to 4096 rows into the cache and beside it 84, 6.2 TB/s; one row 2.1, into the
+// cache 2.6.
 //
 // What that took, on the 32768 rows: vectors by plain loads, one or two passes ahead in registers,
 // 130 to 149 us (loads in flight then cost registers, and with them warps); by cp.async, three
 // passes ahead, 120; a lane's weights in registers and not from L1 in every pass, 106; fewer
-// instructions (packed fp32 arithmetic; addresses by steps; lanes a head known to the compiler)
-// 105, and more where heads are small: 16384 rows of 32 + 8 heads of 80 elements 56 to 41 us, of 64
-// 32.5 to 28.2.
+// instructions (packed fp32 arithmetic; addresses by steps; lanes a head known to the compiler) and
+// frequencies read before the position is there 104, and more where heads are small: 16384 rows of
+// 32 + 8 heads of 80 elements 56 to 38 us, of 64 32.5 to 27.5.
 #pragma once
 
 #include <algorithm>
@@ -41,7 +41,7 @@ namespace {
 constexpr int kWarps = 4, kStages = 4;
 
 // How the pairs of a rotation lie in a lane's two vectors of E elements, number va and vb of the
-// head's D / E (16384 rows of 32 + 8 heads of 128 in bf16: 54 us, 54, and 58 to 78):
+// head's D / E (16384 rows of 32 + 8 heads of 128 in bf16: 53 us, 53, and 54 to 77):
 //   kNeighbours  elements 2 i and 2 i + 1 are in the same vector
 //   kHalves      R a multiple of 2 E (0 included): vb = va + R / 2 E holds va's partners
 //   kCrossed     elements i and i + R / 2 for any other R: rotated in the ring, two pairs a lane
@@ -175,10 +175,9 @@ struct Walk {
   __device__ __forceinline__ bool on() const { return h < of; }
 };
 
-// CTAs an SM: as many as the registers allow without spills
-constexpr int ctas(Pairs pairs, bool append) {
-  return pairs == kCrossed ? (append ? 4 : 5) : append ? 5 : 7;
-}
+// CTAs an SM that the registers are to allow: 7 for rows alone (4096 rows 16.1 us, of 8 16.5, of 5
+// 17.6); 4 for rows for the cache, whose walks want more (2048 tokens 12.3 us, of 5 13.6, of 6 13.9)
+constexpr int ctas(Pairs pairs, bool append) { return append ? 4 : pairs == kCrossed ? 5 : 7; }
 
 template <typename T, int kLanes, Pairs kPairs, bool kAppend>
 __global__ void __launch_bounds__(32 * kWarps, ctas(kPairs, kAppend))
@@ -190,22 +189,14 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   constexpr int D = 2 * E * kLanes;
   const int Hq = a.d.Hq, Hkv = a.d.Hkv, R = a.rope.rotary_dim;
-  if (kAppend) {
-    const int b = blockIdx.x * (32 * kWarps) + threadIdx.x;
-    if (b < a.d.B) {
-      const int first = a.cu[b], stop = a.cu[b + 1], ctx = a.context_len[b];
-      const bool ok = in_range(a.d, first, stop, ctx);
-      if (a.new_len) a.new_len[b] = ok ? (int)((unsigned)ctx + (unsigned)(stop - first)) : ctx;
-      if (!ok && a.dev_status) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
-    }
-  }
   int t = blockIdx.x * kWarps + warp, i0 = 0;
   if (plan.splits > 1) {
     const int unit = t;
     t = unit / plan.splits;
     i0 = (unit - t * plan.splits) * plan.per;
   }
-  if (t >= a.d.T) return;
+  const bool any = t < a.d.T;
+  if (!kAppend && !any) return;
   // (where kLanes does not divide 32, the lanes behind the last whole head have none)
   constexpr int each = 32 / kLanes;
   const int g = lane / kLanes, c = lane % kLanes;
@@ -235,7 +226,7 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   const uint32_t ring_a = smem_u32(&ring[warp][0][slot_a]);
   const uint32_t ring_b = smem_u32(&ring[warp][0][slot_b]);
   Walk in = walk(i0, a.q, a.k, a.v, a.s.q, a.s.k, a.s.v);
-  int coming = i0;  // the pass that is copied next
+  int coming = any ? i0 : i1;  // the pass that is copied next
   uint32_t stage_in = 0;
   const auto fetch = [&] {
     if (coming < i1) {
@@ -267,11 +258,30 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   };
   load_weights(i0 < k0 ? a.q_weight : a.k_weight);
 
-  // the row's position, and its place in the cache (-1: none)
-  long long p = 0, place = -1;
+  // the frequencies of the pairs that this lane makes the cosines and sines of: of kCrossed, where
+  // `wide` lanes take a head, its own pairs m0 and m1 (neighbours where R / 2 is even, so that they
+  // are read and written together), else two of the row's
+  const bool even = R % 4 == 0;
+  const int need = even ? R / 4 : R / 2, wide = need > 16 ? 32 : need > 8 ? 16 : 8;
+  const int m0 = kPairs == kCrossed ? (lane & (wide - 1)) << even : lane;
+  const int m1 = kPairs == kCrossed && even ? m0 + 1 : m0 + 32;
+  const uint64_t f0 = m0 < R / 2 ? a.freq[m0] : 0, f1 = m1 < R / 2 ? a.freq[m1] : 0;
+
+  // The row's position, and its page and row there (-1: none).  (What is read here depends on one
+  // another; everything above is on its way meanwhile.)
+  long long p = 0;
+  int b = -1, page = -1, page_row = 0;
   if (kAppend) {
+    const int mine = blockIdx.x * (32 * kWarps) + threadIdx.x;  // a sequence to be looked at
+    if (mine < a.d.B) {
+      const int first = a.cu[mine], stop = a.cu[mine + 1], ctx = a.context_len[mine];
+      const bool ok = in_range(a.d, first, stop, ctx);
+      if (a.new_len) a.new_len[mine] = ok ? (int)((unsigned)ctx + (unsigned)(stop - first)) : ctx;
+      if (!ok && a.dev_status) atomicMax(a.dev_status + mine, GDN_TREE_STATUS_BAD_LAYOUT);
+    }
+    if (!any) return;  // (nothing was copied)
     int ctx;
-    const int b = sequence_of(a.cu, a.context_len, a.d.B, t, lane, &ctx);
+    b = sequence_of(a.cu, a.context_len, a.d.B, t, lane, &ctx);
     const bool some = b >= 0 && b < a.d.B;
     const int first = some ? a.cu[b] : 0, stop = some ? a.cu[b + 1] : 0;
     if (!some || !in_range(a.d, first, stop, ctx) || t < first || t >= stop) {
@@ -280,37 +290,27 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
     }
     const long long at = (long long)ctx + (t - first);
     p = a.d.prefix_len + at;
-    if (i1 > k0) {
-      if (at < (long long)a.d.table_width * a.d.page_size) {
-        // (at fits 32 bits here)
-        const unsigned entry = (unsigned)at / (unsigned)a.d.page_size;
-        const int page = a.page_table[(size_t)b * a.d.table_width + entry];
-        if (page >= 0 && page < a.d.n_pages)
-          place = (long long)page * a.d.page_size + ((unsigned)at - entry * a.d.page_size);
-      }
-      if (place < 0 && a.dev_status && lane == 0)
-        atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+    if (i1 > k0 && at < (long long)a.d.table_width * a.d.page_size) {
+      // (at fits 32 bits here)
+      const unsigned entry = (unsigned)at / (unsigned)a.d.page_size;
+      page = a.page_table[(size_t)b * a.d.table_width + entry];
+      page_row = (int)((unsigned)at - entry * a.d.page_size);
     }
   } else if (R > 0) {
     p = a.positions[t];
   }
 
-  // The row's cosines and sines, each made by one lane; then those of this lane's pairs: of
-  // kNeighbours, pairs j of both vectors; of kCrossed, where `wide` lanes take a head, the two
-  // pairs m0 and m1: neighbours where R / 2 is even, so that they are read and written together.
+  // The row's cosines and sines, each made by one lane; then those of this lane's pairs (of
+  // kNeighbours, pairs j of both vectors).
   constexpr int kMine = kPairs == kCrossed ? 1 : P;
   float2 co[kMine], si[kMine];
-  const bool even = R % 4 == 0;
-  const int need = even ? R / 4 : R / 2, wide = need > 16 ? 32 : need > 8 ? 16 : 8;
-  const int m0 = (lane & (wide - 1)) << even, m1 = even ? m0 + 1 : m0 + 32;
   if constexpr (kPairs == kCrossed) {
-    const float2 none = {1.f, 0.f};
-    const float2 f = m0 < R / 2 ? turn(p, a.freq[m0], a.rope.scale) : none;
-    const float2 h = m1 < R / 2 ? turn(p, a.freq[m1], a.rope.scale) : none;
+    const float2 f = turn(p, f0, a.rope.scale), h = turn(p, f1, a.rope.scale);
     co[0] = {f.x, h.x}, si[0] = {f.y, h.y};
   } else if (R > 0) {
     float2* const row = reinterpret_cast<float2*>(turns[warp]);
-    for (int i = lane; i < R / 2; i += 32) row[i] = turn(p, a.freq[i], a.rope.scale);
+    if (m0 < R / 2) row[m0] = turn(p, f0, a.rope.scale);
+    if (m1 < R / 2) row[m1] = turn(p, f1, a.rope.scale);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -334,6 +334,13 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
     if (m1 < R / 2) w1.y = from[m1], w2.y = from[m1 + R / 2];
   };
   cross_weights(i0 < k0 ? a.q_weight : a.k_weight);
+
+  // the place in the cache (-1: none)
+  long long place = -1;
+  if (kAppend && i1 > k0) {
+    if (page >= 0 && page < a.d.n_pages) place = (long long)page * a.d.page_size + page_row;
+    else if (a.dev_status && lane == 0) atomicMax(a.dev_status + b, GDN_TREE_STATUS_BAD_LAYOUT);
+  }
 
   const float share = a.rope.norm == GDN_TREE_NORM_RMS ? 1.f / D : 1.f;
   // where a pass's heads go: an output's (at NULL: none), and the cache's
@@ -484,9 +491,10 @@ cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
   const int sms = sm_count();
   // Warps a row: one where the rows alone fill the SMs (what a warp makes once for its row is then
   // made once), more where they do not (a warp's passes follow one another).  Measured with 32 + 8
-  // heads of 128 in bf16, a warp a row against this rule: 1 row 6.5 and 2.5 us, 256 rows 6.8 and
-  // 3.9, 1024 rows 8.6 and 7.8; four warps a row at 4096 rows 22 us against 17.4.
-  const int want = 12 * sms;
+  // heads of 128 in bf16, a warp a row against this rule: 1 row 6.5 and 2.1 us, 256 rows 6.8 and
+  // 3.0, 1024 rows 8.6 and 6.7, 2048 rows 9.8 and 9.1; four warps a row at 4096 rows 22 us against
+  // 16.3.  Rows for the cache take longer to begin: 1024 tokens 10.9 us at 16 warps an SM, 8.9 at 12.
+  const int want = (kAppend ? 12 : 14) * sms;
   int splits = 1;
   if (a.d.T > 0 && a.d.T <= want) splits = std::min(passes, want / a.d.T + 1);
   plan.per = (passes + splits - 1) / splits;
