@@ -433,6 +433,29 @@ def test_append_with_one_of_the_outputs():
     check_append(x, False, before, q, n, k_out, v_out)
 
 
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1], [30, 0, 7]])
+@pytest.mark.parametrize("gated", [False, True])
+def test_append_in_place_on_a_projection(lens, gated):
+    """q, k and v are columns of the same rows (each query head followed by its gate, or not) and
+    are normalised and rotated where they lie; nothing beside them changes."""
+    ctx = [5 * b for b in range(len(lens))]
+    x = append_inputs(lens, ctx, 6, 2, 64, 32, 16, "bf16", "dense", "rms", seed=28, prefix=9)
+    r = np.random.default_rng(29)
+    wide = torch.tensor(r.standard_normal((x["T"], (6 * (1 + gated) + 2 * 2) * 64 + 16)),
+                        dtype=torch.bfloat16, device="cuda")
+    q, k, v, rest = wide.split([6 * (1 + gated) * 64, 128, 128, 16], dim=1)
+    q = q.unflatten(1, (6, -1))[..., :64]
+    k, v = k.unflatten(1, (2, 64)), v.unflatten(1, (2, 64))
+    x.update(q=q.clone(), k=k.clone(), v=v.clone())
+    was, before = wide.clone(), (x["k_cache"].clone(), x["v_cache"].clone())
+    a, n = run_append(dict(x, q=q, k=k, v=v), False, q_out=q, k_out=k, v_out=v)
+    assert a is q
+    check_append(x, False, before, q, n, k, v)
+    for t, old in ((q, x["q"]), (k, x["k"])):
+        t.copy_(old)
+    assert torch.equal(wide, was)
+
+
 def test_append_is_norm_rope_and_cache_append():
     x = append_inputs([50, 1, 0, 200], [10, 63, 5, 0], 8, 2, 128, 128, 64, "bf16", "dense", "rms",
                       seed=4, prefix=3000)
