@@ -815,6 +815,7 @@ def cache_append(k, v, cu_nodes, k_cache, v_cache, page_table, context_len, *, p
 # is wrong.  What the call needs of the shapes is made once for each set of them.)
 
 _i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
+_CODES = {torch.bfloat16: BF16, torch.float32: F32}
 # (asked only where there is a CUDA tensor: the runtime is up then)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -856,14 +857,10 @@ def _check_heads(dev, dtype, T, D, *tensors):
         _check_device(t, name, dev)
 
 
-def _device(t, name):
-    """The current device, which t is on."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != _current_device():
-        raise ValueError(f"{name} is on another device than the current one")
-    return dev
+def _refuse_device(t, name):
+    """Refuses t, which is not on the current device."""
+    raise ValueError(f"{name} must be a CUDA tensor" if t.get_device() < 0 else
+                     f"{name} is on another device than the current one")
 
 
 _NO_STRIDES = (0, 0, 0)
@@ -898,7 +895,9 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
     they are."""
     if stream is not None:
         return _on(stream, tree_positions, locals())
-    dev = _device(cu_nodes, "cu_nodes")
+    dev = cu_nodes.get_device()
+    if dev < 0 or dev != _current_device():
+        _refuse_device(cu_nodes, "cu_nodes")
     B = cu_nodes.shape[0] - 1
     if parent is not None:
         rows = parent.shape[0]
@@ -985,8 +984,12 @@ def norm_rope(q, k=None, positions=None, freq=None, *, interleaved=False, rope_s
         raise ValueError("positions and freq are given together or not at all")
     T, _, D = x.shape
     dt = x.dtype
-    code = _dtype_code(x)
-    dev = _device(x, "q" if x is q else "k")
+    code = _CODES.get(dt)
+    if code is None:
+        _dtype_code(x)
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        _refuse_device(x, "q" if x is q else "k")
     Hq = Hkv = R = 0
     qs = ks = qo = ko = _NO_STRIDES
     qp = kp = qop = kop = pp = fp = wq = wk = None
@@ -1067,8 +1070,12 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
     T, Hkv, D = shape
     B = cu_nodes.shape[0] - 1
     dt = k.dtype
-    code = _dtype_code(k)
-    dev = _device(k, "k")
+    code = _CODES.get(dt)
+    if code is None:
+        _dtype_code(k)
+    dev = k.get_device()
+    if dev < 0 or dev != _current_device():
+        _refuse_device(k, "k")
     cache = k_cache.shape
     n_pages, page = cache[:2]
     width = page_table.shape[1]

@@ -488,8 +488,8 @@ typedef struct {
  *   dims         T, Hq, Hkv, D, dtype; the others are ignored.  D: 16, 32, ..., 128; Hq and
  *                Hkv need not be multiples of one another.
  * Sums, norms and rotations are fp32 and rounded once, to the output's type.  (So are the
- * squares: elements past 1e19 make a head's norm infinite and the head 0; with an eps of 0, a
- * head whose elements are all below 1e-19 has no norm, as has one of zeros.)
+ * squares: a head whose squares sum to more than fp32 holds, 3.4e38, becomes 0; with an eps of 0,
+ * a head whose elements are all below 1e-19 has no norm, as has one of zeros.)
  */
 int gdn_tree_norm_rope(const void *q, const void *k, const int32_t *positions,
                        const uint64_t *freq, const float *q_weight, const float *k_weight,

@@ -304,7 +304,7 @@ def test_everything_of_a_call_is_on_its_stream(monkeypatch, name, given):
     monkeypatch.setattr(torch.cuda, "stream", under)
     monkeypatch.setattr(_binding, "_check", lambda *a: None)
     monkeypatch.setattr(_binding, "_check_device", lambda *a: None)
-    monkeypatch.setattr(_binding, "_device", lambda *a: 0)
+    monkeypatch.setattr(_binding, "_refuse_device", lambda *a: None)
     monkeypatch.setattr(_binding, "_check_heads", lambda *a: None)
     monkeypatch.setattr(_binding, "load", lambda: Library(launched))
     monkeypatch.setattr(_binding, "_raw_stream", lambda device: current[-1])
