@@ -272,7 +272,8 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
   long long p = 0;
   int b = -1, page = -1, page_row = 0;
   if (kAppend) {
-    const int mine = blockIdx.x * (32 * kWarps) + threadIdx.x;  // a sequence to be looked at
+    // a sequence to be looked at (in 64 bits: a row alone has 32 threads)
+    const long long mine = (long long)blockIdx.x * (32 * kWarps) + threadIdx.x;
     if (mine < a.d.B) {
       const int first = a.cu[mine], stop = a.cu[mine + 1], ctx = a.context_len[mine];
       const bool ok = in_range(a.d, first, stop, ctx);
