@@ -863,7 +863,19 @@ def _refuse_device(t, name):
                      f"{name} is on another device than the current one")
 
 
+_LOW, _HIGH = -(1 << 31), (1 << 31) - 1
+
+
+def _check_int32(**values):
+    """Refuses what a 32-bit argument does not hold (ctypes would wrap it without a word)."""
+    for name, x in values.items():
+        if not _LOW <= x <= _HIGH:
+            raise ValueError(f"{name} is {x}, which 32 bits do not hold")
+
+
 _NO_STRIDES = (0, 0, 0)
+_DIMS = ("B", "T", "N_max", "Hq", "Hkv", "D", "dtype", "page_size", "n_pages", "table_width",
+         "prefix_len")
 _rope_cache: dict = {}
 
 
@@ -876,6 +888,7 @@ def _rope_structs(strides, dims, interleaved, norm, rope_scale, eps, R):
     if known is None:
         if norm not in NORMS:
             raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
+        _check_int32(rotary_dim=R, **dict(zip(_DIMS, dims)))
         known = (HeadStrides(*(Strides(*s[:2]) for s in strides)), AttendDims(*dims),
                  Rope(R, interleaved, NORMS[norm], rope_scale, eps))
         if len(_rope_cache) >= 256:  # (a server's rows differ from call to call)
@@ -931,10 +944,14 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
                     (dev_status, "dev_status", torch.int32, (B,)))
     if N_max is None:
         N_max = _most_rows(cu_nodes)
+    prefix_len, N_max = int(prefix_len), int(N_max)
+    if not (_LOW <= prefix_len <= _HIGH and _LOW <= N_max <= _HIGH and B <= _HIGH
+            and rows <= _HIGH):
+        _check_int32(prefix_len=prefix_len, N_max=N_max, B=B, T=rows)
     rc = load().gdn_tree_positions(
         None if parent is None else parent.data_ptr(), cu_nodes.data_ptr(),
-        None if context_len is None else context_len.data_ptr(), int(prefix_len),
-        positions.data_ptr(), B, rows, int(N_max),
+        None if context_len is None else context_len.data_ptr(), prefix_len,
+        positions.data_ptr(), B, rows, N_max,
         None if dev_status is None else dev_status.data_ptr(), _stream_of(dev))
     if rc != OK:
         raise GdnTreeError(rc, "gdn_tree_positions")
@@ -952,7 +969,9 @@ def rope_frequencies(rotary_dim, base=10000.0, *, stretch=None, factor=1.0, trai
     positions are slower by factor, those that turn `fast` times or more keep their speed)."""
     if stretch not in STRETCHES:
         raise ValueError(f"stretch must be one of {list(STRETCHES)}, got {stretch!r}")
-    freq = (ctypes.c_uint64 * max(int(rotary_dim) // 2, 1))()
+    _check_int32(rotary_dim=rotary_dim)
+    # (more than the library takes are refused before they are written)
+    freq = (ctypes.c_uint64 * min(max(int(rotary_dim) // 2, 1), 1 << 16))()
     scale = ctypes.c_float()
     rc = load().gdn_tree_rope_frequencies(
         rotary_dim, base, RopeStretch(STRETCHES[stretch], factor, trained_len, fast, slow), freq,

@@ -316,3 +316,69 @@ def test_everything_of_a_call_is_on_its_stream(monkeypatch, name, given):
     want = stream if given else "current"
     assert done and {where for _, where in done} == {want}
     assert launched == [want] or launched == [stream.cuda_stream]
+
+
+@pytest.fixture
+def taken(monkeypatch):
+    """Calls on host tensors that a stand-in of the library takes: what it was called with."""
+    args = []
+
+    class Takes:
+        def __getattr__(self, name):
+            return lambda *a: args.append(a) or gt.OK
+
+    for name in ("_check", "_check_device", "_refuse_device", "_check_heads"):
+        monkeypatch.setattr(_binding, name, lambda *a: None)
+    monkeypatch.setattr(_binding, "load", Takes)
+    monkeypatch.setattr(_binding, "_raw_stream", lambda device: 0)
+    return args
+
+
+def far_call(name, **kw):
+    cu = torch.tensor([0, 3, 6]).int()
+    if name == "tree_positions":
+        return gt.tree_positions(i32(6), cu, **kw)
+    return gt.cache_append_rope(None, f32(6, 1, 16), f32(6, 1, 16), cu, f32(8, 4, 1, 16),
+                                f32(8, 4, 1, 16), i32(2, 2), i32(2), **kw)
+
+
+@pytest.mark.parametrize("name", ["tree_positions", "cache_append_rope"])
+@pytest.mark.parametrize("arg", ["prefix_len", "N_max"])
+def test_values_that_32_bits_do_not_hold_are_refused(taken, name, arg):
+    for far in (2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5, -2 ** 31 - 1, torch.tensor(2 ** 32 + 5)):
+        with pytest.raises(ValueError, match=arg):
+            far_call(name, **{arg: far})
+    assert not taken
+    far_call(name, **{arg: 2 ** 31 - 1})
+    far_call(name, **{arg: -2 ** 31})  # (the library's own check refuses it)
+    assert len(taken) == 2
+
+
+def test_arrays_that_32_bits_do_not_count_are_refused(taken):
+    """More rows than that: one that lies there once (and 5 are not what is left of them)."""
+    rows = f32(1, 1, 16).expand(2 ** 32 + 5, 1, 16)
+    one = i32(1).expand(2 ** 32 + 5)
+    cu = torch.tensor([0, 3]).int()
+    with pytest.raises(ValueError, match="T is 4294967301"):
+        gt.cache_append_rope(None, rows, rows, cu, f32(8, 4, 1, 16), f32(8, 4, 1, 16), i32(1, 2),
+                             i32(1), N_max=3)
+    with pytest.raises(ValueError, match="T is 4294967301"):
+        gt.norm_rope(None, rows, k_out=rows)
+    with pytest.raises(ValueError, match="T is 4294967301"):
+        gt.tree_positions(None, cu, positions=one, N_max=3)
+    with pytest.raises(ValueError, match="B is 4294967300"):
+        gt.tree_positions(None, one, T=3, N_max=3)
+    with pytest.raises(ValueError, match="rotary_dim"):
+        gt.norm_rope(None, f32(6, 1, 16), i32(6), i32(1).long().expand(2 ** 31 + 8))
+    assert not taken
+    for far in (2 ** 32 + 64, 2 ** 31, -2 ** 32 + 64):
+        with pytest.raises(ValueError, match="rotary_dim"):
+            gt.rope_frequencies(far, device="cpu")
+    assert not taken
+
+
+def test_very_many_frequencies_are_refused(lib):
+    for R in (2 ** 31 - 2, 1 << 20):
+        with pytest.raises(gt.GdnTreeError) as e:
+            gt.rope_frequencies(R, device="cpu")
+        assert e.value.code == gt.EUNSUPPORTED
