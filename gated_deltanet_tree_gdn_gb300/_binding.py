@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from operator import index
 
 import torch
 
@@ -944,7 +945,7 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
                     (dev_status, "dev_status", torch.int32, (B,)))
     if N_max is None:
         N_max = _most_rows(cu_nodes)
-    prefix_len, N_max = int(prefix_len), int(N_max)
+    prefix_len, N_max = index(prefix_len), index(N_max)
     if not (_LOW <= prefix_len <= _HIGH and _LOW <= N_max <= _HIGH and B <= _HIGH
             and rows <= _HIGH):
         _check_int32(prefix_len=prefix_len, N_max=N_max, B=B, T=rows)
@@ -1176,7 +1177,7 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
         N_max = _most_rows(cu_nodes)
     strides, dims, rope = _rope_structs(
         (qs, ks, vs, qo, ko, vo),
-        (B, T, int(N_max), Hq, Hkv, D, code, page, n_pages, width, int(prefix_len)), interleaved,
+        (B, T, index(N_max), Hq, Hkv, D, code, page, n_pages, width, index(prefix_len)), interleaved,
         norm, float(rope_scale), float(eps), R)
     rc = load().gdn_tree_cache_append_rope(
         qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu_nodes.data_ptr(), qop, kop, vop,

@@ -382,3 +382,16 @@ def test_very_many_frequencies_are_refused(lib):
         with pytest.raises(gt.GdnTreeError) as e:
             gt.rope_frequencies(R, device="cpu")
         assert e.value.code == gt.EUNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["tree_positions", "cache_append_rope"])
+@pytest.mark.parametrize("arg", ["prefix_len", "N_max"])
+def test_lengths_that_are_no_whole_numbers_are_refused(taken, name, arg):
+    """As by the calls that read the cache: 5.7 is not 5."""
+    for part in (5.7, "5", torch.tensor(5.7), math.inf):
+        with pytest.raises(TypeError):
+            far_call(name, **{arg: part})
+    assert not taken
+    for whole in (5, np.int64(5), torch.tensor(5)):
+        far_call(name, **{arg: whole})
+    assert len(taken) == 3
