@@ -10,7 +10,8 @@ import torch
 
 import gated_deltanet_tree_gdn_gb300 as gt
 from oracle import rope as ref
-from tests.test_rope_gpu import append_inputs, check, host, ints, run_append, want
+from tests.test_rope_gpu import (append_inputs, check, check_append, host, inputs, laid, run,
+                                 run_append, want)
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,145 @@ def test_append_of_arrays_of_very_many_rows(at_the_end):
           "bf16")
     vc = ref.place(host(before[1]), host(x["v"]), x["cu"], x["table"], x["ctx"])
     assert np.array_equal(host(x["v_cache"]), vc)
+
+
+# Heads enough for 5 to 7 passes of a warp that takes a whole row: more than the copies that it has
+# on their way at once, and a change from queries to keys between them.
+MANY = [
+    # Hq, Hkv, D, R, dtype
+    (16, 5, 128, 128, "bf16"),
+    (16, 5, 128, 32, "bf16"),
+    (14, 6, 128, 40, "bf16"),    # pairs across vectors: two at a time
+    (13, 7, 128, 126, "bf16"),   # and one by one (R / 2 odd)
+    (20, 10, 80, 80, "bf16"),
+    (21, 9, 80, 40, "bf16"),
+    (16, 8, 96, 24, "bf16"),
+    (40, 10, 64, 64, "bf16"),
+    (100, 70, 16, 16, "bf16"),
+    (99, 37, 16, 14, "bf16"),
+    (33, 11, 48, 48, "bf16"),
+    (15, 5, 112, 0, "bf16"),
+    (8, 3, 128, 128, "f32"),
+    (7, 4, 128, 20, "f32"),
+    (14, 5, 80, 20, "f32"),
+    (24, 8, 48, 32, "f32"),
+    (9, 3, 112, 10, "f32"),
+    (64, 40, 16, 16, "f32"),
+]
+
+
+def few(x, rows):
+    """The same call's rows `rows` alone, for the definition."""
+    return dict(x, q=x["q"][rows], k=x["k"][rows], positions=x["positions"][rows.numpy()])
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_of_many_rows(shape, interleaved):
+    """From rows that are divided over several warps, so that one takes the last queries and the
+    first keys, to a warp a row (from 14 rows an SM on)."""
+    Hq, Hkv, D, R, dtype = shape
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for i, T in enumerate((2 * sms + 1, 5 * sms, 9 * sms - 5, 14 * sms + 372)):
+        at = D + R // 2 + i + interleaved
+        x = inputs(T, Hq, Hkv, D, R, dtype, ("dense", "fused", "gated", "heads", "same")[at % 5],
+                   seed=T + D + R, norm=("rms", "rms", "unit", None)[at % 4])
+        q, k = run(x, interleaved)
+        some = np.random.default_rng(T).choice(np.arange(40, T - 40), 120, replace=False)
+        rows = torch.tensor(np.concatenate([np.arange(40), np.sort(some), np.arange(T - 40, T)]))
+        y = few(x, rows)
+        check(q[rows], want(y, "q", interleaved), dtype)
+        check(k[rows], want(y, "k", interleaved), dtype)
+
+
+@pytest.mark.parametrize("shape", [MANY[i] for i in (0, 2, 3, 5, 8, 10, 12, 14)],
+                         ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows", ["fused", "gated"])
+def test_many_rows_in_place_and_into_views(shape, interleaved, rows):
+    """Every row of every kind of output is the same, and nothing beside the heads changes."""
+    Hq, Hkv, D, R, dtype = shape
+    T = 14 * torch.cuda.get_device_properties(0).multi_processor_count + 372
+    x = inputs(T, Hq, Hkv, D, R, dtype, rows, seed=D + R, norm="rms")
+    q, k = run(x, interleaved)
+    part = torch.arange(0, T, 17)
+    y = few(x, part)
+    check(q[part], want(y, "q", interleaved), dtype)
+    check(k[part], want(y, "k", interleaved), dtype)
+    r = np.random.default_rng(5)
+    a, b = laid(r, T, Hq, D, dtype, "gated"), laid(r, T, Hkv, D, dtype, "fused")
+    for out, fresh, n in ((a, q, "q_out"), (b, k, "k_out")):
+        kept, own = out._base.clone(), out.clone()
+        run(x, interleaved, **{n: out})
+        assert torch.equal(out, fresh)
+        out.copy_(own)
+        assert torch.equal(out._base, kept)
+    was = {n: (x[n]._base.clone(), x[n].clone()) for n in "qk"}
+    run(x, interleaved, q_out=x["q"], k_out=x["k"])
+    assert torch.equal(x["q"], q) and torch.equal(x["k"], k)
+    for n, (base, own) in was.items():
+        x[n].copy_(own)
+        assert torch.equal(x[n]._base, base)
+
+
+@pytest.mark.parametrize("missing", ["wq", "wk"])
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 128, 64), ("bf16", 80, 40), ("f32", 80, 20)])
+def test_many_rows_with_weights_of_one_of_the_two(missing, dtype, D, R):
+    """A warp goes from queries with weights to keys without, or the other way round."""
+    T = 14 * torch.cuda.get_device_properties(0).multi_processor_count + 40
+    x = inputs(T, 10, 7, D, R, dtype, "fused", seed=23, norm="rms")
+    x[missing] = None
+    q, k = run(x, False)
+    rows = torch.arange(0, T, 11)
+    check(q[rows], want(few(x, rows), "q", False), dtype)
+    check(k[rows], want(few(x, rows), "k", False), dtype)
+
+
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 128, 64), ("bf16", 80, 40), ("f32", 48, 10)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_rows_infinities_and_nan_stay_in_their_heads(dtype, D, R, interleaved):
+    T = 14 * torch.cuda.get_device_properties(0).multi_processor_count + 40
+    x = inputs(T, 16, 8, D, R, dtype, "dense", seed=8, norm="rms")
+    q, k = run(x, interleaved)
+    r = np.random.default_rng(3)
+    bad = [(int(r.integers(T)), int(r.integers(16)), int(r.integers(D))) for _ in range(50)]
+    for n, (t, h, e) in enumerate(bad):
+        x["q"][t, h, e] = (float("inf"), float("nan"), float("-inf"))[n % 3]
+    got, got_k = run(x, interleaved)
+    for t, h, _ in bad:
+        assert not torch.isfinite(got[t, h]).all()
+        got[t, h] = q[t, h]
+    assert torch.equal(got, q) and torch.equal(got_k, k)
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lens", [[700, 1, 0, 1300, 33, 400], [90, 0, 250, 1, 7], [1] * 900])
+def test_append_of_many_rows(shape, interleaved, lens):
+    """A batch of prompts that has a warp a row (from 12 rows an SM on), and batches whose rows are
+    divided over several, one with the last queries and the first keys, or keys and values; beside
+    the cache, and in place."""
+    Hq, Hkv, D, R, dtype = shape
+    Hq, Hkv = (Hq + 1) // 2, (Hkv + 1) // 2
+    at = D + R // 2 + len(lens) + interleaved
+    rows = ("dense", "fused", "gated", "heads")[at % 4]
+    x = append_inputs(lens, [(37 * b + 5) % 90 for b in range(len(lens))], Hq, Hkv, D, R,
+                      (16, 24, 64)[at % 3], dtype, rows, ("rms", "rms", "unit", None)[at % 4],
+                      seed=sum(lens) + D, prefix=1000, extra=at % 3)
+    x["q"] = None if at % 5 == 0 else x["q"]
+    x["wq"] = None if x["q"] is None else x["wq"]
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    status = torch.full((len(lens),), -7, dtype=torch.int32, device="cuda")
+    k_out, v_out = (torch.empty(x["T"], Hkv, D, dtype=x["k"].dtype, device="cuda") for _ in "kv")
+    q, new_len = run_append(x, interleaved, k_out=k_out, v_out=v_out, dev_status=status)
+    assert (status == 0).all()
+    check_append(x, interleaved, before, q, new_len, k_out, v_out)
+    y = dict(x, k_cache=before[0], v_cache=before[1])
+    y.update({n: x[n] if x[n] is None else x[n].clone() for n in "qkv"})
+    run_append(y, interleaved, q_out=y["q"], k_out=y["k"], v_out=y["v"])
+    assert torch.equal(y["k_cache"], x["k_cache"]) and torch.equal(y["v_cache"], x["v_cache"])
+    n = sum(lens)
+    assert torch.equal(y["k"][:n], k_out[:n]) and torch.equal(y["v"], x["v"])
+    assert torch.equal(y["k"][n:], x["k"][n:])
+    if q is not None:
+        assert torch.equal(y["q"][:n], q[:n]) and torch.equal(y["q"][n:], x["q"][n:])
