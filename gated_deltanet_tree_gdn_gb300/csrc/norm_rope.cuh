@@ -373,7 +373,7 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
     Vec<T>::open(y[0], x);
     Vec<T>::open(y[1], x + P);
     float r = 1.f;
-    if (a.rope.norm != GDN_TREE_NORM_NONE) {
+    if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
       float2 two = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 2 * P; ++j) two = fma(x[j], x[j], two);

@@ -181,3 +181,28 @@ def test_append_of_many_rows(shape, interleaved, lens):
     assert torch.equal(y["k"][n:], x["k"][n:])
     if q is not None:
         assert torch.equal(y["q"][:n], q[:n]) and torch.equal(y["q"][n:], x["q"][n:])
+
+
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 128, 64), ("bf16", 80, 40), ("f32", 48, 32)])
+@pytest.mark.parametrize("lens", [[3, 1], [1500, 0, 800]])
+def test_values_are_copied_whatever_they_are(dtype, D, R, lens):
+    """The norm is the keys': values pass bit for bit, infinities and NaN (with their own bits), and
+    nothing of them reaches another head."""
+    x = append_inputs(lens, [7] * len(lens), 4, 6, D, R, 16, dtype, "dense", "rms", seed=12)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    clean = dict(x, k_cache=x["k_cache"].clone(), v_cache=x["v_cache"].clone())
+    q, _ = run_append(clean, False)
+    r = np.random.default_rng(13)
+    odd = np.array([0x7f80, 0xff80, 0x7fff, 0x7f81, 0xffc1, 1], dtype=np.uint16)  # (of bf16)
+    odd = odd.view(np.int16) if dtype == "bf16" else (odd.astype(np.uint32) << 16).view(np.int32)
+    flat = x["v"].view(bits).view(-1)
+    for n in range(60):
+        flat[int(r.integers(flat.numel()))] = int(odd[n % len(odd)])
+    out = torch.empty_like(x["v"])
+    got, _ = run_append(x, False, v_out=out)
+    assert torch.equal(got, q) and torch.equal(x["k_cache"], clean["k_cache"])
+    assert torch.equal(out.view(bits), x["v"].view(bits))
+    at, _ = ref.append_positions(x["cu"], x["ctx"], 0, x["T"])
+    b = np.repeat(np.arange(len(lens)), lens)
+    pages = torch.tensor(x["table"][b, at // 16].astype(np.int64)), torch.tensor(at % 16)
+    assert torch.equal(x["v_cache"].view(bits)[pages], x["v"].view(bits))
