@@ -851,7 +851,7 @@ int gdn_tree_rope_frequencies(int32_t rotary_dim, double base, gdn_tree_rope_str
     double f = pow(base, -2.0 * i / R);
     double slow = s.kind == GDN_TREE_STRETCH_LINEAR ? 1.0 : 0.0;  // how much of it is slowed down
     if (s.kind == GDN_TREE_STRETCH_YARN)
-      slow = fmin(fmax((i - lo) / fmax(hi - lo, 1e-3), 0.0), 1.0);
+      slow = hi > lo ? fmin(fmax((i - lo) / (hi - lo), 0.0), 1.0) : i >= hi;  // (else all of a kind)
     if (s.kind == GDN_TREE_STRETCH_BANDS)
       slow = 1.0 - fmin(fmax((s.trained_len * f / kTurn - s.slow) / (s.fast - s.slow), 0.0), 1.0);
     if (slow > 0.0) f = f * (1.0 - slow) + f / s.factor * slow;

@@ -91,6 +91,7 @@ def frequencies(R, base, stretch=None, factor=1.0, trained_len=0.0, fast=32.0, s
             return R * math.log(trained_len / (2 * math.pi * n)) / (2 * math.log(base))
 
         lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), R - 1)
-        late = np.clip((i - lo) / max(hi - lo, 1e-3), 0, 1)
+        # (all pairs turn fewer than `slow` times, or all more than `fast`: no blend)
+        late = np.clip((i - lo) / (hi - lo), 0, 1) if hi > lo else (i >= hi).astype(L)
         return (1 - late) * f + late * f / factor, 0.1 * math.log(factor) + 1
     return f, 1.0

@@ -395,3 +395,25 @@ def test_lengths_that_are_no_whole_numbers_are_refused(taken, name, arg):
     for whole in (5, np.int64(5), torch.tensor(5)):
         far_call(name, **{arg: whole})
     assert len(taken) == 3
+
+
+@pytest.mark.parametrize("stretch", ["yarn", "bands"])
+@pytest.mark.parametrize("trained_len", [2.0, 5.0, 2 * math.pi, 6.5, 40.0, 300.0, 4096.0, 1e30])
+def test_which_pairs_are_slower(lib, stretch, trained_len):
+    """Pairs that turn `slow` times or less in the trained length are slower by the factor, those
+    that turn `fast` times or more are not, and the ones between are between: where all pairs are
+    of one kind too."""
+    R, factor, fast, slow = 64, 8.0, 4.0, 1.0
+    freq, _ = gt.rope_frequencies(R, stretch=stretch, factor=factor, trained_len=trained_len,
+                                  fast=fast, slow=slow, device="cpu")
+    plain, _ = gt.rope_frequencies(R, device="cpu")
+    for got, f in zip(freq.tolist(), plain.tolist()):
+        turns = trained_len * f * 2.0 ** -64
+        if turns <= slow * (1 - 1e-12):
+            want = f / factor, f / factor
+        elif turns >= fast * (1 + 1e-12):
+            want = f, f
+        else:
+            want = f / factor, f
+        # (4 roundings of 64 bits, and that to a whole number)
+        assert want[0] * (1 - 2.0 ** -51) - 1 <= got <= want[1] * (1 + 2.0 ** -51) + 1
