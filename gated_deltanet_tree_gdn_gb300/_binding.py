@@ -906,7 +906,7 @@ def tree_positions(parent, cu_nodes, *, context_len=None, prefix_len=0, T=None, 
     parent [T] int32, trees of up to 1024 rows (None: every sequence's rows are a chain of any
     length; T or positions then says how many rows there are); cu_nodes [B+1]; context_len [B]
     int32 (None: 0).  positions is allocated when not given; rows of no sequence are left as
-    they are."""
+    they are (of an allocated one: anything)."""
     if stream is not None:
         return _on(stream, tree_positions, locals())
     dev = cu_nodes.get_device()
@@ -1081,7 +1081,8 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
     q [T,Hq,D] (None: keys and values alone) with strides as for ``norm_rope``, whose freq,
     interleaved, rope_scale, norm, weights and eps these are.  k_cache, v_cache
     [n_pages,page_size,Hkv,D] are written in place, as by ``cache_append``.  q_out (the queries
-    normalised and rotated) is allocated when not given; k_out and v_out, where given, get the
+    normalised and rotated) is allocated when not given, and then holds anything in the rows of no
+    sequence (in a given one they are left as they are); k_out and v_out, where given, get the
     rows' keys and values too (what ``attend`` takes beside the cache).  context_len itself is
     not changed: new_len [B] int32 holds the lengths after the call."""
     if stream is not None:

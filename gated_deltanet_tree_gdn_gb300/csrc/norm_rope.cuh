@@ -12,15 +12,16 @@
 // the same elements, so that the cosines and sines of a row are made once (a pair a lane, through
 // shared memory) for all heads that a warp takes, and a pair's elements are in one lane.
 //
-// Measured on one GB300, calls in a CUDA graph over inputs that do not fit the L2 (a plain copy
-// kernel over as many bytes in brackets): 32768 rows of 32 + 8 heads of 128 in bf16, every second
-// 128 elements read, 104 us, 6.5 TB/s (99); 16384 rows of 16 + 16 heads made unit vectors 43.7
-// (41.5); 8191 rows of 16 + 16 heads rotated 22.9 (22); 4096 rows of 32 + 8 heads 16.3 (14.2: they
-// are one round of the SMs, so that every warp's way from its first load to its last store counts);
-// 16 prompts of 17 to 4096 rows into the cache and beside it 84, 6.2 TB/s; one row 2.1, into the
-// cache 2.6.
+// Measured on one GB300, twelve calls or more in a CUDA graph over inputs that do not fit the L2
+// (an elementwise kernel over as many bytes in brackets): 32768 rows of 32 + 8 heads of 128 in bf16,
+// every second 128 elements read, 99.6 us, 6.7 TB/s (96.2); 16384 rows of 16 + 16 heads made unit
+// vectors 42.1 (40.1); 8191 rows of 16 + 16 heads rotated 22.4 (21.3); 4096 rows of 32 + 8 heads
+// 15.8 (14.3: they are one round of the SMs, so that every warp's way from its first load to its
+// last store counts); 16 prompts of 17 to 4096 rows into the cache and beside it 81.5, 6.4 TB/s
+// (75.8); one row 2.0, into the cache 2.7.
 //
-// What that took, on the 32768 rows: vectors by plain loads, one or two passes ahead in registers,
+// What that took, on the 32768 rows (one call a graph here and below, 4 us of which are the graph's
+// start): vectors by plain loads, one or two passes ahead in registers,
 // 130 to 149 us (loads in flight then cost registers, and with them warps); by cp.async, three
 // passes ahead, 120; a lane's weights in registers and not from L1 in every pass, 106; fewer
 // instructions (packed fp32 arithmetic; addresses by steps; lanes a head known to the compiler) and
@@ -41,7 +42,7 @@ namespace {
 constexpr int kWarps = 4, kStages = 4;
 
 // How the pairs of a rotation lie in a lane's two vectors of E elements, number va and vb of the
-// head's D / E (16384 rows of 32 + 8 heads of 128 in bf16: 53 us, 53, and 54 to 77):
+// head's D / E (16384 rows of 32 + 8 heads of 128 in bf16: 52 us, 52, and 56 to 76):
 //   kNeighbours  elements 2 i and 2 i + 1 are in the same vector
 //   kHalves      R a multiple of 2 E (0 included): vb = va + R / 2 E holds va's partners
 //   kCrossed     elements i and i + R / 2 for any other R: rotated in the ring, two pairs a lane
@@ -176,7 +177,9 @@ struct Walk {
 };
 
 // CTAs an SM that the registers are to allow: 7 for rows alone (4096 rows 16.1 us, of 8 16.5, of 5
-// 17.6); 4 for rows for the cache, whose walks want more (2048 tokens 12.3 us, of 5 13.6, of 6 13.9)
+// 17.6); 5 for kCrossed (16384 rows, of 4, 5, 6 and 7: 40 of 80 elements 63, 56, 56 and 60 us, 126 of
+// 128 75, 77, 79 and 80, 20 of 80 in fp32 78, 75, 69 and 70); 4 for rows for the cache, whose walks
+// want more (2048 tokens 12.3 us, of 5 13.6, of 6 13.9)
 constexpr int ctas(Pairs pairs, bool append) { return append ? 4 : pairs == kCrossed ? 5 : 7; }
 
 template <typename T, int kLanes, Pairs kPairs, bool kAppend>
@@ -373,6 +376,7 @@ norm_rope_kernel(const RopeArgs a, const Plan plan) {
     Vec<T>::open(y[0], x);
     Vec<T>::open(y[1], x + P);
     float r = 1.f;
+    // (values' squares too: 16 prompts 83.4 us for 82.9, their keys and values alone 33.0 for 31.8)
     if (!value && a.rope.norm != GDN_TREE_NORM_NONE) {
       float2 two = {0.f, 0.f};
 #pragma unroll

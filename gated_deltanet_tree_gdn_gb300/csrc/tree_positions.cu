@@ -4,7 +4,7 @@
 // every node adds the count of the ancestor that it points at and then points at that one's, so
 // a tree is done after ceil(log2(depth)) rounds.  Eight bytes a row: the launch, a few dependent
 // reads and a barrier a round are the whole time.  One GB300, in a CUDA graph: 32 trees of 128
-// nodes 1.9 us, 256 of 1 to 1024 nodes 3.4, chains of up to 32768 rows 1.7.
+// nodes 1.8 us, 256 of 1 to 1024 nodes 3.5, chains of up to 32768 rows 1.7.
 #include "common.cuh"
 #include "kernels.h"
 

@@ -517,7 +517,8 @@ int gdn_tree_norm_rope(const void *q, const void *k, const int32_t *positions,
  * a single token's own row too.
  * dev_status[b]: GDN_TREE_STATUS_BAD_LAYOUT.  Rows without a place in the cache (a bad page, or
  * past the table) are not written there, their outputs are; of a sequence whose cu_nodes or
- * context_len is invalid nothing is written and new_len[b] = context_len[b].  Where cu_nodes
+ * context_len is invalid nothing is written and new_len[b] = context_len[b].  Outputs of rows
+ * that belong to no sequence are left as they are, as are such a sequence's.  Where cu_nodes
  * decreases, the other sequences are unspecified too (nothing outside the arrays is touched).
  */
 int gdn_tree_cache_append_rope(const void *q, const void *k, const void *v, const uint64_t *freq,
