@@ -10,8 +10,8 @@ import torch
 
 import gated_deltanet_tree_gdn_gb300 as gt
 from oracle import rope as ref
-from tests.test_rope_gpu import (append_inputs, check, check_append, host, inputs, laid, run,
-                                 run_append, want)
+from tests.test_rope_gpu import (append_inputs, check, check_append, host, inputs, ints, laid,
+                                 run, run_append, want)
 
 pytestmark = pytest.mark.gpu
 
@@ -206,3 +206,61 @@ def test_values_are_copied_whatever_they_are(dtype, D, R, lens):
     b = np.repeat(np.arange(len(lens)), lens)
     pages = torch.tensor(x["table"][b, at // 16].astype(np.int64)), torch.tensor(at % 16)
     assert torch.equal(x["v_cache"].view(bits)[pages], x["v"].view(bits))
+
+
+def test_norm_rope_and_positions_of_very_many_rows():
+    """2^27 rows, that one row lies for, at positions of their own; a chain of as many rows."""
+    T, D, R = (1 << 27) + 5, 16, 16
+    x = inputs(1, 1, 1, D, R, "bf16", "dense", seed=51, norm="rms")
+    x["q"], x["wq"] = None, None
+    x["freq"], x["scale"] = gt.rope_frequencies(R, 1e4)
+    starts, ctx = [0, T - 40, T - 7], [3, 2 ** 31 - 100, 0]
+    cu, ends = ints(starts + [T]), np.array(starts[1:] + [T])
+    status = torch.full((3,), -7, dtype=torch.int32, device="cuda")
+    pos = gt.tree_positions(None, cu, context_len=ints(ctx), T=T, dev_status=status)
+    rows = np.array([0, 1, 77, 1 << 25, (1 << 26) - 1, 1 << 26, (1 << 26) + 1] +
+                    list(range(T - 45, T)))
+    b = np.searchsorted(ends, rows, side="right")
+    want_pos = np.array(ctx)[b] + rows - np.array(starts)[b]
+    assert (status == 0).all() and pos[torch.tensor(rows)].tolist() == want_pos.tolist()
+    _, k = gt.norm_rope(None, x["k"].expand(T, 1, D), pos, x["freq"], rope_scale=x["scale"],
+                        norm="rms", k_weight=x["wk"])
+    y = dict(x, k=x["k"].expand(len(rows), 1, D))
+    check(k[torch.tensor(rows)], want(y, "k", False, want_pos), "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 1 << 19, 1 << 18), (3, 70001, 33), (2500, 300, 1)])
+def test_very_many_heads(dtype, T, Hq, Hkv):
+    x = inputs(T, Hq, Hkv, 16, 16, dtype, "fused", seed=52, norm="rms")
+    q, k = run(x, False)
+    rows = torch.arange(0, T, 40)
+    check(q[rows], want(few(x, rows), "q", False), dtype)
+    check(k[rows], want(few(x, rows), "k", False), dtype)
+
+
+@pytest.mark.parametrize("T", [5, 2500])
+@pytest.mark.parametrize("dtype,D,R", [("bf16", 128, 128), ("bf16", 80, 40), ("f32", 64, 64)])
+def test_one_head_for_all(T, dtype, D, R):
+    """An input's heads may be one head that lies there once, its rows overlapping windows."""
+    x = inputs(T, 8, 4, D, R, dtype, "dense", seed=53, norm="unit")
+    x["k"] = x["k"][:, :1].expand(T, 4, D)
+    flat = x["q"].reshape(-1)
+    step = 16 // flat.element_size()
+    x["q"] = torch.as_strided(flat, (T, 8, D), (step, 2 * step, 1))
+    q, k = run(x, False)
+    rows = torch.arange(0, T, 9)
+    check(q[rows], want(few(x, rows), "q", False), dtype)
+    check(k[rows], want(few(x, rows), "k", False), dtype)
+
+
+@pytest.mark.parametrize("norm", ["rms", "unit"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_no_eps_and_any_frequency(norm, interleaved):
+    """An eps of 0, and frequencies over the whole of 64 bits (backwards, and past a half turn)."""
+    x = inputs(40, 3, 2, 64, 12, "f32", "dense", seed=54, norm=norm, far=2 ** 31)
+    x["freq"] = torch.tensor([-1, -(1 << 63), (1 << 63) - 1, 1 << 62, -12345678901234567, 0],
+                             device="cuda")
+    q, k = run(x, interleaved, eps=0.0)
+    check(q, want(x, "q", interleaved, eps=0.0), "f32")
+    check(k, want(x, "k", interleaved, eps=0.0), "f32")
