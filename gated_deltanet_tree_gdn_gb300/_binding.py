@@ -1178,8 +1178,8 @@ def cache_append_rope(q, k, v, cu_nodes, k_cache, v_cache, page_table, context_l
         N_max = _most_rows(cu_nodes)
     strides, dims, rope = _rope_structs(
         (qs, ks, vs, qo, ko, vo),
-        (B, T, index(N_max), Hq, Hkv, D, code, page, n_pages, width, index(prefix_len)), interleaved,
-        norm, float(rope_scale), float(eps), R)
+        (B, T, index(N_max), Hq, Hkv, D, code, page, n_pages, width, index(prefix_len)),
+        interleaved, norm, float(rope_scale), float(eps), R)
     rc = load().gdn_tree_cache_append_rope(
         qp, k.data_ptr(), v.data_ptr(), fp, wq, wk, cu_nodes.data_ptr(), qop, kop, vop,
         k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), context_len.data_ptr(),
